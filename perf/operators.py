@@ -91,13 +91,14 @@ def draw(rng):
     if op == "preference":
         layout = rng.choice(["padded", "packed"])
         P = _log(rng, 1, 256)
+        loss = rng.choice(["sigmoid", "hinge", "ipo", "robust"])
         return dict(op=op, layout=layout, B=2 * P,
                     S=_log(rng, 1, 2048) if layout == "padded" else _log(rng, 2 * P, 1 << 20),
                     dtype=rng.choice(["fp32", "bf16", "fp16"]),
-                    loss=rng.choice(["sigmoid", "hinge", "ipo", "robust"]),
+                    loss=loss,
                     ref=rng.choice(["token", "scores", "none"]), norm=rng.random() < 0.3,
-                    smooth=rng.choice([0.0, 0.1]), nll=rng.choice([0.0, 0.05]),
-                    pairs=rng.choice(["halves", "interleaved"]))
+                    smooth=rng.choice([0.0, 0.1]) if loss in ("sigmoid", "robust") else 0.0,
+                    nll=rng.choice([0.0, 0.05]), pairs=rng.choice(["halves", "interleaved"]))
     if op == "embed":
         return dict(op=op, N=_log(rng, 1, 16384), H=_log(rng, 32, 3584), V=_log(rng, 100, 152064),
                     dtype=rng.choice(["bf16", "bf16", "fp16", "fp32"]), scaled=rng.random() < 0.5)
