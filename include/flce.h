@@ -87,7 +87,7 @@ typedef enum {
 enum {
   FLCE_OK = 0,
   FLCE_ERR_BAD_ARG = 1,       /* NULL pointer, bad reduction, negative coefficient */
-  FLCE_ERR_BAD_SHAPE = 2,     /* N, H or V out of the supported range */
+  FLCE_ERR_BAD_SHAPE = 2,     /* N, H or V out of the supported range; cu_seqlens out of order */
   FLCE_ERR_ALIGN = 3,         /* H (or a [H,V] weight's V) not a multiple of 8, or a pointer
                                * not 16-byte aligned */
   FLCE_ERR_WS_TOO_SMALL = 4,  /* ws_bytes < flce_workspace_size(...) */
@@ -276,6 +276,169 @@ const char* flce_strerror(int code);
 int flce_forward_noalloc(const flce_params* params, const void* hidden, const void* weight,
                          const int64_t* labels, float* loss, float* entropy, float* lse,
                          float* ez, void* stream);
+
+/* ------------------------------------------------------------------------------------
+ * Losses over sequences of tokens, and the embedding lookup: what stands before and
+ * behind the head in a fine-tuning step.  Conventions as above; these calls use one
+ * launch each for the losses (loss and gradients together), and three for the
+ * embedding's gradient.  Their sums have a fixed order: results repeat bit for bit.
+ * Grids of more than one block are cooperative launches.
+ * ---------------------------------------------------------------------------------- */
+
+enum { FLCE_F32 = 0, FLCE_BF16 = 1, FLCE_F16 = 2 };
+
+/* A batch of B sequences of tokens.
+ *   padded (cu_kind 0): arrays [B, S], each with its own row stride ld_* in elements
+ *     (>= 0; the last dimension dense);
+ *   packed: arrays [S] (S tokens in all), sequence i owning [cu_seqlens[i],
+ *     cu_seqlens[i + 1]), cu_seqlens [B + 1] int32 (cu_kind 1) or int64 (cu_kind 2), rising,
+ *     inside [0, S].  Tokens before the first or behind the last sequence do not count
+ *     and have zero gradients.  Offsets out of order or out of range are reported as
+ *     FLCE_ERR_BAD_SHAPE by flce_status (or with validate), the loss is then NaN; no
+ *     access leaves the arrays.
+ *   mask_kind 0: every token counts; 1: bytes, non-zero counts; 2: int64 labels, those
+ *     other than ignore_index count.  What does not count is not looked at: it may hold
+ *     anything, infinities and NaN included.
+ *   dtype: of the log-probabilities, entropies and their gradients. */
+typedef struct {
+  int64_t B, S;
+  const void* cu_seqlens;
+  const void* mask;
+  int64_t ld_mask;
+  int64_t ignore_index;
+  int32_t cu_kind;
+  int32_t mask_kind;
+  int32_t dtype;
+} flce_seqs;
+
+enum { FLCE_KL_K1 = 1, FLCE_KL_K2 = 2, FLCE_KL_K3 = 3 };
+enum { FLCE_RATIO_TOKEN = 0, FLCE_RATIO_SEQUENCE = 1 };
+enum {
+  FLCE_AGG_TOKEN_MEAN = 0,          /* sum over tokens / counted tokens */
+  FLCE_AGG_SEQ_MEAN_TOKEN_MEAN = 1, /* mean over sequences of the token means */
+  FLCE_AGG_SEQ_MEAN_TOKEN_SUM = 2,  /* mean over sequences of the token sums */
+  FLCE_AGG_SUM = 3                  /* scale * sum over tokens */
+};
+
+/* Clipped policy loss.  Per counted token, with d = logp - old_logp (0 without old_logp),
+ * r = exp(d), A the advantage:
+ *   l = -min(r A, clip(r, 1 - clip_low, 1 + clip_high) A)   (A < 0, dual_clip c > 1: not
+ *                                                            above -c A)
+ *       + kl_coef K(logp, ref_logp) - entropy_coef H
+ *   K: k1 = logp - ref, k2 = (logp - ref)^2 / 2, k3 = exp(ref - logp) - 1 - (ref - logp)
+ * d, and ref - logp in k3, are clamped to +-20, with zero gradient beyond.  With
+ * FLCE_RATIO_SEQUENCE d is its mean over the sequence's counted tokens and A is per
+ * sequence.  Sequences without a counted token do not count.  clip_high may be infinite. */
+typedef struct {
+  flce_seqs seqs;
+  int64_t ld_logp, ld_old, ld_ref, ld_entropy, ld_adv;
+  double clip_low, clip_high, dual_clip, kl_coef, entropy_coef, scale;
+  int32_t kl, ratio, aggregate;
+  int32_t adv_per_token; /* advantages [B, S] / [S] (ld_adv), else [B] */
+  int32_t validate;
+} flce_policy_params;
+
+int flce_policy_check_params(const flce_policy_params* params);
+size_t flce_policy_workspace_size(const flce_policy_params* params);
+
+/* Loss and gradients in one launch.
+ *   logp, old_logp, ref_logp, entropy: seqs.dtype (old_logp NULL: the policy itself;
+ *     ref_logp NULL with kl_coef 0; entropy NULL with entropy_coef 0); advantages fp32.
+ *   loss [1], stats [4] fp32 = aggregated policy term, mean KL to the reference, mean
+ *     entropy, mean KL to the old policy (k3), means over counted tokens; counts [4] int64 =
+ *     counted tokens, sequences with one, clipped tokens (sequences), dual-clipped ones.
+ *     All three or none.
+ *   dlogp, dentropy: dense [B, S] or [S], seqs.dtype: the gradients times g_loss[0] (NULL: 1).
+ *     Either may be NULL. */
+int flce_policy_loss(const flce_policy_params* params, const void* logp, const void* old_logp,
+                     const void* ref_logp, const void* entropy, const float* advantages,
+                     const float* g_loss, float* loss, float* stats, int64_t* counts, void* dlogp,
+                     void* dentropy, void* workspace, size_t ws_bytes, void* stream);
+
+/* flce_forward_backward of the policy loss on top of the head: log-probabilities and
+ * entropies of the labels from hidden and weight, the loss, dhidden and dweight, at
+ * 6*N*H*V flops (the logits are not recomputed).
+ *   params: as flce_forward_backward's with reduction FLCE_RED_NONE, without z-loss, label
+ *     smoothing, class weights or shards; N tokens.
+ *   policy: packed (cu_seqlens) or one sequence (padded, B = 1), S = N, dtype FLCE_F32,
+ *     mask_kind 0: the labels other than ignore_index count.  A sequence ratio needs all
+ *     tokens in one chunk (chunk_n >= N).
+ *   logp, entropy: [N] fp32 outputs.  The others as in the two calls.
+ *   workspace: >= flce_policy_head_workspace_size(params, policy). */
+size_t flce_policy_head_workspace_size(const flce_params* params,
+                                       const flce_policy_params* policy);
+int flce_policy_forward_backward(const flce_params* params, const flce_policy_params* policy,
+                                 const void* hidden, const void* weight, const int64_t* labels,
+                                 const float* old_logp, const float* ref_logp,
+                                 const float* advantages, const float* g_loss, float* loss,
+                                 float* stats, int64_t* counts, float* logp, float* entropy,
+                                 void* dhidden, void* dweight, void* workspace,
+                                 size_t ws_bytes, void* stream);
+
+enum {
+  FLCE_PREF_SIGMOID = 0, /* -(1 - e) ln sig(h) - e ln sig(-h) */
+  FLCE_PREF_ROBUST = 1,  /* (-(1 - e) ln sig(h) + e ln sig(-h)) / (1 - 2 e) */
+  FLCE_PREF_HINGE = 2,   /* max(0, 1 - h) */
+  FLCE_PREF_IPO = 3      /* (h / beta - 1 / (2 beta))^2 */
+};
+
+/* Preference loss over B / 2 pairs of sequences (B even): chosen c, rejected r,
+ *   s_i = sum over counted tokens of (logp - ref_logp)  [/ their number: length_normalised]
+ *         - ref_scores[i],
+ *   h = beta (s_c - s_r) - margin; the loss of the pair by kind, plus
+ *   nll_coef * (-(mean over c's counted tokens of logp)).
+ * interleaved 0: sequence i < B / 2 is chosen and B / 2 + i its rejected one; 1: 2i and
+ * 2i + 1.  Pairs with a side without a counted token do not count. */
+typedef struct {
+  flce_seqs seqs;
+  int64_t ld_logp, ld_ref;
+  double beta, margin, label_smoothing, nll_coef;
+  int32_t kind, length_normalised, interleaved;
+  int32_t reduction; /* flce_reduction, over the counted pairs */
+  int32_t validate;
+} flce_preference_params;
+
+int flce_preference_check_params(const flce_preference_params* params);
+size_t flce_preference_workspace_size(const flce_preference_params* params);
+
+/* Loss and gradient in one launch.
+ *   ref_logp: as logp, or NULL; ref_scores: [B] fp32 reference scores, or NULL.
+ *   loss: [1], or [B / 2] for FLCE_RED_NONE; rewards [B] = beta s_i (0 where nothing
+ *     counts).  Both or none.
+ *   dlogp: dense, seqs.dtype, times g_loss ([1], or [B / 2] for FLCE_RED_NONE; NULL: 1). */
+int flce_preference_loss(const flce_preference_params* params, const void* logp,
+                         const void* ref_logp, const float* ref_scores, const float* g_loss,
+                         float* loss, float* rewards, void* dlogp, void* workspace,
+                         size_t ws_bytes, void* stream);
+
+/* Embedding lookup out[n] = scale * weight[ids[n]] and its gradient. */
+typedef struct {
+  int64_t N, H, V;     /* ids, row length, rows of weight (any H >= 1) */
+  int64_t v_offset;    /* weight holds rows [v_offset, v_offset + V) of a table of v_total */
+  int64_t v_total;     /* 0: the whole table */
+  int64_t padding_idx; /* an id without a gradient, -1: none */
+  double scale;
+  int32_t dtype;       /* of weight, out and dout */
+  int32_t grad_dtype;  /* of dweight: dtype or FLCE_F32 */
+  int32_t ids_int64;   /* 1: int64, 0: int32 */
+  int32_t accumulate;  /* backward: add to dweight, whose other rows stay untouched */
+  int32_t validate;
+} flce_embedding_params;
+
+int flce_embedding_check_params(const flce_embedding_params* params);
+size_t flce_embedding_workspace_size(const flce_embedding_params* params);
+
+/* Lookup.  A row of another shard is zero; an id outside the table gives a row of NaN and
+ * FLCE_ERR_LABEL with validate, which needs a workspace of 256 bytes (else NULL, 0). */
+int flce_embedding(const flce_embedding_params* params, const void* ids, const void* weight,
+                   void* out, void* workspace, size_t ws_bytes, void* stream);
+
+/* dweight[v] = scale * sum of dout[n] over the n with ids[n] = v (added to dweight[v] with
+ * accumulate), summed in fp32 in the order of n and rounded once.  Ids outside the table
+ * are left out and reported as FLCE_ERR_LABEL by flce_status. */
+int flce_embedding_backward(const flce_embedding_params* params, const void* dout,
+                            const void* ids, void* dweight, void* workspace, size_t ws_bytes,
+                            void* stream);
 
 /* Library version as MAJOR*10000 + MINOR*100 + PATCH. */
 int flce_version(void);

@@ -40,6 +40,42 @@ class FlceParams(ctypes.Structure):
                 ("dhidden_fp32", ctypes.c_int32)]
 
 
+class FlceSeqs(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("S", ctypes.c_int64), ("cu_seqlens", ctypes.c_void_p),
+                ("mask", ctypes.c_void_p), ("ld_mask", ctypes.c_int64),
+                ("ignore_index", ctypes.c_int64), ("cu_kind", ctypes.c_int32),
+                ("mask_kind", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class FlcePolicyParams(ctypes.Structure):
+    _fields_ = [("seqs", FlceSeqs), ("ld_logp", ctypes.c_int64), ("ld_old", ctypes.c_int64),
+                ("ld_ref", ctypes.c_int64), ("ld_entropy", ctypes.c_int64),
+                ("ld_adv", ctypes.c_int64), ("clip_low", ctypes.c_double),
+                ("clip_high", ctypes.c_double), ("dual_clip", ctypes.c_double),
+                ("kl_coef", ctypes.c_double), ("entropy_coef", ctypes.c_double),
+                ("scale", ctypes.c_double), ("kl", ctypes.c_int32), ("ratio", ctypes.c_int32),
+                ("aggregate", ctypes.c_int32), ("adv_per_token", ctypes.c_int32),
+                ("validate", ctypes.c_int32)]
+
+
+class FlcePreferenceParams(ctypes.Structure):
+    _fields_ = [("seqs", FlceSeqs), ("ld_logp", ctypes.c_int64), ("ld_ref", ctypes.c_int64),
+                ("beta", ctypes.c_double), ("margin", ctypes.c_double),
+                ("label_smoothing", ctypes.c_double), ("nll_coef", ctypes.c_double),
+                ("kind", ctypes.c_int32), ("length_normalised", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("reduction", ctypes.c_int32),
+                ("validate", ctypes.c_int32)]
+
+
+class FlceEmbeddingParams(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int64), ("H", ctypes.c_int64), ("V", ctypes.c_int64),
+                ("v_offset", ctypes.c_int64), ("v_total", ctypes.c_int64),
+                ("padding_idx", ctypes.c_int64), ("scale", ctypes.c_double),
+                ("dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32),
+                ("ids_int64", ctypes.c_int32), ("accumulate", ctypes.c_int32),
+                ("validate", ctypes.c_int32)]
+
+
 WEIGHT_HV, WEIGHT_VH = 0, 1
 
 
@@ -59,7 +95,12 @@ EXPORTED = ("flce_workspace_size", "flce_forward", "flce_backward", "flce_status
             "flce_kernel_launches", "flce_strerror", "flce_version", "flce_forward_noalloc",
             "flce_shard_stats", "flce_combine_shards", "flce_forward_backward",
             "flce_scale_bf16", "flce_selftest_wait_timeout", "flce_plan_tiles",
-            "flce_check_params")
+            "flce_check_params", "flce_policy_check_params", "flce_policy_workspace_size",
+            "flce_policy_loss", "flce_policy_head_workspace_size",
+            "flce_policy_forward_backward", "flce_preference_check_params",
+            "flce_preference_workspace_size", "flce_preference_loss",
+            "flce_embedding_check_params", "flce_embedding_workspace_size", "flce_embedding",
+            "flce_embedding_backward")
 
 
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
@@ -129,6 +170,26 @@ def _open(path: str) -> ctypes.CDLL:
     lib.flce_plan_tiles.argtypes = [i32, i32, i32, ctypes.c_int64, i32, i32, i32,
                                     ctypes.POINTER(i32)]
     lib.flce_plan_tiles.restype = ctypes.c_int
+    for name, params in (("policy", FlcePolicyParams), ("preference", FlcePreferenceParams),
+                         ("embedding", FlceEmbeddingParams)):
+        check = getattr(lib, f"flce_{name}_check_params")
+        check.argtypes, check.restype = [ctypes.POINTER(params)], ctypes.c_int
+        size = getattr(lib, f"flce_{name}_workspace_size")
+        size.argtypes, size.restype = [ctypes.POINTER(params)], ctypes.c_size_t
+    Q, sz = ctypes.POINTER(FlcePolicyParams), ctypes.c_size_t
+    lib.flce_policy_loss.argtypes = [Q] + [vp] * 12 + [sz, vp]
+    lib.flce_policy_loss.restype = ctypes.c_int
+    lib.flce_policy_head_workspace_size.argtypes = [P, Q]
+    lib.flce_policy_head_workspace_size.restype = sz
+    lib.flce_policy_forward_backward.argtypes = [P, Q] + [vp] * 15 + [sz, vp]
+    lib.flce_policy_forward_backward.restype = ctypes.c_int
+    lib.flce_preference_loss.argtypes = [ctypes.POINTER(FlcePreferenceParams)] + [vp] * 8 + [sz, vp]
+    lib.flce_preference_loss.restype = ctypes.c_int
+    E = ctypes.POINTER(FlceEmbeddingParams)
+    lib.flce_embedding.argtypes = [E, vp, vp, vp, vp, sz, vp]
+    lib.flce_embedding.restype = ctypes.c_int
+    lib.flce_embedding_backward.argtypes = [E, vp, vp, vp, vp, sz, vp]
+    lib.flce_embedding_backward.restype = ctypes.c_int
     lib.flce_version.argtypes = []
     lib.flce_version.restype = ctypes.c_int
     return lib

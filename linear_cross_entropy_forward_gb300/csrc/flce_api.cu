@@ -29,6 +29,7 @@
 
 #include "../../include/flce.h"
 #include "flce_gemm.cuh"
+#include "flce_host.h"
 #include "flce_kernels.cuh"
 
 namespace flce {
@@ -293,6 +294,15 @@ int device_info(DevInfo* out) {
   return FLCE_OK;
 }
 
+}  // namespace
+
+int require_device(int* sms) {
+  DevInfo di;
+  const int rc = device_info(&di);
+  *sms = di.sms;
+  return rc;
+}
+
 // The error word is copied on `st` itself, after the call's work, so that reading it
 // waits for nothing but that stream (a plain cudaMemcpy would also wait for the legacy
 // default stream).
@@ -304,9 +314,12 @@ int read_status(const void* workspace, cudaStream_t st) {
     return FLCE_ERR_CUDA;
   if (word & FLCE_DEVERR_BOUNDS) return FLCE_ERR_BOUNDS;
   if (word & FLCE_DEVERR_TIMEOUT) return FLCE_ERR_TIMEOUT;
+  if (word & FLCE_DEVERR_SEQS) return FLCE_ERR_BAD_SHAPE;
   if (word & FLCE_DEVERR_LABEL) return FLCE_ERR_LABEL;
   return FLCE_OK;
 }
+
+namespace {
 
 inline int cuda_rc(cudaError_t e) { return e == cudaSuccess ? FLCE_OK : FLCE_ERR_CUDA; }
 
@@ -890,11 +903,17 @@ int flce_backward(const flce_params* p, const void* hidden, const void* weight,
   return p->validate ? read_status(ws, st) : FLCE_OK;
 }
 
-int flce_forward_backward(const flce_params* p, const void* hidden, const void* weight,
-                          const int64_t* labels, const float* g_loss, const float* g_entropy,
-                          float* loss, float* entropy, float* lse, float* ez, void* dhidden,
-                          void* dweight, void* workspace, size_t ws_bytes, void* stream) {
-  using namespace flce;
+}  // extern "C"
+
+namespace flce {
+
+int64_t fused_chunks(const flce_params* p) { return fused_layout(p).chunks; }
+
+int forward_backward(const flce_params* p, const void* hidden, const void* weight,
+                     const int64_t* labels, const float* g_loss, const float* g_entropy,
+                     float* loss, float* entropy, float* lse, float* ez, void* dhidden,
+                     void* dweight, void* workspace, size_t ws_bytes, void* stream,
+                     const GradHook* hook) {
   int rc = check_params(p);
   if (rc) return rc;
   // the dlogits of a shard need the whole vocabulary's logsumexp first
@@ -913,10 +932,12 @@ int flce_forward_backward(const flce_params* p, const void* hidden, const void* 
   if ((rc = begin_call(workspace, ws_bytes, L.total, stream, &st, &err))) return rc;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const int64_t N = p->N, H = p->H, V = p->V;
+  if (hook) hook->begin(hook->ctx, err);
   if (N == 0) {
     if ((rc = zero_reduced(p, loss, entropy, st))) return rc;
     if ((rc = cuda_rc(cudaMemsetAsync(dweight, 0, static_cast<size_t>(H * V) * 2, st))))
       return rc;
+    if (hook && (rc = hook->end(hook->ctx, 0, st))) return rc;
     return p->validate ? read_status(ws, st) : FLCE_OK;
   }
   const bool vh = p->weight_layout == FLCE_WEIGHT_VH;
@@ -968,6 +989,7 @@ int flce_forward_backward(const flce_params* p, const void* hidden, const void* 
         pt, rows, so.zlabel, lab, V, p->ignore_index, p->zloss_coef, sm, lse + n0, ez + n0,
         loss_row + n0, ent_row + n0, err);
     if ((rc = cuda_rc(cudaGetLastError()))) return rc;
+    if (hook && (rc = hook->mid(hook->ctx, n0, rows, L.chunks, st))) return rc;
     bwd_prep_kernel<<<1, 1024, 0, st>>>(
         lab, labels, N, lse + n0, ez + n0, g_loss && per_token ? g_loss + n0 : g_loss,
         g_entropy && per_token ? g_entropy + n0 : g_entropy, rows, V, p->ignore_index,
@@ -1063,7 +1085,20 @@ int flce_forward_backward(const flce_params* p, const void* hidden, const void* 
                                            p->zloss_coef, loss, entropy);
     if ((rc = cuda_rc(cudaGetLastError()))) return rc;
   }
+  if (hook && (rc = hook->end(hook->ctx, L.chunks, st))) return rc;
   return p->validate ? read_status(ws, st) : FLCE_OK;
+}
+
+}  // namespace flce
+
+extern "C" {
+
+int flce_forward_backward(const flce_params* p, const void* hidden, const void* weight,
+                          const int64_t* labels, const float* g_loss, const float* g_entropy,
+                          float* loss, float* entropy, float* lse, float* ez, void* dhidden,
+                          void* dweight, void* workspace, size_t ws_bytes, void* stream) {
+  return flce::forward_backward(p, hidden, weight, labels, g_loss, g_entropy, loss, entropy, lse,
+                                ez, dhidden, dweight, workspace, ws_bytes, stream, nullptr);
 }
 
 int flce_scale_bf16(void* x, int64_t n, const float* g, void* stream) {

@@ -31,6 +31,7 @@ enum : uint32_t {
   FLCE_DEVERR_TIMEOUT = 1u,
   FLCE_DEVERR_LABEL = 2u,
   FLCE_DEVERR_BOUNDS = 4u,  // an in-kernel bounds check of the FLCE_DEBUG build failed
+  FLCE_DEVERR_SEQS = 8u,    // cu_seqlens out of order or outside the token axis
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {

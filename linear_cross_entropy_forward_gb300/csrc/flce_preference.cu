@@ -1,0 +1,318 @@
+// Preference loss over pairs of sequences, and its gradient.
+//
+// Sequence i scores s_i = sum_t (lp_t - ref_t) over its counted tokens (divided by their
+// number where lengths are normalised); a pair of a chosen c and a rejected sequence r has
+//   h = beta (s_c - s_r) - margin
+//   sigmoid  -(1 - e) ln sig(h) - e ln sig(-h)          (e: label smoothing)
+//   robust   (-(1 - e) ln sig(h) + e ln sig(-h)) / (1 - 2e)
+//   hinge    max(0, 1 - h)
+//   ipo      (h / beta - 1 / (2 beta))^2
+// plus nll_coef times the chosen side's mean negative log-likelihood.  A pair with a side
+// of which nothing counts is left out.  The gradient of a counted token is its sequence's
+// coefficient.
+//
+// One launch: sums of the pieces; a warp per pair, which adds its two sequences' pieces in
+// order in fp64; totals, the loss and the gradients.  The gradient pass reads only the mask.
+#include <cmath>
+
+#include "flce_device.cuh"
+#include "flce_host.h"
+#include "flce_seq.cuh"
+
+namespace flce {
+
+namespace {
+
+struct PrefPiece {
+  float score, like;
+  int n;
+  int pad;
+};
+
+struct PrefArgs {
+  Seqs q;
+  const void *lp, *ref;
+  int64_t lp_skip, ref_skip;
+  const float* ref_scores;
+  double beta, margin, smooth, nll;
+  int kind, norm, interleaved, reduction, want_loss;
+  int64_t pieces;
+  const float* g_loss;
+  float *loss, *rewards;
+  void* dlp;
+  uint32_t* err;
+  PrefPiece* piece;
+  float* coef;       // [B] gradient of the pair's own loss by a token of sequence i
+  float* pair_loss;  // [B / 2]
+  int* pair_ok;      // [B / 2]
+};
+
+__device__ __forceinline__ double softplus(double x) {  // ln(1 + e^x)
+  return fmax(x, 0.0) + log1p(exp(-fabs(x)));
+}
+__device__ __forceinline__ double sigmoid(double x) { return 1.0 / (1.0 + exp(-x)); }
+
+// The pair's loss and its derivative by h.
+__device__ void pair_value(const PrefArgs& a, double h, double& l, double& dh) {
+  const double e = a.smooth;
+  switch (a.kind) {
+    case FLCE_PREF_SIGMOID:
+      l = (1.0 - e) * softplus(-h) + e * softplus(h);
+      dh = -(1.0 - e) * sigmoid(-h) + e * sigmoid(h);
+      break;
+    case FLCE_PREF_ROBUST:
+      l = ((1.0 - e) * softplus(-h) - e * softplus(h)) / (1.0 - 2.0 * e);
+      dh = (-(1.0 - e) * sigmoid(-h) - e * sigmoid(h)) / (1.0 - 2.0 * e);
+      break;
+    case FLCE_PREF_HINGE:
+      l = h < 1.0 ? 1.0 - h : (h != h ? h : 0.0);
+      dh = h < 1.0 ? -1.0 : 0.0;
+      break;
+    default: {
+      const double u = (h - 0.5) / a.beta;
+      l = u * u;
+      dh = 2.0 * u / a.beta;
+    }
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kSeqThreads, kSeqBlocksPerSm) preference_kernel(PrefArgs a) {
+  const Seqs& q = a.q;
+  const T* lp_ = static_cast<const T*>(a.lp);
+  const T* ref_ = static_cast<const T*>(a.ref);
+  for (int64_t u = blockIdx.x; u < a.pieces; u += gridDim.x) {
+    const Piece pc = find_piece(q, u);
+    float f[2] = {0, 0};
+    int c[1] = {0};
+#pragma unroll
+    for (int k = 0; k < kSeqPerThread; ++k) {
+      const int64_t p = pc.begin + threadIdx.x + k * kSeqThreads;
+      if (p >= pc.end || !token_counts(q, pc.seq, p)) continue;
+      const float lp = load_f(lp_ + p + pc.seq * a.lp_skip);
+      f[0] += ref_ ? lp - load_f(ref_ + p + pc.seq * a.ref_skip) : lp;
+      f[1] += lp;
+      ++c[0];
+    }
+    block_sums(f, c);
+    if (threadIdx.x == 0) a.piece[u] = {f[0], f[1], c[0], 0};
+  }
+  grid_barrier();
+
+  const int64_t pairs = q.B / 2;
+  const int lane = threadIdx.x & 31;
+  for (int64_t i = blockIdx.x * int64_t(kSeqWarps) + (threadIdx.x >> 5); i < pairs;
+       i += gridDim.x * int64_t(kSeqWarps)) {
+    int64_t id[2];
+    double score[2], like = 0.0;
+    long long n[2];
+    id[0] = a.interleaved ? 2 * i : i;
+    id[1] = a.interleaved ? 2 * i + 1 : pairs + i;
+    for (int side = 0; side < 2; ++side) {
+      const int64_t s = id[side], s0 = seq_start(q, s), s1 = seq_start(q, s + 1);
+      const int64_t last = s1 > s0 ? (s1 - 1) / kTile + s : -1;
+      double sc = 0.0, lk = 0.0;
+      long long c = 0;
+      for (int64_t u = s0 / kTile + s + lane; u <= last; u += 32) {
+        const PrefPiece r = a.piece[u];
+        sc += r.score;
+        lk += r.like;
+        c += r.n;
+      }
+      score[side] = warp_sum(sc);
+      n[side] = warp_sum(c);
+      lk = warp_sum(lk);
+      if (side == 0) like = lk;
+    }
+    if (lane == 0) {
+      const double per[2] = {n[0] > 0 ? 1.0 / static_cast<double>(n[0]) : 0.0,
+                             n[1] > 0 ? 1.0 / static_cast<double>(n[1]) : 0.0};
+      for (int side = 0; side < 2; ++side) {
+        if (a.norm) score[side] *= per[side];
+        if (a.ref_scores) score[side] -= __ldg(a.ref_scores + id[side]);
+        if (n[side] == 0) score[side] = 0.0;
+      }
+      const bool ok = n[0] > 0 && n[1] > 0;
+      double l = 0.0, dh = 0.0;
+      if (ok) {
+        pair_value(a, a.beta * (score[0] - score[1]) - a.margin, l, dh);
+        l -= a.nll * like * per[0];
+      }
+      a.pair_loss[i] = static_cast<float>(l);
+      a.pair_ok[i] = ok;
+      const double d = a.beta * dh;
+      a.coef[id[0]] = ok ? static_cast<float>(d * (a.norm ? per[0] : 1.0) - a.nll * per[0]) : 0.0f;
+      a.coef[id[1]] = ok ? static_cast<float>(-d * (a.norm ? per[1] : 1.0)) : 0.0f;
+      if (a.want_loss) {
+        a.rewards[id[0]] = static_cast<float>(a.beta * score[0]);
+        a.rewards[id[1]] = static_cast<float>(a.beta * score[1]);
+      }
+    }
+  }
+  grid_barrier();
+
+  long long live = 0;
+  for (int64_t i = threadIdx.x; i < pairs; i += kSeqThreads) live += a.pair_ok[i];
+  live = block_total(live);
+  const float scale =
+      a.reduction == FLCE_RED_MEAN ? (live > 0 ? 1.0f / static_cast<float>(live) : 0.0f) : 1.0f;
+  if (blockIdx.x == 0) {
+    const bool ok = seqs_ok(q);
+    const float nan = __int_as_float(0x7fc00000);
+    if (threadIdx.x == 0) *a.err = ok ? 0u : FLCE_DEVERR_SEQS;
+    if (a.want_loss) {
+      double l = 0.0;
+      for (int64_t i = threadIdx.x; i < pairs; i += kSeqThreads) {
+        const float v = ok ? a.pair_loss[i] : nan;
+        if (a.reduction == FLCE_RED_NONE) a.loss[i] = v;
+        l += v;
+      }
+      if (a.reduction != FLCE_RED_NONE) {
+        l = block_total(l);
+        if (threadIdx.x == 0) {
+          if (a.reduction == FLCE_RED_MEAN && live > 0) l /= static_cast<double>(live);
+          a.loss[0] = ok ? static_cast<float>(l) : nan;
+        }
+      }
+    }
+  }
+  T* dlp_ = static_cast<T*>(a.dlp);
+  if (!dlp_) return;
+  if (q.cu) {
+    const int64_t first = seq_start(q, 0), end = seq_start(q, q.B);
+    for (int64_t p = blockIdx.x * int64_t(kSeqThreads) + threadIdx.x; p < q.total;
+         p += gridDim.x * int64_t(kSeqThreads))
+      if (p < first || p >= end) store_f(dlp_ + p, 0.0f);
+  }
+  for (int64_t u = blockIdx.x; u < a.pieces; u += gridDim.x) {
+    const Piece pc = find_piece(q, u);
+    if (pc.begin >= pc.end) continue;
+    float g = a.coef[pc.seq] * scale;
+    if (a.g_loss) {
+      const int64_t pair = a.interleaved ? pc.seq / 2 : pc.seq % pairs;
+      g *= __ldg(a.g_loss + (a.reduction == FLCE_RED_NONE ? pair : 0));
+    }
+#pragma unroll
+    for (int k = 0; k < kSeqPerThread; ++k) {
+      const int64_t p = pc.begin + threadIdx.x + k * kSeqThreads;
+      if (p < pc.end) store_f(dlp_ + p, token_counts(q, pc.seq, p) ? g : 0.0f);
+    }
+  }
+}
+
+inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+struct PrefLayout {
+  size_t piece, coef, pair_loss, pair_ok, total;
+};
+
+PrefLayout pref_layout(const Seqs& q) {
+  PrefLayout L{};
+  const int64_t B = q.B > 0 ? q.B : 1;
+  size_t off = 256;
+  L.piece = off; off += align256(seq_pieces(q.B, q.total) * sizeof(PrefPiece));
+  L.coef = off; off += align256(B * 4);
+  L.pair_loss = off; off += align256(B * 4);
+  L.pair_ok = off; off += align256(B * 4);
+  L.total = off;
+  return L;
+}
+
+int pref_check(const flce_preference_params* p, Seqs* q) {
+  if (!p) return FLCE_ERR_BAD_ARG;
+  const int rc = make_seqs(&p->seqs, q);
+  if (rc) return rc;
+  if (q->B % 2) return FLCE_ERR_BAD_SHAPE;
+  if (p->kind < FLCE_PREF_SIGMOID || p->kind > FLCE_PREF_IPO) return FLCE_ERR_BAD_ARG;
+  if (p->reduction < FLCE_RED_NONE || p->reduction > FLCE_RED_SUM) return FLCE_ERR_BAD_ARG;
+  if (!(p->beta > 0.0) || !std::isfinite(p->beta) || !std::isfinite(p->margin) ||
+      !std::isfinite(p->nll_coef))
+    return FLCE_ERR_BAD_ARG;
+  if (!(p->label_smoothing >= 0.0 && p->label_smoothing < 0.5)) return FLCE_ERR_BAD_ARG;
+  // smoothing flips labels: only the logistic losses have that reading
+  if (p->label_smoothing != 0.0 && p->kind != FLCE_PREF_SIGMOID && p->kind != FLCE_PREF_ROBUST)
+    return FLCE_ERR_BAD_ARG;
+  if ((p->length_normalised | p->interleaved | 1) != 1) return FLCE_ERR_BAD_ARG;
+  return FLCE_OK;
+}
+
+inline bool misaligned(const void* p, int bytes) {
+  return reinterpret_cast<uintptr_t>(p) & (bytes - 1);
+}
+
+}  // namespace
+}  // namespace flce
+
+using namespace flce;
+
+extern "C" {
+
+int flce_preference_check_params(const flce_preference_params* p) {
+  Seqs q;
+  return pref_check(p, &q);
+}
+
+size_t flce_preference_workspace_size(const flce_preference_params* p) {
+  Seqs q;
+  return pref_check(p, &q) == FLCE_OK ? pref_layout(q).total : 0;
+}
+
+int flce_preference_loss(const flce_preference_params* p, const void* logp, const void* ref_logp,
+                         const float* ref_scores, const float* g_loss, float* loss,
+                         float* rewards, void* dlogp, void* workspace, size_t ws_bytes,
+                         void* stream) {
+  PrefArgs a{};
+  int rc = pref_check(p, &a.q);
+  if (rc) return rc;
+  if (!workspace || (!loss && !dlogp) || (loss && !rewards && a.q.B > 0)) return FLCE_ERR_BAD_ARG;
+  if (a.q.total > 0 && !logp) return FLCE_ERR_BAD_ARG;
+  const int dt = p->seqs.dtype, eb = seq_elem_bytes(dt);
+  if (misaligned(logp, eb) || misaligned(ref_logp, eb) || misaligned(dlogp, eb) ||
+      misaligned(ref_scores, 4) || misaligned(g_loss, 4) || misaligned(loss, 4) ||
+      misaligned(rewards, 4) || misaligned(workspace, 256))
+    return FLCE_ERR_ALIGN;
+  const PrefLayout L = pref_layout(a.q);
+  if (ws_bytes < L.total) return FLCE_ERR_WS_TOO_SMALL;
+  int sms;
+  if ((rc = require_device(&sms))) return rc;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const bool packed = p->seqs.cu_kind != 0;
+  a.lp = logp;
+  a.ref = ref_logp;
+  a.lp_skip = packed ? 0 : p->ld_logp - p->seqs.S;
+  a.ref_skip = packed ? 0 : p->ld_ref - p->seqs.S;
+  a.ref_scores = ref_scores;
+  a.beta = p->beta;
+  a.margin = p->margin;
+  a.smooth = p->label_smoothing;
+  a.nll = p->nll_coef;
+  a.kind = p->kind;
+  a.norm = p->length_normalised;
+  a.interleaved = p->interleaved;
+  a.reduction = p->reduction;
+  a.want_loss = loss != nullptr;
+  a.pieces = seq_pieces(a.q.B, a.q.total);
+  a.g_loss = g_loss;
+  a.loss = loss;
+  a.rewards = rewards;
+  a.dlp = dlogp;
+  a.err = reinterpret_cast<uint32_t*>(ws);
+  a.piece = reinterpret_cast<PrefPiece*>(ws + L.piece);
+  a.coef = reinterpret_cast<float*>(ws + L.coef);
+  a.pair_loss = reinterpret_cast<float*>(ws + L.pair_loss);
+  a.pair_ok = reinterpret_cast<int*>(ws + L.pair_ok);
+  const int64_t cap = int64_t(sms) * kSeqBlocksPerSm;
+  const int64_t blocks = a.pieces < cap ? a.pieces : cap;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (dt == FLCE_F32)
+    e = launch_seq(preference_kernel<float>, a, blocks, st);
+  else if (dt == FLCE_BF16)
+    e = launch_seq(preference_kernel<__nv_bfloat16>, a, blocks, st);
+  else
+    e = launch_seq(preference_kernel<__half>, a, blocks, st);
+  if (e != cudaSuccess) return FLCE_ERR_CUDA;
+  return p->validate ? read_status(workspace, st) : FLCE_OK;
+}
+
+}  // extern "C"

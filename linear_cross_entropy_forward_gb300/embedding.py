@@ -1,0 +1,141 @@
+"""Embedding lookup with scaling, and its gradient by sorted tokens.
+
+The table is [V, H], the layout of an LM head with weight_layout 'vh', so that one matrix
+can be both (a tied model): the head's dweight then takes the lookup's gradient in place
+with accumulate=True.  Argument marshalling only; the library's kernels do the work.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import _binding as B
+from .losses import _DTYPES, _allocate_on, _workspace
+
+
+def embedding_params(N, H, V, scale=1.0, dtype=torch.bfloat16, grad_dtype=None, ids_int64=True,
+                     accumulate=False, padding_idx=None, v_offset=0, v_total=0, validate=False):
+    """FlceEmbeddingParams; padding_idx None: none."""
+    for d in (dtype, grad_dtype or dtype):
+        if d not in _DTYPES:
+            raise TypeError(f"embedding types are float32, bfloat16 and float16, got {d}")
+    return B.FlceEmbeddingParams(int(N), int(H), int(V), int(v_offset), int(v_total),
+                                 -1 if padding_idx is None else int(padding_idx), float(scale),
+                                 _DTYPES[dtype], _DTYPES[grad_dtype or dtype], int(ids_int64),
+                                 int(accumulate), int(validate))
+
+
+def embedding_workspace_size(params: "B.FlceEmbeddingParams") -> int:
+    """Bytes of workspace a flce_embedding_backward call with these parameters needs."""
+    lib = B.load_library()
+    B._check(lib.flce_embedding_check_params(ctypes.byref(params)))
+    return int(lib.flce_embedding_workspace_size(ctypes.byref(params)))
+
+
+def _need_ids(ids):
+    if not isinstance(ids, torch.Tensor) or not ids.is_cuda:
+        raise TypeError("ids must be a CUDA tensor")
+    if ids.dtype not in (torch.int64, torch.int32):
+        raise TypeError(f"ids must be int64 or int32, got {ids.dtype}")
+    if not ids.is_contiguous():
+        raise ValueError("ids must be contiguous")
+
+
+def flce_embedding(ids, weight, scale=1.0, v_offset=0, v_total=0, validate=False, stream=None,
+                   out=None):
+    """scale * weight[ids], of shape [*ids.shape, H].
+
+    weight [V, H] bf16, fp16 or fp32; ids int64 or int32 of any shape.  With v_total > 0
+    weight holds rows [v_offset, v_offset + V) of a table of v_total rows and other shards'
+    rows are zero, so that the shards' sum is the lookup.  An id outside the table gives a
+    row of NaN; with validate the call waits and raises.
+    """
+    lib = B.load_library()
+    _need_ids(ids)
+    dev = B._on_current_device(ids)
+    if not isinstance(weight, torch.Tensor) or not weight.is_cuda or weight.dtype not in _DTYPES:
+        raise TypeError("weight must be a bf16, fp16 or fp32 CUDA tensor")
+    if weight.dim() != 2:
+        raise ValueError(f"weight must be [V, H], got shape {tuple(weight.shape)}")
+    V, H = weight.shape
+    B._need(weight, "weight", weight.dtype, (V, H), dev)
+    shape = (*ids.shape, H)
+    p = embedding_params(ids.numel(), H, V, scale, weight.dtype,
+                         ids_int64=ids.dtype == torch.int64, v_offset=v_offset, v_total=v_total,
+                         validate=validate)
+    with _allocate_on(stream):
+        if out is None:
+            out = torch.empty(shape, dtype=weight.dtype, device=dev)
+        else:
+            B._need(out, "out", weight.dtype, shape, dev)
+        ws = torch.empty(256, dtype=torch.uint8, device=dev) if validate else None
+        B._check(lib.flce_embedding(ctypes.byref(p), ids.data_ptr(), weight.data_ptr(),
+                                    out.data_ptr(), B._ptr(ws), 256 if validate else 0,
+                                    B._stream(stream)))
+    return out
+
+
+def flce_embedding_backward(dout, ids, V, scale=1.0, padding_idx=None, dweight=None,
+                            accumulate=False, grad_dtype=None, v_offset=0, v_total=0,
+                            validate=False, workspace=None, stream=None):
+    """The gradient [V, H] of flce_embedding by weight: row v is scale times the sum of
+    dout's rows whose id is v, summed in fp32 in the tokens' order and rounded once.
+
+    dweight: where it goes (dout's type, or fp32), a new tensor if None; accumulate=True adds
+    to it and touches no other row.  Ids equal to padding_idx have no gradient, nor have
+    those of other shards.
+    """
+    lib = B.load_library()
+    _need_ids(ids)
+    dev = B._on_current_device(ids)
+    if not isinstance(dout, torch.Tensor) or not dout.is_cuda or dout.dtype not in _DTYPES:
+        raise TypeError("dout must be a bf16, fp16 or fp32 CUDA tensor")
+    if dout.dim() < 1:
+        raise ValueError("dout must be [*ids.shape, H]")
+    H = dout.shape[-1]
+    B._need(dout, "dout", dout.dtype, (*ids.shape, H), dev)
+    if dweight is None:
+        if accumulate:
+            raise ValueError("accumulate needs dweight")
+        gdt = grad_dtype or dout.dtype
+    else:
+        gdt = dweight.dtype if isinstance(dweight, torch.Tensor) else None
+        if grad_dtype is not None and grad_dtype != gdt:
+            raise TypeError(f"dweight must be {grad_dtype}, got {gdt}")
+        if gdt not in (dout.dtype, torch.float32):
+            raise TypeError(f"dweight must be {dout.dtype} or float32, got {gdt}")
+        B._need(dweight, "dweight", gdt, (V, H), dev)
+    p = embedding_params(ids.numel(), H, V, scale, dout.dtype, gdt, ids.dtype == torch.int64,
+                         accumulate, padding_idx, v_offset, v_total, validate)
+    size = embedding_workspace_size(p)
+    with _allocate_on(stream):
+        if dweight is None:
+            dweight = torch.empty(V, H, dtype=gdt, device=dev)
+        ws = _workspace(size, dev, workspace)
+        B._check(lib.flce_embedding_backward(
+            ctypes.byref(p), dout.data_ptr(), ids.data_ptr(), dweight.data_ptr(), ws.data_ptr(),
+            ws.numel(), B._stream(stream)))
+    return dweight
+
+
+class _Embedding(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, ids, weight, scale, padding_idx, v_offset, v_total):
+        ctx.save_for_backward(ids)
+        ctx.cfg = (weight.shape[0], scale, padding_idx, v_offset, v_total)
+        return flce_embedding(ids, weight, scale, v_offset, v_total)
+
+    @staticmethod
+    def backward(ctx, g):
+        (ids,) = ctx.saved_tensors
+        V, scale, padding_idx, v_offset, v_total = ctx.cfg
+        dw = flce_embedding_backward(g.contiguous(), ids, V, scale, padding_idx,
+                                     v_offset=v_offset, v_total=v_total)
+        return None, dw, None, None, None, None
+
+
+def embedding(ids, weight, scale=1.0, padding_idx=None, v_offset=0, v_total=0):
+    """scale * weight[ids], differentiable by weight (a dense gradient of weight's type; ids
+    equal to padding_idx get none)."""
+    return _Embedding.apply(ids, weight, scale, padding_idx, v_offset, v_total)
