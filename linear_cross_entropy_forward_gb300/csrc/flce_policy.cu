@@ -8,12 +8,13 @@
 // with w from the aggregate: 1 / tokens, 1 / (sequences n_i), 1 / sequences, or a scale.
 //
 // One launch does all of it, loss and gradients:
-//   A  a block per piece of at most 1024 tokens: its sums;
-//   S  a warp per sequence: its pieces' sums, added in order in fp64;
-//   B  the totals (each block for itself, over the sequences' records), the loss (block
-//      0), and a second pass over the tokens for the gradients, which by then sit in L2.
-// between which the blocks of the (cooperative) grid meet.  The sums have a fixed order:
-// results do not change from run to run.
+//   1  a warp per piece of at most 256 tokens: its sums;
+//   2  a warp per sequence: its pieces' sums, added in a fixed order in pairs of floats;
+//   3  the totals (each block for itself, over the sequences' records), the loss (block
+//      0), and a second pass over the tokens for the gradients, which by then sit in L2,
+// between which the blocks meet.  The sums have a fixed order: results do not change from
+// run to run.  The two passes over the tokens share one body of code: a launch finds the
+// instruction cache cold, and a second copy would be fetched while nothing else runs.
 //
 // Clipping tests compare d, not r, with log(1 + hi), log(1 - lo), log c: d is formed as
 // an exact sum of two floats and the borders are given the same way, so a token at a
@@ -28,6 +29,7 @@ namespace flce {
 namespace {
 
 constexpr float kLogRatioLimit = 20.0f;
+constexpr int kBatch = 4;  // tokens per lane whose loads are in flight together
 
 __device__ __forceinline__ bool pair_above(float h, float l, float bh, float bl) {
   return __fadd_rn(__fadd_rn(h, -bh), __fadd_rn(l, -bl)) > 0.0f;
@@ -38,6 +40,11 @@ __device__ __forceinline__ void exact_diff(float a, float b, float& h, float& l)
   h = __fadd_rn(a, -b);
   const float z = __fadd_rn(h, -a);
   l = __fadd_rn(__fadd_rn(a, -__fadd_rn(h, -z)), __fadd_rn(-b, -z));
+}
+
+// A NaN stays one (fmaxf alone would drop it).
+__device__ __forceinline__ float clamp_ratio(float h) {
+  return h != h ? h : fminf(fmaxf(h, -kLogRatioLimit), kLogRatioLimit);
 }
 
 struct Ratio {
@@ -55,9 +62,7 @@ __device__ __forceinline__ Ratio clip_ratio(const PolicyArgs& a, float h, float 
   } else if (adv < 0.0f && a.r_dual != 0.0f && pair_above(h, l, a.dual_h, a.dual_l)) {
     o = {a.r_dual, false, false, true};
   } else {
-    o.value = expf(fminf(fmaxf(h, -kLogRatioLimit), kLogRatioLimit));
-    // a NaN log-ratio stays one (fmaxf would drop it)
-    if (h != h) o.value = h;
+    o.value = expf(clamp_ratio(h));
     o.live = !(fabsf(h) > kLogRatioLimit);
   }
   return o;
@@ -73,7 +78,7 @@ __device__ __forceinline__ void kl_term(int kind, float lp, float ref, float& k,
     k = 0.5f * e * e;
     dk = -e;
   } else {
-    const float c = e != e ? e : fminf(fmaxf(e, -kLogRatioLimit), kLogRatioLimit);
+    const float c = clamp_ratio(e);
     k = exp_m1_mx(c);
     dk = fabsf(e) > kLogRatioLimit ? 0.0f : -(c + k);  // 1 - exp(c)
   }
@@ -82,220 +87,222 @@ __device__ __forceinline__ void kl_term(int kind, float lp, float ref, float& k,
 template <typename T>
 __global__ void __launch_bounds__(kSeqThreads, kSeqBlocksPerSm) policy_kernel(PolicyArgs a) {
   const Seqs& q = a.q;
-  const T* lp_ = static_cast<const T*>(a.lp);
-  const T* old_ = static_cast<const T*>(a.old_lp);
-  const T* ref_ = static_cast<const T*>(a.ref);
-  const T* ent_ = static_cast<const T*>(a.ent);
   const bool want_loss = a.what & POLICY_LOSS;
   const bool by_seq = a.ratio == FLCE_RATIO_SEQUENCE;
+  const bool mean_seq = a.aggregate == FLCE_AGG_SEQ_MEAN_TOKEN_MEAN;
+  const int lane = threadIdx.x & 31;
+  const int warp = blockIdx.x * kSeqWarps + (threadIdx.x >> 5);
+  const int warps = gridDim.x * kSeqWarps;
+  float wg_all = 0.0f;  // the gradients' weight before a sequence's own
 
-  // ---- A: sums of the pieces
-  for (int64_t u = blockIdx.x; u < a.pieces; u += gridDim.x) {
-    const Piece pc = find_piece(q, u);
-    float f[5] = {0, 0, 0, 0, 0};
-    int c[3] = {0, 0, 0};
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+    const bool grad = pass == 1;
+    if (grad && !(a.what & POLICY_GRAD)) break;
+    // the first pass of a launch without the loss counts tokens, no more
+    const bool values = grad || want_loss || by_seq;
+#pragma unroll 1
+    for (int u = warp; u < q.pieces; u += warps) {
+      const Piece pc = find_piece(q, u);
+      int t0 = 0, t1 = pc.len;
+      float wg = wg_all, coef = 0.0f;
+      if (grad) {
+        if (pc.len == 0 || pc.begin >= a.g_end || pc.begin + pc.len <= a.g_begin) continue;
+        if (pc.begin < a.g_begin) t0 = static_cast<int>(a.g_begin - pc.begin);
+        if (pc.begin + pc.len > a.g_end) t1 = static_cast<int>(a.g_end - pc.begin);
+        if (mean_seq || by_seq) {
+          const PolicySeq& r = a.seq[pc.seq];
+          if (mean_seq) wg = r.n > 0 ? wg / static_cast<float>(r.n) : 0.0f;
+          coef = r.coef;
+        }
+      }
+      const Counted counted(q, pc);
+      const T* lp_ = static_cast<const T*>(a.lp) + pc.begin + pc.seq * a.lp_skip;
+      const T* old_ = static_cast<const T*>(a.old_lp) + pc.begin + pc.seq * a.old_skip;
+      const T* ref_ = static_cast<const T*>(a.ref) + pc.begin + pc.seq * a.ref_skip;
+      const T* ent_ = static_cast<const T*>(a.ent) + pc.begin + pc.seq * a.ent_skip;
+      const float* adv_ = a.adv + (a.adv_per_token ? pc.begin + pc.seq * a.adv_skip : pc.seq);
+      T* dlp_ = static_cast<T*>(a.dlp) + pc.begin;  // outputs are dense
+      T* dent_ = static_cast<T*>(a.dent) + pc.begin;
+      float f[5] = {0, 0, 0, 0, 0};
+      int c[3] = {0, 0, 0};
+#pragma unroll 1
+      for (int k0 = 0; k0 < kPerLane * 32 && k0 < t1; k0 += kBatch * 32) {
+        // every load of the batch first, masked tokens' too: one wait instead of one per token
+        float lp[kBatch], old[kBatch], ref[kBatch], ent[kBatch], adv[kBatch];
+        bool on[kBatch];
 #pragma unroll
-    for (int k = 0; k < kSeqPerThread; ++k) {
-      const int64_t p = pc.begin + threadIdx.x + k * kSeqThreads;
-      if (p >= pc.end || !token_counts(q, pc.seq, p)) continue;
-      ++c[0];
-      if (!want_loss && !by_seq) continue;
-      const float lp = a.lp_sign * load_f(lp_ + p + pc.seq * a.lp_skip);
-      float h = 0.0f, l = 0.0f;
-      if (old_) exact_diff(lp, load_f(old_ + p + pc.seq * a.old_skip), h, l);
-      if (by_seq) {
-        f[4] += h;
-      } else {
-        const float adv = __ldg(a.adv + (a.adv_per_token ? p + pc.seq * a.adv_skip : pc.seq));
-        const Ratio r = clip_ratio(a, h, l, adv);
-        f[0] -= r.value * adv;
+        for (int j = 0; j < kBatch; ++j) {
+          const int t = k0 + j * 32 + lane;
+          const bool in = t >= t0 && t < t1;
+          on[j] = in && counted(t);
+          lp[j] = old[j] = ref[j] = ent[j] = adv[j] = 0.0f;
+          if (in && values) {
+            lp[j] = load_f(lp_ + t);
+            if (a.old_lp) old[j] = load_f(old_ + t);
+            if (a.ref) ref[j] = load_f(ref_ + t);
+            if (a.ent && !grad) ent[j] = load_f(ent_ + t);
+            if (!by_seq) adv[j] = __ldg(adv_ + (a.adv_per_token ? t : 0));
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          const int t = k0 + j * 32 + lane;
+          const float x = a.lp_sign * lp[j];
+          float h = 0.0f, l = 0.0f, dl = coef;
+          if (a.old_lp) exact_diff(x, old[j], h, l);
+          if (by_seq) {
+            if (on[j]) f[4] += h;
+          } else {
+            const Ratio r = clip_ratio(a, h, l, adv[j]);
+            const float ra = r.value * adv[j];
+            dl = r.live ? -ra : 0.0f;
+            if (on[j]) {
+              f[0] -= ra;
+              c[1] += r.clipped;
+              c[2] += r.dual;
+            }
+          }
+          if (a.ref) {
+            float kl, dkl;
+            kl_term(a.kl, x, ref[j], kl, dkl);
+            if (on[j]) f[1] += kl;
+            dl = fmaf(a.kl_coef, dkl, dl);
+          }
+          if (grad) {
+            if (t >= t0 && t < t1) {
+              if (a.dlp) store_f(dlp_ + t, on[j] ? dl * (wg * a.lp_sign) : 0.0f);
+              if (a.dent) store_f(dent_ + t, on[j] ? -a.ent_coef * wg : 0.0f);
+            }
+          } else if (on[j]) {
+            ++c[0];
+            f[3] += exp_m1_mx(clamp_ratio(h));
+            f[2] += ent[j];
+          }
+        }
+      }
+      if (!grad) {
+#pragma unroll
+        for (int k = 0; k < 5; ++k) f[k] = warp_sum(f[k]);
+#pragma unroll
+        for (int k = 0; k < 3; ++k) c[k] = warp_sum(c[k]);
+        if (lane == 0) a.piece[u] = {f[0], f[1], f[2], f[3], f[4], c[0], c[1], c[2]};
+      }
+    }
+    if (grad) break;
+    meet(q.meet);
+
+    // ---- sums of the sequences
+    for (int64_t i = warp; i < q.B; i += warps) {
+      int first, last;
+      seq_pieces(q, i, first, last);
+      Pair f[5] = {};
+      int c[3] = {0, 0, 0};
+      long long n = 0;
+      for (int u = first + lane; u < last; u += 32) {
+        const PolicyPiece r = a.piece[u];
+        f[0] = f[0] + r.pg;
+        f[1] = f[1] + r.kl;
+        f[2] = f[2] + r.ent;
+        f[3] = f[3] + r.old_kl;
+        f[4] = f[4] + r.d;
+        n += r.n;
         c[1] += r.clipped;
         c[2] += r.dual;
       }
-      if (!want_loss) continue;
-      const float hc = h != h ? h : fminf(fmaxf(h, -kLogRatioLimit), kLogRatioLimit);
-      f[3] += exp_m1_mx(hc);
-      if (ref_) {
-        float kl, dkl;
-        kl_term(a.kl, lp, load_f(ref_ + p + pc.seq * a.ref_skip), kl, dkl);
-        f[1] += kl;
-      }
-      if (ent_) f[2] += load_f(ent_ + p + pc.seq * a.ent_skip);
-    }
-    block_sums(f, c);
-    if (threadIdx.x == 0) a.piece[u] = {f[0], f[1], f[2], f[3], f[4], c[0], c[1], c[2]};
-  }
-  grid_barrier();
-
-  // ---- S: sums of the sequences
-  for (int64_t i = blockIdx.x * int64_t(kSeqWarps) + (threadIdx.x >> 5); i < q.B;
-       i += gridDim.x * int64_t(kSeqWarps)) {
-    const int64_t s0 = seq_start(q, i), s1 = seq_start(q, i + 1);
-    double f[5] = {0, 0, 0, 0, 0};
-    long long c[3] = {0, 0, 0};
-    const int64_t last = s1 > s0 ? (s1 - 1) / kTile + i : -1;
-    for (int64_t u = s0 / kTile + i + (threadIdx.x & 31); u <= last; u += 32) {
-      const PolicyPiece r = a.piece[u];
-      f[0] += r.pg;
-      f[1] += r.kl;
-      f[2] += r.ent;
-      f[3] += r.old_kl;
-      f[4] += r.d;
-      c[0] += r.n;
-      c[1] += r.clipped;
-      c[2] += r.dual;
-    }
 #pragma unroll
-    for (int k = 0; k < 5; ++k) f[k] = warp_sum(f[k]);
-#pragma unroll
-    for (int k = 0; k < 3; ++k) c[k] = warp_sum(c[k]);
-    if ((threadIdx.x & 31) == 0) {
-      PolicySeq o{f[0], f[1], f[2], f[3], c[0], static_cast<int>(c[1]), static_cast<int>(c[2]),
-                  0.0f, 0};
-      if (by_seq) {
-        o.clipped = o.dual = 0;
-        o.pg = 0.0;
-        if (c[0] > 0) {
-          const double s = f[4] / static_cast<double>(c[0]);
-          const float h = static_cast<float>(s), l = static_cast<float>(s - h);
+      for (int k = 0; k < 5; ++k) f[k] = warp_sum(f[k]);
+      n = warp_sum(n);
+      c[1] = warp_sum(c[1]);
+      c[2] = warp_sum(c[2]);
+      if (lane == 0) {
+        PolicySeq o{f[0], f[1], f[2], f[3], n, c[1], c[2], 0.0f, 0.0f};
+        if (by_seq && n > 0) {
+          // the mean as a pair again: the quotient, and the quotient of what it leaves
+          const float fn = static_cast<float>(n);
+          const float h = f[4].value() / fn;
+          const float l = (fmaf(-h, fn, f[4].h) + f[4].l) / fn;
           const float adv = __ldg(a.adv + i);
           const Ratio r = clip_ratio(a, h, l, adv);
-          o.pg = -static_cast<double>(c[0]) * (static_cast<double>(r.value) * adv);
-          o.coef = r.live ? -r.value * adv : 0.0f;
+          const float ra = r.value * adv;
+          o.pg = {-fn * ra, fmaf(-fn, ra, fn * ra)};
+          o.coef = r.live ? -ra : 0.0f;
           o.clipped = r.clipped;
           o.dual = r.dual;
         }
+        a.seq[i] = o;
       }
-      a.seq[i] = o;
     }
-  }
-  grid_barrier();
+    meet(q.meet);
 
-  // ---- B: totals and the loss
-  long long tokens = 0, live = 0;
-  for (int64_t i = threadIdx.x; i < q.B; i += kSeqThreads) {
-    const long long n = a.seq[i].n;
-    tokens += n;
-    live += n > 0;
-  }
-  tokens = block_total(tokens);
-  live = block_total(live);
-  const bool mean_seq = a.aggregate == FLCE_AGG_SEQ_MEAN_TOKEN_MEAN;
-  // fp64 runs at a fraction of the fp32 rate: one thread for the block
-  __shared__ double s_one_token, s_w_all;
-  __shared__ float s_wg;
-  if (threadIdx.x == 0) {
-    s_one_token = tokens > 0 ? 1.0 / static_cast<double>(tokens) : 0.0;
-    const double one_seq = live > 0 ? 1.0 / static_cast<double>(live) : 0.0;
-    s_w_all = a.aggregate == FLCE_AGG_TOKEN_MEAN ? s_one_token
-              : a.aggregate == FLCE_AGG_SUM      ? a.scale
-                                                 : one_seq;
-    s_wg = static_cast<float>((a.g_loss ? __ldg(a.g_loss) : 1.0f) * s_w_all);
-  }
-  __syncthreads();
-  if (blockIdx.x == 0) {
-    const bool ok = seqs_ok(q);
-    if (threadIdx.x == 0) {
-      if (a.err_store)
-        *a.err = ok ? 0u : FLCE_DEVERR_SEQS;
-      else if (!ok)
-        atomicOr(a.err, FLCE_DEVERR_SEQS);
-    }
-  }
-  if (want_loss && blockIdx.x == 0) {
-    double f[6] = {0, 0, 0, 0, 0, 0};
-    long long c[2] = {0, 0};
+    // ---- totals and the loss
+    const bool first_block = blockIdx.x == 0;
+    Pair f[5] = {};
+    long long c[4] = {0, 0, 0, 0};
     for (int64_t i = threadIdx.x; i < q.B; i += kSeqThreads) {
-      const PolicySeq r = a.seq[i];
-      const double w = mean_seq && r.n > 0 ? 1.0 / static_cast<double>(r.n) : 1.0;
-      f[0] += w * r.pg;
-      f[1] += w * (a.kl_coef * r.kl - a.ent_coef * r.ent);
-      f[2] += r.kl;
-      f[3] += r.ent;
-      f[4] += r.old_kl;
-      c[0] += r.clipped;
-      c[1] += r.dual;
-    }
-#pragma unroll
-    for (int k = 0; k < 5; ++k) f[k] = block_total(f[k]);
-    c[0] = block_total(c[0]);
-    c[1] = block_total(c[1]);
-    const bool ok = seqs_ok(q);
-    if (threadIdx.x == 0) {
-      const float nan = __int_as_float(0x7fc00000);
-      const double w_all = s_w_all, one_token = s_one_token;
-      a.loss[0] = ok ? static_cast<float>(w_all * (f[0] + f[1])) : nan;
-      a.stats[0] = ok ? static_cast<float>(w_all * f[0]) : nan;
-      a.stats[1] = static_cast<float>(one_token * f[2]);
-      a.stats[2] = static_cast<float>(one_token * f[3]);
-      a.stats[3] = static_cast<float>(one_token * f[4]);
-      a.counts[0] = tokens;
-      a.counts[1] = live;
-      a.counts[2] = c[0];
-      a.counts[3] = c[1];
-    }
-  }
-  if (a.lp_out) {
-    // positions of a packed axis (the head's tokens)
-    for (int64_t p = blockIdx.x * int64_t(kSeqThreads) + threadIdx.x; p < q.total;
-         p += gridDim.x * int64_t(kSeqThreads))
-      a.lp_out[p] = 0.0f + a.lp_sign * load_f(lp_ + p);
-  }
-  if (!(a.what & POLICY_GRAD)) return;
-
-  // ---- B: gradients
-  T* dlp_ = static_cast<T*>(a.dlp);
-  T* dent_ = static_cast<T*>(a.dent);
-  if (q.cu) {
-    // positions outside every sequence
-    const int64_t first = seq_start(q, 0), end = seq_start(q, q.B);
-    for (int64_t p = a.g_begin + blockIdx.x * int64_t(kSeqThreads) + threadIdx.x; p < a.g_end;
-         p += gridDim.x * int64_t(kSeqThreads))
-      if (p < first || p >= end) {
-        if (dlp_) store_f(dlp_ + p, 0.0f);
-        if (dent_) store_f(dent_ + p, 0.0f);
+      const PolicySeq& r = a.seq[i];
+      const long long n = r.n;
+      c[0] += n;
+      c[1] += n > 0;
+      if (first_block && want_loss) {
+        const float w = mean_seq && n > 0 ? 1.0f / static_cast<float>(n) : 1.0f;
+        f[0] = f[0] + Pair{w * r.pg.h, fmaf(w, r.pg.h, -(w * r.pg.h)) + w * r.pg.l};
+        f[1] = f[1] + w * (a.kl_coef * r.kl.value() - a.ent_coef * r.ent.value());
+        f[2] = f[2] + r.kl;
+        f[3] = f[3] + r.ent;
+        f[4] = f[4] + r.old_kl;
+        c[2] += r.clipped;
+        c[3] += r.dual;
       }
-  }
-  for (int64_t u = blockIdx.x; u < a.pieces; u += gridDim.x) {
-    const Piece pc = find_piece(q, u);
-    const int64_t b = pc.begin > a.g_begin ? pc.begin : a.g_begin;
-    const int64_t e = pc.end < a.g_end ? pc.end : a.g_end;
-    if (b >= e) continue;
-    float wg = s_wg, coef = 0.0f;
-    if (mean_seq || by_seq) {
-      const PolicySeq& r = a.seq[pc.seq];
-      if (mean_seq) wg = r.n > 0 ? wg / static_cast<float>(r.n) : 0.0f;
-      coef = r.coef;
     }
-#pragma unroll
-    for (int k = 0; k < kSeqPerThread; ++k) {
-      const int64_t p = b + threadIdx.x + k * kSeqThreads;
-      if (p >= e) continue;
-      float dl = 0.0f, dh = 0.0f;
-      if (token_counts(q, pc.seq, p)) {
-        if (dlp_) {
-          const float lp = a.lp_sign * load_f(lp_ + p + pc.seq * a.lp_skip);
-          if (by_seq) {
-            dl = coef;
-          } else {
-            float h = 0.0f, l = 0.0f;
-            if (old_) exact_diff(lp, load_f(old_ + p + pc.seq * a.old_skip), h, l);
-            const float adv = __ldg(a.adv + (a.adv_per_token ? p + pc.seq * a.adv_skip : pc.seq));
-            const Ratio r = clip_ratio(a, h, l, adv);
-            dl = r.live ? -r.value * adv : 0.0f;
-          }
-          if (ref_ && a.kl_coef != 0.0f) {
-            float kl, dkl;
-            kl_term(a.kl, lp, load_f(ref_ + p + pc.seq * a.ref_skip), kl, dkl);
-            dl = fmaf(a.kl_coef, dkl, dl);
-          }
-          dl *= wg * a.lp_sign;
+    if (first_block) {
+      block_sums(f, c);
+    } else {
+      Pair none[1] = {};
+      long long two[2] = {c[0], c[1]};
+      block_sums(none, two);
+      c[0] = two[0];
+      c[1] = two[1];
+    }
+    const float one_token = c[0] > 0 ? 1.0f / static_cast<float>(c[0]) : 0.0f;
+    const float one_seq = c[1] > 0 ? 1.0f / static_cast<float>(c[1]) : 0.0f;
+    const float w_all = a.aggregate == FLCE_AGG_TOKEN_MEAN ? one_token
+                        : a.aggregate == FLCE_AGG_SUM      ? a.scale
+                                                           : one_seq;
+    wg_all = a.g_loss ? w_all * __ldg(a.g_loss) : w_all;
+    if (first_block) {
+      const bool ok = seqs_ok(q);
+      if (threadIdx.x == 0) {
+        if (a.err_store)
+          *a.err = ok ? 0u : FLCE_DEVERR_SEQS;
+        else if (!ok)
+          atomicOr(a.err, FLCE_DEVERR_SEQS);
+        if (want_loss) {
+          const float nan = __int_as_float(0x7fc00000);
+          a.loss[0] = ok ? w_all * (f[0] + f[1]).value() : nan;
+          a.stats[0] = ok ? w_all * f[0].value() : nan;
+          a.stats[1] = one_token * f[2].value();
+          a.stats[2] = one_token * f[3].value();
+          a.stats[3] = one_token * f[4].value();
+          a.counts[0] = c[0];
+          a.counts[1] = c[1];
+          a.counts[2] = c[2];
+          a.counts[3] = c[3];
         }
-        dh = -a.ent_coef * wg;
       }
-      // outputs are dense: a padded batch's position is its index
-      if (dlp_) store_f(dlp_ + p, dl);
-      if (dent_) store_f(dent_ + p, dh);
+    }
+    const int64_t thread = warp * int64_t(32) + lane, threads = warps * int64_t(32);
+    if (a.lp_out)  // the head's tokens: a packed axis
+      for (int64_t p = thread; p < q.total; p += threads)
+        a.lp_out[p] = 0.0f + a.lp_sign * load_f(static_cast<const T*>(a.lp) + p);
+    if (q.cu && (a.what & POLICY_GRAD)) {
+      // positions outside every sequence
+      const int64_t begin = seq_start(q, 0), end = seq_start(q, q.B);
+      for (int64_t p = a.g_begin + thread; p < a.g_end; p += threads)
+        if (p < begin || p >= end) {
+          if (a.dlp) store_f(static_cast<T*>(a.dlp) + p, 0.0f);
+          if (a.dent) store_f(static_cast<T*>(a.dent) + p, 0.0f);
+        }
     }
   }
 }
@@ -336,7 +343,7 @@ int policy_check(const flce_policy_params* p) {
 size_t policy_workspace(const flce_policy_params* p) {
   Seqs q;
   if (make_seqs(&p->seqs, &q)) return 0;
-  return 256 + align256(seq_pieces(q.B, q.total) * sizeof(PolicyPiece)) +
+  return 256 + align256(static_cast<size_t>(q.pieces) * sizeof(PolicyPiece)) +
          align256((q.B > 0 ? q.B : 1) * sizeof(PolicySeq));
 }
 
@@ -361,30 +368,27 @@ int policy_args(const flce_policy_params* p, void* workspace, PolicyArgs* a) {
   a->r_dual = static_cast<float>(p->dual_clip);
   a->kl_coef = static_cast<float>(p->kl_coef);
   a->ent_coef = static_cast<float>(p->entropy_coef);
-  a->scale = p->scale;
+  a->scale = static_cast<float>(p->scale);
   a->kl = p->kl;
   a->ratio = p->ratio;
   a->aggregate = p->aggregate;
-  a->pieces = seq_pieces(a->q.B, a->q.total);
   a->g_end = a->q.total;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a->err = reinterpret_cast<uint32_t*>(ws);
   a->err_store = 1;
   a->piece = reinterpret_cast<PolicyPiece*>(ws + 256);
-  a->seq = reinterpret_cast<PolicySeq*>(ws + 256 + align256(a->pieces * sizeof(PolicyPiece)));
+  a->seq = reinterpret_cast<PolicySeq*>(ws + 256 + align256(static_cast<size_t>(a->q.pieces) * sizeof(PolicyPiece)));
   return FLCE_OK;
 }
 
 int launch_policy(const PolicyArgs& a, int dtype, int sms, cudaStream_t st) {
-  const int64_t cap = int64_t(sms) * kSeqBlocksPerSm;
-  const int64_t blocks = a.pieces < cap ? a.pieces : cap;
   cudaError_t e;
   if (dtype == FLCE_F32)
-    e = launch_seq(policy_kernel<float>, a, blocks, st);
+    e = launch_seq(policy_kernel<float>, a, sms, st);
   else if (dtype == FLCE_BF16)
-    e = launch_seq(policy_kernel<__nv_bfloat16>, a, blocks, st);
+    e = launch_seq(policy_kernel<__nv_bfloat16>, a, sms, st);
   else
-    e = launch_seq(policy_kernel<__half>, a, blocks, st);
+    e = launch_seq(policy_kernel<__half>, a, sms, st);
   return e == cudaSuccess ? FLCE_OK : FLCE_ERR_CUDA;
 }
 

@@ -7,13 +7,13 @@
 
 namespace flce {
 
-// One sequence's sums over its tokens (fp64: their terms have both signs).
+// One sequence's sums over its tokens.
 struct PolicySeq {
-  double pg, kl, ent, old_kl;
+  Pair pg, kl, ent, old_kl;
   long long n;
   int clipped, dual;
   float coef;  // d(loss)/d(mean log-ratio) before the weight (sequence ratios only)
-  int pad;
+  float pad;
 };
 
 // A piece's sums.
@@ -39,9 +39,9 @@ struct PolicyArgs {
   float hi_h, hi_l, lo_h, lo_l, dual_h, dual_l;
   float r_hi, r_lo, r_dual;  // the ratio beyond the borders; r_dual 0: no dual clip
   float kl_coef, ent_coef;
-  double scale;
+  float scale;
   int kl, ratio, aggregate, what;
-  int64_t pieces, g_begin, g_end;
+  int64_t g_begin, g_end;
   const float* g_loss;
   float *loss, *stats;
   long long* counts;

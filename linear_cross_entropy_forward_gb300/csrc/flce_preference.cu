@@ -11,8 +11,8 @@
 // of which nothing counts is left out.  The gradient of a counted token is its sequence's
 // coefficient.
 //
-// One launch: sums of the pieces; a warp per pair, which adds its two sequences' pieces in
-// order in fp64; totals, the loss and the gradients.  The gradient pass reads only the mask.
+// One launch: sums of the pieces; a warp per pair, which adds its two sequences' pieces in a
+// fixed order in pairs of floats; totals, the loss and the gradients.  The gradient pass reads only the mask.
 #include <cmath>
 
 #include "flce_device.cuh"
@@ -34,9 +34,8 @@ struct PrefArgs {
   const void *lp, *ref;
   int64_t lp_skip, ref_skip;
   const float* ref_scores;
-  double beta, margin, smooth, nll;
+  float beta, margin, smooth, nll;
   int kind, norm, interleaved, reduction, want_loss;
-  int64_t pieces;
   const float* g_loss;
   float *loss, *rewards;
   void* dlp;
@@ -47,31 +46,31 @@ struct PrefArgs {
   int* pair_ok;      // [B / 2]
 };
 
-__device__ __forceinline__ double softplus(double x) {  // ln(1 + e^x)
-  return fmax(x, 0.0) + log1p(exp(-fabs(x)));
+__device__ __forceinline__ float softplus(float x) {  // ln(1 + e^x)
+  return fmaxf(x, 0.0f) + log1pf(expf(-fabsf(x)));
 }
-__device__ __forceinline__ double sigmoid(double x) { return 1.0 / (1.0 + exp(-x)); }
+__device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
 
 // The pair's loss and its derivative by h.
-__device__ void pair_value(const PrefArgs& a, double h, double& l, double& dh) {
-  const double e = a.smooth;
+__device__ void pair_value(const PrefArgs& a, float h, float& l, float& dh) {
+  const float e = a.smooth;
   switch (a.kind) {
     case FLCE_PREF_SIGMOID:
-      l = (1.0 - e) * softplus(-h) + e * softplus(h);
-      dh = -(1.0 - e) * sigmoid(-h) + e * sigmoid(h);
+      l = (1.0f - e) * softplus(-h) + e * softplus(h);
+      dh = -(1.0f - e) * sigmoid(-h) + e * sigmoid(h);
       break;
     case FLCE_PREF_ROBUST:
-      l = ((1.0 - e) * softplus(-h) - e * softplus(h)) / (1.0 - 2.0 * e);
-      dh = (-(1.0 - e) * sigmoid(-h) - e * sigmoid(h)) / (1.0 - 2.0 * e);
+      l = ((1.0f - e) * softplus(-h) - e * softplus(h)) / (1.0f - 2.0f * e);
+      dh = (-(1.0f - e) * sigmoid(-h) - e * sigmoid(h)) / (1.0f - 2.0f * e);
       break;
     case FLCE_PREF_HINGE:
-      l = h < 1.0 ? 1.0 - h : (h != h ? h : 0.0);
-      dh = h < 1.0 ? -1.0 : 0.0;
+      l = h < 1.0f ? 1.0f - h : (h != h ? h : 0.0f);
+      dh = h < 1.0f ? -1.0f : 0.0f;
       break;
     default: {
-      const double u = (h - 0.5) / a.beta;
+      const float u = (h - 0.5f) / a.beta;
       l = u * u;
-      dh = 2.0 * u / a.beta;
+      dh = 2.0f * u / a.beta;
     }
   }
 }
@@ -79,123 +78,138 @@ __device__ void pair_value(const PrefArgs& a, double h, double& l, double& dh) {
 template <typename T>
 __global__ void __launch_bounds__(kSeqThreads, kSeqBlocksPerSm) preference_kernel(PrefArgs a) {
   const Seqs& q = a.q;
-  const T* lp_ = static_cast<const T*>(a.lp);
-  const T* ref_ = static_cast<const T*>(a.ref);
-  for (int64_t u = blockIdx.x; u < a.pieces; u += gridDim.x) {
+  const int lane = threadIdx.x & 31;
+  const int warp = blockIdx.x * kSeqWarps + (threadIdx.x >> 5);
+  const int warps = gridDim.x * kSeqWarps;
+  for (int u = warp; u < q.pieces; u += warps) {
     const Piece pc = find_piece(q, u);
-    float f[2] = {0, 0};
-    int c[1] = {0};
+    const Counted counted(q, pc);
+    const T* lp_ = static_cast<const T*>(a.lp) + pc.begin + pc.seq * a.lp_skip;
+    const T* ref_ = static_cast<const T*>(a.ref) + pc.begin + pc.seq * a.ref_skip;
+    float score = 0.0f, like = 0.0f;
+    int n = 0;
+    // the loads of all the lane's tokens first, masked ones' too
+    float lp[kPerLane], ref[kPerLane];
+    bool on[kPerLane];
 #pragma unroll
-    for (int k = 0; k < kSeqPerThread; ++k) {
-      const int64_t p = pc.begin + threadIdx.x + k * kSeqThreads;
-      if (p >= pc.end || !token_counts(q, pc.seq, p)) continue;
-      const float lp = load_f(lp_ + p + pc.seq * a.lp_skip);
-      f[0] += ref_ ? lp - load_f(ref_ + p + pc.seq * a.ref_skip) : lp;
-      f[1] += lp;
-      ++c[0];
+    for (int k = 0; k < kPerLane; ++k) {
+      const int t = lane + 32 * k;
+      const bool in = t < pc.len;
+      on[k] = in && counted(t);
+      lp[k] = in ? load_f(lp_ + t) : 0.0f;
+      ref[k] = in && a.ref ? load_f(ref_ + t) : 0.0f;
     }
-    block_sums(f, c);
-    if (threadIdx.x == 0) a.piece[u] = {f[0], f[1], c[0], 0};
+#pragma unroll
+    for (int k = 0; k < kPerLane; ++k)
+      if (on[k]) {
+        score += lp[k] - ref[k];
+        like += lp[k];
+        ++n;
+      }
+    score = warp_sum(score);
+    like = warp_sum(like);
+    n = warp_sum(n);
+    if (lane == 0) a.piece[u] = {score, like, n, 0};
   }
-  grid_barrier();
+  meet(q.meet);
 
   const int64_t pairs = q.B / 2;
-  const int lane = threadIdx.x & 31;
-  for (int64_t i = blockIdx.x * int64_t(kSeqWarps) + (threadIdx.x >> 5); i < pairs;
-       i += gridDim.x * int64_t(kSeqWarps)) {
+  for (int64_t i = warp; i < pairs; i += warps) {
     int64_t id[2];
-    double score[2], like = 0.0;
+    Pair score[2], like{};
     long long n[2];
     id[0] = a.interleaved ? 2 * i : i;
     id[1] = a.interleaved ? 2 * i + 1 : pairs + i;
+#pragma unroll
     for (int side = 0; side < 2; ++side) {
-      const int64_t s = id[side], s0 = seq_start(q, s), s1 = seq_start(q, s + 1);
-      const int64_t last = s1 > s0 ? (s1 - 1) / kTile + s : -1;
-      double sc = 0.0, lk = 0.0;
+      int first, last;
+      seq_pieces(q, id[side], first, last);
+      Pair sc{}, lk{};
       long long c = 0;
-      for (int64_t u = s0 / kTile + s + lane; u <= last; u += 32) {
+      for (int u = first + lane; u < last; u += 32) {
         const PrefPiece r = a.piece[u];
-        sc += r.score;
-        lk += r.like;
+        sc = sc + r.score;
+        lk = lk + r.like;
         c += r.n;
       }
       score[side] = warp_sum(sc);
       n[side] = warp_sum(c);
-      lk = warp_sum(lk);
-      if (side == 0) like = lk;
+      if (side == 0) like = warp_sum(lk);
     }
     if (lane == 0) {
-      const double per[2] = {n[0] > 0 ? 1.0 / static_cast<double>(n[0]) : 0.0,
-                             n[1] > 0 ? 1.0 / static_cast<double>(n[1]) : 0.0};
+      const float per[2] = {n[0] > 0 ? 1.0f / static_cast<float>(n[0]) : 0.0f,
+                            n[1] > 0 ? 1.0f / static_cast<float>(n[1]) : 0.0f};
       for (int side = 0; side < 2; ++side) {
-        if (a.norm) score[side] *= per[side];
-        if (a.ref_scores) score[side] -= __ldg(a.ref_scores + id[side]);
-        if (n[side] == 0) score[side] = 0.0;
+        if (a.norm) {
+          const float x = score[side].h * per[side];
+          score[side] = {x, fmaf(score[side].h, per[side], -x) + score[side].l * per[side]};
+        }
+        if (a.ref_scores) score[side] = score[side] + -__ldg(a.ref_scores + id[side]);
+        if (n[side] == 0) score[side] = {};
       }
       const bool ok = n[0] > 0 && n[1] > 0;
-      double l = 0.0, dh = 0.0;
+      float l = 0.0f, dh = 0.0f;
       if (ok) {
-        pair_value(a, a.beta * (score[0] - score[1]) - a.margin, l, dh);
-        l -= a.nll * like * per[0];
+        pair_value(a, fmaf(a.beta, (score[0] + -score[1]).value(), -a.margin), l, dh);
+        l -= a.nll * like.value() * per[0];
       }
-      a.pair_loss[i] = static_cast<float>(l);
+      a.pair_loss[i] = l;
       a.pair_ok[i] = ok;
-      const double d = a.beta * dh;
-      a.coef[id[0]] = ok ? static_cast<float>(d * (a.norm ? per[0] : 1.0) - a.nll * per[0]) : 0.0f;
-      a.coef[id[1]] = ok ? static_cast<float>(-d * (a.norm ? per[1] : 1.0)) : 0.0f;
+      const float d = a.beta * dh;
+      a.coef[id[0]] = ok ? d * (a.norm ? per[0] : 1.0f) - a.nll * per[0] : 0.0f;
+      a.coef[id[1]] = ok ? -d * (a.norm ? per[1] : 1.0f) : 0.0f;
       if (a.want_loss) {
-        a.rewards[id[0]] = static_cast<float>(a.beta * score[0]);
-        a.rewards[id[1]] = static_cast<float>(a.beta * score[1]);
+        a.rewards[id[0]] = a.beta * score[0].value();
+        a.rewards[id[1]] = a.beta * score[1].value();
       }
     }
   }
-  grid_barrier();
+  meet(q.meet);
 
-  long long live = 0;
-  for (int64_t i = threadIdx.x; i < pairs; i += kSeqThreads) live += a.pair_ok[i];
-  live = block_total(live);
-  const float scale =
-      a.reduction == FLCE_RED_MEAN ? (live > 0 ? 1.0f / static_cast<float>(live) : 0.0f) : 1.0f;
-  if (blockIdx.x == 0) {
-    const bool ok = seqs_ok(q);
-    const float nan = __int_as_float(0x7fc00000);
-    if (threadIdx.x == 0) *a.err = ok ? 0u : FLCE_DEVERR_SEQS;
-    if (a.want_loss) {
-      double l = 0.0;
-      for (int64_t i = threadIdx.x; i < pairs; i += kSeqThreads) {
-        const float v = ok ? a.pair_loss[i] : nan;
-        if (a.reduction == FLCE_RED_NONE) a.loss[i] = v;
-        l += v;
-      }
-      if (a.reduction != FLCE_RED_NONE) {
-        l = block_total(l);
-        if (threadIdx.x == 0) {
-          if (a.reduction == FLCE_RED_MEAN && live > 0) l /= static_cast<double>(live);
-          a.loss[0] = ok ? static_cast<float>(l) : nan;
-        }
-      }
+  Pair l[1] = {};
+  long long live[1] = {0};
+  const bool ok = blockIdx.x == 0 ? seqs_ok(q) : true;
+  const float nan = __int_as_float(0x7fc00000);
+  for (int64_t i = threadIdx.x; i < pairs; i += kSeqThreads) {
+    live[0] += a.pair_ok[i];
+    if (blockIdx.x == 0 && a.want_loss) {
+      const float v = ok ? a.pair_loss[i] : nan;
+      if (a.reduction == FLCE_RED_NONE) a.loss[i] = v;
+      l[0] = l[0] + v;
     }
+  }
+  block_sums(l, live);
+  const float scale =
+      a.reduction == FLCE_RED_MEAN ? (live[0] > 0 ? 1.0f / static_cast<float>(live[0]) : 0.0f)
+                                   : 1.0f;
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    *a.err = ok ? 0u : FLCE_DEVERR_SEQS;
+    if (a.want_loss && a.reduction != FLCE_RED_NONE)
+      a.loss[0] = ok ? l[0].value() * scale : nan;
   }
   T* dlp_ = static_cast<T*>(a.dlp);
   if (!dlp_) return;
   if (q.cu) {
-    const int64_t first = seq_start(q, 0), end = seq_start(q, q.B);
-    for (int64_t p = blockIdx.x * int64_t(kSeqThreads) + threadIdx.x; p < q.total;
-         p += gridDim.x * int64_t(kSeqThreads))
-      if (p < first || p >= end) store_f(dlp_ + p, 0.0f);
+    const int64_t begin = seq_start(q, 0), end = seq_start(q, q.B);
+    for (int64_t p = warp * int64_t(32) + lane; p < q.total; p += warps * int64_t(32))
+      if (p < begin || p >= end) store_f(dlp_ + p, 0.0f);
   }
-  for (int64_t u = blockIdx.x; u < a.pieces; u += gridDim.x) {
+  for (int u = warp; u < q.pieces; u += warps) {
     const Piece pc = find_piece(q, u);
-    if (pc.begin >= pc.end) continue;
+    if (pc.len == 0) continue;
+    const Counted counted(q, pc);
     float g = a.coef[pc.seq] * scale;
     if (a.g_loss) {
       const int64_t pair = a.interleaved ? pc.seq / 2 : pc.seq % pairs;
       g *= __ldg(a.g_loss + (a.reduction == FLCE_RED_NONE ? pair : 0));
     }
+    bool on[kPerLane];
 #pragma unroll
-    for (int k = 0; k < kSeqPerThread; ++k) {
-      const int64_t p = pc.begin + threadIdx.x + k * kSeqThreads;
-      if (p < pc.end) store_f(dlp_ + p, token_counts(q, pc.seq, p) ? g : 0.0f);
+    for (int k = 0; k < kPerLane; ++k) on[k] = lane + 32 * k < pc.len && counted(lane + 32 * k);
+#pragma unroll
+    for (int k = 0; k < kPerLane; ++k) {
+      const int t = lane + 32 * k;
+      if (t < pc.len) store_f(dlp_ + pc.begin + t, on[k] ? g : 0.0f);
     }
   }
 }
@@ -210,7 +224,7 @@ PrefLayout pref_layout(const Seqs& q) {
   PrefLayout L{};
   const int64_t B = q.B > 0 ? q.B : 1;
   size_t off = 256;
-  L.piece = off; off += align256(seq_pieces(q.B, q.total) * sizeof(PrefPiece));
+  L.piece = off; off += align256(static_cast<size_t>(q.pieces) * sizeof(PrefPiece));
   L.coef = off; off += align256(B * 4);
   L.pair_loss = off; off += align256(B * 4);
   L.pair_ok = off; off += align256(B * 4);
@@ -282,16 +296,15 @@ int flce_preference_loss(const flce_preference_params* p, const void* logp, cons
   a.lp_skip = packed ? 0 : p->ld_logp - p->seqs.S;
   a.ref_skip = packed ? 0 : p->ld_ref - p->seqs.S;
   a.ref_scores = ref_scores;
-  a.beta = p->beta;
-  a.margin = p->margin;
-  a.smooth = p->label_smoothing;
-  a.nll = p->nll_coef;
+  a.beta = static_cast<float>(p->beta);
+  a.margin = static_cast<float>(p->margin);
+  a.smooth = static_cast<float>(p->label_smoothing);
+  a.nll = static_cast<float>(p->nll_coef);
   a.kind = p->kind;
   a.norm = p->length_normalised;
   a.interleaved = p->interleaved;
   a.reduction = p->reduction;
   a.want_loss = loss != nullptr;
-  a.pieces = seq_pieces(a.q.B, a.q.total);
   a.g_loss = g_loss;
   a.loss = loss;
   a.rewards = rewards;
@@ -301,16 +314,14 @@ int flce_preference_loss(const flce_preference_params* p, const void* logp, cons
   a.coef = reinterpret_cast<float*>(ws + L.coef);
   a.pair_loss = reinterpret_cast<float*>(ws + L.pair_loss);
   a.pair_ok = reinterpret_cast<int*>(ws + L.pair_ok);
-  const int64_t cap = int64_t(sms) * kSeqBlocksPerSm;
-  const int64_t blocks = a.pieces < cap ? a.pieces : cap;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (dt == FLCE_F32)
-    e = launch_seq(preference_kernel<float>, a, blocks, st);
+    e = launch_seq(preference_kernel<float>, a, sms, st);
   else if (dt == FLCE_BF16)
-    e = launch_seq(preference_kernel<__nv_bfloat16>, a, blocks, st);
+    e = launch_seq(preference_kernel<__nv_bfloat16>, a, sms, st);
   else
-    e = launch_seq(preference_kernel<__half>, a, blocks, st);
+    e = launch_seq(preference_kernel<__half>, a, sms, st);
   if (e != cudaSuccess) return FLCE_ERR_CUDA;
   return p->validate ? read_status(workspace, st) : FLCE_OK;
 }

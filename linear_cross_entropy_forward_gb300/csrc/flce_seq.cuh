@@ -6,13 +6,15 @@
 // padded batch starts at position i * S, and an array's element for position p of
 // sequence i is base[p + i * skip] with skip = row stride - S (0 when packed).
 //
-// The axis is cut at every multiple of kTile positions and at every sequence's start.
-// The pieces need no list: the piece of sequence i in tile j has number i + j (each new
-// piece moves on to the next tile or to the next sequence), so the first piece of
-// sequence i is f(i) = start(i) / kTile + i, which rises strictly, and piece u belongs
-// to the last i with f(i) <= u.  There are at most S / kTile + B + 1 numbers; the unused
-// ones are empty pieces.  One long sequence is spread over the GPU as well as many short
-// ones, whatever their lengths, and nothing about them is read on the host.
+// The axis is cut into pieces of at most kTile positions, none of which holds tokens of
+// two sequences; a warp takes a piece.  A padded row has ceil(S / kTile) of them.  A packed
+// axis is cut at every multiple of kTile and at every sequence's start, which needs no
+// list: the piece of sequence i in tile j has number i + j (each new piece moves on to the
+// next tile or to the next sequence), so the first piece of sequence i is
+// f(i) = start(i) / kTile + i, which rises strictly, and piece u belongs to the last i with
+// f(i) <= u.  The numbers that no piece has (a sequence that ends at a cut) are empty
+// pieces.  One long sequence is spread over the GPU as well as many short ones, whatever
+// their lengths, and nothing about them is read on the host.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -24,13 +26,15 @@
 
 namespace flce {
 
-constexpr int kSeqThreads = 256;
+constexpr int kSeqThreads = 512;
 constexpr int kSeqWarps = kSeqThreads / 32;
-constexpr int kSeqPerThread = 4;
-constexpr int64_t kTile = int64_t(kSeqThreads) * kSeqPerThread;
-// Blocks an SM holds at once (the launch bounds of the kernels): the grid of a
-// cooperative launch is at most this times the SM count.
-constexpr int kSeqBlocksPerSm = 4;
+constexpr int kSeqBlocksPerSm = 2;  // the kernels' launch bounds: 64 registers
+constexpr int kPerLane = 8;
+constexpr int kTile = 32 * kPerLane;
+constexpr int kClusterBlocks = 8;   // the portable cluster size
+
+// How the blocks of a grid meet between the phases of a kernel.
+enum : int { MEET_BLOCK = 0, MEET_CLUSTER = 1, MEET_GRID = 2 };
 
 struct Seqs {
   int64_t B, S, total;  // total: positions (B * S padded, S packed)
@@ -40,9 +44,10 @@ struct Seqs {
   int mask_labels;      // 0: bytes, non-zero counts; 1: int64 labels != ignore_index
   int64_t ignore_index;
   int64_t mask_skip;
+  int per_row;          // pieces of a padded row
+  int pieces;
+  int meet;
 };
-
-inline int64_t seq_pieces(int64_t B, int64_t total) { return total / kTile + B + 1; }
 
 __device__ __forceinline__ int64_t clamp64(int64_t x, int64_t lo, int64_t hi) {
   return x < lo ? lo : (x > hi ? hi : x);
@@ -57,53 +62,76 @@ __device__ __forceinline__ int64_t seq_start(const Seqs& q, int64_t i) {
   return clamp64(v, 0, q.total);
 }
 
-__device__ __forceinline__ int64_t seq_first_piece(const Seqs& q, int64_t i) {
-  return seq_start(q, i) / kTile + i;
+// The pieces of sequence i: [first, last), the empty ones left out of a packed axis.
+__device__ __forceinline__ void seq_pieces(const Seqs& q, int64_t i, int& first, int& last) {
+  if (!q.cu) {
+    first = static_cast<int>(i) * q.per_row;
+    last = first + q.per_row;
+    return;
+  }
+  const int64_t a = seq_start(q, i), b = seq_start(q, i + 1);
+  first = static_cast<int>(a / kTile + i);
+  last = b > a ? static_cast<int>((b - 1) / kTile + i + 1) : first;
 }
 
 struct Piece {
-  int64_t seq, begin, end;  // empty: begin >= end
+  int seq;
+  int len;        // 0: empty
+  int64_t begin;  // position
 };
 
-// The piece with number u; called by the whole block (a search over cu takes one
-// coalesced load per 256-fold narrowing instead of a chain of dependent ones).
-__device__ __forceinline__ Piece find_piece(const Seqs& q, int64_t u) {
-  int64_t i;
+// The piece with number u; called by a whole warp (a search over cu takes one load by all
+// lanes per 32-fold narrowing).
+__device__ __forceinline__ Piece find_piece(const Seqs& q, int u) {
+  Piece p{-1, 0, 0};
   if (!q.cu) {
-    // f(i) = i * S / kTile + i: off by at most one from the real quotient
-    i = clamp64(static_cast<int64_t>(static_cast<double>(u) * kTile / (q.S + kTile)), 0, q.B - 1);
-    while (i > 0 && i * q.S / kTile + i > u) --i;
-    while (i + 1 < q.B && (i + 1) * q.S / kTile + i + 1 <= u) ++i;
-  } else {
-    int64_t lo = 0, n = q.B;  // the answer is in [lo - 1, lo + n)
-    while (n > 0) {
-      const int64_t step = (n + kSeqThreads - 1) / kSeqThreads;
-      const int64_t k = threadIdx.x * step;
-      const int below =
-          __syncthreads_count(k < n && seq_first_piece(q, lo + k) <= u);
-      if (below == 0) break;
-      const int64_t from = (below - 1) * step;
-      const int64_t left = n - from;
-      lo += from + 1;
-      n = (left < step ? left : step) - 1;
-    }
-    i = lo - 1;
+    p.seq = static_cast<int>(static_cast<unsigned>(u) / static_cast<unsigned>(q.per_row));
+    const int64_t off = int64_t(u - p.seq * q.per_row) * kTile;
+    p.begin = p.seq * q.S + off;
+    const int64_t left = q.S - off;
+    p.len = static_cast<int>(left < kTile ? left : kTile);
+    return p;
   }
-  Piece p{i, 0, 0};
-  if (i < 0) return p;
-  const int64_t a = seq_start(q, i), b = seq_start(q, i + 1);
-  const int64_t tile = (u - i) * kTile;
+  int lo = 0, n = static_cast<int>(q.B);  // the answer is in [lo - 1, lo + n)
+  while (n > 0) {
+    const int step = (n + 31) / 32;
+    const int64_t k = int64_t(threadIdx.x & 31) * step;
+    const int below =
+        __popc(__ballot_sync(~0u, k < n && seq_start(q, lo + k) / kTile + lo + k <= u));
+    if (below == 0) break;
+    const int from = (below - 1) * step;
+    const int left = n - from;
+    lo += from + 1;
+    n = (left < step ? left : step) - 1;
+  }
+  p.seq = lo - 1;
+  if (p.seq < 0) return p;
+  const int64_t a = seq_start(q, p.seq), b = seq_start(q, p.seq + 1);
+  const int64_t tile = int64_t(u - p.seq) * kTile;
   p.begin = a > tile ? a : tile;
-  p.end = b < tile + kTile ? b : tile + kTile;
+  const int64_t end = b < tile + kTile ? b : tile + kTile;
+  p.len = end > p.begin ? static_cast<int>(end - p.begin) : 0;
   return p;
 }
 
-__device__ __forceinline__ bool token_counts(const Seqs& q, int64_t i, int64_t p) {
-  if (!q.mask) return true;
-  const int64_t o = p + i * q.mask_skip;
-  if (q.mask_labels) return __ldg(static_cast<const long long*>(q.mask) + o) != q.ignore_index;
-  return __ldg(static_cast<const unsigned char*>(q.mask) + o) != 0;
-}
+// Which of a piece's tokens count.
+struct Counted {
+  const void* mask;
+  int labels;
+  int64_t ignore_index;
+  __device__ __forceinline__ Counted(const Seqs& q, const Piece& p)
+      : mask(nullptr), labels(q.mask_labels), ignore_index(q.ignore_index) {
+    const int64_t o = p.begin + p.seq * q.mask_skip;
+    if (q.mask)
+      mask = labels ? static_cast<const void*>(static_cast<const long long*>(q.mask) + o)
+                    : static_cast<const void*>(static_cast<const unsigned char*>(q.mask) + o);
+  }
+  __device__ __forceinline__ bool operator()(int t) const {
+    if (!mask) return true;
+    if (labels) return __ldg(static_cast<const long long*>(mask) + t) != ignore_index;
+    return __ldg(static_cast<const unsigned char*>(mask) + t) != 0;
+  }
+};
 
 __device__ __forceinline__ float load_f(const float* p) { return __ldg(p); }
 __device__ __forceinline__ float load_f(const __nv_bfloat16* p) {
@@ -120,9 +148,34 @@ __device__ __forceinline__ float warp_sum(float v) {
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
   return v;
 }
-__device__ __forceinline__ double warp_sum(double v) {
+// A sum as an unevaluated pair of floats (h + l, about 48 bits): the sums over pieces and
+// sequences, whose terms have both signs.  An fp64 addition takes a warp 16 times as long
+// here as an fp32 one: with fp64 sums these phases took 45 of the policy kernel's 57 us at
+// a million tokens.
+struct Pair {
+  float h, l;
+  __device__ __forceinline__ float value() const {
+    return fabsf(h) <= 3.4028235e38f ? h + l : h;  // infinities and NaN: l means nothing
+  }
+};
+
+__device__ __forceinline__ Pair operator+(Pair a, float b) {
+  const float s = __fadd_rn(a.h, b);
+  const float z = __fadd_rn(s, -a.h);
+  const float e = __fadd_rn(__fadd_rn(a.h, -__fadd_rn(s, -z)), __fadd_rn(b, -z));
+  return {s, __fadd_rn(a.l, e)};
+}
+__device__ __forceinline__ Pair operator+(Pair a, Pair b) {
+  Pair s = a + b.h;
+  s.l = __fadd_rn(s.l, b.l);
+  return s;
+}
+__device__ __forceinline__ Pair operator-(Pair a) { return {-a.h, -a.l}; }
+
+__device__ __forceinline__ Pair warp_sum(Pair v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+  for (int o = 16; o > 0; o >>= 1)
+    v = v + Pair{__shfl_xor_sync(~0u, v.h, o), __shfl_xor_sync(~0u, v.l, o)};
   return v;
 }
 __device__ __forceinline__ long long warp_sum(long long v) {
@@ -131,70 +184,53 @@ __device__ __forceinline__ long long warp_sum(long long v) {
   return v;
 }
 
-// Sums of NF floats and NI counts over the block, in a fixed order; valid in thread 0.
-template <int NF, int NI>
-__device__ __forceinline__ void block_sums(float (&f)[NF], int (&c)[NI]) {
-  __shared__ float sf[NF][kSeqWarps];
-  __shared__ int sc[NI][kSeqWarps];
+__device__ __forceinline__ int warp_sum(int v) { return __reduce_add_sync(~0u, v); }
+
+// Sums of ND values and NI counts over the block, in a fixed order, in every thread.
+template <int ND, int NI>
+__device__ __forceinline__ void block_sums(Pair (&d)[ND], long long (&c)[NI]) {
+  __shared__ Pair sd[kSeqWarps][ND];
+  __shared__ long long sc[kSeqWarps][NI];
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
-  for (int k = 0; k < NF; ++k) f[k] = warp_sum(f[k]);
+  for (int k = 0; k < ND; ++k) d[k] = warp_sum(d[k]);
 #pragma unroll
-  for (int k = 0; k < NI; ++k) c[k] = __reduce_add_sync(~0u, c[k]);
-  __syncthreads();  // the previous sums have been read
+  for (int k = 0; k < NI; ++k) c[k] = warp_sum(c[k]);
   if (lane == 0) {
 #pragma unroll
-    for (int k = 0; k < NF; ++k) sf[k][w] = f[k];
+    for (int k = 0; k < ND; ++k) sd[w][k] = d[k];
 #pragma unroll
-    for (int k = 0; k < NI; ++k) sc[k][w] = c[k];
+    for (int k = 0; k < NI; ++k) sc[w][k] = c[k];
   }
   __syncthreads();
-  if (threadIdx.x == 0) {
 #pragma unroll
-    for (int k = 0; k < NF; ++k) {
-      f[k] = 0.0f;
-      for (int j = 0; j < kSeqWarps; ++j) f[k] += sf[k][j];
-    }
+  for (int k = 0; k < ND; ++k) d[k] = warp_sum(lane < kSeqWarps ? sd[lane][k] : Pair{0, 0});
 #pragma unroll
-    for (int k = 0; k < NI; ++k) {
-      c[k] = 0;
-      for (int j = 0; j < kSeqWarps; ++j) c[k] += sc[k][j];
-    }
-  }
+  for (int k = 0; k < NI; ++k) c[k] = warp_sum(lane < kSeqWarps ? sc[lane][k] : 0ll);
+  __syncthreads();
 }
 
-template <typename T>
-__device__ __forceinline__ T block_total(T v) {
-  __shared__ T s[kSeqWarps];
-  v = warp_sum(v);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
-  __syncthreads();
-  T t = 0;
-  for (int j = 0; j < kSeqWarps; ++j) t += s[j];
-  return t;
-}
-
-// Everything written by any block before is visible to every block after.  A grid of
-// one block is launched plainly, larger ones cooperatively.
-__device__ __forceinline__ void grid_barrier() {
-  if (gridDim.x == 1)
-    __syncthreads();
-  else
+// Everything written by any block before is visible to every block after.
+__device__ __forceinline__ void meet(int how) {
+  if (how == MEET_GRID)
     cooperative_groups::this_grid().sync();
+  else if (how == MEET_CLUSTER)
+    cooperative_groups::this_cluster().sync();
+  else
+    __syncthreads();
 }
 
-// Whether cu is in order and inside the axis (block-wide).
+// Whether cu is in order and inside the axis (by a whole block).
 __device__ __forceinline__ bool seqs_ok(const Seqs& q) {
+  if (!q.cu) return true;
   int bad = 0;
-  if (q.cu)
-    for (int64_t i = threadIdx.x; i < q.B; i += kSeqThreads) {
-      const int64_t a = q.cu64 ? __ldg(static_cast<const long long*>(q.cu) + i)
-                               : __ldg(static_cast<const int*>(q.cu) + i);
-      const int64_t b = q.cu64 ? __ldg(static_cast<const long long*>(q.cu) + i + 1)
-                               : __ldg(static_cast<const int*>(q.cu) + i + 1);
-      bad |= a < 0 || b < a || b > q.total;
-    }
+  for (int64_t i = threadIdx.x; i < q.B; i += kSeqThreads) {
+    const int64_t a = q.cu64 ? __ldg(static_cast<const long long*>(q.cu) + i)
+                             : __ldg(static_cast<const int*>(q.cu) + i);
+    const int64_t b = q.cu64 ? __ldg(static_cast<const long long*>(q.cu) + i + 1)
+                             : __ldg(static_cast<const int*>(q.cu) + i + 1);
+    bad |= a < 0 || b < a || b > q.total;
+  }
   return __syncthreads_or(bad) == 0;
 }
 
@@ -220,11 +256,11 @@ __device__ __forceinline__ float exp_m1_mx(float x) {
 inline int make_seqs(const flce_seqs* a, Seqs* q) {
   if (a->B < 0 || a->S < 0) return FLCE_ERR_BAD_SHAPE;
   const int64_t lim = (int64_t(1) << 31) - 1;
-  if (a->B > lim || a->S > (int64_t(1) << 40)) return FLCE_ERR_BAD_SHAPE;
+  if (a->B > lim || a->S > (int64_t(1) << 38)) return FLCE_ERR_BAD_SHAPE;
   if (a->dtype < FLCE_F32 || a->dtype > FLCE_F16) return FLCE_ERR_BAD_ARG;
   if (a->cu_kind < 0 || a->cu_kind > 2 || a->mask_kind < 0 || a->mask_kind > 2)
     return FLCE_ERR_BAD_ARG;
-  if (a->cu_kind == 0 && a->B > 0 && a->S > (int64_t(1) << 40) / a->B) return FLCE_ERR_BAD_SHAPE;
+  if (a->cu_kind == 0 && a->B > 0 && a->S > (int64_t(1) << 38) / a->B) return FLCE_ERR_BAD_SHAPE;
   if ((a->cu_kind != 0) != (a->cu_seqlens != nullptr)) return FLCE_ERR_BAD_ARG;
   if ((a->mask_kind != 0) != (a->mask != nullptr)) return FLCE_ERR_BAD_ARG;
   const uintptr_t cu = reinterpret_cast<uintptr_t>(a->cu_seqlens);
@@ -239,21 +275,44 @@ inline int make_seqs(const flce_seqs* a, Seqs* q) {
   q->mask_labels = a->mask_kind == 2;
   q->ignore_index = a->ignore_index;
   q->mask_skip = a->cu_kind ? 0 : a->ld_mask - a->S;
+  const int64_t per_row = a->S > 0 ? (a->S + kTile - 1) / kTile : 1;
+  const int64_t pieces = a->cu_kind ? q->total / kTile + q->B + 1 : q->B * per_row;
+  if (pieces > lim - kTile) return FLCE_ERR_BAD_SHAPE;
+  q->per_row = a->cu_kind ? 0 : static_cast<int>(per_row);
+  q->pieces = static_cast<int>(pieces);
   return FLCE_OK;
 }
 
 inline int seq_elem_bytes(int dtype) { return dtype == FLCE_F32 ? 4 : 2; }
 
-// Plain for one block, cooperative (all blocks resident, as the barrier needs) otherwise.
+// A warp per piece: one block where its warps suffice, else a cluster of at most eight
+// (whose hardware barrier takes a fraction of a grid's), else a cooperative grid of at most
+// the blocks that the GPU holds at once, whose warps take several pieces each.
 template <typename Args>
-inline cudaError_t launch_seq(void (*kernel)(Args), const Args& args, int64_t blocks,
-                              cudaStream_t st) {
+inline cudaError_t launch_seq(void (*kernel)(Args), const Args& args, int sms, cudaStream_t st) {
   Args a = args;
   void* params[] = {&a};
-  const dim3 grid(static_cast<unsigned>(blocks)), block(kSeqThreads);
-  return blocks == 1 ? cudaLaunchKernel(reinterpret_cast<const void*>(kernel), grid, block, params, 0, st)
-                     : cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(kernel), grid,
-                                                   block, params, 0, st);
+  int64_t blocks = (int64_t(a.q.pieces) + kSeqWarps - 1) / kSeqWarps;
+  if (blocks < 1) blocks = 1;
+  const int64_t cap = int64_t(sms) * kSeqBlocksPerSm;
+  a.q.meet = blocks == 1 ? MEET_BLOCK : blocks <= kClusterBlocks ? MEET_CLUSTER : MEET_GRID;
+  if (a.q.meet == MEET_CLUSTER) blocks = blocks <= 2 ? 2 : blocks <= 4 ? 4 : 8;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks < cap ? blocks : cap));
+  cfg.blockDim = dim3(kSeqThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  if (a.q.meet == MEET_CLUSTER) {
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = cfg.gridDim.x;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  } else {
+    attr.id = cudaLaunchAttributeCooperative;
+    attr.val.cooperative = 1;
+  }
+  cfg.attrs = &attr;
+  cfg.numAttrs = a.q.meet == MEET_BLOCK ? 0 : 1;
+  return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(kernel), params);
 }
 
 }  // namespace flce
