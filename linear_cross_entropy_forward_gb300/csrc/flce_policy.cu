@@ -11,7 +11,8 @@
 //   1  a warp per piece of at most 256 tokens: its sums;
 //   2  a warp per sequence: its pieces' sums, added in a fixed order in pairs of floats;
 //   3  the totals (each block for itself, over the sequences' records), the loss (block
-//      0), and a second pass over the tokens for the gradients, which by then sit in L2,
+//      0), and the gradients: of a warp's first piece from what pass 1 left in shared
+//      memory, of further ones (beyond 1.2M tokens) by a second pass over the tokens,
 // between which the blocks meet.  The sums have a fixed order: results do not change from
 // run to run.  The two passes over the tokens share one body of code: a launch finds the
 // instruction cache cold, and a second copy would be fetched while nothing else runs.
@@ -21,7 +22,6 @@
 // border falls on the side that the exact difference falls on.
 #include <cmath>
 
-#include "flce_device.cuh"
 #include "flce_policy.cuh"
 
 namespace flce {
@@ -53,18 +53,16 @@ struct Ratio {
   bool clipped, dual;
 };
 
-__device__ __forceinline__ Ratio clip_ratio(const PolicyArgs& a, float h, float l, float adv) {
-  Ratio o{0.0f, true, false, false};
-  if (adv > 0.0f && pair_above(h, l, a.hi_h, a.hi_l)) {
-    o = {a.r_hi, false, true, false};
-  } else if (adv < 0.0f && pair_above(-h, -l, -a.lo_h, -a.lo_l)) {
-    o = {a.r_lo, false, true, false};
-  } else if (adv < 0.0f && a.r_dual != 0.0f && pair_above(h, l, a.dual_h, a.dual_l)) {
-    o = {a.r_dual, false, false, true};
-  } else {
-    o.value = expf(clamp_ratio(h));
-    o.live = !(fabsf(h) > kLogRatioLimit);
-  }
+// The clipped ratio of the log-ratio h + l, r = exp(h clamped).
+__device__ __forceinline__ Ratio clip_ratio(const PolicyArgs& a, float h, float l, float r,
+                                            float adv) {
+  const bool up = adv > 0.0f && pair_above(h, l, a.hi_h, a.hi_l);
+  const bool down = adv < 0.0f && pair_above(-h, -l, -a.lo_h, -a.lo_l);
+  Ratio o;
+  o.dual = adv < 0.0f && a.r_dual != 0.0f && pair_above(h, l, a.dual_h, a.dual_l);
+  o.clipped = up || down;
+  o.value = up ? a.r_hi : down ? a.r_lo : o.dual ? a.r_dual : r;
+  o.live = !(o.clipped || o.dual || fabsf(h) > kLogRatioLimit);
   return o;
 }
 
@@ -79,13 +77,13 @@ __device__ __forceinline__ void kl_term(int kind, float lp, float ref, float& k,
     dk = -e;
   } else {
     const float c = clamp_ratio(e);
-    k = exp_m1_mx(c);
+    k = exp_m1_mx(c, expf(c));
     dk = fabsf(e) > kLogRatioLimit ? 0.0f : -(c + k);  // 1 - exp(c)
   }
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kSeqThreads, kSeqBlocksPerSm) policy_kernel(PolicyArgs a) {
+__global__ void __launch_bounds__(kSeqThreads, 1) policy_kernel(PolicyArgs a) {
   const Seqs& q = a.q;
   const bool want_loss = a.what & POLICY_LOSS;
   const bool by_seq = a.ratio == FLCE_RATIO_SEQUENCE;
@@ -93,6 +91,14 @@ __global__ void __launch_bounds__(kSeqThreads, kSeqBlocksPerSm) policy_kernel(Po
   const int lane = threadIdx.x & 31;
   const int warp = blockIdx.x * kSeqWarps + (threadIdx.x >> 5);
   const int warps = gridDim.x * kSeqWarps;
+  // gradients before their weight, and which tokens count, of this warp's first piece
+  __shared__ float kept[kPerLane][kSeqThreads];
+  unsigned int kept_on = 0;
+  const bool keep = a.what == (POLICY_LOSS | POLICY_GRAD) && !by_seq;
+  if (warp == 0 && lane == 0) {
+    *a.done = 0;
+    if (a.err_store) *a.err = 0;
+  }
   float wg_all = 0.0f;  // the gradients' weight before a sequence's own
 
 #pragma unroll 1
@@ -124,6 +130,17 @@ __global__ void __launch_bounds__(kSeqThreads, kSeqBlocksPerSm) policy_kernel(Po
       const float* adv_ = a.adv + (a.adv_per_token ? pc.begin + pc.seq * a.adv_skip : pc.seq);
       T* dlp_ = static_cast<T*>(a.dlp) + pc.begin;  // outputs are dense
       T* dent_ = static_cast<T*>(a.dent) + pc.begin;
+      if (grad && keep && u == warp) {
+#pragma unroll
+        for (int k = 0; k < kPerLane; ++k) {
+          const int t = lane + 32 * k;
+          if (t < t0 || t >= t1) continue;
+          const bool on = kept_on >> k & 1;
+          if (a.dlp) store_f(dlp_ + t, kept[k][threadIdx.x] * (wg * a.lp_sign));
+          if (a.dent) store_f(dent_ + t, on ? -a.ent_coef * wg : 0.0f);
+        }
+        continue;
+      }
       float f[5] = {0, 0, 0, 0, 0};
       int c[3] = {0, 0, 0};
 #pragma unroll 1
@@ -151,10 +168,11 @@ __global__ void __launch_bounds__(kSeqThreads, kSeqBlocksPerSm) policy_kernel(Po
           const float x = a.lp_sign * lp[j];
           float h = 0.0f, l = 0.0f, dl = coef;
           if (a.old_lp) exact_diff(x, old[j], h, l);
+          const float hc = clamp_ratio(h), e = expf(hc);
           if (by_seq) {
             if (on[j]) f[4] += h;
           } else {
-            const Ratio r = clip_ratio(a, h, l, adv[j]);
+            const Ratio r = clip_ratio(a, h, l, e, adv[j]);
             const float ra = r.value * adv[j];
             dl = r.live ? -ra : 0.0f;
             if (on[j]) {
@@ -169,6 +187,10 @@ __global__ void __launch_bounds__(kSeqThreads, kSeqBlocksPerSm) policy_kernel(Po
             if (on[j]) f[1] += kl;
             dl = fmaf(a.kl_coef, dkl, dl);
           }
+          if (!grad && keep && u == warp) {
+            kept[k0 / 32 + j][threadIdx.x] = on[j] ? dl : 0.0f;
+            kept_on |= static_cast<unsigned int>(on[j]) << (k0 / 32 + j);
+          }
           if (grad) {
             if (t >= t0 && t < t1) {
               if (a.dlp) store_f(dlp_ + t, on[j] ? dl * (wg * a.lp_sign) : 0.0f);
@@ -176,14 +198,13 @@ __global__ void __launch_bounds__(kSeqThreads, kSeqBlocksPerSm) policy_kernel(Po
             }
           } else if (on[j]) {
             ++c[0];
-            f[3] += exp_m1_mx(clamp_ratio(h));
+            f[3] += exp_m1_mx(hc, e);
             f[2] += ent[j];
           }
         }
       }
       if (!grad) {
-#pragma unroll
-        for (int k = 0; k < 5; ++k) f[k] = warp_sum(f[k]);
+        warp_sums(f);
 #pragma unroll
         for (int k = 0; k < 3; ++k) c[k] = warp_sum(c[k]);
         if (lane == 0) a.piece[u] = {f[0], f[1], f[2], f[3], f[4], c[0], c[1], c[2]};
@@ -210,8 +231,7 @@ __global__ void __launch_bounds__(kSeqThreads, kSeqBlocksPerSm) policy_kernel(Po
         c[1] += r.clipped;
         c[2] += r.dual;
       }
-#pragma unroll
-      for (int k = 0; k < 5; ++k) f[k] = warp_sum(f[k]);
+      warp_sums(f);
       n = warp_sum(n);
       c[1] = warp_sum(c[1]);
       c[2] = warp_sum(c[2]);
@@ -223,7 +243,7 @@ __global__ void __launch_bounds__(kSeqThreads, kSeqBlocksPerSm) policy_kernel(Po
           const float h = f[4].value() / fn;
           const float l = (fmaf(-h, fn, f[4].h) + f[4].l) / fn;
           const float adv = __ldg(a.adv + i);
-          const Ratio r = clip_ratio(a, h, l, adv);
+          const Ratio r = clip_ratio(a, h, l, expf(clamp_ratio(h)), adv);
           const float ra = r.value * adv;
           o.pg = {-fn * ra, fmaf(-fn, ra, fn * ra)};
           o.coef = r.live ? -ra : 0.0f;
@@ -232,8 +252,9 @@ __global__ void __launch_bounds__(kSeqThreads, kSeqBlocksPerSm) policy_kernel(Po
         }
         a.seq[i] = o;
       }
+      sequence_done(q, a.done);
     }
-    meet(q.meet);
+    meet_sequences(q, a.done, static_cast<unsigned int>(q.B), a.err);
 
     // ---- totals and the loss
     const bool first_block = blockIdx.x == 0;
@@ -255,15 +276,8 @@ __global__ void __launch_bounds__(kSeqThreads, kSeqBlocksPerSm) policy_kernel(Po
         c[3] += r.dual;
       }
     }
-    if (first_block) {
-      block_sums(f, c);
-    } else {
-      Pair none[1] = {};
-      long long two[2] = {c[0], c[1]};
-      block_sums(none, two);
-      c[0] = two[0];
-      c[1] = two[1];
-    }
+    block_counts(c);
+    if (first_block && want_loss) block_sums(f, q.B);
     const float one_token = c[0] > 0 ? 1.0f / static_cast<float>(c[0]) : 0.0f;
     const float one_seq = c[1] > 0 ? 1.0f / static_cast<float>(c[1]) : 0.0f;
     const float w_all = a.aggregate == FLCE_AGG_TOKEN_MEAN ? one_token
@@ -273,10 +287,7 @@ __global__ void __launch_bounds__(kSeqThreads, kSeqBlocksPerSm) policy_kernel(Po
     if (first_block) {
       const bool ok = seqs_ok(q);
       if (threadIdx.x == 0) {
-        if (a.err_store)
-          *a.err = ok ? 0u : FLCE_DEVERR_SEQS;
-        else if (!ok)
-          atomicOr(a.err, FLCE_DEVERR_SEQS);
+        if (!ok) atomicOr(a.err, FLCE_DEVERR_SEQS);
         if (want_loss) {
           const float nan = __int_as_float(0x7fc00000);
           a.loss[0] = ok ? w_all * (f[0] + f[1]).value() : nan;
@@ -376,6 +387,7 @@ int policy_args(const flce_policy_params* p, void* workspace, PolicyArgs* a) {
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a->err = reinterpret_cast<uint32_t*>(ws);
   a->err_store = 1;
+  a->done = a->err + 16;
   a->piece = reinterpret_cast<PolicyPiece*>(ws + 256);
   a->seq = reinterpret_cast<PolicySeq*>(ws + 256 + align256(static_cast<size_t>(a->q.pieces) * sizeof(PolicyPiece)));
   return FLCE_OK;

@@ -48,7 +48,8 @@ struct PolicyArgs {
   void *dlp, *dent;
   float* lp_out;
   uint32_t* err;
-  int err_store;  // the word is this launch's own: stored; else set bits are added to it
+  int err_store;  // the word is this launch's own and cleared by it
+  unsigned int* done;
   PolicyPiece* piece;
   PolicySeq* seq;
 };

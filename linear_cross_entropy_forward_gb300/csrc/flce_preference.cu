@@ -40,6 +40,7 @@ struct PrefArgs {
   float *loss, *rewards;
   void* dlp;
   uint32_t* err;
+  unsigned int* done;
   PrefPiece* piece;
   float* coef;       // [B] gradient of the pair's own loss by a token of sequence i
   float* pair_loss;  // [B / 2]
@@ -76,17 +77,21 @@ __device__ void pair_value(const PrefArgs& a, float h, float& l, float& dh) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kSeqThreads, kSeqBlocksPerSm) preference_kernel(PrefArgs a) {
+__global__ void __launch_bounds__(kSeqThreads, 1) preference_kernel(PrefArgs a) {
   const Seqs& q = a.q;
   const int lane = threadIdx.x & 31;
   const int warp = blockIdx.x * kSeqWarps + (threadIdx.x >> 5);
   const int warps = gridDim.x * kSeqWarps;
+  if (warp == 0 && lane == 0) {
+    *a.done = 0;
+    *a.err = 0;
+  }
   for (int u = warp; u < q.pieces; u += warps) {
     const Piece pc = find_piece(q, u);
     const Counted counted(q, pc);
     const T* lp_ = static_cast<const T*>(a.lp) + pc.begin + pc.seq * a.lp_skip;
     const T* ref_ = static_cast<const T*>(a.ref) + pc.begin + pc.seq * a.ref_skip;
-    float score = 0.0f, like = 0.0f;
+    float f[2] = {0.0f, 0.0f};
     int n = 0;
     // the loads of all the lane's tokens first, masked ones' too
     float lp[kPerLane], ref[kPerLane];
@@ -102,39 +107,41 @@ __global__ void __launch_bounds__(kSeqThreads, kSeqBlocksPerSm) preference_kerne
 #pragma unroll
     for (int k = 0; k < kPerLane; ++k)
       if (on[k]) {
-        score += lp[k] - ref[k];
-        like += lp[k];
+        f[0] += lp[k] - ref[k];
+        f[1] += lp[k];
         ++n;
       }
-    score = warp_sum(score);
-    like = warp_sum(like);
+    warp_sums(f);
     n = warp_sum(n);
-    if (lane == 0) a.piece[u] = {score, like, n, 0};
+    if (lane == 0) a.piece[u] = {f[0], f[1], n, 0};
   }
   meet(q.meet);
 
   const int64_t pairs = q.B / 2;
   for (int64_t i = warp; i < pairs; i += warps) {
     int64_t id[2];
-    Pair score[2], like{};
-    long long n[2];
+    Pair score[2] = {}, like{};
+    long long n[2] = {0, 0};
     id[0] = a.interleaved ? 2 * i : i;
     id[1] = a.interleaved ? 2 * i + 1 : pairs + i;
-#pragma unroll
-    for (int side = 0; side < 2; ++side) {
+#pragma unroll 1
+    for (int side = 1; side >= 0; --side) {
       int first, last;
       seq_pieces(q, id[side], first, last);
-      Pair sc{}, lk{};
+      Pair f[2] = {};
       long long c = 0;
       for (int u = first + lane; u < last; u += 32) {
         const PrefPiece r = a.piece[u];
-        sc = sc + r.score;
-        lk = lk + r.like;
+        f[0] = f[0] + r.score;
+        f[1] = f[1] + r.like;
         c += r.n;
       }
-      score[side] = warp_sum(sc);
-      n[side] = warp_sum(c);
-      if (side == 0) like = warp_sum(lk);
+      warp_sums(f);
+      score[1] = side == 1 ? f[0] : score[1];
+      score[0] = f[0];
+      like = f[1];
+      n[1] = side == 1 ? warp_sum(c) : n[1];
+      n[0] = side == 1 ? 0 : warp_sum(c);
     }
     if (lane == 0) {
       const float per[2] = {n[0] > 0 ? 1.0f / static_cast<float>(n[0]) : 0.0f,
@@ -163,8 +170,9 @@ __global__ void __launch_bounds__(kSeqThreads, kSeqBlocksPerSm) preference_kerne
         a.rewards[id[1]] = a.beta * score[1].value();
       }
     }
+    sequence_done(q, a.done);
   }
-  meet(q.meet);
+  meet_sequences(q, a.done, static_cast<unsigned int>(pairs), a.err);
 
   Pair l[1] = {};
   long long live[1] = {0};
@@ -178,12 +186,13 @@ __global__ void __launch_bounds__(kSeqThreads, kSeqBlocksPerSm) preference_kerne
       l[0] = l[0] + v;
     }
   }
-  block_sums(l, live);
+  block_counts(live);
+  if (blockIdx.x == 0 && a.want_loss) block_sums(l, pairs);
   const float scale =
       a.reduction == FLCE_RED_MEAN ? (live[0] > 0 ? 1.0f / static_cast<float>(live[0]) : 0.0f)
                                    : 1.0f;
   if (blockIdx.x == 0 && threadIdx.x == 0) {
-    *a.err = ok ? 0u : FLCE_DEVERR_SEQS;
+    if (!ok) atomicOr(a.err, FLCE_DEVERR_SEQS);
     if (a.want_loss && a.reduction != FLCE_RED_NONE)
       a.loss[0] = ok ? l[0].value() * scale : nan;
   }
@@ -310,6 +319,7 @@ int flce_preference_loss(const flce_preference_params* p, const void* logp, cons
   a.rewards = rewards;
   a.dlp = dlogp;
   a.err = reinterpret_cast<uint32_t*>(ws);
+  a.done = a.err + 16;
   a.piece = reinterpret_cast<PrefPiece*>(ws + L.piece);
   a.coef = reinterpret_cast<float*>(ws + L.coef);
   a.pair_loss = reinterpret_cast<float*>(ws + L.pair_loss);

@@ -23,12 +23,12 @@
 #include <stdint.h>
 
 #include "../../include/flce.h"
+#include "flce_device.cuh"
 
 namespace flce {
 
-constexpr int kSeqThreads = 512;
+constexpr int kSeqThreads = 1024;  // one block per SM, 64 registers: few blocks to meet
 constexpr int kSeqWarps = kSeqThreads / 32;
-constexpr int kSeqBlocksPerSm = 2;  // the kernels' launch bounds: 64 registers
 constexpr int kPerLane = 8;
 constexpr int kTile = 32 * kPerLane;
 constexpr int kClusterBlocks = 8;   // the portable cluster size
@@ -143,15 +143,10 @@ __device__ __forceinline__ void store_f(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_f(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void store_f(__half* p, float v) { *p = __float2half_rn(v); }
 
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
-  return v;
-}
 // A sum as an unevaluated pair of floats (h + l, about 48 bits): the sums over pieces and
-// sequences, whose terms have both signs.  An fp64 addition takes a warp 16 times as long
-// here as an fp32 one: with fp64 sums these phases took 45 of the policy kernel's 57 us at
-// a million tokens.
+// sequences, whose terms have both signs.  fp64 adds run at a small fraction of the
+// fp32 rate here: with fp64 sums the policy kernel took 58 us at a million tokens, with
+// pairs 44.
 struct Pair {
   float h, l;
   __device__ __forceinline__ float value() const {
@@ -172,42 +167,78 @@ __device__ __forceinline__ Pair operator+(Pair a, Pair b) {
 }
 __device__ __forceinline__ Pair operator-(Pair a) { return {-a.h, -a.l}; }
 
-__device__ __forceinline__ Pair warp_sum(Pair v) {
+// Sums over a warp or a block.  Their loops stay rolled: a launch finds the instruction
+// caches cold, and with every SM fetching the same lines at once straight-line code cost
+// some 60 cycles an instruction (the unrolled forms of these sums took 40000 cycles of the
+// policy kernel's 88000 at a million tokens).
+template <int N>
+__device__ __forceinline__ void warp_sums(float (&v)[N]) {
+#pragma unroll 1
+  for (int o = 16; o > 0; o >>= 1) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    v = v + Pair{__shfl_xor_sync(~0u, v.h, o), __shfl_xor_sync(~0u, v.l, o)};
-  return v;
+    for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(~0u, v[k], o);
+  }
 }
-__device__ __forceinline__ long long warp_sum(long long v) {
+
+template <int N>
+__device__ __forceinline__ void warp_sums(Pair (&v)[N]) {
+#pragma unroll 1
+  for (int o = 16; o > 0; o >>= 1) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
-  return v;
+    for (int k = 0; k < N; ++k)
+      v[k] = v[k] + Pair{__shfl_xor_sync(~0u, v[k].h, o), __shfl_xor_sync(~0u, v[k].l, o)};
+  }
 }
 
 __device__ __forceinline__ int warp_sum(int v) { return __reduce_add_sync(~0u, v); }
 
-// Sums of ND values and NI counts over the block, in a fixed order, in every thread.
-template <int ND, int NI>
-__device__ __forceinline__ void block_sums(Pair (&d)[ND], long long (&c)[NI]) {
-  __shared__ Pair sd[kSeqWarps][ND];
-  __shared__ long long sc[kSeqWarps][NI];
+// 0 <= v < 2^38, as its low 20 and its other bits.
+__device__ __forceinline__ long long warp_sum(long long v) {
+  const int lo = __reduce_add_sync(~0u, static_cast<int>(v & 0xfffff));
+  const int hi = __reduce_add_sync(~0u, static_cast<int>(v >> 20));
+  return (static_cast<long long>(hi) << 20) + lo;
+}
+
+// In a fixed order, valid in warp 0; only the threads below `used` hold values.
+template <int N>
+__device__ __forceinline__ void block_sums(Pair (&v)[N], int64_t used) {
+  __shared__ Pair s[kSeqWarps][N];
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int busy = used < kSeqThreads ? static_cast<int>(used + 31) / 32 : kSeqWarps;
+#pragma unroll 1
+  for (int stage = 0; stage < 2; ++stage) {
+    if (w < busy) warp_sums(v);
+    if (stage == 1) break;
+    if (lane == 0 && w < busy) {
 #pragma unroll
-  for (int k = 0; k < ND; ++k) d[k] = warp_sum(d[k]);
+      for (int k = 0; k < N; ++k) s[w][k] = v[k];
+    }
+    __syncthreads();
+    if (w > 0) break;
 #pragma unroll
-  for (int k = 0; k < NI; ++k) c[k] = warp_sum(c[k]);
-  if (lane == 0) {
+    for (int k = 0; k < N; ++k) v[k] = lane < busy ? s[lane][k] : Pair{0.0f, 0.0f};
+  }
+}
+
+// Sums of non-negative whole numbers below 2^38, the same in any order, in every thread.
+// Called once per kernel.  (32-bit halves: a 64-bit atomic in shared memory is a loop.)
+template <int N>
+__device__ __forceinline__ void block_counts(long long (&c)[N]) {
+  __shared__ unsigned int s[2][N];
+  if (threadIdx.x < 2 * N) s[threadIdx.x / N][threadIdx.x % N] = 0;
+  __syncthreads();
 #pragma unroll
-    for (int k = 0; k < ND; ++k) sd[w][k] = d[k];
-#pragma unroll
-    for (int k = 0; k < NI; ++k) sc[w][k] = c[k];
+  for (int k = 0; k < N; ++k) {
+    const unsigned int lo = __reduce_add_sync(~0u, static_cast<unsigned int>(c[k] & 0xfffff));
+    const unsigned int hi = __reduce_add_sync(~0u, static_cast<unsigned int>(c[k] >> 20));
+    if ((threadIdx.x & 31) == 0 && (lo | hi)) {
+      atomicAdd(&s[0][k], lo);
+      atomicAdd(&s[1][k], hi);
+    }
   }
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < ND; ++k) d[k] = warp_sum(lane < kSeqWarps ? sd[lane][k] : Pair{0, 0});
-#pragma unroll
-  for (int k = 0; k < NI; ++k) c[k] = warp_sum(lane < kSeqWarps ? sc[lane][k] : 0ll);
-  __syncthreads();
+  for (int k = 0; k < N; ++k) c[k] = (static_cast<long long>(s[1][k]) << 20) + s[0][k];
 }
 
 // Everything written by any block before is visible to every block after.
@@ -218,6 +249,42 @@ __device__ __forceinline__ void meet(int how) {
     cooperative_groups::this_cluster().sync();
   else
     __syncthreads();
+}
+
+// The second meeting of a grid, at which most blocks have nothing left to do: polled at full
+// speed by all of them, the barrier's word kept its part of L2 from the few that still
+// read there (the sequences' sums took 15000 cycles instead of 1700).  So these blocks
+// sleep between looks.  `done` counts the warps' finished sequences and was cleared before
+// the first meeting.  A wait ends after 2 s at the latest, with the time-out bit set.
+__device__ __forceinline__ void sequence_done(const Seqs& q, unsigned int* done) {
+  if (q.meet != MEET_GRID) return;
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) {
+    __threadfence();
+    atomicAdd(done, 1u);
+  }
+}
+
+__device__ __forceinline__ void meet_sequences(const Seqs& q, const unsigned int* done,
+                                               unsigned int expected, uint32_t* err) {
+  if (q.meet != MEET_GRID) {
+    meet(q.meet);
+    return;
+  }
+  if (threadIdx.x == 0) {
+    const uint64_t t0 = global_timer_ns();
+    unsigned int n;
+    while (true) {
+      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(n) : "l"(done) : "memory");
+      if (n >= expected) break;
+      if (global_timer_ns() - t0 > FLCE_WAIT_LIMIT_NS) {
+        atomicOr(err, FLCE_DEVERR_TIMEOUT);
+        break;
+      }
+      __nanosleep(100);
+    }
+  }
+  __syncthreads();
 }
 
 // Whether cu is in order and inside the axis (by a whole block).
@@ -234,9 +301,9 @@ __device__ __forceinline__ bool seqs_ok(const Seqs& q) {
   return __syncthreads_or(bad) == 0;
 }
 
-// exp(x) - 1 - x for |x| <= 20: near 0 the series x^2 (1/2! + x/3! + x^2/4! + ...), whose
-// terms do not cancel (the difference itself would leave nothing of a small x^2 / 2).
-__device__ __forceinline__ float exp_m1_mx(float x) {
+// exp(x) - 1 - x given e = exp(x), |x| <= 20: near 0 the series x^2 (1/2! + x/3! + x^2/4! +
+// ...), whose terms do not cancel (the difference would leave nothing of a small x^2 / 2).
+__device__ __forceinline__ float exp_m1_mx(float x, float e) {
   if (fabsf(x) < 0.5f) {
     float s = 1.0f / 3628800.0f;
     s = fmaf(s, x, 1.0f / 362880.0f);
@@ -249,7 +316,7 @@ __device__ __forceinline__ float exp_m1_mx(float x) {
     s = fmaf(s, x, 0.5f);
     return x * x * s;
   }
-  return expf(x) - 1.0f - x;
+  return e - 1.0f - x;
 }
 
 // Host: the layout of an entry point's arguments; FLCE_OK or the refusal.
@@ -294,7 +361,7 @@ inline cudaError_t launch_seq(void (*kernel)(Args), const Args& args, int sms, c
   void* params[] = {&a};
   int64_t blocks = (int64_t(a.q.pieces) + kSeqWarps - 1) / kSeqWarps;
   if (blocks < 1) blocks = 1;
-  const int64_t cap = int64_t(sms) * kSeqBlocksPerSm;
+  const int64_t cap = sms;
   a.q.meet = blocks == 1 ? MEET_BLOCK : blocks <= kClusterBlocks ? MEET_CLUSTER : MEET_GRID;
   if (a.q.meet == MEET_CLUSTER) blocks = blocks <= 2 ? 2 : blocks <= 4 ? 4 : 8;
   cudaLaunchConfig_t cfg{};
