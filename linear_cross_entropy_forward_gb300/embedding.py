@@ -11,35 +11,42 @@ import ctypes
 import torch
 
 from . import _binding as B
-from .losses import _DTYPES, _allocate_on, _workspace
+from .losses import _DTYPES, _current_device, _on, _raw_stream, _workspace
 
 
 def embedding_params(N, H, V, scale=1.0, dtype=torch.bfloat16, grad_dtype=None, ids_int64=True,
                      accumulate=False, padding_idx=None, v_offset=0, v_total=0, validate=False):
     """FlceEmbeddingParams; padding_idx None: none."""
-    for d in (dtype, grad_dtype or dtype):
-        if d not in _DTYPES:
-            raise TypeError(f"embedding types are float32, bfloat16 and float16, got {d}")
-    return B.FlceEmbeddingParams(int(N), int(H), int(V), int(v_offset), int(v_total),
-                                 -1 if padding_idx is None else int(padding_idx), float(scale),
-                                 _DTYPES[dtype], _DTYPES[grad_dtype or dtype], int(ids_int64),
-                                 int(accumulate), int(validate))
+    try:
+        dt, gdt = _DTYPES[dtype], _DTYPES[grad_dtype or dtype]
+    except KeyError as e:
+        raise TypeError(f"embedding types are float32, bfloat16 and float16, got {e}") from None
+    return B.FlceEmbeddingParams(N, H, V, v_offset, v_total,
+                                 -1 if padding_idx is None else padding_idx, scale, dt, gdt,
+                                 bool(ids_int64), bool(accumulate), bool(validate))
 
 
 def embedding_workspace_size(params: "B.FlceEmbeddingParams") -> int:
     """Bytes of workspace a flce_embedding_backward call with these parameters needs."""
-    lib = B.load_library()
-    B._check(lib.flce_embedding_check_params(ctypes.byref(params)))
-    return int(lib.flce_embedding_workspace_size(ctypes.byref(params)))
+    lib = B._lib or B.load_library()
+    size = lib.flce_embedding_workspace_size(ctypes.byref(params))
+    if size == 0:
+        B._check(lib.flce_embedding_check_params(ctypes.byref(params)))
+    return size
 
 
 def _need_ids(ids):
+    """Checks the ids; their device's index."""
     if not isinstance(ids, torch.Tensor) or not ids.is_cuda:
         raise TypeError("ids must be a CUDA tensor")
     if ids.dtype not in (torch.int64, torch.int32):
         raise TypeError(f"ids must be int64 or int32, got {ids.dtype}")
     if not ids.is_contiguous():
         raise ValueError("ids must be contiguous")
+    index = ids.get_device()
+    if index != _current_device():
+        B._on_current_device(ids)
+    return index
 
 
 def flce_embedding(ids, weight, scale=1.0, v_offset=0, v_total=0, validate=False, stream=None,
@@ -51,28 +58,31 @@ def flce_embedding(ids, weight, scale=1.0, v_offset=0, v_total=0, validate=False
     rows are zero, so that the shards' sum is the lookup.  An id outside the table gives a
     row of NaN; with validate the call waits and raises.
     """
-    lib = B.load_library()
-    _need_ids(ids)
-    dev = B._on_current_device(ids)
+    if stream is not None:
+        return _on(stream, flce_embedding, ids, weight, scale, v_offset, v_total, validate,
+                   out=out)
+    lib = B._lib or B.load_library()
+    dev = _need_ids(ids)
     if not isinstance(weight, torch.Tensor) or not weight.is_cuda or weight.dtype not in _DTYPES:
         raise TypeError("weight must be a bf16, fp16 or fp32 CUDA tensor")
-    if weight.dim() != 2:
-        raise ValueError(f"weight must be [V, H], got shape {tuple(weight.shape)}")
+    if weight.dim() != 2 or not weight.is_contiguous():
+        raise ValueError(f"weight must be a contiguous [V, H], got shape {tuple(weight.shape)}")
+    if weight.get_device() != dev:
+        raise ValueError(f"weight is on {weight.device}, ids on {ids.device}")
     V, H = weight.shape
-    B._need(weight, "weight", weight.dtype, (V, H), dev)
     shape = (*ids.shape, H)
-    p = embedding_params(ids.numel(), H, V, scale, weight.dtype,
-                         ids_int64=ids.dtype == torch.int64, v_offset=v_offset, v_total=v_total,
-                         validate=validate)
-    with _allocate_on(stream):
-        if out is None:
-            out = torch.empty(shape, dtype=weight.dtype, device=dev)
-        else:
-            B._need(out, "out", weight.dtype, shape, dev)
-        ws = torch.empty(256, dtype=torch.uint8, device=dev) if validate else None
-        B._check(lib.flce_embedding(ctypes.byref(p), ids.data_ptr(), weight.data_ptr(),
-                                    out.data_ptr(), B._ptr(ws), 256 if validate else 0,
-                                    B._stream(stream)))
+    p = embedding_params(ids.numel(), H, V, scale, weight.dtype, None, ids.dtype is torch.int64,
+                         False, None, v_offset, v_total, validate)
+    if out is None:
+        out = torch.empty(shape, dtype=weight.dtype, device=dev)
+    else:
+        B._need(out, "out", weight.dtype, shape, ids.device)
+    ws = torch.empty(256, dtype=torch.uint8, device=dev) if validate else None
+    code = lib.flce_embedding(ctypes.byref(p), ids.data_ptr(), weight.data_ptr(), out.data_ptr(),
+                              None if ws is None else ws.data_ptr(), 256 if validate else 0,
+                              _raw_stream(dev))
+    if code:
+        B._check(code)
     return out
 
 
@@ -86,15 +96,17 @@ def flce_embedding_backward(dout, ids, V, scale=1.0, padding_idx=None, dweight=N
     to it and touches no other row.  Ids equal to padding_idx have no gradient, nor have
     those of other shards.
     """
-    lib = B.load_library()
-    _need_ids(ids)
-    dev = B._on_current_device(ids)
+    if stream is not None:
+        return _on(stream, flce_embedding_backward, dout, ids, V, scale, padding_idx, dweight,
+                   accumulate, grad_dtype, v_offset, v_total, validate, workspace)
+    lib = B._lib or B.load_library()
+    dev = _need_ids(ids)
     if not isinstance(dout, torch.Tensor) or not dout.is_cuda or dout.dtype not in _DTYPES:
         raise TypeError("dout must be a bf16, fp16 or fp32 CUDA tensor")
     if dout.dim() < 1:
         raise ValueError("dout must be [*ids.shape, H]")
     H = dout.shape[-1]
-    B._need(dout, "dout", dout.dtype, (*ids.shape, H), dev)
+    B._need(dout, "dout", dout.dtype, (*ids.shape, H), ids.device)
     if dweight is None:
         if accumulate:
             raise ValueError("accumulate needs dweight")
@@ -103,19 +115,20 @@ def flce_embedding_backward(dout, ids, V, scale=1.0, padding_idx=None, dweight=N
         gdt = dweight.dtype if isinstance(dweight, torch.Tensor) else None
         if grad_dtype is not None and grad_dtype != gdt:
             raise TypeError(f"dweight must be {grad_dtype}, got {gdt}")
-        if gdt not in (dout.dtype, torch.float32):
-            raise TypeError(f"dweight must be {dout.dtype} or float32, got {gdt}")
-        B._need(dweight, "dweight", gdt, (V, H), dev)
-    p = embedding_params(ids.numel(), H, V, scale, dout.dtype, gdt, ids.dtype == torch.int64,
+        B._need(dweight, "dweight", gdt, (V, H), ids.device)
+    if gdt not in (dout.dtype, torch.float32):
+        raise TypeError(f"dweight must be {dout.dtype} or float32, got {gdt}")
+    p = embedding_params(ids.numel(), H, V, scale, dout.dtype, gdt, ids.dtype is torch.int64,
                          accumulate, padding_idx, v_offset, v_total, validate)
     size = embedding_workspace_size(p)
-    with _allocate_on(stream):
-        if dweight is None:
-            dweight = torch.empty(V, H, dtype=gdt, device=dev)
-        ws = _workspace(size, dev, workspace)
-        B._check(lib.flce_embedding_backward(
-            ctypes.byref(p), dout.data_ptr(), ids.data_ptr(), dweight.data_ptr(), ws.data_ptr(),
-            ws.numel(), B._stream(stream)))
+    if dweight is None:
+        dweight = torch.empty(V, H, dtype=gdt, device=dev)
+    ws = _workspace(size, dev, workspace)
+    code = lib.flce_embedding_backward(
+        ctypes.byref(p), dout.data_ptr(), ids.data_ptr(), dweight.data_ptr(), ws.data_ptr(),
+        ws.numel(), _raw_stream(dev))
+    if code:
+        B._check(code)
     return dweight
 
 

@@ -13,7 +13,6 @@ per call, is the library's.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 import torch
@@ -36,38 +35,59 @@ def _code(table, value, name):
         raise ValueError(f"{name} must be one of {'/'.join(table)}, got {value!r}") from None
 
 
-def _allocate_on(stream):
-    """New tensors belong to the stream that the call runs on: memory of another stream's
-    pool could still be in use there."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+_MASKS = {torch.bool: 1, torch.uint8: 1, torch.int64: 2}
+
+# the plain integers behind torch.cuda.current_device() and current_stream(), which cost
+# a few microseconds where a small call takes twenty
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") \
+    else torch.cuda.current_device
 
 
-def _rows(t, name, dtype, shape, device):
-    """Checks one array of a batch; its row stride in elements."""
+def _raw_stream(index):
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _on(stream, call, *args, **kw):
+    """call(...) with `stream` current: new tensors then belong to the stream that the kernels
+    run on (memory of another stream's pool could still be in use there)."""
+    with torch.cuda.stream(stream):
+        return call(*args, **kw)
+
+
+def _refuse(t, name, dtype, shape, index):
+    """Says what is wrong with one array of a batch."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
-    if shape[-1] > 1 and t.stride(-1) != 1:
+    raise ValueError(f"{name} is on {t.device}, the other tensors on cuda:{index}")
+
+
+def _rows(t, name, dtype, shape, index):
+    """Checks one array of a batch; its row stride in elements."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.get_device() == index):
+        _refuse(t, name, dtype, shape, index)
+    s = t.stride()
+    if s[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name}'s last dimension must be dense")
-    return t.stride(0) if len(shape) == 2 else 0
+    return s[0]
 
 
 def _batch(logp, mask, cu_seqlens, ignore_index):
-    """(FlceSeqs, device, number of sequences) of a batch laid out like logp."""
+    """(FlceSeqs, device index, number of sequences) of a batch laid out like logp."""
     if not isinstance(logp, torch.Tensor) or not logp.is_cuda:
         raise TypeError("logp must be a CUDA tensor")
-    if logp.dtype not in _DTYPES:
+    dt = _DTYPES.get(logp.dtype)
+    if dt is None:
         raise TypeError(f"logp must be float32, bfloat16 or float16, got {logp.dtype}")
-    dev = B._on_current_device(logp)
-    q = B.FlceSeqs()
-    q.dtype = _DTYPES[logp.dtype]
-    q.ignore_index = ignore_index
+    index = logp.get_device()
+    if index != _current_device():
+        B._on_current_device(logp)
     shape = logp.shape
+    cu_kind = cu_ptr = mask_kind = mask_ptr = ld_mask = 0
     if cu_seqlens is not None:
         if len(shape) != 1:
             raise ValueError("with cu_seqlens, logp must be 1-D")
@@ -76,96 +96,86 @@ def _batch(logp, mask, cu_seqlens, ignore_index):
             raise TypeError("cu_seqlens must be an int32 or int64 CUDA tensor")
         if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1 or not cu_seqlens.is_contiguous():
             raise ValueError("cu_seqlens must be a contiguous [B + 1] tensor")
-        if cu_seqlens.device != dev:
-            raise ValueError(f"cu_seqlens is on {cu_seqlens.device}, logp on {dev}")
-        q.B, q.S = cu_seqlens.numel() - 1, shape[0]
-        q.cu_kind = 1 if cu_seqlens.dtype == torch.int32 else 2
-        q.cu_seqlens = cu_seqlens.data_ptr()
+        if cu_seqlens.get_device() != index:
+            raise ValueError(f"cu_seqlens is on {cu_seqlens.device}, logp on {logp.device}")
+        n_seq, S = cu_seqlens.numel() - 1, shape[0]
+        cu_kind = 1 if cu_seqlens.dtype is torch.int32 else 2
+        cu_ptr = cu_seqlens.data_ptr()
     elif len(shape) == 1:
-        q.B, q.S = 1, shape[0]
+        n_seq, S = 1, shape[0]
     elif len(shape) == 2:
-        q.B, q.S = shape
+        n_seq, S = shape
     else:
         raise ValueError(f"logp must be [B, S] or [T], got shape {tuple(shape)}")
     if mask is not None:
-        if not isinstance(mask, torch.Tensor) \
-                or mask.dtype not in (torch.bool, torch.uint8, torch.int64):
+        if not isinstance(mask, torch.Tensor) or mask.dtype not in _MASKS:
             raise TypeError("mask must be a bool, uint8 or int64 (labels) tensor")
-        q.ld_mask = _rows(mask, "mask", mask.dtype, shape, dev)
-        # an array of no elements has no address; the kind still needs one
-        q.mask_kind = 2 if mask.dtype == torch.int64 else 1
-        q.mask = mask.data_ptr() or 8
-    return q, dev, q.B
+        ld_mask = _rows(mask, "mask", mask.dtype, shape, index)
+        mask_kind = _MASKS[mask.dtype]
+        mask_ptr = mask.data_ptr() or 8  # an array of no elements has no address
+    return B.FlceSeqs(n_seq, S, cu_ptr, mask_ptr, ld_mask, ignore_index, cu_kind, mask_kind,
+                      dt), index, n_seq
 
 
-def _check_cu(q):
-    if q.cu_kind and not q.cu_seqlens:
-        raise ValueError("cu_seqlens is empty")
-
-
-def _scalar_grad(g, n, device):
-    if g is None:
-        return None
-    B._need(g, "g_loss", torch.float32, (n,), device)
-    return g
+def _scalar_grad(g, n, index):
+    if g is not None:
+        _rows(g, "g_loss", torch.float32, torch.Size((n,)), index)
 
 
 def policy_params(logp, old_logp=None, advantages=None, ref_logp=None, entropy=None, mask=None,
                   cu_seqlens=None, clip_low=0.2, clip_high=0.2, dual_clip=0.0, kl_coef=0.0,
                   kl="k3", entropy_coef=0.0, ratio="token", aggregate="token_mean", scale=1.0,
                   ignore_index=IGNORE_INDEX, validate=False):
-    """(FlcePolicyParams, device) of a flce_policy_loss call, its tensors checked."""
-    p = B.FlcePolicyParams()
-    q, dev, n_seq = _batch(logp, mask, cu_seqlens, ignore_index)
-    p.seqs = q
+    """(FlcePolicyParams, device index) of a flce_policy_loss call, its tensors checked."""
+    seqs, index, n_seq = _batch(logp, mask, cu_seqlens, ignore_index)
     shape, dt = logp.shape, logp.dtype
-    p.ld_logp = _rows(logp, "logp", dt, shape, dev)
+    ld_logp = _rows(logp, "logp", dt, shape, index)
+    ld_old = ld_ref = ld_ent = 0
     if old_logp is not None:
-        p.ld_old = _rows(old_logp, "old_logp", dt, shape, dev)
+        ld_old = _rows(old_logp, "old_logp", dt, shape, index)
     if ref_logp is not None:
-        p.ld_ref = _rows(ref_logp, "ref_logp", dt, shape, dev)
+        ld_ref = _rows(ref_logp, "ref_logp", dt, shape, index)
     elif kl_coef:
         raise ValueError("kl_coef needs ref_logp")
     if entropy is not None:
-        p.ld_entropy = _rows(entropy, "entropy", dt, shape, dev)
+        ld_ent = _rows(entropy, "entropy", dt, shape, index)
     elif entropy_coef:
         raise ValueError("entropy_coef needs entropy")
     if not isinstance(advantages, torch.Tensor):
         raise TypeError("advantages must be a CUDA tensor")
     # one per sequence, unless the shape is the tokens' and that reading is the only one
-    per_token = advantages.shape == shape and (ratio != "sequence") and not (
-        advantages.dim() == 1 and n_seq == advantages.shape[0])
-    p.adv_per_token = per_token
-    p.ld_adv = _rows(advantages, "advantages", torch.float32, shape if per_token else
-                     torch.Size((n_seq,)), dev)
-    p.clip_low, p.clip_high, p.dual_clip = clip_low, clip_high, dual_clip
-    p.kl_coef, p.entropy_coef, p.scale = kl_coef, entropy_coef, scale
-    p.kl = _code(_KL, kl, "kl")
-    p.ratio = _code(_RATIO, ratio, "ratio")
-    p.aggregate = _code(_AGGREGATE, aggregate, "aggregate")
-    p.validate = bool(validate)
-    return p, dev
+    per_seq = torch.Size((n_seq,))
+    per_token = advantages.shape != per_seq and ratio != "sequence"
+    ld_adv = _rows(advantages, "advantages", torch.float32, shape if per_token else per_seq, index)
+    if not per_token and not advantages.is_contiguous():
+        raise ValueError("advantages must be contiguous")
+    return B.FlcePolicyParams(
+        seqs, ld_logp, ld_old, ld_ref, ld_ent, ld_adv, clip_low, clip_high, dual_clip, kl_coef,
+        entropy_coef, scale, _code(_KL, kl, "kl"), _code(_RATIO, ratio, "ratio"),
+        _code(_AGGREGATE, aggregate, "aggregate"), per_token, bool(validate)), index
 
 
-def _workspace(size, device, workspace):
+def _workspace(size, index, workspace):
     if workspace is None:
-        return torch.empty(size, dtype=torch.uint8, device=device)
+        return torch.empty(size, dtype=torch.uint8, device=index)
     if not isinstance(workspace, torch.Tensor) or workspace.dtype != torch.uint8 \
-            or not workspace.is_contiguous() or workspace.device != device:
-        raise TypeError(f"workspace must be a contiguous uint8 tensor on {device}")
+            or not workspace.is_contiguous() or workspace.get_device() != index:
+        raise TypeError(f"workspace must be a contiguous uint8 tensor on cuda:{index}")
     if workspace.numel() < size:
         raise ValueError(f"workspace holds {workspace.numel()} bytes; this call needs {size}")
     return workspace
 
 
-def _size(lib, name, p):
-    B._check(getattr(lib, f"flce_{name}_check_params")(ctypes.byref(p)))
-    return getattr(lib, f"flce_{name}_workspace_size")(ctypes.byref(p))
+def _size(lib, name, ref):
+    size = getattr(lib, f"flce_{name}_workspace_size")(ref)
+    if size == 0:
+        B._check(getattr(lib, f"flce_{name}_check_params")(ref))
+    return size
 
 
 def policy_workspace_size(params: "B.FlcePolicyParams") -> int:
     """Bytes of workspace a flce_policy_loss call with these parameters needs."""
-    return int(_size(B.load_library(), "policy", params))
+    return int(_size(B.load_library(), "policy", ctypes.byref(params)))
 
 
 def _addr(t):
@@ -176,7 +186,7 @@ def flce_policy_loss(logp, old_logp, advantages, ref_logp=None, entropy=None, ma
                      cu_seqlens=None, clip_low=0.2, clip_high=0.2, dual_clip=0.0, kl_coef=0.0,
                      kl="k3", entropy_coef=0.0, ratio="token", aggregate="token_mean", scale=1.0,
                      ignore_index=IGNORE_INDEX, g_loss=None, need_loss=True, need_grad=True,
-                     validate=False, workspace=None, stream=None):
+                     need_entropy_grad=True, validate=False, workspace=None, stream=None):
     """Clipped policy loss and its gradients, in one launch.
 
     Per counted token, with d = logp - old_logp, r = exp(d) and A its advantage:
@@ -193,34 +203,48 @@ def flce_policy_loss(logp, old_logp, advantages, ref_logp=None, entropy=None, ma
     policy term, mean KL to the reference, mean entropy, mean k3 to the old policy.
     counts (int64): counted tokens, sequences with one, clipped tokens (sequences),
     dual-clipped ones.  The gradients are times g_loss ([1] fp32, None: 1).  Parts that
-    are not wanted (need_loss, need_grad; dentropy without entropy) are None.
+    are not wanted (need_loss, need_grad, need_entropy_grad) or not there (dentropy without
+    entropy) are None.
     """
-    lib = B.load_library()
+    if stream is not None:
+        return _on(stream, flce_policy_loss, logp, old_logp, advantages, ref_logp, entropy, mask,
+                   cu_seqlens, clip_low, clip_high, dual_clip, kl_coef, kl, entropy_coef, ratio,
+                   aggregate, scale, ignore_index, g_loss, need_loss, need_grad,
+                   need_entropy_grad, validate, workspace)
+    lib = B._lib or B.load_library()
     p, dev = policy_params(logp, old_logp, advantages, ref_logp, entropy, mask, cu_seqlens,
                            clip_low, clip_high, dual_clip, kl_coef, kl, entropy_coef, ratio,
                            aggregate, scale, ignore_index, validate)
     if not need_loss and not need_grad:
         raise ValueError("neither the loss nor the gradients are wanted")
     _scalar_grad(g_loss, 1, dev)
-    size = _size(lib, "policy", p)
+    ref = ctypes.byref(p)
+    size = _size(lib, "policy", ref)
     loss = stats = counts = dlogp = dent = None
-    with _allocate_on(stream):
-        if need_loss:
-            loss = torch.empty(1, dtype=torch.float32, device=dev)
-            stats = torch.empty(4, dtype=torch.float32, device=dev)
-            counts = torch.empty(4, dtype=torch.int64, device=dev)
-        if need_grad:
-            dlogp = torch.empty(logp.shape, dtype=logp.dtype, device=dev)
-            if entropy is not None:
-                dent = torch.empty(logp.shape, dtype=logp.dtype, device=dev)
-        ws = _workspace(size, dev, workspace)
-        if need_grad and not need_loss and logp.numel() == 0:
-            return loss, stats, counts, dlogp, dent
-        B._check(lib.flce_policy_loss(
-            ctypes.byref(p), _addr(logp), _addr(old_logp), _addr(ref_logp), _addr(entropy),
-            _addr(advantages), _addr(g_loss), _addr(loss), _addr(stats), _addr(counts),
-            _addr(dlogp), _addr(dent), ws.data_ptr(), ws.numel(), B._stream(stream)))
+    if need_loss:
+        loss = torch.empty(1, dtype=torch.float32, device=dev)
+        stats = torch.empty(4, dtype=torch.float32, device=dev)
+        counts = torch.empty(4, dtype=torch.int64, device=dev)
+    if need_grad:
+        dlogp = torch.empty(logp.shape, dtype=logp.dtype, device=dev)
+        if entropy is not None and need_entropy_grad:
+            dent = torch.empty(logp.shape, dtype=logp.dtype, device=dev)
+    ws = _workspace(size, dev, workspace)
+    if not need_loss and logp.numel() == 0:
+        return loss, stats, counts, dlogp, dent
+    code = lib.flce_policy_loss(
+        ref, logp.data_ptr(), _addr(old_logp), _addr(ref_logp), _addr(entropy),
+        advantages.data_ptr(), _addr(g_loss), _addr(loss), _addr(stats), _addr(counts),
+        _addr(dlogp), _addr(dent), ws.data_ptr(), ws.numel(), _raw_stream(dev))
+    if code:
+        B._check(code)
     return loss, stats, counts, dlogp, dent
+
+
+def _upstream(g):
+    """An upstream gradient as the library takes it: dense fp32 of one dimension."""
+    g = g.reshape(-1)
+    return g if g.dtype is torch.float32 and g.is_contiguous() else g.float().contiguous()
 
 
 class _PolicyLoss(torch.autograd.Function):
@@ -237,9 +261,11 @@ class _PolicyLoss(torch.autograd.Function):
     @staticmethod
     def backward(ctx, g_loss, _g_stats, _g_counts):
         logp, entropy, old_logp, advantages, ref_logp, mask, cu = ctx.saved_tensors
-        g = g_loss.detach().reshape(1).to(torch.float32).contiguous()
+        g = _upstream(g_loss)
         _, _, _, dlogp, dent = flce_policy_loss(logp, old_logp, advantages, ref_logp, entropy,
-                                                mask, cu, g_loss=g, need_loss=False, **ctx.kw)
+                                                mask, cu, g_loss=g, need_loss=False,
+                                                need_entropy_grad=ctx.needs_input_grad[1],
+                                                **ctx.kw)
         return dlogp, dent, None, None, None, None, None, None
 
 
@@ -279,7 +305,12 @@ def flce_policy_forward_backward(hidden, weight, labels, old_logp, advantages, r
     Returns (loss [1], stats [4], counts [4], logp [N], entropy [N], dhidden, dweight);
     the gradients are times g_loss ([1] fp32, None: 1).
     """
-    lib = B.load_library()
+    if stream is not None:
+        return _on(stream, flce_policy_forward_backward, hidden, weight, labels, old_logp,
+                   advantages, ref_logp, cu_seqlens, clip_low, clip_high, dual_clip, kl_coef, kl,
+                   entropy_coef, ratio, aggregate, scale, ignore_index, softcap, weight_layout,
+                   chunk_n, dhidden_fp32, g_loss, validate, workspace)
+    lib = B._lib or B.load_library()
     N, H, V, wshape = B._dims(hidden, weight, weight_layout)
     B._need(hidden, "hidden", torch.bfloat16, (N, H))
     dev = B._on_current_device(hidden)
@@ -287,30 +318,29 @@ def flce_policy_forward_backward(hidden, weight, labels, old_logp, advantages, r
     B._need(labels, "labels", torch.int64, (N,), dev)
     p = B.make_params(N, H, V, "none", ignore_index, 0.0, softcap, validate,
                       weight_layout=weight_layout, chunk_n=chunk_n, dhidden_fp32=dhidden_fp32)
-    with _allocate_on(stream):
-        logp = torch.empty(N, dtype=torch.float32, device=dev)
-        entropy = torch.empty(N, dtype=torch.float32, device=dev)
-        q, _ = policy_params(logp, old_logp, advantages, ref_logp, entropy, None, cu_seqlens,
+    logp = torch.empty(N, dtype=torch.float32, device=dev)
+    entropy = torch.empty(N, dtype=torch.float32, device=dev)
+    q, index = policy_params(logp, old_logp, advantages, ref_logp, entropy, None, cu_seqlens,
                              clip_low, clip_high, dual_clip, kl_coef, kl, entropy_coef, ratio,
                              aggregate, scale, ignore_index, validate)
-        _scalar_grad(g_loss, 1, dev)
+    _scalar_grad(g_loss, 1, index)
+    size = lib.flce_policy_head_workspace_size(ctypes.byref(p), ctypes.byref(q))
+    if size == 0:
         B._check(lib.flce_check_params(ctypes.byref(p)))
-        _size(lib, "policy", q)
-        size = lib.flce_policy_head_workspace_size(ctypes.byref(p), ctypes.byref(q))
-        if size == 0:
-            raise B.FlceError(1, "the head cannot take these parameters (a sequence ratio needs "
-                                 "all tokens in one chunk)")
-        loss = torch.empty(1, dtype=torch.float32, device=dev)
-        stats = torch.empty(4, dtype=torch.float32, device=dev)
-        counts = torch.empty(4, dtype=torch.int64, device=dev)
-        dh = torch.empty(N, H, dtype=torch.float32 if dhidden_fp32 else torch.bfloat16, device=dev)
-        dw = torch.empty(wshape, dtype=torch.bfloat16, device=dev)
-        ws = _workspace(size, dev, workspace)
-        B._check(lib.flce_policy_forward_backward(
-            ctypes.byref(p), ctypes.byref(q), _addr(hidden), _addr(weight), _addr(labels),
-            _addr(old_logp), _addr(ref_logp), _addr(advantages), _addr(g_loss), _addr(loss),
-            _addr(stats), _addr(counts), _addr(logp), _addr(entropy), _addr(dh), _addr(dw),
-            ws.data_ptr(), ws.numel(), B._stream(stream)))
+        _size(lib, "policy", ctypes.byref(q))
+        raise B.FlceError(1, "the head cannot take these parameters (a sequence ratio needs all "
+                             "tokens in one chunk)")
+    loss = torch.empty(1, dtype=torch.float32, device=dev)
+    stats = torch.empty(4, dtype=torch.float32, device=dev)
+    counts = torch.empty(4, dtype=torch.int64, device=dev)
+    dh = torch.empty(N, H, dtype=torch.float32 if dhidden_fp32 else torch.bfloat16, device=dev)
+    dw = torch.empty(wshape, dtype=torch.bfloat16, device=dev)
+    ws = _workspace(size, index, workspace)
+    B._check(lib.flce_policy_forward_backward(
+        ctypes.byref(p), ctypes.byref(q), _addr(hidden), _addr(weight), _addr(labels),
+        _addr(old_logp), _addr(ref_logp), _addr(advantages), _addr(g_loss), _addr(loss),
+        _addr(stats), _addr(counts), _addr(logp), _addr(entropy), _addr(dh), _addr(dw),
+        ws.data_ptr(), ws.numel(), _raw_stream(index)))
     return loss, stats, counts, logp, entropy, dh, dw
 
 
@@ -329,7 +359,7 @@ class _LinearPolicyLoss(torch.autograd.Function):
     @staticmethod
     def backward(ctx, g_loss, *_):
         dh, dw = ctx.saved_tensors
-        g = g_loss.detach().reshape(1).to(torch.float32).contiguous()
+        g = _upstream(g_loss)
         dh = B.flce_scale_bf16(dh.clone(), g) if ctx.needs_input_grad[0] else None
         dw = B.flce_scale_bf16(dw.clone(), g) if ctx.needs_input_grad[1] else None
         return dh, dw, None, None, None, None, None, None
@@ -358,29 +388,25 @@ def preference_params(logp, ref_logp=None, ref_scores=None, mask=None, cu_seqlen
                       loss_type="sigmoid", label_smoothing=0.0, margin=0.0,
                       length_normalised=False, nll_coef=0.0, pairs="halves", reduction="mean",
                       ignore_index=IGNORE_INDEX, validate=False):
-    """(FlcePreferenceParams, device) of a flce_preference_loss call, its tensors checked."""
-    p = B.FlcePreferenceParams()
-    q, dev, n_seq = _batch(logp, mask, cu_seqlens, ignore_index)
-    p.seqs = q
+    """(FlcePreferenceParams, device index) of a flce_preference_loss call, its tensors checked."""
+    seqs, index, n_seq = _batch(logp, mask, cu_seqlens, ignore_index)
     if n_seq % 2:
         raise ValueError(f"pairs need an even number of sequences, got {n_seq}")
-    p.ld_logp = _rows(logp, "logp", logp.dtype, logp.shape, dev)
+    ld_logp = _rows(logp, "logp", logp.dtype, logp.shape, index)
+    ld_ref = 0
     if ref_logp is not None:
-        p.ld_ref = _rows(ref_logp, "ref_logp", logp.dtype, logp.shape, dev)
+        ld_ref = _rows(ref_logp, "ref_logp", logp.dtype, logp.shape, index)
     if ref_scores is not None:
-        B._need(ref_scores, "ref_scores", torch.float32, (n_seq,), dev)
-    p.beta, p.margin, p.label_smoothing, p.nll_coef = beta, margin, label_smoothing, nll_coef
-    p.kind = _code(_PREFERENCE, loss_type, "loss_type")
-    p.length_normalised = bool(length_normalised)
-    p.interleaved = _code(_PAIRS, pairs, "pairs")
-    p.reduction = reduction_code(reduction)
-    p.validate = bool(validate)
-    return p, dev
+        _rows(ref_scores, "ref_scores", torch.float32, torch.Size((n_seq,)), index)
+    return B.FlcePreferenceParams(
+        seqs, ld_logp, ld_ref, beta, margin, label_smoothing, nll_coef,
+        _code(_PREFERENCE, loss_type, "loss_type"), bool(length_normalised),
+        _code(_PAIRS, pairs, "pairs"), reduction_code(reduction), bool(validate)), index
 
 
 def preference_workspace_size(params: "B.FlcePreferenceParams") -> int:
     """Bytes of workspace a flce_preference_loss call with these parameters needs."""
-    return int(_size(B.load_library(), "preference", params))
+    return int(_size(B.load_library(), "preference", ctypes.byref(params)))
 
 
 def flce_preference_loss(logp, ref_logp=None, ref_scores=None, mask=None, cu_seqlens=None,
@@ -401,30 +427,36 @@ def flce_preference_loss(logp, ref_logp=None, ref_scores=None, mask=None, cu_seq
     Returns (loss, rewards [B], dlogp): loss [1], or [B / 2] with reduction 'none'; rewards =
     beta s_i; dlogp times g_loss (fp32, loss's shape, None: 1).
     """
-    lib = B.load_library()
+    if stream is not None:
+        return _on(stream, flce_preference_loss, logp, ref_logp, ref_scores, mask, cu_seqlens,
+                   beta, loss_type, label_smoothing, margin, length_normalised, nll_coef, pairs,
+                   reduction, ignore_index, g_loss, need_loss, need_grad, validate, workspace)
+    lib = B._lib or B.load_library()
     p, dev = preference_params(logp, ref_logp, ref_scores, mask, cu_seqlens, beta, loss_type,
                                label_smoothing, margin, length_normalised, nll_coef, pairs,
                                reduction, ignore_index, validate)
     if not need_loss and not need_grad:
         raise ValueError("neither the loss nor the gradient is wanted")
-    n_out = p.seqs.B // 2 if p.reduction == RED_NONE else 1
+    n_seq = p.seqs.B
+    n_out = n_seq // 2 if p.reduction == RED_NONE else 1
     _scalar_grad(g_loss, n_out, dev)
-    size = _size(lib, "preference", p)
+    ref = ctypes.byref(p)
+    size = _size(lib, "preference", ref)
     loss = rewards = dlogp = None
-    with _allocate_on(stream):
-        if need_loss:
-            loss = torch.empty(n_out, dtype=torch.float32, device=dev)
-            rewards = torch.empty(p.seqs.B, dtype=torch.float32, device=dev)
-        if need_grad:
-            dlogp = torch.empty(logp.shape, dtype=logp.dtype, device=dev)
-        ws = _workspace(size, dev, workspace)
-        if p.seqs.B == 0 and n_out == 0 or (not need_loss and logp.numel() == 0):
-            # no pair: nothing to compute
-            return loss, rewards, None if dlogp is None else dlogp.zero_()
-        B._check(lib.flce_preference_loss(
-            ctypes.byref(p), _addr(logp), _addr(ref_logp), _addr(ref_scores), _addr(g_loss),
-            _addr(loss), _addr(rewards), _addr(dlogp), ws.data_ptr(), ws.numel(),
-            B._stream(stream)))
+    if need_loss:
+        loss = torch.empty(n_out, dtype=torch.float32, device=dev)
+        rewards = torch.empty(n_seq, dtype=torch.float32, device=dev)
+    if need_grad:
+        dlogp = torch.empty(logp.shape, dtype=logp.dtype, device=dev)
+    ws = _workspace(size, dev, workspace)
+    if n_out == 0 or (not need_loss and logp.numel() == 0):
+        # no pair: nothing to compute
+        return loss, rewards, None if dlogp is None else dlogp.zero_()
+    code = lib.flce_preference_loss(
+        ref, logp.data_ptr(), _addr(ref_logp), _addr(ref_scores), _addr(g_loss), _addr(loss),
+        _addr(rewards), _addr(dlogp), ws.data_ptr(), ws.numel(), _raw_stream(dev))
+    if code:
+        B._check(code)
     return loss, rewards, dlogp
 
 
@@ -441,7 +473,7 @@ class _PreferenceLoss(torch.autograd.Function):
     @staticmethod
     def backward(ctx, g_loss, _g_rewards):
         logp, ref_logp, ref_scores, mask, cu = ctx.saved_tensors
-        g = g_loss.detach().reshape(-1).to(torch.float32).contiguous()
+        g = _upstream(g_loss)
         _, _, dlogp = flce_preference_loss(logp, ref_logp, ref_scores, mask, cu, g_loss=g,
                                            need_loss=False, **ctx.kw)
         return dlogp, None, None, None, None, None
