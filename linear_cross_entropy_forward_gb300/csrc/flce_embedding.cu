@@ -4,13 +4,14 @@
 //   dweight[v] (+)= scale * sum over { n : ids[n] = v }, in the order of n, of dout[n]
 //
 // The gradient sorts the tokens by id first: a stable radix sort with digits of at most
-// 9 bits (18-bit ids: two passes), all passes in one cooperative launch of at most 64
-// blocks.  The sorted order is then cut into units of 32 positions.  A warp takes 256
-// (16-bit types) columns of a unit, adds the rows of each run of equal ids in fp32 and
-// stores a run that lies inside the unit at once, rounded once.  A run that crosses a
-// unit's border leaves its part in fp32, and a last launch joins each such run's parts in
-// order.  Frequent ids (padding, the commonest words) are thus spread over many warps;
-// no atomics add anything, so results do not change from run to run.
+// 9 bits (18-bit ids: two passes), all passes in one launch: one block up to 2048 tokens, a
+// cluster of at most eight up to 32768, a cooperative grid of at most 64 beyond.  The
+// sorted order is then cut into units of 32 positions.  A warp takes 256 (16-bit types)
+// columns of a unit, adds the rows of each run of equal ids in fp32 and stores a run that
+// lies inside the unit at once, rounded once.  A run that crosses a unit's border leaves
+// its part in fp32, and a last launch joins each such run's parts in order.  Frequent ids
+// (padding, the commonest words) are thus spread over many warps; no atomics add anything,
+// so results do not change from run to run.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -20,6 +21,7 @@
 #include "../../include/flce.h"
 #include "flce_device.cuh"
 #include "flce_host.h"
+#include "flce_seq.cuh"
 
 namespace flce {
 
@@ -31,7 +33,9 @@ constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kMaxDigit = 9;
 constexpr int kBins = 1 << kMaxDigit;
 constexpr int kSortBlocks = 64;  // every block reads every block's histogram: 64 x 2 KB
-constexpr int64_t kSortChunk = 1024;
+constexpr int64_t kSortSmall = 32768;
+constexpr int kSortBatch = 4;    // a lane's tokens that are loaded together
+constexpr int64_t kSortChunk = int64_t(kSortThreads) * kSortBatch;
 
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -124,8 +128,10 @@ struct SortArgs {
   Ids d;
   int64_t chunk;  // tokens per block, a multiple of kSortThreads
   int passes, digit;
-  uint32_t *key[2], *pos[2];  // the sorted result is in [passes & 1]
-  uint32_t* hist;             // [blocks][kBins]
+  uint32_t *key0, *pos0, *key1, *pos1;  // the sorted result is in [passes & 1]
+  int meet;
+  uint32_t* hist;   // [blocks][kBins]
+  uint32_t* lists;  // the join's two counts, cleared here
   uint32_t* err;
 };
 
@@ -142,104 +148,127 @@ __device__ __forceinline__ uint32_t token_key(const Ids& d, int64_t n, bool* bad
 // order; warps, blocks and digits follow in order by the prefix sums.
 __global__ void __launch_bounds__(kSortThreads) sort_kernel(SortArgs a) {
   __shared__ uint32_t cnt[kSortWarps][kBins];
+  __shared__ uint32_t mine[kBins];  // this block's histogram
   __shared__ uint32_t base[kBins];
   __shared__ uint32_t wsum[kSortWarps];
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t lower_lanes = (1u << lane) - 1;
   const int64_t per_warp = a.chunk / kSortWarps;
   const int64_t n0 = blockIdx.x * a.chunk + w * per_warp;
   const int64_t n1 = n0 + per_warp < a.d.N ? n0 + per_warp : a.d.N;
+  const bool one_batch = per_warp <= 32 * kSortBatch;
   const uint32_t mask = (1u << a.digit) - 1;
-  if (blockIdx.x == 0 && threadIdx.x == 0) *a.err = 0u;
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    *a.err = 0u;
+    a.lists[0] = a.lists[1] = 0u;
+  }
+  bool bad = false;
+#pragma unroll 1
   for (int pass = 0; pass < a.passes; ++pass) {
     const int shift = pass * a.digit;
-    const uint32_t* ikey = a.key[pass & 1];
-    const uint32_t* ipos = a.pos[pass & 1];
-    uint32_t* okey = a.key[(pass + 1) & 1];
-    uint32_t* opos = a.pos[(pass + 1) & 1];
-    for (int i = threadIdx.x; i < kSortWarps * kBins; i += kSortThreads) (&cnt[0][0])[i] = 0;
+    const uint32_t* ikey = pass & 1 ? a.key1 : a.key0;
+    const uint32_t* ipos = pass & 1 ? a.pos1 : a.pos0;
+    uint32_t* okey = pass & 1 ? a.key0 : a.key1;
+    uint32_t* opos = pass & 1 ? a.pos0 : a.pos1;
+    for (int i = threadIdx.x; i < kSortWarps * kBins / 4; i += kSortThreads)
+      reinterpret_cast<uint4*>(&cnt[0][0])[i] = make_uint4(0, 0, 0, 0);
+    uint32_t key[kSortBatch], pos[kSortBatch];
     __syncthreads();
-    for (int64_t b = n0; b < n1; b += 32) {
-      const bool have = b + lane < n1;
-      bool bad = false;
-      uint32_t key = 0;
-      if (have) key = pass ? ikey[b + lane] : token_key(a.d, b + lane, &bad);
-      const uint32_t dig = have ? (key >> shift) & mask : kBins;
-      const uint32_t same = __match_any_sync(~0u, dig);
-      if (have && (same & ((1u << lane) - 1)) == 0) cnt[w][dig] += __popc(same);
-      __syncwarp();
-    }
-    __syncthreads();
-    // threads are digits: the warps' counts become offsets inside the block
-    uint32_t run = 0;
-    for (int k = 0; k < kSortWarps; ++k) {
-      const uint32_t c = cnt[k][threadIdx.x];
-      cnt[k][threadIdx.x] = run;
-      run += c;
-    }
-    uint32_t total = run, before = 0;
-    if (gridDim.x > 1) {
-      a.hist[blockIdx.x * kBins + threadIdx.x] = run;
-      cooperative_groups::this_grid().sync();
-      total = 0;
-#pragma unroll 8
-      for (int b = 0; b < gridDim.x; ++b) {
-        const uint32_t c = a.hist[b * kBins + threadIdx.x];
-        if (b < blockIdx.x) before += c;
-        total += c;
-      }
-    }
-    uint32_t incl = total;
+    // twice over the warp's tokens: their digits' counts, then, with every count known,
+    // their places
+#pragma unroll 1
+    for (int place = 0; place < 2; ++place) {
+#pragma unroll 1
+      for (int64_t b = n0; b < n1; b += 32 * kSortBatch) {
+        if (!(place && one_batch)) {
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t y = __shfl_up_sync(~0u, incl, o);
-      if (lane >= o) incl += y;
-    }
-    if (lane == 31) wsum[w] = incl;
-    __syncthreads();
-    uint32_t lower = 0;
-    for (int k = 0; k < w; ++k) lower += wsum[k];
-    base[threadIdx.x] = lower + incl - total + before;
-    __syncthreads();
-    for (int64_t b = n0; b < n1; b += 32) {
-      const bool have = b + lane < n1;
-      bool bad = false;
-      uint32_t key = 0, pos = static_cast<uint32_t>(b + lane);
-      if (have) {
-        if (pass) {
-          key = ikey[b + lane];
-          pos = ipos[b + lane];
-        } else {
-          key = token_key(a.d, b + lane, &bad);
+          for (int k = 0; k < kSortBatch; ++k) {
+            const int64_t n = b + 32 * k + lane;
+            key[k] = 0;
+            pos[k] = static_cast<uint32_t>(n);
+            if (n < n1) {
+              if (pass == 0) {
+                bool out;
+                key[k] = token_key(a.d, n, &out);
+                bad |= out;
+              } else {
+                key[k] = ikey[n];
+                pos[k] = ipos[n];
+              }
+            }
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < kSortBatch; ++k) {
+          if (b + 32 * k >= n1) break;
+          const bool have = b + 32 * k + lane < n1;
+          const uint32_t dig = have ? (key[k] >> shift) & mask : kBins;
+          const uint32_t same = __match_any_sync(~0u, dig);
+          const uint32_t ahead = __popc(same & lower_lanes);
+          if (place && have) {
+            const uint32_t to = base[dig] + cnt[w][dig] + ahead;
+            okey[to] = key[k];
+            opos[to] = pos[k];
+          }
+          __syncwarp();
+          if (have && ahead == 0) cnt[w][dig] += __popc(same);
+          __syncwarp();
         }
       }
-      const uint32_t dig = have ? (key >> shift) & mask : kBins;
-      const uint32_t same = __match_any_sync(~0u, dig);
-      const uint32_t ahead = __popc(same & ((1u << lane) - 1));
-      uint32_t to = 0;
-      if (have) to = base[dig] + cnt[w][dig] + ahead;
-      __syncwarp();
-      if (have && ahead == 0) cnt[w][dig] += __popc(same);
-      __syncwarp();
-      if (have) {
-        okey[to] = key;
-        opos[to] = pos;
+      if (place) break;
+      __syncthreads();
+      // threads are digits: the warps' counts become offsets inside the block
+      uint32_t run = 0;
+#pragma unroll
+      for (int k = 0; k < kSortWarps; ++k) {
+        const uint32_t c = cnt[k][threadIdx.x];
+        cnt[k][threadIdx.x] = run;
+        run += c;
       }
-      // block 0 cleared the word before the histograms met
-      if (bad) atomicOr(a.err, FLCE_DEVERR_LABEL);
+      uint32_t total = run, before = 0;
+      if (a.meet != MEET_BLOCK) {
+        if (a.meet == MEET_CLUSTER)
+          mine[threadIdx.x] = run;
+        else
+          a.hist[blockIdx.x * kBins + threadIdx.x] = run;
+        meet(a.meet);
+        total = 0;
+#pragma unroll 8
+        for (int b = 0; b < gridDim.x; ++b) {
+          const uint32_t c =
+              a.meet == MEET_CLUSTER
+                  ? cooperative_groups::this_cluster().map_shared_rank(mine, b)[threadIdx.x]
+                  : a.hist[b * kBins + threadIdx.x];
+          if (b < blockIdx.x) before += c;
+          total += c;
+        }
+      }
+      uint32_t incl = total;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(~0u, incl, o);
+        if (lane >= o) incl += y;
+      }
+      if (lane == 31) wsum[w] = incl;
+      __syncthreads();
+      const uint32_t lower = __reduce_add_sync(~0u, lane < w ? wsum[lane] : 0u);  // 16 warps
+      base[threadIdx.x] = lower + incl - total + before;
+      __syncthreads();
     }
-    if (pass + 1 < a.passes) {
-      if (gridDim.x > 1)
-        cooperative_groups::this_grid().sync();
-      else
-        __syncthreads();
-    }
+    // also before the end: a block's shared memory may still be read by its cluster
+    if (pass + 1 < a.passes || a.meet == MEET_CLUSTER) meet(a.meet);
   }
+  // block 0 cleared the word before the histograms met
+  if (bad) atomicOr(a.err, FLCE_DEVERR_LABEL);
 }
 
 // ------------------------------------------------------------------ sums
 constexpr int kSumThreads = 128;
 constexpr int kSumWarps = kSumThreads / 32;
 constexpr int kFillRows = 64;  // table rows per filling block
+constexpr int kRing = 16;      // rows of a warp's slab in flight or in use
+constexpr int kGroup = 4;      // rows per asynchronous copy group
+constexpr int kLong = 8;       // units beyond its head from which a block joins a run
 
 struct SumArgs {
   const uint32_t *key, *pos;  // sorted
@@ -247,18 +276,20 @@ struct SumArgs {
   const void* dout;
   void* dweight;
   float* part;  // [units][2][H]: a unit's run from the left, a run that goes on to the right
+  uint64_t* jobs[2];  // runs to join, (head's unit << 32) + slab: up to kLong units, longer ones
+  uint32_t* lists;    // their numbers
   float scale;
   int accumulate;
   int64_t units, slabs, sum_blocks;
 };
 
 template <typename TO, int VEC>
-__device__ __forceinline__ void store_row(TO* p, const float (&acc)[VEC], float scale,
+__device__ __forceinline__ void store_row(TO* p, const float (&acc)[VEC],
+                                          const Pack<TO, VEC>& old, float scale,
                                           bool accumulate) {
   using P = Pack<TO, VEC>;
   P o;
   if (accumulate) {
-    const P old = *reinterpret_cast<const P*>(p);
 #pragma unroll
     for (int j = 0; j < VEC; ++j) from_f(fmaf(scale, acc[j], to_f(old.v[j])), o.v[j]);
   } else {
@@ -266,6 +297,32 @@ __device__ __forceinline__ void store_row(TO* p, const float (&acc)[VEC], float 
     for (int j = 0; j < VEC; ++j) from_f(scale * acc[j], o.v[j]);
   }
   *reinterpret_cast<P*>(p) = o;
+}
+
+// Copies one lane's vector to shared memory: asynchronously where the hardware does (4, 8
+// and 16 bytes), else at once.
+template <typename P>
+__device__ __forceinline__ void copy_vec(P* to, const P* from) {
+  if constexpr (sizeof(P) < 4) {
+    *to = *from;
+  } else {
+    constexpr int step = sizeof(P) < 16 ? sizeof(P) : 16;
+#pragma unroll
+    for (int o = 0; o < static_cast<int>(sizeof(P)); o += step) {
+      const uint32_t dst = smem_u32(to) + o;
+      const char* src = reinterpret_cast<const char*>(from) + o;
+      if constexpr (step == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+      else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(step)
+                     : "memory");
+    }
+  }
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // The first sorted position whose key is not below k.
@@ -283,8 +340,42 @@ __device__ __forceinline__ int64_t lower_bound(const uint32_t* key, int64_t N, u
   return lo;
 }
 
+// What a unit's warps need to know of its 32 positions.
+struct Unit {
+  uint32_t key, pos;  // this lane's
+  int live;           // positions with a row (they come first: keys rise)
+  uint32_t ends;      // positions that end a run, or the unit
+  uint32_t whole;     // those of runs that lie inside the unit
+  bool from_left, to_right;
+};
+
+__device__ __forceinline__ Unit load_unit(const SumArgs& a, int64_t u) {
+  const int lane = threadIdx.x & 31;
+  const int64_t s0 = u * kUnit;
+  const uint32_t none = static_cast<uint32_t>(a.V);
+  Unit t;
+  t.key = s0 + lane < a.N ? a.key[s0 + lane] : none;
+  t.pos = s0 + lane < a.N ? a.pos[s0 + lane] : 0;
+  const uint32_t left = u > 0 ? a.key[s0 - 1] : none;
+  const uint32_t right = s0 + kUnit < a.N ? a.key[s0 + kUnit] : none;
+  t.live = __popc(__ballot_sync(~0u, t.key != none));
+  const uint32_t next = __shfl_down_sync(~0u, t.key, 1);
+  t.ends = __ballot_sync(~0u, lane < t.live && (lane + 1 == t.live || next != t.key));
+  t.from_left = t.live > 0 && left == __shfl_sync(~0u, t.key, 0);
+  t.to_right = t.live == kUnit && right == __shfl_sync(~0u, t.key, kUnit - 1);
+  t.whole = t.ends;
+  if (t.from_left) t.whole &= t.whole - 1;  // the first run's end
+  if (t.to_right) t.whole &= ~(1u << (kUnit - 1));
+  return t;
+}
+
+// The rows pass through a ring of shared memory that each warp fills for itself, twelve to
+// sixteen rows ahead: the copies in flight need no registers, and the loop over the rows
+// stays short (unrolled over rows in registers it took 44 us where this one takes 30, a
+// launch's instructions being fetched cold by every SM at once).
 template <typename T, typename TO, int VEC>
 __global__ void __launch_bounds__(kSumThreads) sum_kernel(SumArgs a) {
+  extern __shared__ __align__(16) unsigned char ring_bytes[];
   if (blockIdx.x >= a.sum_blocks) {
     // zeros for the rows of this block that no token names
     __shared__ int used[kFillRows];
@@ -311,61 +402,76 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(SumArgs a) {
     }
     return;
   }
+  using PT = Pack<T, VEC>;
+  using PO = Pack<TO, VEC>;
   const int64_t w = blockIdx.x * int64_t(kSumWarps) + (threadIdx.x >> 5);
   const int64_t u = w / a.slabs;
   if (u >= a.units) return;
   const int lane = threadIdx.x & 31;
   const int64_t c = ((w - u * a.slabs) * 32 + lane) * VEC;
-  const int64_t s0 = u * kUnit;
-  const int rows = static_cast<int>(a.N - s0 < kUnit ? a.N - s0 : kUnit);
-  const uint32_t none = static_cast<uint32_t>(a.V);
-  const uint32_t key = lane < rows ? a.key[s0 + lane] : none;
-  const uint32_t pos = lane < rows ? a.pos[s0 + lane] : 0;
-  const uint32_t left = u > 0 ? a.key[s0 - 1] : none;
-  const uint32_t right = s0 + kUnit < a.N ? a.key[s0 + kUnit] : none;
-  // keys rise: those of no row are at the end
-  const int live = __popc(__ballot_sync(~0u, key != none));
   const bool col = c < a.H;
+  const Unit t = load_unit(a, u);
   const T* dout = static_cast<const T*>(a.dout) + c;
+  TO* dweight = static_cast<TO*>(a.dweight) + c;
+  PT* rows = reinterpret_cast<PT*>(ring_bytes) + (threadIdx.x >> 5) * kRing * 32 + lane;
+  PO* olds = reinterpret_cast<PO*>(ring_bytes + sizeof(PT) * kSumThreads * kRing) +
+             (threadIdx.x >> 5) * kRing * 32 + lane;
+  auto fetch = [&](int g) {
+    for (int j = g * kGroup; j < (g + 1) * kGroup; ++j) {
+      const uint32_t n = __shfl_sync(~0u, t.pos, j & 31);
+      const uint32_t id = __shfl_sync(~0u, t.key, j & 31);
+      if (j < t.live && col) {
+        const int slot = (j & (kRing - 1)) * 32;
+        copy_vec(rows + slot, reinterpret_cast<const PT*>(dout + int64_t(n) * a.H));
+        if (a.accumulate && (t.whole >> j & 1))
+          copy_vec(olds + slot, reinterpret_cast<const PO*>(dweight + int64_t(id) * a.H));
+      }
+    }
+    copy_commit();
+  };
+#pragma unroll 1
+  for (int g = 0; g < kRing / kGroup; ++g) fetch(g);
   float acc[VEC];
 #pragma unroll
   for (int j = 0; j < VEC; ++j) acc[j] = 0.0f;
-  bool first = true;  // the unit's first run
-  for (int b = 0; b < live; b += 8) {
-    Pack<T, VEC> x[8];
+  int side = t.from_left ? 0 : 1;  // of a part, until the first run has ended
+#pragma unroll 1
+  for (int g = 0; g * kGroup < t.live; ++g) {
+    copy_wait<kRing / kGroup - 1>();  // lanes read back what they copied themselves
+#pragma unroll 1
+    for (int j = g * kGroup; j < (g + 1) * kGroup && j < t.live; ++j) {
+      const int slot = (j & (kRing - 1)) * 32;
+      const PT x = rows[slot];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const uint32_t n = __shfl_sync(~0u, pos, (b + k) & 31);
-      if (b + k < live && col)
-        x[k] = *reinterpret_cast<const Pack<T, VEC>*>(dout + int64_t(n) * a.H);
-    }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const uint32_t id = __shfl_sync(~0u, key, (b + k) & 31);
-      const uint32_t next = __shfl_sync(~0u, key, (b + k + 1) & 31);
-      if (b + k >= live) continue;
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) acc[j] += to_f(x[k].v[j]);
-      const bool end = b + k + 1 == live;
-      if (!end && next == id) continue;
-      // the run ends here, or the unit does
-      const bool from_left = first && left == id;
-      const bool to_right = b + k + 1 == kUnit && right == id;
+      for (int i = 0; i < VEC; ++i) acc[i] += to_f(x.v[i]);
+      if (!(t.ends >> j & 1)) continue;
+      const uint32_t id = __shfl_sync(~0u, t.key, j);
       if (col) {
-        if (from_left || to_right) {
+        if (t.whole >> j & 1) {
+          store_row<TO, VEC>(dweight + int64_t(id) * a.H, acc, olds[slot], a.scale, a.accumulate);
+        } else {
           Pack<float, VEC> o;
 #pragma unroll
-          for (int j = 0; j < VEC; ++j) o.v[j] = acc[j];
-          *reinterpret_cast<Pack<float, VEC>*>(a.part + (2 * u + (from_left ? 0 : 1)) * a.H + c) =
-              o;
-        } else {
-          store_row<TO, VEC>(static_cast<TO*>(a.dweight) + int64_t(id) * a.H + c, acc, a.scale,
-                             a.accumulate);
+          for (int i = 0; i < VEC; ++i) o.v[i] = acc[i];
+          *reinterpret_cast<Pack<float, VEC>*>(a.part + (2 * u + side) * a.H + c) = o;
         }
       }
+      side = 1;
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) acc[j] = 0.0f;
-      first = false;
+      for (int i = 0; i < VEC; ++i) acc[i] = 0.0f;
+    }
+    fetch(g + kRing / kGroup);
+  }
+  // the head of a run that goes on: a job for the join
+  if (t.to_right && !(t.from_left && t.ends == 1u << (kUnit - 1))) {
+    const uint32_t id = __shfl_sync(~0u, t.key, kUnit - 1);
+    const int64_t s = (u + 1 + lane) * kUnit;
+    const bool more = lane <= kLong && s < a.N && a.key[s < a.N ? s : 0] == id;
+    const int n = __popc(__ballot_sync(~0u, more));
+    if (lane == 0) {
+      const int list = n > kLong;
+      a.jobs[list][atomicAdd(a.lists + list, 1u)] =
+          (static_cast<uint64_t>(u) << 32) + static_cast<uint64_t>(w - u * a.slabs);
     }
   }
 }
@@ -374,41 +480,78 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(SumArgs a) {
 constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
 
-// A block per unit; those whose last run starts there and goes on to the right add the
-// run's parts: each warp a consecutive share of the units, the shares in order.
-template <typename TO>
+// Adds up the parts of the runs that cross units.  Their number is known on the GPU alone:
+// the grid is fixed and strides over the two lists, a warp per short run's slab, a block
+// per long one's (each warp takes consecutive units, and their sums follow in order).  The
+// lists' order changes from run to run; nothing depends on it.
+template <typename TO, int VEC>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(SumArgs a) {
-  __shared__ float share[kJoinWarps][32];
-  __shared__ int64_t s_end;
-  const int64_t u = blockIdx.x;
-  const int64_t s1 = (u + 1) * kUnit;
-  if (s1 >= a.N) return;
-  const uint32_t id = a.key[s1 - 1];
-  if (id == static_cast<uint32_t>(a.V) || a.key[s1] != id) return;
-  // a run that came from the left is joined where it started
-  if (a.key[s1 - kUnit] == id && u > 0 && a.key[s1 - kUnit - 1] == id) return;
-  if (threadIdx.x == 0) s_end = lower_bound(a.key + s1, a.N - s1, id + 1) + s1;
-  __syncthreads();
-  const int64_t n = (s_end - 1) / kUnit - u;  // units after this one
+  using PF = Pack<float, VEC>;
+  using PO = Pack<TO, VEC>;
+  __shared__ PF share[kJoinWarps][32];
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t per = (n + kJoinWarps - 1) / kJoinWarps;
-  const int64_t k0 = w * per, k1 = k0 + per < n ? k0 + per : n;
-  for (int64_t c = lane + blockIdx.y * 32; c - lane < a.H; c += 32 * gridDim.y) {
-    float acc = 0.0f;
-    if (c < a.H) {
-      if (w == 0) acc = a.part[(2 * u + 1) * a.H + c];
-#pragma unroll 8
-      for (int64_t k = k0; k < k1; ++k) acc += a.part[2 * (u + 1 + k) * a.H + c];
+#pragma unroll 1
+  for (int list = 0; list < 2; ++list) {
+    const uint32_t jobs = a.lists[list];
+    const uint32_t stride = list ? gridDim.x : gridDim.x * kJoinWarps;
+#pragma unroll 1
+    for (uint32_t k = list ? blockIdx.x : blockIdx.x * kJoinWarps + w; k < jobs; k += stride) {
+      const uint64_t job = a.jobs[list][k];
+      const int64_t u = static_cast<int64_t>(job >> 32);
+      const int64_t c = (static_cast<int64_t>(job & 0xffffffffu) * 32 + lane) * VEC;
+      const uint32_t id = a.key[(u + 1) * kUnit];
+      // the units after the head's that the run reaches
+      int64_t n = 0;
+      if (list) {
+        while (true) {
+          const int64_t s = (u + 1 + n + threadIdx.x) * kUnit;
+          const int more = __syncthreads_count(s < a.N && a.key[s < a.N ? s : 0] == id);
+          n += more;
+          if (more < kJoinThreads) break;
+        }
+      } else {
+        const int64_t s = (u + 1 + lane) * kUnit;
+        n = __popc(__ballot_sync(~0u, lane <= kLong && s < a.N && a.key[s < a.N ? s : 0] == id));
+      }
+      const int64_t per = list ? (n + kJoinWarps - 1) / kJoinWarps : n;
+      const int64_t k0 = list ? w * per : 0, k1 = k0 + per < n ? k0 + per : n;
+      const bool head = !list || w == 0;
+      float acc[VEC];
+      PO old{};
+      TO* row = static_cast<TO*>(a.dweight) + int64_t(id) * a.H + c;
+      const float* part = a.part + 2 * u * a.H + c;
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) acc[j] = 0.0f;
+      if (c < a.H) {
+        if (head && a.accumulate) old = *reinterpret_cast<const PO*>(row);
+        if (head) {
+          const PF x = *reinterpret_cast<const PF*>(part + a.H);
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) acc[j] = x.v[j];
+        }
+#pragma unroll 4
+        for (int64_t i = k0; i < k1; ++i) {
+          const PF x = *reinterpret_cast<const PF*>(part + 2 * (i + 1) * a.H);
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) acc[j] += x.v[j];
+        }
+      }
+      if (list) {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) share[w][lane].v[j] = acc[j];
+        __syncthreads();
+        if (w == 0) {
+#pragma unroll 1
+          for (int i = 1; i < kJoinWarps; ++i) {
+            const PF x = share[i][lane];
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) acc[j] += x.v[j];
+          }
+        }
+        __syncthreads();
+      }
+      if (head && c < a.H) store_row<TO, VEC>(row, acc, old, a.scale, a.accumulate);
     }
-    share[w][lane] = acc;
-    __syncthreads();
-    if (w == 0 && c < a.H) {
-      for (int k = 1; k < kJoinWarps; ++k) acc += share[k][lane];
-      const float one[1] = {acc};
-      store_row<TO, 1>(static_cast<TO*>(a.dweight) + int64_t(id) * a.H + c, one, a.scale,
-                       a.accumulate);
-    }
-    __syncthreads();
   }
 }
 
@@ -433,16 +576,18 @@ int check(const flce_embedding_params* p) {
 }
 
 struct Layout {
-  size_t key[2], pos[2], hist, part, total;
+  size_t key[2], pos[2], hist, jobs[2], part, total;
   int64_t chunk, blocks, units;
-  int passes, digit;
+  int passes, digit, meet;
 };
 
 Layout layout(const flce_embedding_params* p) {
   Layout L{};
-  const int64_t per = cdiv(p->N, kSortBlocks);
+  const int64_t per = cdiv(p->N, p->N <= kSortSmall ? kClusterBlocks : kSortBlocks);
   L.chunk = cdiv(per > kSortChunk ? per : kSortChunk, kSortThreads) * kSortThreads;
   L.blocks = p->N > 0 ? cdiv(p->N, L.chunk) : 1;
+  L.meet = L.blocks == 1 ? MEET_BLOCK : p->N <= kSortSmall ? MEET_CLUSTER : MEET_GRID;
+  if (L.meet == MEET_CLUSTER) L.blocks = L.blocks <= 2 ? 2 : L.blocks <= 4 ? 4 : 8;
   L.units = cdiv(p->N, kUnit);
   int bits = 1;
   while ((p->V >> bits) != 0) ++bits;  // keys are 0 .. V
@@ -454,6 +599,10 @@ Layout layout(const flce_embedding_params* p) {
     L.pos[k] = off; off += align256(p->N * 4);
   }
   L.hist = off; off += align256(L.blocks * kBins * 4);
+  // a unit has one run at most that goes on; the most slabs are those of 32 columns
+  for (int k = 0; k < 2; ++k) {
+    L.jobs[k] = off; off += align256(static_cast<size_t>(L.units) * cdiv(p->H, 32) * 8);
+  }
   L.part = off; off += align256(static_cast<size_t>(L.units) * 2 * p->H * 4);
   L.total = off;
   return L;
@@ -495,28 +644,36 @@ int launch_lookup_vec(const EmbedArgs& a, int vec, cudaStream_t st) {
 }
 
 template <typename T, typename TO, int VEC>
-int launch_sum(SumArgs a, cudaStream_t st) {
+int launch_sum(SumArgs a, int sms, cudaStream_t st) {
   a.slabs = cdiv(a.H, 32 * VEC);
   a.sum_blocks = cdiv(a.units * a.slabs, kSumWarps);
   const int64_t blocks = a.sum_blocks + (a.accumulate ? 0 : cdiv(a.V, kFillRows));
   if (blocks > (int64_t(1) << 31) - 1) return FLCE_ERR_BAD_SHAPE;
   if (blocks == 0) return FLCE_OK;  // no token, nothing to add
-  sum_kernel<T, TO, VEC><<<static_cast<unsigned>(blocks), kSumThreads, 0, st>>>(a);
+  // the rows' ring, and the old rows' where there are any
+  const int ring = kSumThreads * kRing *
+                   static_cast<int>(sizeof(Pack<T, VEC>) +
+                                    (a.accumulate ? sizeof(Pack<TO, VEC>) : 0));
+  if (ring > 47 * 1024) {  // beside the static 272 bytes
+    const int rc = rc_of(cudaFuncSetAttribute(
+        sum_kernel<T, TO, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, ring));
+    if (rc) return rc;
+  }
+  sum_kernel<T, TO, VEC><<<static_cast<unsigned>(blocks), kSumThreads, ring, st>>>(a);
   int rc = rc_of(cudaGetLastError());
   if (rc || a.units < 2) return rc;
-  const int64_t y = cdiv(a.H, 32);
-  join_kernel<TO><<<dim3(static_cast<unsigned>(a.units), static_cast<unsigned>(y < 16 ? y : 16)),
-                    kJoinThreads, 0, st>>>(a);
+  const int64_t most = a.units * a.slabs, join = cdiv(most, kJoinWarps), cap = 2 * sms;
+  join_kernel<TO, VEC><<<static_cast<unsigned>(join < cap ? join : cap), kJoinThreads, 0, st>>>(a);
   return rc_of(cudaGetLastError());
 }
 
 template <typename T, typename TO>
-int launch_sum_vec(const SumArgs& a, int vec, cudaStream_t st) {
+int launch_sum_vec(const SumArgs& a, int vec, int sms, cudaStream_t st) {
   if constexpr (sizeof(T) == 2)
-    if (vec == 8) return launch_sum<T, TO, 8>(a, st);
-  if (vec == 4) return launch_sum<T, TO, 4>(a, st);
-  if (vec == 2) return launch_sum<T, TO, 2>(a, st);
-  return launch_sum<T, TO, 1>(a, st);
+    if (vec == 8) return launch_sum<T, TO, 8>(a, sms, st);
+  if (vec == 4) return launch_sum<T, TO, 4>(a, sms, st);
+  if (vec == 2) return launch_sum<T, TO, 2>(a, sms, st);
+  return launch_sum<T, TO, 1>(a, sms, st);
 }
 
 }  // namespace
@@ -586,21 +743,22 @@ int flce_embedding_backward(const flce_embedding_params* p, const void* dout, co
   s.chunk = L.chunk;
   s.passes = L.passes;
   s.digit = L.digit;
-  for (int k = 0; k < 2; ++k) {
-    s.key[k] = reinterpret_cast<uint32_t*>(ws + L.key[k]);
-    s.pos[k] = reinterpret_cast<uint32_t*>(ws + L.pos[k]);
-  }
+  s.meet = L.meet;
+  s.key0 = reinterpret_cast<uint32_t*>(ws + L.key[0]);
+  s.pos0 = reinterpret_cast<uint32_t*>(ws + L.pos[0]);
+  s.key1 = reinterpret_cast<uint32_t*>(ws + L.key[1]);
+  s.pos1 = reinterpret_cast<uint32_t*>(ws + L.pos[1]);
+  s.lists = reinterpret_cast<uint32_t*>(ws + 64);
   s.hist = reinterpret_cast<uint32_t*>(ws + L.hist);
   s.err = reinterpret_cast<uint32_t*>(ws);
-  void* params[] = {&s};
-  const void* sort = reinterpret_cast<const void*>(sort_kernel);
-  const dim3 grid(static_cast<unsigned>(L.blocks)), block(kSortThreads);
-  rc = rc_of(L.blocks == 1 ? cudaLaunchKernel(sort, grid, block, params, 0, st)
-                           : cudaLaunchCooperativeKernel(sort, grid, block, params, 0, st));
-  if (rc) return rc;
+  if ((rc = rc_of(launch_meeting(reinterpret_cast<const void*>(sort_kernel), &s, L.blocks,
+                                 kSortThreads, L.meet, st))))
+    return rc;
   SumArgs a{};
-  a.key = s.key[L.passes & 1];
-  a.pos = s.pos[L.passes & 1];
+  a.key = L.passes & 1 ? s.key1 : s.key0;
+  a.pos = L.passes & 1 ? s.pos1 : s.pos0;
+  a.lists = s.lists;
+  for (int k = 0; k < 2; ++k) a.jobs[k] = reinterpret_cast<uint64_t*>(ws + L.jobs[k]);
   a.N = p->N;
   a.H = p->H;
   a.V = p->V;
@@ -615,13 +773,13 @@ int flce_embedding_backward(const flce_embedding_params* p, const void* dout, co
   int vec = vec_for(b, p->H, addr(dout));
   while (vec > 1 && addr(dweight) % (vec * gb < align_to ? vec * gb : align_to) != 0) vec /= 2;
   if (p->dtype == FLCE_F32)
-    rc = launch_sum_vec<float, float>(a, vec, st);
+    rc = launch_sum_vec<float, float>(a, vec, sms, st);
   else if (p->dtype == FLCE_BF16)
-    rc = gb == 4 ? launch_sum_vec<__nv_bfloat16, float>(a, vec, st)
-                 : launch_sum_vec<__nv_bfloat16, __nv_bfloat16>(a, vec, st);
+    rc = gb == 4 ? launch_sum_vec<__nv_bfloat16, float>(a, vec, sms, st)
+                 : launch_sum_vec<__nv_bfloat16, __nv_bfloat16>(a, vec, sms, st);
   else
-    rc = gb == 4 ? launch_sum_vec<__half, float>(a, vec, st)
-                 : launch_sum_vec<__half, __half>(a, vec, st);
+    rc = gb == 4 ? launch_sum_vec<__half, float>(a, vec, sms, st)
+                 : launch_sum_vec<__half, __half>(a, vec, sms, st);
   if (rc) return rc;
   return p->validate ? read_status(workspace, st) : FLCE_OK;
 }

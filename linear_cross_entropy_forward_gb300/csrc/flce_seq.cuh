@@ -352,24 +352,17 @@ inline int make_seqs(const flce_seqs* a, Seqs* q) {
 
 inline int seq_elem_bytes(int dtype) { return dtype == FLCE_F32 ? 4 : 2; }
 
-// A warp per piece: one block where its warps suffice, else a cluster of at most eight
-// (whose hardware barrier takes a fraction of a grid's), else a cooperative grid of at most
-// the blocks that the GPU holds at once, whose warps take several pieces each.
-template <typename Args>
-inline cudaError_t launch_seq(void (*kernel)(Args), const Args& args, int sms, cudaStream_t st) {
-  Args a = args;
-  void* params[] = {&a};
-  int64_t blocks = (int64_t(a.q.pieces) + kSeqWarps - 1) / kSeqWarps;
-  if (blocks < 1) blocks = 1;
-  const int64_t cap = sms;
-  a.q.meet = blocks == 1 ? MEET_BLOCK : blocks <= kClusterBlocks ? MEET_CLUSTER : MEET_GRID;
-  if (a.q.meet == MEET_CLUSTER) blocks = blocks <= 2 ? 2 : blocks <= 4 ? 4 : 8;
+// A grid whose blocks meet: plain for one block, one cluster (of 2, 4 or 8 blocks), or
+// cooperative.
+inline cudaError_t launch_meeting(const void* kernel, void* args, int64_t blocks, int threads,
+                                  int meet, cudaStream_t st) {
+  void* params[] = {args};
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks < cap ? blocks : cap));
-  cfg.blockDim = dim3(kSeqThreads);
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.stream = st;
   cudaLaunchAttribute attr{};
-  if (a.q.meet == MEET_CLUSTER) {
+  if (meet == MEET_CLUSTER) {
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = cfg.gridDim.x;
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
@@ -378,8 +371,22 @@ inline cudaError_t launch_seq(void (*kernel)(Args), const Args& args, int sms, c
     attr.val.cooperative = 1;
   }
   cfg.attrs = &attr;
-  cfg.numAttrs = a.q.meet == MEET_BLOCK ? 0 : 1;
-  return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(kernel), params);
+  cfg.numAttrs = meet == MEET_BLOCK ? 0 : 1;
+  return cudaLaunchKernelExC(&cfg, kernel, params);
+}
+
+// A warp per piece: one block where its warps suffice, else a cluster of at most eight
+// (whose hardware barrier takes a fraction of a grid's), else a cooperative grid of at most
+// one block per SM, whose warps take several pieces each.
+template <typename Args>
+inline cudaError_t launch_seq(void (*kernel)(Args), const Args& args, int sms, cudaStream_t st) {
+  Args a = args;
+  int64_t blocks = (int64_t(a.q.pieces) + kSeqWarps - 1) / kSeqWarps;
+  if (blocks < 1) blocks = 1;
+  a.q.meet = blocks == 1 ? MEET_BLOCK : blocks <= kClusterBlocks ? MEET_CLUSTER : MEET_GRID;
+  if (a.q.meet == MEET_CLUSTER) blocks = blocks <= 2 ? 2 : blocks <= 4 ? 4 : 8;
+  return launch_meeting(reinterpret_cast<const void*>(kernel), &a, blocks < sms ? blocks : sms,
+                        kSeqThreads, a.q.meet, st);
 }
 
 }  // namespace flce
