@@ -457,21 +457,28 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(SumArgs a) {
   const int64_t c = ((w - u * a.slabs) * 32 + lane) * VEC;
   const bool col = c < a.H;
   const Unit t = load_unit(a, u);
-  const T* dout = static_cast<const T*>(a.dout) + c;
-  TO* dweight = static_cast<TO*>(a.dweight) + c;
+  const char* dout = reinterpret_cast<const char*>(static_cast<const T*>(a.dout) + c);
+  char* dweight = reinterpret_cast<char*>(static_cast<TO*>(a.dweight) + c);
+  const uint32_t row_bytes = static_cast<uint32_t>(a.H * sizeof(T));
+  const uint32_t out_bytes = static_cast<uint32_t>(a.H * sizeof(TO));
   PT* rows = reinterpret_cast<PT*>(ring_bytes) + (threadIdx.x >> 5) * kRing * 32 + lane;
   PO* olds = reinterpret_cast<PO*>(ring_bytes + sizeof(PT) * kSumThreads * kRing) +
              (threadIdx.x >> 5) * kRing * 32 + lane;
+  // positions whose rows this lane copies; and whose old rows
+  const uint32_t want = !col ? 0u : t.live == kUnit ? ~0u : (1u << t.live) - 1;
+  const uint32_t want_old = a.accumulate ? want & t.whole : 0u;
   auto fetch = [&](int g) {
-    for (int j = g * kGroup; j < (g + 1) * kGroup; ++j) {
-      const uint32_t n = __shfl_sync(~0u, t.pos, j & 31);
-      const uint32_t id = __shfl_sync(~0u, t.key, j & 31);
-      if (j < t.live && col) {
-        const int slot = (j & (kRing - 1)) * 32;
-        copy_vec(rows + slot, reinterpret_cast<const PT*>(dout + int64_t(n) * a.H));
-        if (a.accumulate && (t.whole >> j & 1))
-          copy_vec(olds + slot, reinterpret_cast<const PO*>(dweight + int64_t(id) * a.H));
-      }
+#pragma unroll
+    for (int k = 0; k < kGroup; ++k) {
+      const int j = g * kGroup + k;  // past the unit's end: nothing wanted
+      if (j >= kUnit) break;
+      const uint32_t n = __shfl_sync(~0u, t.pos, j);
+      const uint32_t id = __shfl_sync(~0u, t.key, j);
+      const int slot = (j & (kRing - 1)) * 32;
+      if (want >> j & 1)
+        copy_vec(rows + slot, reinterpret_cast<const PT*>(dout + uint64_t(n) * row_bytes));
+      if (want_old >> j & 1)
+        copy_vec(olds + slot, reinterpret_cast<const PO*>(dweight + uint64_t(id) * out_bytes));
     }
     copy_commit();
   };
@@ -481,20 +488,24 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(SumArgs a) {
 #pragma unroll
   for (int j = 0; j < VEC; ++j) acc[j] = 0.0f;
   int side = t.from_left ? 0 : 1;  // of a part, until the first run has ended
+  uint32_t ends = t.ends;
 #pragma unroll 1
-  for (int g = 0; g * kGroup < t.live; ++g) {
+  for (int g = 0; g * kGroup < t.live; ++g, ends >>= kGroup) {
     copy_wait<kRing / kGroup - 1>();  // lanes read back what they copied themselves
+    const PT* in = rows + (g * kGroup & (kRing - 1)) * 32;
+    const int count = t.live - g * kGroup < kGroup ? t.live - g * kGroup : kGroup;
 #pragma unroll 1
-    for (int j = g * kGroup; j < (g + 1) * kGroup && j < t.live; ++j) {
-      const int slot = (j & (kRing - 1)) * 32;
-      const PT x = rows[slot];
+    for (int k = 0; k < count; ++k) {
+      const PT x = in[k * 32];
 #pragma unroll
       for (int i = 0; i < VEC; ++i) acc[i] += to_f(x.v[i]);
-      if (!(t.ends >> j & 1)) continue;
+      if (!(ends >> k & 1)) continue;
+      const int j = g * kGroup + k;
       const uint32_t id = __shfl_sync(~0u, t.key, j);
       if (col) {
         if (t.whole >> j & 1) {
-          store_row<TO, VEC>(dweight + int64_t(id) * a.H, acc, olds[slot], a.scale, a.accumulate);
+          store_row<TO, VEC>(reinterpret_cast<TO*>(dweight + uint64_t(id) * out_bytes), acc,
+                             olds[(j & (kRing - 1)) * 32], a.scale, a.accumulate);
         } else {
           Pack<float, VEC> o;
 #pragma unroll
@@ -513,15 +524,16 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(SumArgs a) {
     const uint32_t id = __shfl_sync(~0u, t.key, kUnit - 1);
     const uint32_t n = units_after(a, u, id);
     if (lane == 0) {
-      const int list = n > kLong;
-      a.jobs[list][atomicAdd(a.lists + list, 1u)] =
+      const bool is_long = n > kLong;
+      uint4* jobs = is_long ? a.jobs[1] : a.jobs[0];
+      jobs[atomicAdd(a.lists + is_long, 1u)] =
           make_uint4(static_cast<uint32_t>(u), static_cast<uint32_t>(w - u * a.slabs), id, n);
     }
   }
 }
 
 // ------------------------------------------------------------------ joins
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 1024;
 constexpr int kJoinWarps = kJoinThreads / 32;
 
 // Adds up the parts of the runs that cross units.  Their number is known on the GPU alone:
@@ -712,7 +724,7 @@ int launch_sum(SumArgs a, int sms, cudaStream_t st) {
   }
   int rc = launch_next(sum_kernel<T, TO, VEC>, a, blocks, kSumThreads, ring, st);
   if (rc || a.units < 2) return rc;
-  const int64_t join = cdiv(a.units * a.slabs, kJoinWarps), cap = 2 * sms;
+  const int64_t join = cdiv(a.units * a.slabs, kJoinWarps), cap = sms;
   return launch_next(join_kernel<TO, VEC>, a, join < cap ? join : cap, kJoinThreads, 0, st);
 }
 
