@@ -56,12 +56,14 @@ struct Ratio {
 // The clipped ratio of the log-ratio h + l, r = exp(h clamped).
 __device__ __forceinline__ Ratio clip_ratio(const PolicyArgs& a, float h, float l, float r,
                                             float adv) {
-  const bool up = adv > 0.0f && pair_above(h, l, a.hi_h, a.hi_l);
-  const bool down = adv < 0.0f && pair_above(-h, -l, -a.lo_h, -a.lo_l);
+  // above the upper border where A > 0, below the lower where A < 0
+  const bool up = adv > 0.0f, down = adv < 0.0f;
   Ratio o;
-  o.dual = adv < 0.0f && a.r_dual != 0.0f && pair_above(h, l, a.dual_h, a.dual_l);
-  o.clipped = up || down;
-  o.value = up ? a.r_hi : down ? a.r_lo : o.dual ? a.r_dual : r;
+  o.clipped = (up || down) && pair_above(up ? h : -h, up ? l : -l, up ? a.hi_h : -a.lo_h,
+                                         up ? a.hi_l : -a.lo_l);
+  o.dual = false;
+  if (a.r_dual != 0.0f) o.dual = down && pair_above(h, l, a.dual_h, a.dual_l);
+  o.value = o.clipped ? (up ? a.r_hi : a.r_lo) : o.dual ? a.r_dual : r;
   o.live = !(o.clipped || o.dual || fabsf(h) > kLogRatioLimit);
   return o;
 }
@@ -94,7 +96,7 @@ __global__ void __launch_bounds__(kSeqThreads, 1) policy_kernel(PolicyArgs a) {
   // gradients before their weight, and which tokens count, of this warp's first piece
   __shared__ float kept[kPerLane][kSeqThreads];
   unsigned int kept_on = 0;
-  const bool keep = a.what == (POLICY_LOSS | POLICY_GRAD) && !by_seq;
+  const bool keep = a.what == (POLICY_LOSS | POLICY_GRAD);
   if (warp == 0 && lane == 0) {
     *a.done = 0;
     if (a.err_store) *a.err = 0;
@@ -106,7 +108,8 @@ __global__ void __launch_bounds__(kSeqThreads, 1) policy_kernel(PolicyArgs a) {
     const bool grad = pass == 1;
     if (grad && !(a.what & POLICY_GRAD)) break;
     // the first pass of a launch without the loss counts tokens, no more
-    const bool values = grad || want_loss || by_seq;
+    // (and a second pass of a sequence's ratio without a reference knows the gradient)
+    const bool values = grad ? !by_seq || a.ref : want_loss || by_seq;
 #pragma unroll 1
     for (int u = warp; u < q.pieces; u += warps) {
       const Piece pc = find_piece(q, u);
@@ -136,7 +139,8 @@ __global__ void __launch_bounds__(kSeqThreads, 1) policy_kernel(PolicyArgs a) {
           const int t = lane + 32 * k;
           if (t < t0 || t >= t1) continue;
           const bool on = kept_on >> k & 1;
-          if (a.dlp) store_f(dlp_ + t, kept[k][threadIdx.x] * (wg * a.lp_sign));
+          if (a.dlp)
+            store_f(dlp_ + t, on ? __fadd_rn(kept[k][threadIdx.x], coef) * (wg * a.lp_sign) : 0.0f);
           if (a.dent) store_f(dent_ + t, on ? -a.ent_coef * wg : 0.0f);
         }
         continue;
@@ -166,7 +170,7 @@ __global__ void __launch_bounds__(kSeqThreads, 1) policy_kernel(PolicyArgs a) {
         for (int j = 0; j < kBatch; ++j) {
           const int t = k0 + j * 32 + lane;
           const float x = a.lp_sign * lp[j];
-          float h = 0.0f, l = 0.0f, dl = coef;
+          float h = 0.0f, l = 0.0f, dl = 0.0f;
           if (a.old_lp) exact_diff(x, old[j], h, l);
           const float hc = clamp_ratio(h), e = expf(hc);
           if (by_seq) {
@@ -191,6 +195,7 @@ __global__ void __launch_bounds__(kSeqThreads, 1) policy_kernel(PolicyArgs a) {
             kept[k0 / 32 + j][threadIdx.x] = on[j] ? dl : 0.0f;
             kept_on |= static_cast<unsigned int>(on[j]) << (k0 / 32 + j);
           }
+          dl = __fadd_rn(dl, coef);  // a sequence's; as where it meets the kept part
           if (grad) {
             if (t >= t0 && t < t1) {
               if (a.dlp) store_f(dlp_ + t, on[j] ? dl * (wg * a.lp_sign) : 0.0f);
