@@ -413,7 +413,7 @@ int flce_preference_loss(const flce_preference_params* params, const void* logp,
 
 /* Embedding lookup out[n] = scale * weight[ids[n]] and its gradient. */
 typedef struct {
-  int64_t N, H, V;     /* ids, row length, rows of weight (any H >= 1) */
+  int64_t N, H, V;     /* ids, row length, rows of weight (1 <= H <= 2^28) */
   int64_t v_offset;    /* weight holds rows [v_offset, v_offset + V) of a table of v_total */
   int64_t v_total;     /* 0: the whole table */
   int64_t padding_idx; /* an id without a gradient, -1: none */

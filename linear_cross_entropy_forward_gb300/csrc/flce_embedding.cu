@@ -620,6 +620,7 @@ int check(const flce_embedding_params* p) {
   const int64_t lim = (int64_t(1) << 31) - 2;
   if (p->N < 0 || p->H < 1 || p->V < 1 || p->N > lim || p->H > lim || p->V > lim)
     return FLCE_ERR_BAD_SHAPE;
+  if (p->H > (int64_t(1) << 28)) return FLCE_ERR_BAD_SHAPE;  // a row's bytes are 32-bit
   if (p->N > 0 && p->H > (int64_t(1) << 46) / p->N) return FLCE_ERR_BAD_SHAPE;
   if (p->dtype < FLCE_F32 || p->dtype > FLCE_F16) return FLCE_ERR_BAD_ARG;
   if (p->grad_dtype != p->dtype && p->grad_dtype != FLCE_F32) return FLCE_ERR_BAD_ARG;

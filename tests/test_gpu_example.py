@@ -1,0 +1,78 @@
+"""The example's steps: they learn, and a policy step's gradient of the tied table is the
+definition's."""
+import importlib.util
+import math
+import os
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+PATH = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                    "tied_policy_step.py")
+
+
+@pytest.fixture(scope="module")
+def ex():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from linear_cross_entropy_forward_gb300.build import build
+    build()
+    spec = importlib.util.spec_from_file_location("tied_policy_step", PATH)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    return mod
+
+
+def test_losses_fall(ex):
+    policy, preference = ex.main(steps=12, quiet=True)
+    assert all(math.isfinite(x) for x in policy + preference)
+    assert policy[-1] < policy[0] and preference[-1] < preference[0]
+    # before the first update the policy is the reference: -ln sig(0)
+    assert abs(preference[0] - math.log(2)) < 1e-4
+
+
+def test_tied_gradient_is_the_definitions(ex):
+    """Both uses of the table in one fp64 graph.  The head's gradients are within its bound
+    (1e-2 relative: dlogits rounded to bf16), and so is their sum."""
+    g = torch.Generator().manual_seed(3)
+    table = (torch.randn(ex.V, ex.H, generator=g) / 8).to(torch.bfloat16).cuda()
+    ids = torch.randint(0, ex.V, (ex.B, ex.S), generator=g).cuda()
+    labels = ex.next_labels(ids, 16).view(-1)
+    adv = torch.randn(ex.B, generator=g).cuda()
+    old = ex.log_probs(table, ids, 16) + 0.1 * torch.randn(ex.B * ex.S, generator=g).cuda()
+    before = table.clone()
+    new = table.clone()
+    loss, _, _ = ex.policy_step(new, ids, 16, adv, old, old, lr=1.0)
+    # the step itself: bf16(table - grad); here from the calls' own gradient
+    hidden = ex.hidden_states(before, ids)
+    out = ex.flce.flce_policy_forward_backward(
+        hidden, before, labels, old, adv, ref_logp=old, cu_seqlens=ex.sequence_ends("cuda"),
+        clip_low=0.2, clip_high=0.28, kl_coef=0.01, entropy_coef=0.001,
+        aggregate="seq_mean_token_mean", weight_layout="vh")
+    grad = ex.add_lookup_gradient(out[6], out[5], ids)
+    assert torch.equal(new, before.sub(grad, alpha=1.0)) and torch.equal(out[0], loss)
+
+    w = before.double().requires_grad_(True)
+    x = w[ids] * math.sqrt(ex.H)
+    h = x + torch.nn.functional.pad(x[:, :-1], (0, 0, 1, 0))
+    # the head reads the hidden states that the lookup and the addition rounded to bf16
+    h = h + (hidden.double().view_as(h) - h).detach()
+    logq = torch.log_softmax(h.reshape(-1, ex.H) @ w.t(), 1)
+    m = labels != -100
+    lp = logq.gather(1, labels.clamp(min=0)[:, None])[:, 0][m]
+    ent = -(logq.exp() * logq).sum(1)[m]
+    o = old.double()[m]
+    a = adv.double().repeat_interleave(ex.S)[m]
+    r = (lp - o).exp()
+    obj = torch.minimum(r * a, r.clamp(0.8, 1.28) * a)
+    e = o - lp
+    per = -obj + 0.01 * (torch.expm1(e) - e) - 0.001 * ent
+    n = m.view(ex.B, ex.S).sum(1)
+    want = (per / n.repeat_interleave(ex.S)[m]).sum() / ex.B
+    want.backward()
+    want = want.detach()
+    assert abs(float(loss) - float(want)) < 1e-4 * max(1.0, abs(float(want)))
+    rel = float((grad.double() - w.grad).norm() / w.grad.norm())
+    assert rel < 1e-2, rel
