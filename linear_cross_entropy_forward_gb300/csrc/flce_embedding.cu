@@ -550,8 +550,8 @@ constexpr int kJoinThreads = 1024;
 constexpr int kJoinWarps = kJoinThreads / 32;
 
 // Adds up the parts of the runs that cross units.  Their number is known on the GPU alone:
-// the grid is fixed and strides over the two lists, a warp per short run's slab, a block
-// per long one's (each warp takes consecutive units, and their sums follow in order).  The
+// the grid is fixed and strides over the two lists, a block per long run's slab (each warp
+// takes consecutive units, and their sums follow in order), a warp per short one's.  The
 // lists' order changes from run to run; nothing depends on it.
 template <typename TO, int VEC>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(SumArgs a) {
@@ -560,15 +560,15 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(SumArgs a) {
   __shared__ PF share[kJoinWarps][32];
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
   wait_launch();
-  const uint32_t counts[2] = {a.lists[0], a.lists[1]};
+  // a block's jobs: a long run's slab, or a short one's for each warp
+  const uint32_t n_short = a.lists[0], n_long = a.lists[1];
+  const uint32_t items = n_long + (n_short + kJoinWarps - 1) / kJoinWarps;
 #pragma unroll 1
-  for (int list = 1; list >= 0; --list) {
-    const uint32_t jobs = list ? counts[1] : counts[0];
-    const uint4* job_list = list ? a.jobs[1] : a.jobs[0];
-    const uint32_t stride = list ? gridDim.x : gridDim.x * kJoinWarps;
-#pragma unroll 1
-    for (uint32_t k = list ? blockIdx.x : blockIdx.x * kJoinWarps + w; k < jobs; k += stride) {
-      const uint4 job = job_list[k];
+  for (uint32_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const bool list = item < n_long;
+    const uint32_t k = list ? item : (item - n_long) * kJoinWarps + w;
+    if (list || k < n_short) {
+      const uint4 job = list ? a.jobs[1][k] : a.jobs[0][k];
       const int64_t u = job.x, n = job.w;
       const int64_t c = (int64_t(job.y) * 32 + lane) * VEC;
       const uint32_t id = job.z;
