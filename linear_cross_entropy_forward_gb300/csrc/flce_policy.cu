@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(kSeqThreads, 1) policy_kernel(PolicyArgs a) {
   unsigned int kept_on = 0;
   const bool keep = a.what == (POLICY_LOSS | POLICY_GRAD);
   if (warp == 0 && lane == 0) {
-    *a.done = 0;
+    *a.totals = SeqTotals{};
     if (a.err_store) *a.err = 0;
   }
   float wg_all = 0.0f;  // the gradients' weight before a sequence's own
@@ -219,6 +219,8 @@ __global__ void __launch_bounds__(kSeqThreads, 1) policy_kernel(PolicyArgs a) {
     meet(q.meet);
 
     // ---- sums of the sequences
+    unsigned long long my_tokens = 0;
+    unsigned int my_live = 0, my_seqs = 0;
     for (int64_t i = warp; i < q.B; i += warps) {
       int first, last;
       seq_pieces(q, i, first, last);
@@ -257,34 +259,35 @@ __global__ void __launch_bounds__(kSeqThreads, 1) policy_kernel(PolicyArgs a) {
         }
         a.seq[i] = o;
       }
-      sequence_done(q, a.done);
+      my_tokens += n;
+      my_live += n > 0;
+      ++my_seqs;
     }
-    meet_sequences(q, a.done, static_cast<unsigned int>(q.B), a.err);
+    meet_sequences(q, a.totals, my_tokens, my_live, my_seqs, static_cast<unsigned int>(q.B), a.err);
 
     // ---- totals and the loss
     const bool first_block = blockIdx.x == 0;
+    const unsigned long long tokens = __ldcg(&a.totals->tokens);
+    const unsigned int live = __ldcg(&a.totals->live);
     Pair f[5] = {};
-    long long c[4] = {0, 0, 0, 0};
-    for (int64_t i = threadIdx.x; i < q.B; i += kSeqThreads) {
-      const PolicySeq& r = a.seq[i];
-      const long long n = r.n;
-      c[0] += n;
-      c[1] += n > 0;
-      if (first_block && want_loss) {
-        const float w = mean_seq && n > 0 ? 1.0f / static_cast<float>(n) : 1.0f;
+    long long c[2] = {0, 0};
+    if (first_block && want_loss) {
+      for (int64_t i = threadIdx.x; i < q.B; i += kSeqThreads) {
+        const PolicySeq& r = a.seq[i];
+        const float w = mean_seq && r.n > 0 ? 1.0f / static_cast<float>(r.n) : 1.0f;
         f[0] = f[0] + Pair{w * r.pg.h, fmaf(w, r.pg.h, -(w * r.pg.h)) + w * r.pg.l};
         f[1] = f[1] + w * (a.kl_coef * r.kl.value() - a.ent_coef * r.ent.value());
         f[2] = f[2] + r.kl;
         f[3] = f[3] + r.ent;
         f[4] = f[4] + r.old_kl;
-        c[2] += r.clipped;
-        c[3] += r.dual;
+        c[0] += r.clipped;
+        c[1] += r.dual;
       }
+      block_counts(c);
+      block_sums(f, q.B);
     }
-    block_counts(c);
-    if (first_block && want_loss) block_sums(f, q.B);
-    const float one_token = c[0] > 0 ? 1.0f / static_cast<float>(c[0]) : 0.0f;
-    const float one_seq = c[1] > 0 ? 1.0f / static_cast<float>(c[1]) : 0.0f;
+    const float one_token = tokens > 0 ? 1.0f / static_cast<float>(tokens) : 0.0f;
+    const float one_seq = live > 0 ? 1.0f / static_cast<float>(live) : 0.0f;
     const float w_all = a.aggregate == FLCE_AGG_TOKEN_MEAN ? one_token
                         : a.aggregate == FLCE_AGG_SUM      ? a.scale
                                                            : one_seq;
@@ -300,10 +303,10 @@ __global__ void __launch_bounds__(kSeqThreads, 1) policy_kernel(PolicyArgs a) {
           a.stats[1] = one_token * f[2].value();
           a.stats[2] = one_token * f[3].value();
           a.stats[3] = one_token * f[4].value();
-          a.counts[0] = c[0];
-          a.counts[1] = c[1];
-          a.counts[2] = c[2];
-          a.counts[3] = c[3];
+          a.counts[0] = static_cast<long long>(tokens);
+          a.counts[1] = live;
+          a.counts[2] = c[0];
+          a.counts[3] = c[1];
         }
       }
     }
@@ -342,6 +345,7 @@ int policy_check(const flce_policy_params* p) {
   Seqs q;
   const int rc = make_seqs(&p->seqs, &q);
   if (rc) return rc;
+  if ((p->ld_logp | p->ld_old | p->ld_ref | p->ld_entropy | p->ld_adv) < 0) return FLCE_ERR_BAD_ARG;
   if (p->kl < FLCE_KL_K1 || p->kl > FLCE_KL_K3) return FLCE_ERR_BAD_ARG;
   if (p->ratio != FLCE_RATIO_TOKEN && p->ratio != FLCE_RATIO_SEQUENCE) return FLCE_ERR_BAD_ARG;
   if (p->aggregate < FLCE_AGG_TOKEN_MEAN || p->aggregate > FLCE_AGG_SUM) return FLCE_ERR_BAD_ARG;
@@ -392,7 +396,7 @@ int policy_args(const flce_policy_params* p, void* workspace, PolicyArgs* a) {
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a->err = reinterpret_cast<uint32_t*>(ws);
   a->err_store = 1;
-  a->done = a->err + 16;
+  a->totals = reinterpret_cast<SeqTotals*>(ws + 64);
   a->piece = reinterpret_cast<PolicyPiece*>(ws + 256);
   a->seq = reinterpret_cast<PolicySeq*>(ws + 256 + align256(static_cast<size_t>(a->q.pieces) * sizeof(PolicyPiece)));
   return FLCE_OK;

@@ -49,7 +49,7 @@ struct PolicyArgs {
   float* lp_out;
   uint32_t* err;
   int err_store;  // the word is this launch's own and cleared by it
-  unsigned int* done;
+  SeqTotals* totals;
   PolicyPiece* piece;
   PolicySeq* seq;
 };

@@ -40,11 +40,10 @@ struct PrefArgs {
   float *loss, *rewards;
   void* dlp;
   uint32_t* err;
-  unsigned int* done;
+  SeqTotals* totals;
   PrefPiece* piece;
   float* coef;       // [B] gradient of the pair's own loss by a token of sequence i
   float* pair_loss;  // [B / 2]
-  int* pair_ok;      // [B / 2]
 };
 
 __device__ __forceinline__ float softplus(float x) {  // ln(1 + e^x)
@@ -83,7 +82,7 @@ __global__ void __launch_bounds__(kSeqThreads, 1) preference_kernel(PrefArgs a) 
   const int warp = blockIdx.x * kSeqWarps + (threadIdx.x >> 5);
   const int warps = gridDim.x * kSeqWarps;
   if (warp == 0 && lane == 0) {
-    *a.done = 0;
+    *a.totals = SeqTotals{};
     *a.err = 0;
   }
   for (int u = warp; u < q.pieces; u += warps) {
@@ -118,6 +117,7 @@ __global__ void __launch_bounds__(kSeqThreads, 1) preference_kernel(PrefArgs a) 
   meet(q.meet);
 
   const int64_t pairs = q.B / 2;
+  unsigned int my_live = 0, my_pairs = 0;
   for (int64_t i = warp; i < pairs; i += warps) {
     int64_t id[2];
     Pair score[2] = {}, like{};
@@ -161,7 +161,6 @@ __global__ void __launch_bounds__(kSeqThreads, 1) preference_kernel(PrefArgs a) 
         l -= a.nll * like.value() * per[0];
       }
       a.pair_loss[i] = l;
-      a.pair_ok[i] = ok;
       const float d = a.beta * dh;
       a.coef[id[0]] = ok ? d * (a.norm ? per[0] : 1.0f) - a.nll * per[0] : 0.0f;
       a.coef[id[1]] = ok ? -d * (a.norm ? per[1] : 1.0f) : 0.0f;
@@ -170,26 +169,25 @@ __global__ void __launch_bounds__(kSeqThreads, 1) preference_kernel(PrefArgs a) 
         a.rewards[id[1]] = a.beta * score[1].value();
       }
     }
-    sequence_done(q, a.done);
+    my_live += n[0] > 0 && n[1] > 0;
+    ++my_pairs;
   }
-  meet_sequences(q, a.done, static_cast<unsigned int>(pairs), a.err);
+  meet_sequences(q, a.totals, 0, my_live, my_pairs, static_cast<unsigned int>(pairs), a.err);
 
-  Pair l[1] = {};
-  long long live[1] = {0};
+  const unsigned int live = __ldcg(&a.totals->live);
   const bool ok = blockIdx.x == 0 ? seqs_ok(q) : true;
   const float nan = __int_as_float(0x7fc00000);
-  for (int64_t i = threadIdx.x; i < pairs; i += kSeqThreads) {
-    live[0] += a.pair_ok[i];
-    if (blockIdx.x == 0 && a.want_loss) {
+  Pair l[1] = {};
+  if (blockIdx.x == 0 && a.want_loss) {
+    for (int64_t i = threadIdx.x; i < pairs; i += kSeqThreads) {
       const float v = ok ? a.pair_loss[i] : nan;
       if (a.reduction == FLCE_RED_NONE) a.loss[i] = v;
       l[0] = l[0] + v;
     }
+    block_sums(l, pairs);
   }
-  block_counts(live);
-  if (blockIdx.x == 0 && a.want_loss) block_sums(l, pairs);
   const float scale =
-      a.reduction == FLCE_RED_MEAN ? (live[0] > 0 ? 1.0f / static_cast<float>(live[0]) : 0.0f)
+      a.reduction == FLCE_RED_MEAN ? (live > 0 ? 1.0f / static_cast<float>(live) : 0.0f)
                                    : 1.0f;
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     if (!ok) atomicOr(a.err, FLCE_DEVERR_SEQS);
@@ -226,7 +224,7 @@ __global__ void __launch_bounds__(kSeqThreads, 1) preference_kernel(PrefArgs a) 
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct PrefLayout {
-  size_t piece, coef, pair_loss, pair_ok, total;
+  size_t piece, coef, pair_loss, total;
 };
 
 PrefLayout pref_layout(const Seqs& q) {
@@ -236,7 +234,6 @@ PrefLayout pref_layout(const Seqs& q) {
   L.piece = off; off += align256(static_cast<size_t>(q.pieces) * sizeof(PrefPiece));
   L.coef = off; off += align256(B * 4);
   L.pair_loss = off; off += align256(B * 4);
-  L.pair_ok = off; off += align256(B * 4);
   L.total = off;
   return L;
 }
@@ -246,6 +243,7 @@ int pref_check(const flce_preference_params* p, Seqs* q) {
   const int rc = make_seqs(&p->seqs, q);
   if (rc) return rc;
   if (q->B % 2) return FLCE_ERR_BAD_SHAPE;
+  if ((p->ld_logp | p->ld_ref) < 0) return FLCE_ERR_BAD_ARG;
   if (p->kind < FLCE_PREF_SIGMOID || p->kind > FLCE_PREF_IPO) return FLCE_ERR_BAD_ARG;
   if (p->reduction < FLCE_RED_NONE || p->reduction > FLCE_RED_SUM) return FLCE_ERR_BAD_ARG;
   if (!(p->beta > 0.0) || !std::isfinite(p->beta) || !std::isfinite(p->margin) ||
@@ -319,11 +317,10 @@ int flce_preference_loss(const flce_preference_params* p, const void* logp, cons
   a.rewards = rewards;
   a.dlp = dlogp;
   a.err = reinterpret_cast<uint32_t*>(ws);
-  a.done = a.err + 16;
+  a.totals = reinterpret_cast<SeqTotals*>(ws + 64);
   a.piece = reinterpret_cast<PrefPiece*>(ws + L.piece);
   a.coef = reinterpret_cast<float*>(ws + L.coef);
   a.pair_loss = reinterpret_cast<float*>(ws + L.pair_loss);
-  a.pair_ok = reinterpret_cast<int*>(ws + L.pair_ok);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (dt == FLCE_F32)

@@ -251,22 +251,32 @@ __device__ __forceinline__ void meet(int how) {
     __syncthreads();
 }
 
-// The second meeting of a grid, at which most blocks have nothing left to do: polled at full
-// speed by all of them, the barrier's word kept its part of L2 from the few that still
-// read there (the sequences' sums took 15000 cycles instead of 1700).  So these blocks
-// sleep between looks.  `done` counts the warps' finished sequences and was cleared before
-// the first meeting.  A wait ends after 2 s at the latest, with the time-out bit set.
-__device__ __forceinline__ void sequence_done(const Seqs& q, unsigned int* done) {
-  if (q.meet != MEET_GRID) return;
-  __syncwarp();
-  if ((threadIdx.x & 31) == 0) {
-    __threadfence();
-    atomicAdd(done, 1u);
-  }
-}
+// What the sequences add up to: whole numbers, the same in any order.  Cleared before the
+// first meeting.
+struct SeqTotals {
+  unsigned long long tokens;  // counted tokens
+  unsigned int live;          // sequences (pairs) that count
+  unsigned int done;          // sequences (pairs) summed up
+};
 
-__device__ __forceinline__ void meet_sequences(const Seqs& q, const unsigned int* done,
-                                               unsigned int expected, uint32_t* err) {
+// The second meeting, by a warp that has summed up `mine` sequences.  Most blocks of a grid
+// have nothing left to do there: polled at full speed by all of them, the barrier's word kept
+// its part of L2 from the few that still read (their sums took 15000 cycles instead of
+// 1700).  So a grid's blocks wait for the count of finished sequences, and sleep between
+// looks.  A wait ends after 2 s at the latest, with the time-out bit set.
+__device__ __forceinline__ void meet_sequences(const Seqs& q, SeqTotals* t,
+                                               unsigned long long tokens, unsigned int live,
+                                               unsigned int mine, unsigned int expected,
+                                               uint32_t* err) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0 && mine > 0) {
+    if (tokens) atomicAdd(&t->tokens, tokens);
+    if (live) atomicAdd(&t->live, live);
+    if (q.meet == MEET_GRID) {
+      __threadfence();
+      atomicAdd(&t->done, mine);
+    }
+  }
   if (q.meet != MEET_GRID) {
     meet(q.meet);
     return;
@@ -275,7 +285,7 @@ __device__ __forceinline__ void meet_sequences(const Seqs& q, const unsigned int
     const uint64_t t0 = global_timer_ns();
     unsigned int n;
     while (true) {
-      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(n) : "l"(done) : "memory");
+      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(n) : "l"(&t->done) : "memory");
       if (n >= expected) break;
       if (global_timer_ns() - t0 > FLCE_WAIT_LIMIT_NS) {
         atomicOr(err, FLCE_DEVERR_TIMEOUT);
@@ -325,7 +335,7 @@ inline int make_seqs(const flce_seqs* a, Seqs* q) {
   const int64_t lim = (int64_t(1) << 31) - 1;
   if (a->B > lim || a->S > (int64_t(1) << 38)) return FLCE_ERR_BAD_SHAPE;
   if (a->dtype < FLCE_F32 || a->dtype > FLCE_F16) return FLCE_ERR_BAD_ARG;
-  if (a->cu_kind < 0 || a->cu_kind > 2 || a->mask_kind < 0 || a->mask_kind > 2)
+  if (a->ld_mask < 0 || a->cu_kind < 0 || a->cu_kind > 2 || a->mask_kind < 0 || a->mask_kind > 2)
     return FLCE_ERR_BAD_ARG;
   if (a->cu_kind == 0 && a->B > 0 && a->S > (int64_t(1) << 38) / a->B) return FLCE_ERR_BAD_SHAPE;
   if ((a->cu_kind != 0) != (a->cu_seqlens != nullptr)) return FLCE_ERR_BAD_ARG;

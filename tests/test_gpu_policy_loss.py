@@ -487,3 +487,34 @@ def test_head_bad_label_is_reported(F):
     with pytest.raises(F.FlceError) as e:
         F.flce_policy_forward_backward(hidden, weight, labels, old, adv, cu_seqlens=cu, validate=True)
     assert e.value.code == 5
+
+
+@pytest.mark.parametrize("lens", [[5000] * 9, [90000, 3, 40000]])
+def test_clusters_and_grids_in_a_graph(F, lens):
+    """More pieces than one block takes: a cluster's launch, and a cooperative grid's."""
+    lp, old, ref, ent, adv, mask = (x.cuda() for x in make(lens, 91))
+    cu = torch.tensor([0] + list(torch.tensor(lens).cumsum(0)), dtype=torch.int32).cuda()
+    kw = dict(KW, aggregate="seq_mean_token_mean", ref_logp=ref, entropy=ent, mask=mask, cu_seqlens=cu)
+    want = F.flce_policy_loss(lp, old, adv, **kw)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        cap = F.flce_policy_loss(lp, old, adv, **kw)
+    for _ in range(3):
+        for x in cap:
+            x.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(want, cap))
+
+
+def test_many_short_sequences(F):
+    run(F, [3, 0, 1, 7] * 20000, seed=95, kw=dict(KW, aggregate="seq_mean_token_mean"))
+
+
+@pytest.mark.parametrize("ratio", ["token", "sequence"])
+def test_more_tokens_than_warps_keep(F, ratio):
+    """Beyond a piece per warp of the GPU: kept gradients and recomputed ones in one launch."""
+    run(F, [700000, 5, 900000, 30000], seed=97, dtype="bf16",
+        kw=dict(KW, ratio=ratio, aggregate="seq_mean_token_mean"))
