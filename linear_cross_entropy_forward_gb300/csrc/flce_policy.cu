@@ -11,8 +11,8 @@
 //   1  a warp per piece of at most 256 tokens: its sums;
 //   2  a warp per sequence: its pieces' sums, added in a fixed order in pairs of floats;
 //   3  the totals (each block for itself, over the sequences' records), the loss (block
-//      0), and the gradients: of a warp's first piece from what pass 1 left in shared
-//      memory, of further ones (beyond 1.2M tokens) by a second pass over the tokens,
+//      0), and the gradients: of a warp's first four pieces from what pass 1 left in shared
+//      memory, of further ones (beyond 5M tokens) by a second pass over the tokens,
 // between which the blocks meet.  The sums have a fixed order: results do not change from
 // run to run.  The two passes over the tokens share one body of code: a launch finds the
 // instruction cache cold, and a second copy would be fetched while nothing else runs.
@@ -29,7 +29,6 @@ namespace flce {
 namespace {
 
 constexpr float kLogRatioLimit = 20.0f;
-constexpr int kBatch = 4;  // tokens per lane whose loads are in flight together
 
 __device__ __forceinline__ bool pair_above(float h, float l, float bh, float bl) {
   return __fadd_rn(__fadd_rn(h, -bh), __fadd_rn(l, -bl)) > 0.0f;
@@ -93,10 +92,10 @@ __global__ void __launch_bounds__(kSeqThreads, 1) policy_kernel(PolicyArgs a) {
   const int lane = threadIdx.x & 31;
   const int warp = blockIdx.x * kSeqWarps + (threadIdx.x >> 5);
   const int warps = gridDim.x * kSeqWarps;
-  // gradients before their weight, and which tokens count, of this warp's first piece
-  __shared__ float kept[kPerLane][kSeqThreads];
+  // gradients before their weight, and which tokens count, of this warp's first pieces
+  extern __shared__ float4 kept[];  // [piece][kGroups][kSeqThreads]
   unsigned int kept_on = 0;
-  const bool keep = a.what == (POLICY_LOSS | POLICY_GRAD);
+  const bool keep_all = a.what == (POLICY_LOSS | POLICY_GRAD);
   if (warp == 0 && lane == 0) {
     *a.totals = SeqTotals{};
     if (a.err_store) *a.err = 0;
@@ -111,7 +110,7 @@ __global__ void __launch_bounds__(kSeqThreads, 1) policy_kernel(PolicyArgs a) {
     // (and a second pass of a sequence's ratio without a reference knows the gradient)
     const bool values = grad ? !by_seq || a.ref : want_loss || by_seq;
 #pragma unroll 1
-    for (int u = warp; u < q.pieces; u += warps) {
+    for (int u = warp, round = 0; u < q.pieces; u += warps, ++round) {
       const Piece pc = find_piece(q, u);
       int t0 = 0, t1 = pc.len;
       float wg = wg_all, coef = 0.0f;
@@ -125,6 +124,8 @@ __global__ void __launch_bounds__(kSeqThreads, 1) policy_kernel(PolicyArgs a) {
           coef = r.coef;
         }
       }
+      const bool keep = keep_all && round < q.kept;
+      const float w_lp = wg * a.lp_sign, w_ent = -a.ent_coef * wg;
       const Counted counted(q, pc);
       const T* lp_ = static_cast<const T*>(a.lp) + pc.begin + pc.seq * a.lp_skip;
       const T* old_ = static_cast<const T*>(a.old_lp) + pc.begin + pc.seq * a.old_skip;
@@ -133,79 +134,84 @@ __global__ void __launch_bounds__(kSeqThreads, 1) policy_kernel(PolicyArgs a) {
       const float* adv_ = a.adv + (a.adv_per_token ? pc.begin + pc.seq * a.adv_skip : pc.seq);
       T* dlp_ = static_cast<T*>(a.dlp) + pc.begin;  // outputs are dense
       T* dent_ = static_cast<T*>(a.dent) + pc.begin;
-      if (grad && keep && u == warp) {
-#pragma unroll
-        for (int k = 0; k < kPerLane; ++k) {
-          const int t = lane + 32 * k;
-          if (t < t0 || t >= t1) continue;
-          const bool on = kept_on >> k & 1;
-          if (a.dlp)
-            store_f(dlp_ + t, on ? __fadd_rn(kept[k][threadIdx.x], coef) * (wg * a.lp_sign) : 0.0f);
-          if (a.dent) store_f(dent_ + t, on ? -a.ent_coef * wg : 0.0f);
-        }
-        continue;
-      }
+      const bool vec_in = !(misfit(lp_, a.lp) | misfit(old_, a.old_lp) | misfit(ref_, a.ref) |
+                            misfit(ent_, a.ent) | misfit(adv_, a.adv_per_token));
+      const bool vec_out = !(misfit(dlp_, a.dlp) | misfit(dent_, a.dent));
+      float adv_seq = 0.0f;
+      if (!a.adv_per_token && !by_seq && pc.len > 0) adv_seq = __ldg(adv_);
       float f[5] = {0, 0, 0, 0, 0};
       int c[3] = {0, 0, 0};
 #pragma unroll 1
-      for (int k0 = 0; k0 < kPerLane * 32 && k0 < t1; k0 += kBatch * 32) {
-        // every load of the batch first, masked tokens' too: one wait instead of one per token
-        float lp[kBatch], old[kBatch], ref[kBatch], ent[kBatch], adv[kBatch];
-        bool on[kBatch];
+      for (int g = 0; g < kGroups && g * kGroup4 < t1; ++g) {
+        const int t = g * kGroup4 + lane * kVec;
+        const unsigned int in = tokens_in(t, t0, t1);
+        unsigned int on;
+        float dl[kVec];
+        if (grad && keep) {
+          on = kept_on >> ((round * kGroups + g) * kVec);
+          const float4 x = kept[(round * kGroups + g) * kSeqThreads + threadIdx.x];
+          dl[0] = x.x; dl[1] = x.y; dl[2] = x.z; dl[3] = x.w;
+        } else {
+          // every load first, masked tokens' too: one wait
+          float lp[kVec] = {}, old[kVec] = {}, ref[kVec] = {}, ent[kVec] = {}, adv[kVec] = {};
+          const bool vec = vec_in && in == 15u;
+          on = counted(t, in);
+          if (values) {
+            load4(lp_ + t, vec, in, lp);
+            if (a.old_lp) load4(old_ + t, vec, in, old);
+            if (a.ref) load4(ref_ + t, vec, in, ref);
+            if (a.ent && !grad) load4(ent_ + t, vec, in, ent);
+            if (a.adv_per_token && !by_seq) load4(adv_ + t, vec, in, adv);
+          }
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-          const int t = k0 + j * 32 + lane;
-          const bool in = t >= t0 && t < t1;
-          on[j] = in && counted(t);
-          lp[j] = old[j] = ref[j] = ent[j] = adv[j] = 0.0f;
-          if (in && values) {
-            lp[j] = load_f(lp_ + t);
-            if (a.old_lp) old[j] = load_f(old_ + t);
-            if (a.ref) ref[j] = load_f(ref_ + t);
-            if (a.ent && !grad) ent[j] = load_f(ent_ + t);
-            if (!by_seq) adv[j] = __ldg(adv_ + (a.adv_per_token ? t : 0));
+          for (int j = 0; j < kVec; ++j) {
+            const bool counts = on >> j & 1;
+            const float x = a.lp_sign * lp[j];
+            float h = 0.0f, l = 0.0f;
+            if (a.old_lp) exact_diff(x, old[j], h, l);
+            const float hc = clamp_ratio(h), e = expf(hc);
+            dl[j] = 0.0f;
+            if (by_seq) {
+              if (counts) f[4] += h;
+            } else {
+              const float A = a.adv_per_token ? adv[j] : adv_seq;
+              const Ratio r = clip_ratio(a, h, l, e, A);
+              const float ra = r.value * A;
+              dl[j] = r.live ? -ra : 0.0f;
+              if (counts) {
+                f[0] -= ra;
+                c[1] += r.clipped;
+                c[2] += r.dual;
+              }
+            }
+            if (a.ref) {
+              float kl, dkl;
+              kl_term(a.kl, x, ref[j], kl, dkl);
+              if (counts) f[1] += kl;
+              dl[j] = fmaf(a.kl_coef, dkl, dl[j]);
+            }
+            if (!grad && counts) {
+              f[3] += exp_m1_mx(hc, e);
+              f[2] += ent[j];
+            }
+          }
+          c[0] += __popc(on);
+          if (!grad && keep) {
+            kept[(round * kGroups + g) * kSeqThreads + threadIdx.x] =
+                make_float4(dl[0], dl[1], dl[2], dl[3]);
+            kept_on |= on << ((round * kGroups + g) * kVec);
           }
         }
+        if (grad) {
+          float o[kVec];
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-          const int t = k0 + j * 32 + lane;
-          const float x = a.lp_sign * lp[j];
-          float h = 0.0f, l = 0.0f, dl = 0.0f;
-          if (a.old_lp) exact_diff(x, old[j], h, l);
-          const float hc = clamp_ratio(h), e = expf(hc);
-          if (by_seq) {
-            if (on[j]) f[4] += h;
-          } else {
-            const Ratio r = clip_ratio(a, h, l, e, adv[j]);
-            const float ra = r.value * adv[j];
-            dl = r.live ? -ra : 0.0f;
-            if (on[j]) {
-              f[0] -= ra;
-              c[1] += r.clipped;
-              c[2] += r.dual;
-            }
-          }
-          if (a.ref) {
-            float kl, dkl;
-            kl_term(a.kl, x, ref[j], kl, dkl);
-            if (on[j]) f[1] += kl;
-            dl = fmaf(a.kl_coef, dkl, dl);
-          }
-          if (!grad && keep && u == warp) {
-            kept[k0 / 32 + j][threadIdx.x] = on[j] ? dl : 0.0f;
-            kept_on |= static_cast<unsigned int>(on[j]) << (k0 / 32 + j);
-          }
-          dl = __fadd_rn(dl, coef);  // a sequence's; as where it meets the kept part
-          if (grad) {
-            if (t >= t0 && t < t1) {
-              if (a.dlp) store_f(dlp_ + t, on[j] ? dl * (wg * a.lp_sign) : 0.0f);
-              if (a.dent) store_f(dent_ + t, on[j] ? -a.ent_coef * wg : 0.0f);
-            }
-          } else if (on[j]) {
-            ++c[0];
-            f[3] += exp_m1_mx(hc, e);
-            f[2] += ent[j];
-          }
+          for (int j = 0; j < kVec; ++j)
+            o[j] = on >> j & 1 ? __fadd_rn(dl[j], coef) * w_lp : 0.0f;
+          const bool vec = vec_out && in == 15u;
+          if (a.dlp) store4(dlp_ + t, vec, in, o);
+#pragma unroll
+          for (int j = 0; j < kVec; ++j) o[j] = on >> j & 1 ? w_ent : 0.0f;
+          if (a.dent) store4(dent_ + t, vec, in, o);
         }
       }
       if (!grad) {
@@ -403,13 +409,15 @@ int policy_args(const flce_policy_params* p, void* workspace, PolicyArgs* a) {
 }
 
 int launch_policy(const PolicyArgs& a, int dtype, int sms, cudaStream_t st) {
+  // loss and gradients in one launch: gradients wait in shared memory
+  const int kept = a.what == (POLICY_LOSS | POLICY_GRAD) ? kTile * 4 : 0;
   cudaError_t e;
   if (dtype == FLCE_F32)
-    e = launch_seq(policy_kernel<float>, a, sms, st);
+    e = launch_seq(policy_kernel<float>, a, kept, sms, st);
   else if (dtype == FLCE_BF16)
-    e = launch_seq(policy_kernel<__nv_bfloat16>, a, sms, st);
+    e = launch_seq(policy_kernel<__nv_bfloat16>, a, kept, sms, st);
   else
-    e = launch_seq(policy_kernel<__half>, a, sms, st);
+    e = launch_seq(policy_kernel<__half>, a, kept, sms, st);
   return e == cudaSuccess ? FLCE_OK : FLCE_ERR_CUDA;
 }
 

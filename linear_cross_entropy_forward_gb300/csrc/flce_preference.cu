@@ -92,24 +92,29 @@ __global__ void __launch_bounds__(kSeqThreads, 1) preference_kernel(PrefArgs a) 
     const T* ref_ = static_cast<const T*>(a.ref) + pc.begin + pc.seq * a.ref_skip;
     float f[2] = {0.0f, 0.0f};
     int n = 0;
+    const bool vec_in = !(misfit(lp_, true) | misfit(ref_, a.ref));
     // the loads of all the lane's tokens first, masked ones' too
-    float lp[kPerLane], ref[kPerLane];
-    bool on[kPerLane];
+    float lp[kGroups][kVec] = {}, ref[kGroups][kVec] = {};
+    unsigned int on[kGroups];
 #pragma unroll
-    for (int k = 0; k < kPerLane; ++k) {
-      const int t = lane + 32 * k;
-      const bool in = t < pc.len;
-      on[k] = in && counted(t);
-      lp[k] = in ? load_f(lp_ + t) : 0.0f;
-      ref[k] = in && a.ref ? load_f(ref_ + t) : 0.0f;
+    for (int g = 0; g < kGroups; ++g) {
+      const int t = g * kGroup4 + lane * kVec;
+      const unsigned int in = tokens_in(t, 0, pc.len);
+      const bool vec = vec_in && in == 15u;
+      on[g] = counted(t, in);
+      load4(lp_ + t, vec, in, lp[g]);
+      if (a.ref) load4(ref_ + t, vec, in, ref[g]);
     }
 #pragma unroll
-    for (int k = 0; k < kPerLane; ++k)
-      if (on[k]) {
-        f[0] += lp[k] - ref[k];
-        f[1] += lp[k];
-        ++n;
-      }
+    for (int g = 0; g < kGroups; ++g) {
+      n += __popc(on[g]);
+#pragma unroll
+      for (int j = 0; j < kVec; ++j)
+        if (on[g] >> j & 1) {
+          f[0] += lp[g][j] - ref[g][j];
+          f[1] += lp[g][j];
+        }
+    }
     warp_sums(f);
     n = warp_sum(n);
     if (lane == 0) a.piece[u] = {f[0], f[1], n, 0};
@@ -210,13 +215,16 @@ __global__ void __launch_bounds__(kSeqThreads, 1) preference_kernel(PrefArgs a) 
       const int64_t pair = a.interleaved ? pc.seq / 2 : pc.seq % pairs;
       g *= __ldg(a.g_loss + (a.reduction == FLCE_RED_NONE ? pair : 0));
     }
-    bool on[kPerLane];
+    T* out = dlp_ + pc.begin;
+    const bool vec_out = !misfit(out, true);
 #pragma unroll
-    for (int k = 0; k < kPerLane; ++k) on[k] = lane + 32 * k < pc.len && counted(lane + 32 * k);
+    for (int k = 0; k < kGroups; ++k) {
+      const int t = k * kGroup4 + lane * kVec;
+      const unsigned int in = tokens_in(t, 0, pc.len), on = counted(t, in);
+      float o[kVec];
 #pragma unroll
-    for (int k = 0; k < kPerLane; ++k) {
-      const int t = lane + 32 * k;
-      if (t < pc.len) store_f(dlp_ + pc.begin + t, on[k] ? g : 0.0f);
+      for (int j = 0; j < kVec; ++j) o[j] = on >> j & 1 ? g : 0.0f;
+      store4(out + t, vec_out && in == 15u, in, o);
     }
   }
 }
@@ -324,11 +332,11 @@ int flce_preference_loss(const flce_preference_params* p, const void* logp, cons
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (dt == FLCE_F32)
-    e = launch_seq(preference_kernel<float>, a, sms, st);
+    e = launch_seq(preference_kernel<float>, a, 0, sms, st);
   else if (dt == FLCE_BF16)
-    e = launch_seq(preference_kernel<__nv_bfloat16>, a, sms, st);
+    e = launch_seq(preference_kernel<__nv_bfloat16>, a, 0, sms, st);
   else
-    e = launch_seq(preference_kernel<__half>, a, sms, st);
+    e = launch_seq(preference_kernel<__half>, a, 0, sms, st);
   if (e != cudaSuccess) return FLCE_ERR_CUDA;
   return p->validate ? read_status(workspace, st) : FLCE_OK;
 }

@@ -29,8 +29,10 @@ namespace flce {
 
 constexpr int kSeqThreads = 1024;  // one block per SM, 64 registers: few blocks to meet
 constexpr int kSeqWarps = kSeqThreads / 32;
-constexpr int kPerLane = 8;
-constexpr int kTile = 32 * kPerLane;
+constexpr int kVec = 4;             // a lane's consecutive tokens
+constexpr int kGroup4 = 32 * kVec;  // a warp's
+constexpr int kGroups = 2;
+constexpr int kTile = kGroups * kGroup4;
 constexpr int kClusterBlocks = 8;   // the portable cluster size
 
 // How the blocks of a grid meet between the phases of a kernel.
@@ -47,6 +49,7 @@ struct Seqs {
   int per_row;          // pieces of a padded row
   int pieces;
   int meet;
+  int kept;             // pieces per warp that shared memory holds values of
 };
 
 __device__ __forceinline__ int64_t clamp64(int64_t x, int64_t lo, int64_t hi) {
@@ -114,34 +117,114 @@ __device__ __forceinline__ Piece find_piece(const Seqs& q, int u) {
   return p;
 }
 
-// Which of a piece's tokens count.
-struct Counted {
-  const void* mask;
-  int labels;
-  int64_t ignore_index;
-  __device__ __forceinline__ Counted(const Seqs& q, const Piece& p)
-      : mask(nullptr), labels(q.mask_labels), ignore_index(q.ignore_index) {
-    const int64_t o = p.begin + p.seq * q.mask_skip;
-    if (q.mask)
-      mask = labels ? static_cast<const void*>(static_cast<const long long*>(q.mask) + o)
-                    : static_cast<const void*>(static_cast<const unsigned char*>(q.mask) + o);
-  }
-  __device__ __forceinline__ bool operator()(int t) const {
-    if (!mask) return true;
-    if (labels) return __ldg(static_cast<const long long*>(mask) + t) != ignore_index;
-    return __ldg(static_cast<const unsigned char*>(mask) + t) != 0;
-  }
-};
-
 __device__ __forceinline__ float load_f(const float* p) { return __ldg(p); }
 __device__ __forceinline__ float load_f(const __nv_bfloat16* p) {
   return __uint_as_float(static_cast<uint32_t>(__ldg(reinterpret_cast<const unsigned short*>(p)))
                          << 16);
 }
 __device__ __forceinline__ float load_f(const __half* p) { return __half2float(__ldg(p)); }
+// Four consecutive values: as one access where `vec` (the pointer is aligned and all four are
+// inside), else those of `in`.
+__device__ __forceinline__ void load4(const float* p, bool vec, unsigned int in, float (&v)[kVec]) {
+  if (vec) {
+    const float4 x = __ldg(reinterpret_cast<const float4*>(p));
+    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+  } else {
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) v[j] = in >> j & 1 ? __ldg(p + j) : 0.0f;
+  }
+}
+template <typename T>
+__device__ __forceinline__ void load4(const T* p, bool vec, unsigned int in, float (&v)[kVec]) {
+  static_assert(sizeof(T) == 2, "16-bit types");
+  if (vec) {
+    const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
+    const T* h = reinterpret_cast<const T*>(&x);
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) v[j] = static_cast<float>(h[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) v[j] = in >> j & 1 ? load_f(p + j) : 0.0f;
+  }
+}
 __device__ __forceinline__ void store_f(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_f(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void store_f(__half* p, float v) { *p = __float2half_rn(v); }
+template <typename T>
+__device__ __forceinline__ void store4(T* p, bool vec, unsigned int in, const float (&v)[kVec]) {
+  if (vec) {
+    struct alignas(kVec * sizeof(T)) { T x[kVec]; } o;
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) store_f(&o.x[j], v[j]);
+    *reinterpret_cast<decltype(o)*>(p) = o;
+  } else {
+#pragma unroll
+    for (int j = 0; j < kVec; ++j)
+      if (in >> j & 1) store_f(p + j, v[j]);
+  }
+}
+
+// Whether every given array (NULL: not there) takes four values in one access.
+template <typename T>
+__device__ __forceinline__ uintptr_t misfit(const T* p, bool there) {
+  return there ? reinterpret_cast<uintptr_t>(p) & (kVec * sizeof(T) - 1) : 0;
+}
+
+// Which of a piece's tokens count.
+struct Counted {
+  const void* mask;
+  int labels;
+  int64_t ignore_index;
+  bool vec;
+  __device__ __forceinline__ Counted(const Seqs& q, const Piece& p)
+      : mask(nullptr), labels(q.mask_labels), ignore_index(q.ignore_index), vec(false) {
+    const int64_t o = p.begin + p.seq * q.mask_skip;
+    if (q.mask)
+      mask = labels ? static_cast<const void*>(static_cast<const long long*>(q.mask) + o)
+                    : static_cast<const void*>(static_cast<const unsigned char*>(q.mask) + o);
+    // four bytes, or two pairs of labels
+    vec = (reinterpret_cast<uintptr_t>(mask) & (labels ? 15 : 3)) == 0;
+  }
+  // Of the four tokens from t on, those of `in` that count.
+  __device__ __forceinline__ unsigned int operator()(int t, unsigned int in) const {
+    if (!mask) return in;
+    unsigned int on = 0;
+    if (labels) {
+      const long long* m = static_cast<const long long*>(mask) + t;
+      if (vec && in == 15u) {
+        const longlong2 a = __ldg(reinterpret_cast<const longlong2*>(m));
+        const longlong2 b = __ldg(reinterpret_cast<const longlong2*>(m) + 1);
+        on = (a.x != ignore_index) | (a.y != ignore_index) << 1 | (b.x != ignore_index) << 2 |
+             (b.y != ignore_index) << 3;
+      } else {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j)
+          if (in >> j & 1) on |= static_cast<unsigned int>(__ldg(m + j) != ignore_index) << j;
+      }
+    } else {
+      const unsigned char* m = static_cast<const unsigned char*>(mask) + t;
+      if (vec && in == 15u) {
+        const unsigned int x = __ldg(reinterpret_cast<const unsigned int*>(m));
+#pragma unroll
+        for (int j = 0; j < kVec; ++j)
+          on |= static_cast<unsigned int>((x >> (8 * j) & 255u) != 0) << j;
+      } else {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j)
+          if (in >> j & 1) on |= static_cast<unsigned int>(__ldg(m + j) != 0) << j;
+      }
+    }
+    return on;
+  }
+};
+
+// Of the four tokens from t on, those inside [t0, t1).
+__device__ __forceinline__ unsigned int tokens_in(int t, int t0, int t1) {
+  unsigned int in = 15u;
+  if (t < t0) in = t0 - t >= kVec ? 0u : in << (t0 - t) & 15u;
+  if (t + kVec > t1) in &= t >= t1 ? 0u : (1u << (t1 - t)) - 1;
+  return in;
+}
 
 // A sum as an unevaluated pair of floats (h + l, about 48 bits): the sums over pieces and
 // sequences, whose terms have both signs.  fp64 adds run at a small fraction of the
@@ -365,11 +448,12 @@ inline int seq_elem_bytes(int dtype) { return dtype == FLCE_F32 ? 4 : 2; }
 // A grid whose blocks meet: plain for one block, one cluster (of 2, 4 or 8 blocks), or
 // cooperative.
 inline cudaError_t launch_meeting(const void* kernel, void* args, int64_t blocks, int threads,
-                                  int meet, cudaStream_t st) {
+                                  int meet, cudaStream_t st, int smem = 0) {
   void* params[] = {args};
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks));
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = st;
   cudaLaunchAttribute attr{};
   if (meet == MEET_CLUSTER) {
@@ -388,15 +472,28 @@ inline cudaError_t launch_meeting(const void* kernel, void* args, int64_t blocks
 // A warp per piece: one block where its warps suffice, else a cluster of at most eight
 // (whose hardware barrier takes a fraction of a grid's), else a cooperative grid of at most
 // one block per SM, whose warps take several pieces each.
+// `kept` bytes of dynamic shared memory per warp's piece, for at most kKept of them.
+constexpr int kKept = 4;
+
 template <typename Args>
-inline cudaError_t launch_seq(void (*kernel)(Args), const Args& args, int sms, cudaStream_t st) {
+inline cudaError_t launch_seq(void (*kernel)(Args), const Args& args, int kept, int sms,
+                              cudaStream_t st) {
   Args a = args;
   int64_t blocks = (int64_t(a.q.pieces) + kSeqWarps - 1) / kSeqWarps;
   if (blocks < 1) blocks = 1;
   a.q.meet = blocks == 1 ? MEET_BLOCK : blocks <= kClusterBlocks ? MEET_CLUSTER : MEET_GRID;
   if (a.q.meet == MEET_CLUSTER) blocks = blocks <= 2 ? 2 : blocks <= 4 ? 4 : 8;
-  return launch_meeting(reinterpret_cast<const void*>(kernel), &a, blocks < sms ? blocks : sms,
-                        kSeqThreads, a.q.meet, st);
+  if (blocks > sms) blocks = sms;
+  const int64_t rounds = (a.q.pieces + blocks * kSeqWarps - 1) / (blocks * kSeqWarps);
+  a.q.kept = static_cast<int>(rounds < kKept ? rounds : kKept);
+  const int smem = kept * kSeqWarps * a.q.kept;
+  const void* k = reinterpret_cast<const void*>(kernel);
+  if (smem > 40 * 1024) {  // more than the default, beside the kernel's static arrays
+    const cudaError_t e =
+        cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_meeting(k, &a, blocks, kSeqThreads, a.q.meet, st, smem);
 }
 
 }  // namespace flce
