@@ -9,6 +9,7 @@ from __future__ import annotations
 import ctypes
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _binding as B
 from .losses import _DTYPES, _current_device, _on, _raw_stream, _workspace
@@ -140,6 +141,7 @@ class _Embedding(torch.autograd.Function):
         return flce_embedding(ids, weight, scale, v_offset, v_total)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, g):
         (ids,) = ctx.saved_tensors
         V, scale, padding_idx, v_offset, v_total = ctx.cfg

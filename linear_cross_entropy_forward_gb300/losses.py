@@ -16,6 +16,7 @@ from __future__ import annotations
 import ctypes
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _binding as B
 from .workloads import IGNORE_INDEX, RED_NONE, reduction_code
@@ -259,6 +260,7 @@ class _PolicyLoss(torch.autograd.Function):
         return loss[0], stats, counts
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, g_loss, _g_stats, _g_counts):
         logp, entropy, old_logp, advantages, ref_logp, mask, cu = ctx.saved_tensors
         g = _upstream(g_loss)
@@ -357,6 +359,7 @@ class _LinearPolicyLoss(torch.autograd.Function):
         return loss[0], stats, counts, logp, entropy
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, g_loss, *_):
         dh, dw = ctx.saved_tensors
         g = _upstream(g_loss)
@@ -471,6 +474,7 @@ class _PreferenceLoss(torch.autograd.Function):
         return loss if reduction_code(kw["reduction"]) == RED_NONE else loss[0], rewards
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, g_loss, _g_rewards):
         logp, ref_logp, ref_scores, mask, cu = ctx.saved_tensors
         g = _upstream(g_loss)

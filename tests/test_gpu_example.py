@@ -76,3 +76,59 @@ def test_tied_gradient_is_the_definitions(ex):
     assert abs(float(loss) - float(want)) < 1e-4 * max(1.0, abs(float(want)))
     rel = float((grad.double() - w.grad).norm() / w.grad.norm())
     assert rel < 1e-2, rel
+
+
+def _functions(ex):
+    """Each differentiable call as (leaf, scalar of the leaf)."""
+    F = ex.flce
+    g = torch.Generator().manual_seed(5)
+    lp = -torch.rand(4, 700, generator=g).cuda()
+    adv = torch.randn(4, generator=g).cuda()
+    table = torch.randn(50, 64, generator=g).cuda()
+    ids = torch.randint(0, 50, (300,), generator=g).cuda()
+    up = torch.randn(300, 64, generator=g).cuda()
+    return {"policy": (lp, lambda x: F.policy_loss(x, lp - 0.1, adv)[0]),
+            "policy_bf16": (lp.bfloat16(), lambda x: F.policy_loss(x, lp.bfloat16(), adv)[0]),
+            "preference": (lp, lambda x: F.preference_loss(x, lp * 0.5)[0]),
+            "embedding": (table, lambda x: (F.embedding(ids, x, 2.0) * up).sum())}
+
+
+@pytest.mark.parametrize("name", ["policy", "policy_bf16", "preference", "embedding"])
+def test_backward_passes_replay_from_a_graph(ex, name):
+    """The gradient of a leaf captured on a stream of its own (torch.autograd.grad: a backward()
+    into .grad would also need the leaf's accumulation on that stream)."""
+    leaf, f = _functions(ex)[name]
+    x = leaf.clone().requires_grad_(True)
+    (want,) = torch.autograd.grad(f(x), x)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        torch.autograd.grad(f(x), x)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        (got,) = torch.autograd.grad(f(x), x)
+    got.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("name", ["policy", "preference", "embedding"])
+def test_second_derivatives_are_refused(ex, name):
+    leaf, f = _functions(ex)[name]
+    x = leaf.clone().requires_grad_(True)
+    (g,) = torch.autograd.grad(f(x) ** 2, x, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        g.sum().backward()
+
+
+def test_gradient_of_a_broadcast_input(ex):
+    F = ex.flce
+    base = -torch.rand(1, 700).cuda().requires_grad_(True)
+    adv = torch.randn(4).cuda()
+    old = base.detach().expand(4, 700) - 0.05
+    loss, _, _ = F.policy_loss(base.expand(4, 700), old, adv)
+    (got,) = torch.autograd.grad(loss, base)
+    full = F.flce_policy_loss(base.detach().expand(4, 700), old, adv)[3]
+    assert torch.allclose(got, full.sum(0, keepdim=True), rtol=1e-6, atol=1e-9)
