@@ -101,6 +101,7 @@ __global__ void __launch_bounds__(kSeqThreads, 1) policy_kernel(PolicyArgs a) {
     if (a.err_store) *a.err = 0;
   }
   float wg_all = 0.0f;  // the gradients' weight before a sequence's own
+  float g_up = 1.0f;    // the upstream gradient, a factor with a rounding of its own
 
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
@@ -206,11 +207,11 @@ __global__ void __launch_bounds__(kSeqThreads, 1) policy_kernel(PolicyArgs a) {
           float o[kVec];
 #pragma unroll
           for (int j = 0; j < kVec; ++j)
-            o[j] = on >> j & 1 ? __fadd_rn(dl[j], coef) * w_lp : 0.0f;
+            o[j] = on >> j & 1 ? __fadd_rn(dl[j], coef) * w_lp * g_up : 0.0f;
           const bool vec = vec_out && in == 15u;
           if (a.dlp) store4(dlp_ + t, vec, in, o);
 #pragma unroll
-          for (int j = 0; j < kVec; ++j) o[j] = on >> j & 1 ? w_ent : 0.0f;
+          for (int j = 0; j < kVec; ++j) o[j] = on >> j & 1 ? w_ent * g_up : 0.0f;
           if (a.dent) store4(dent_ + t, vec, in, o);
         }
       }
@@ -297,7 +298,8 @@ __global__ void __launch_bounds__(kSeqThreads, 1) policy_kernel(PolicyArgs a) {
     const float w_all = a.aggregate == FLCE_AGG_TOKEN_MEAN ? one_token
                         : a.aggregate == FLCE_AGG_SUM      ? a.scale
                                                            : one_seq;
-    wg_all = a.g_loss ? w_all * __ldg(a.g_loss) : w_all;
+    wg_all = w_all;
+    if (a.g_loss) g_up = __ldg(a.g_loss);
     if (first_block) {
       const bool ok = seqs_ok(q);
       if (threadIdx.x == 0) {

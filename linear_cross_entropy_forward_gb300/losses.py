@@ -249,25 +249,39 @@ def _upstream(g):
 
 
 class _PolicyLoss(torch.autograd.Function):
+    """fp32: the launch that forms the loss forms the gradients of it, and the backward
+    multiplies them by the upstream gradient (as the kernel would, with the same rounding;
+    290 us a step with autograd against 340).  A 16-bit gradient would be rounded twice that
+    way: there the backward is a launch of its own."""
+
     @staticmethod
     def forward(ctx, logp, entropy, old_logp, advantages, ref_logp, mask, cu_seqlens, kw):
-        loss, stats, counts, _, _ = flce_policy_loss(logp, old_logp, advantages, ref_logp,
-                                                     entropy, mask, cu_seqlens, need_grad=False,
-                                                     **kw)
-        ctx.save_for_backward(logp, entropy, old_logp, advantages, ref_logp, mask, cu_seqlens)
-        ctx.kw = kw
+        need_lp, need_ent = ctx.needs_input_grad[:2]
+        ctx.formed = logp.dtype is torch.float32
+        loss, stats, counts, dlogp, dent = flce_policy_loss(
+            logp, old_logp, advantages, ref_logp, entropy, mask, cu_seqlens,
+            need_grad=ctx.formed and (need_lp or need_ent), need_entropy_grad=need_ent, **kw)
+        if ctx.formed:
+            ctx.save_for_backward(dlogp, dent)
+        else:
+            ctx.save_for_backward(logp, entropy, old_logp, advantages, ref_logp, mask, cu_seqlens)
+            ctx.kw = kw
         ctx.mark_non_differentiable(stats, counts)
         return loss[0], stats, counts
 
     @staticmethod
     @once_differentiable
     def backward(ctx, g_loss, _g_stats, _g_counts):
-        logp, entropy, old_logp, advantages, ref_logp, mask, cu = ctx.saved_tensors
-        g = _upstream(g_loss)
-        _, _, _, dlogp, dent = flce_policy_loss(logp, old_logp, advantages, ref_logp, entropy,
-                                                mask, cu, g_loss=g, need_loss=False,
-                                                need_entropy_grad=ctx.needs_input_grad[1],
-                                                **ctx.kw)
+        need_lp, need_ent = ctx.needs_input_grad[:2]
+        if ctx.formed:
+            dlogp, dent = ctx.saved_tensors
+            dlogp = dlogp * g_loss if need_lp else None
+            dent = dent * g_loss if need_ent else None
+        else:
+            logp, entropy, old_logp, advantages, ref_logp, mask, cu = ctx.saved_tensors
+            _, _, _, dlogp, dent = flce_policy_loss(
+                logp, old_logp, advantages, ref_logp, entropy, mask, cu, g_loss=_upstream(g_loss),
+                need_loss=False, need_entropy_grad=need_ent, **ctx.kw)
         return dlogp, dent, None, None, None, None, None, None
 
 
@@ -464,22 +478,32 @@ def flce_preference_loss(logp, ref_logp=None, ref_scores=None, mask=None, cu_seq
 
 
 class _PreferenceLoss(torch.autograd.Function):
+    """As _PolicyLoss; a loss per pair has an upstream gradient per pair, which the kernel
+    spreads over the tokens."""
+
     @staticmethod
     def forward(ctx, logp, ref_logp, ref_scores, mask, cu_seqlens, kw):
-        loss, rewards, _ = flce_preference_loss(logp, ref_logp, ref_scores, mask, cu_seqlens,
-                                                need_grad=False, **kw)
-        ctx.save_for_backward(logp, ref_logp, ref_scores, mask, cu_seqlens)
-        ctx.kw = kw
+        per_pair = reduction_code(kw["reduction"]) == RED_NONE
+        ctx.formed = logp.dtype is torch.float32 and not per_pair
+        loss, rewards, dlogp = flce_preference_loss(
+            logp, ref_logp, ref_scores, mask, cu_seqlens,
+            need_grad=ctx.formed and ctx.needs_input_grad[0], **kw)
+        if ctx.formed:
+            ctx.save_for_backward(dlogp)
+        else:
+            ctx.save_for_backward(logp, ref_logp, ref_scores, mask, cu_seqlens)
+            ctx.kw = kw
         ctx.mark_non_differentiable(rewards)
-        return loss if reduction_code(kw["reduction"]) == RED_NONE else loss[0], rewards
+        return loss if per_pair else loss[0], rewards
 
     @staticmethod
     @once_differentiable
     def backward(ctx, g_loss, _g_rewards):
+        if ctx.formed:
+            return ctx.saved_tensors[0] * g_loss, None, None, None, None, None
         logp, ref_logp, ref_scores, mask, cu = ctx.saved_tensors
-        g = _upstream(g_loss)
-        _, _, dlogp = flce_preference_loss(logp, ref_logp, ref_scores, mask, cu, g_loss=g,
-                                           need_loss=False, **ctx.kw)
+        _, _, dlogp = flce_preference_loss(logp, ref_logp, ref_scores, mask, cu,
+                                           g_loss=_upstream(g_loss), need_loss=False, **ctx.kw)
         return dlogp, None, None, None, None, None
 
 

@@ -103,6 +103,14 @@ def test_policy_parameters_refused(lib, kw):
     assert lib.flce_policy_check_params(ctypes.byref(policy(**kw))) == BAD_ARG
 
 
+def test_negative_strides_refused(lib):
+    for f in ("ld_logp", "ld_old", "ld_ref", "ld_entropy", "ld_adv"):
+        assert lib.flce_policy_check_params(ctypes.byref(policy(**{f: -1}))) == BAD_ARG
+    for f in ("ld_logp", "ld_ref"):
+        assert lib.flce_preference_check_params(ctypes.byref(preference(**{f: -1}))) == BAD_ARG
+    assert lib.flce_policy_check_params(ctypes.byref(policy(seqs(ld_mask=-1)))) == BAD_ARG
+
+
 def test_policy_pointers_refused(lib):
     p = policy()
     need = lib.flce_policy_workspace_size(ctypes.byref(p))
