@@ -24,7 +24,7 @@ namespace flce {
 namespace {
 
 struct PrefPiece {
-  float score, like;
+  Pair score, like;  // a score meets reference scores of its size: every digit counts
   int n;
   int pad;
 };
@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(kSeqThreads, 1) preference_kernel(PrefArgs a) 
     const Counted counted(q, pc);
     const T* lp_ = static_cast<const T*>(a.lp) + pc.begin + pc.seq * a.lp_skip;
     const T* ref_ = static_cast<const T*>(a.ref) + pc.begin + pc.seq * a.ref_skip;
-    float f[2] = {0.0f, 0.0f};
+    Pair f[2] = {};
     int n = 0;
     const bool vec_in = !(misfit(lp_, true) | misfit(ref_, a.ref));
     // the loads of all the lane's tokens first, masked ones' too
@@ -111,8 +111,8 @@ __global__ void __launch_bounds__(kSeqThreads, 1) preference_kernel(PrefArgs a) 
 #pragma unroll
       for (int j = 0; j < kVec; ++j)
         if (on[g] >> j & 1) {
-          f[0] += lp[g][j] - ref[g][j];
-          f[1] += lp[g][j];
+          f[0] = f[0] + lp[g][j] + -ref[g][j];
+          f[1] = f[1] + lp[g][j];
         }
     }
     warp_sums(f);
@@ -153,8 +153,10 @@ __global__ void __launch_bounds__(kSeqThreads, 1) preference_kernel(PrefArgs a) 
                             n[1] > 0 ? 1.0f / static_cast<float>(n[1]) : 0.0f};
       for (int side = 0; side < 2; ++side) {
         if (a.norm) {
-          const float x = score[side].h * per[side];
-          score[side] = {x, fmaf(score[side].h, per[side], -x) + score[side].l * per[side]};
+          // a pair again: the quotient, and the quotient of what it leaves
+          const float fn = n[side] > 0 ? static_cast<float>(n[side]) : 1.0f;
+          const float x = score[side].value() / fn;
+          score[side] = {x, (fmaf(-x, fn, score[side].h) + score[side].l) / fn};
         }
         if (a.ref_scores) score[side] = score[side] + -__ldg(a.ref_scores + id[side]);
         if (n[side] == 0) score[side] = {};

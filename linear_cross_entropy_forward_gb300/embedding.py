@@ -50,6 +50,19 @@ def _need_ids(ids):
     return index
 
 
+_IDS = {torch.int64: 1, torch.int32: 0}
+
+
+def _refuse_lookup(ids, weight):
+    _need_ids(ids)
+    if not isinstance(weight, torch.Tensor) or not weight.is_cuda or weight.dtype not in _DTYPES:
+        raise TypeError("weight must be a bf16, fp16 or fp32 CUDA tensor")
+    if weight.dim() != 2 or not weight.is_contiguous():
+        raise ValueError(f"weight must be a contiguous [V, H], got shape {tuple(weight.shape)}")
+    if weight.get_device() != ids.get_device():
+        raise ValueError(f"weight is on {weight.device}, ids on {ids.device}")
+
+
 def flce_embedding(ids, weight, scale=1.0, v_offset=0, v_total=0, validate=False, stream=None,
                    out=None):
     """scale * weight[ids], of shape [*ids.shape, H].
@@ -63,17 +76,20 @@ def flce_embedding(ids, weight, scale=1.0, v_offset=0, v_total=0, validate=False
         return _on(stream, flce_embedding, ids, weight, scale, v_offset, v_total, validate,
                    out=out)
     lib = B._lib or B.load_library()
-    dev = _need_ids(ids)
-    if not isinstance(weight, torch.Tensor) or not weight.is_cuda or weight.dtype not in _DTYPES:
-        raise TypeError("weight must be a bf16, fp16 or fp32 CUDA tensor")
-    if weight.dim() != 2 or not weight.is_contiguous():
-        raise ValueError(f"weight must be a contiguous [V, H], got shape {tuple(weight.shape)}")
-    if weight.get_device() != dev:
-        raise ValueError(f"weight is on {weight.device}, ids on {ids.device}")
-    V, H = weight.shape
+    # one pass over what is right, as a small lookup's time is these checks; _refuse_lookup
+    # says what is wrong
+    try:
+        ids64, dt, dev = _IDS[ids.dtype], _DTYPES[weight.dtype], ids.get_device()
+        V, H = weight.shape
+        if not (dev >= 0 and dev == weight.get_device() and dev == _current_device()
+                and ids.is_contiguous() and weight.is_contiguous()):
+            raise ValueError
+    except (AttributeError, KeyError, ValueError):
+        _refuse_lookup(ids, weight)
+        raise
     shape = (*ids.shape, H)
-    p = embedding_params(ids.numel(), H, V, scale, weight.dtype, None, ids.dtype is torch.int64,
-                         False, None, v_offset, v_total, validate)
+    p = B.FlceEmbeddingParams(ids.numel(), H, V, v_offset, v_total, -1, scale, dt, dt, ids64, 0,
+                              bool(validate))
     if out is None:
         out = torch.empty(shape, dtype=weight.dtype, device=dev)
     else:

@@ -4,7 +4,7 @@ Tolerances.  A token's term is a product of a ratio (exp of an exact difference 
 fp32: |d| <= 20 makes that 20 half steps of 2^-24 at most, and two steps of expf), an
 advantage and a weight, plus a KL term with a few roundings of its own: 2^-19 of the sum of
 the terms' magnitudes covers them (32 half steps).  Sums over tokens add at most 2^-19 of
-the summed magnitudes as well (a tree over 1024 fp32 values, then fp64).  A gradient stored
+the summed magnitudes as well (a tree over 256 fp32 values, then pairs of floats).  A gradient stored
 in 16 bits adds half a step of its type, and fp16 half of its smallest subnormal."""
 import math
 

@@ -1,8 +1,7 @@
 """The preference loss against a plain loop over pairs in 64 bits.
 
 Tolerances.  A sequence's score is a sum over tokens of fp32 differences (half a step each)
-added in fp32 trees of at most 1024 and then in fp64: within 2^-19 of the summed magnitudes
-M.  h is then off by beta 2^-19 M at most; the losses' derivatives by h are bounded by the
+added in fp32 or wider: within 2^-19 of the summed magnitudes M.  h is then off by beta 2^-19 M at most; the losses' derivatives by h are bounded by the
 factors below (curvature 1/4 for the logistic ones, scaled for robust; ipo's is 2 / beta^2).
 A gradient stored in 16 bits adds half a step of its type."""
 import math
