@@ -434,7 +434,8 @@ int flce_embedding(const flce_embedding_params* params, const void* ids, const v
                    void* out, void* workspace, size_t ws_bytes, void* stream);
 
 /* dweight[v] = scale * sum of dout[n] over the n with ids[n] = v (added to dweight[v] with
- * accumulate), summed in fp32 in the order of n and rounded once.  Ids outside the table
+ * accumulate), summed in fp32 in a fixed order (32 rows of n at a time, then those) and
+ * rounded once.  Ids outside the table
  * are left out and reported as FLCE_ERR_LABEL by flce_status. */
 int flce_embedding_backward(const flce_embedding_params* params, const void* dout,
                             const void* ids, void* dweight, void* workspace, size_t ws_bytes,

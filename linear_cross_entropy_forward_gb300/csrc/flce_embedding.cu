@@ -685,7 +685,11 @@ int vec_for(int bytes, int64_t H, uintptr_t ptrs) {
   return v;
 }
 
-inline int rc_of(cudaError_t e) { return e == cudaSuccess ? FLCE_OK : FLCE_ERR_CUDA; }
+inline int rc_of(cudaError_t e) {
+  if (e == cudaSuccess) return FLCE_OK;
+  cudaGetLastError();  // reported here, not by a later call
+  return FLCE_ERR_CUDA;
+}
 
 template <typename T, int VEC>
 int launch_lookup(EmbedArgs a, cudaStream_t st) {

@@ -466,7 +466,9 @@ inline cudaError_t launch_meeting(const void* kernel, void* args, int64_t blocks
   }
   cfg.attrs = &attr;
   cfg.numAttrs = meet == MEET_BLOCK ? 0 : 1;
-  return cudaLaunchKernelExC(&cfg, kernel, params);
+  const cudaError_t e = cudaLaunchKernelExC(&cfg, kernel, params);
+  if (e != cudaSuccess) cudaGetLastError();  // reported here, not by a later call
+  return e;
 }
 
 // A warp per piece: one block where its warps suffice, else a cluster of at most eight
@@ -491,7 +493,10 @@ inline cudaError_t launch_seq(void (*kernel)(Args), const Args& args, int kept, 
   if (smem > 40 * 1024) {  // more than the default, beside the kernel's static arrays
     const cudaError_t e =
         cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess) {
+      cudaGetLastError();
+      return e;
+    }
   }
   return launch_meeting(k, &a, blocks, kSeqThreads, a.q.meet, st, smem);
 }

@@ -132,3 +132,45 @@ def test_gradient_of_a_broadcast_input(ex):
     (got,) = torch.autograd.grad(loss, base)
     full = F.flce_policy_loss(base.detach().expand(4, 700), old, adv)[3]
     assert torch.allclose(got, full.sum(0, keepdim=True), rtol=1e-6, atol=1e-9)
+
+
+def test_calls_on_several_streams_and_threads(ex):
+    """Cooperative grids, clusters and the head's GEMMs side by side: the same results."""
+    import threading
+    F = ex.flce
+    g = torch.Generator().manual_seed(9)
+    lp = -torch.rand(64, 2000, generator=g).cuda()
+    adv = torch.randn(64, generator=g).cuda()
+    ids = torch.randint(0, 3000, (70000,), generator=g).cuda()
+    dout = torch.randn(70000, 32, generator=g).cuda()
+    hidden = torch.randn(512, 256, generator=g).to(torch.bfloat16).cuda()
+    weight = torch.randn(256, 2048, generator=g).to(torch.bfloat16).cuda()
+    labels = torch.randint(0, 2048, (512,), generator=g).cuda()
+    one = torch.ones(1, device="cuda")
+
+    def calls():
+        return [F.flce_policy_loss(lp, lp - 0.1, adv)[3], F.flce_preference_loss(lp)[2],
+                F.flce_embedding_backward(dout, ids, 3000),
+                F.flce_forward_backward(hidden, weight, labels, one, None)[5],
+                F.flce_policy_loss(lp[:4, :100], None, adv[:4])[3]]
+
+    want = calls()
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work():
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(25):
+                got = calls()
+                s.synchronize()
+                if not all(torch.equal(x, y) for x, y in zip(got, want)):
+                    wrong.append(1)
+                del got
+
+    threads = [threading.Thread(target=work) for _ in range(3)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
