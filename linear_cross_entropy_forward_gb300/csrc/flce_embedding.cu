@@ -304,7 +304,9 @@ constexpr int kSumWarps = kSumThreads / 32;
 constexpr int kFillRows = 64;  // table rows per filling block
 constexpr int kRing = 16;      // rows of a warp's slab in flight or in use
 constexpr int kGroup = 4;      // rows per asynchronous copy group
-constexpr int kLong = 8;       // units beyond its head from which a block joins a run
+// Units beyond its head from which a block joins a run, not a warp: with 2, 8 and 30 the
+// gradient of 65536 tokens of 4096 columns took 198, 187 and 189 us, of 16384 45.8, 43.6, 45.3.
+constexpr int kLong = 8;
 
 struct SumArgs {
   const uint2* kp;  // sorted (key, token)

@@ -228,29 +228,27 @@ __global__ void __launch_bounds__(kSeqThreads, 1) policy_kernel(PolicyArgs a) {
     // ---- sums of the sequences
     unsigned long long my_tokens = 0;
     unsigned int my_live = 0, my_seqs = 0;
-    for (int64_t i = warp; i < q.B; i += warps) {
+    const SeqShare share(q, q.B);
+    for (int64_t i = share.first; i < q.B; i += share.stride) {
       int first, last;
       seq_pieces(q, i, first, last);
       Pair f[5] = {};
-      int c[3] = {0, 0, 0};
-      long long n = 0;
-      for (int u = first + lane; u < last; u += 32) {
+      long long c[3] = {0, 0, 0};
+      for (int u = first + share.offset; u < last; u += share.step) {
         const PolicyPiece r = a.piece[u];
         f[0] = f[0] + r.pg;
         f[1] = f[1] + r.kl;
         f[2] = f[2] + r.ent;
         f[3] = f[3] + r.old_kl;
         f[4] = f[4] + r.d;
-        n += r.n;
+        c[0] += r.n;
         c[1] += r.clipped;
         c[2] += r.dual;
       }
-      warp_sums(f);
-      n = warp_sum(n);
-      c[1] = warp_sum(c[1]);
-      c[2] = warp_sum(c[2]);
-      if (lane == 0) {
-        PolicySeq o{f[0], f[1], f[2], f[3], n, c[1], c[2], 0.0f, 0.0f};
+      share.sum(f, c);
+      const long long n = c[0];
+      if (share.writes()) {
+        PolicySeq o{f[0], f[1], f[2], f[3], n, c[1], c[2], 0.0f};
         if (by_seq && n > 0) {
           // the mean as a pair again: the quotient, and the quotient of what it leaves
           const float fn = static_cast<float>(n);
@@ -266,9 +264,11 @@ __global__ void __launch_bounds__(kSeqThreads, 1) policy_kernel(PolicyArgs a) {
         }
         a.seq[i] = o;
       }
-      my_tokens += n;
-      my_live += n > 0;
-      ++my_seqs;
+      if (share.counts()) {
+        my_tokens += n;
+        my_live += n > 0;
+        ++my_seqs;
+      }
     }
     meet_sequences(q, a.totals, my_tokens, my_live, my_seqs, static_cast<unsigned int>(q.B), a.err);
 

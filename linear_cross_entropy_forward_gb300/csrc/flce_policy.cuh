@@ -11,9 +11,8 @@ namespace flce {
 struct PolicySeq {
   Pair pg, kl, ent, old_kl;
   long long n;
-  int clipped, dual;
+  long long clipped, dual;
   float coef;  // d(loss)/d(mean log-ratio) before the weight (sequence ratios only)
-  float pad;
 };
 
 // A piece's sums.

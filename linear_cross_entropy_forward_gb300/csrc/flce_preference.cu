@@ -123,7 +123,8 @@ __global__ void __launch_bounds__(kSeqThreads, 1) preference_kernel(PrefArgs a) 
 
   const int64_t pairs = q.B / 2;
   unsigned int my_live = 0, my_pairs = 0;
-  for (int64_t i = warp; i < pairs; i += warps) {
+  const SeqShare share(q, pairs);
+  for (int64_t i = share.first; i < pairs; i += share.stride) {
     int64_t id[2];
     Pair score[2] = {}, like{};
     long long n[2] = {0, 0};
@@ -134,21 +135,21 @@ __global__ void __launch_bounds__(kSeqThreads, 1) preference_kernel(PrefArgs a) 
       int first, last;
       seq_pieces(q, id[side], first, last);
       Pair f[2] = {};
-      long long c = 0;
-      for (int u = first + lane; u < last; u += 32) {
+      long long c[1] = {0};
+      for (int u = first + share.offset; u < last; u += share.step) {
         const PrefPiece r = a.piece[u];
         f[0] = f[0] + r.score;
         f[1] = f[1] + r.like;
-        c += r.n;
+        c[0] += r.n;
       }
-      warp_sums(f);
+      share.sum(f, c);
       score[1] = side == 1 ? f[0] : score[1];
       score[0] = f[0];
       like = f[1];
-      n[1] = side == 1 ? warp_sum(c) : n[1];
-      n[0] = side == 1 ? 0 : warp_sum(c);
+      n[1] = side == 1 ? c[0] : n[1];
+      n[0] = c[0];
     }
-    if (lane == 0) {
+    if (share.writes()) {
       const float per[2] = {n[0] > 0 ? 1.0f / static_cast<float>(n[0]) : 0.0f,
                             n[1] > 0 ? 1.0f / static_cast<float>(n[1]) : 0.0f};
       for (int side = 0; side < 2; ++side) {
@@ -176,8 +177,10 @@ __global__ void __launch_bounds__(kSeqThreads, 1) preference_kernel(PrefArgs a) 
         a.rewards[id[1]] = a.beta * score[1].value();
       }
     }
-    my_live += n[0] > 0 && n[1] > 0;
-    ++my_pairs;
+    if (share.counts()) {
+      my_live += n[0] > 0 && n[1] > 0;
+      ++my_pairs;
+    }
   }
   meet_sequences(q, a.totals, 0, my_live, my_pairs, static_cast<unsigned int>(pairs), a.err);
 

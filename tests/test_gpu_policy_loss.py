@@ -518,3 +518,9 @@ def test_more_tokens_than_warps_keep(F, ratio):
     """Beyond a piece per warp of the GPU: kept gradients and recomputed ones in one launch."""
     run(F, [700000, 5, 900000, 30000], seed=97, dtype="bf16",
         kw=dict(KW, ratio=ratio, aggregate="seq_mean_token_mean"))
+
+
+@pytest.mark.parametrize("ratio", ["token", "sequence"])
+def test_few_long_sequences(F, ratio):
+    """Sequences whose sums a block adds up."""
+    run(F, [200000, 0, 150001], seed=99, kw=dict(KW, ratio=ratio, aggregate="seq_mean_token_mean"))

@@ -260,3 +260,10 @@ def test_other_stream_graph_and_repeats(F):
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(x, y) for x, y in zip(want, cap))
+
+
+def test_few_long_pairs(F):
+    """Pairs whose sums a block adds up."""
+    for pairs in ("halves", "interleaved"):
+        run(F, [200000, 90000, 150001, 300000], seed=12, kw=dict(pairs=pairs, beta=0.01, nll_coef=0.1))
+        run(F, [400000, 0], seed=13, ref="scores", kw=dict(pairs=pairs, beta=0.01))
