@@ -47,14 +47,16 @@ __device__ __forceinline__ float clamp_ratio(float h) {
 }
 
 struct Ratio {
-  float value;  // the objective is value * A
+  float value, low;  // the objective is (value + low) * A
   bool live;    // whether it moves with d
   bool clipped, dual;
 };
 
-// The clipped ratio of the log-ratio h + l, r = exp(h clamped).
-__device__ __forceinline__ Ratio clip_ratio(const PolicyArgs& a, float h, float l, float r,
-                                            float adv) {
+// The clipped ratio of the log-ratio h + l; e = exp(hc), k = e - 1 - hc of the clamped hc.
+// Near 1 the ratio is 1 + (hc + k), more exact than e: where the objective's terms cancel,
+// its last bits are what the loss is made of.
+__device__ __forceinline__ Ratio clip_ratio(const PolicyArgs& a, float h, float l, float hc,
+                                            float e, float k, float adv) {
   // above the upper border where A > 0, below the lower where A < 0
   const bool up = adv > 0.0f, down = adv < 0.0f;
   Ratio o;
@@ -62,7 +64,20 @@ __device__ __forceinline__ Ratio clip_ratio(const PolicyArgs& a, float h, float 
                                          up ? a.hi_l : -a.lo_l);
   o.dual = false;
   if (a.r_dual != 0.0f) o.dual = down && pair_above(h, l, a.dual_h, a.dual_l);
-  o.value = o.clipped ? (up ? a.r_hi : a.r_lo) : o.dual ? a.r_dual : r;
+  o.value = e;
+  o.low = 0.0f;
+  if (fabsf(hc) < 0.5f) {
+    const float y = hc + k;
+    o.value = 1.0f + y;
+    o.low = y - (o.value - 1.0f) + l;
+  }
+  if (o.clipped) {
+    o.value = up ? a.r_hi : a.r_lo;
+    o.low = up ? a.r_hi_l : a.r_lo_l;
+  } else if (o.dual) {
+    o.value = a.r_dual;
+    o.low = a.r_dual_l;
+  }
   o.live = !(o.clipped || o.dual || fabsf(h) > kLogRatioLimit);
   return o;
 }
@@ -140,7 +155,8 @@ __global__ void __launch_bounds__(kSeqThreads, 1) policy_kernel(PolicyArgs a) {
       const bool vec_out = !(misfit(dlp_, a.dlp) | misfit(dent_, a.dent));
       float adv_seq = 0.0f;
       if (!a.adv_per_token && !by_seq && pc.len > 0) adv_seq = __ldg(adv_);
-      float f[5] = {0, 0, 0, 0, 0};
+      Pair f[3] = {};  // policy term, KL, log-ratio: terms of both signs
+      float pos[2] = {0, 0};  // entropy, KL to the old policy
       int c[3] = {0, 0, 0};
 #pragma unroll 1
       for (int g = 0; g < kGroups && g * kGroup4 < t1; ++g) {
@@ -170,17 +186,18 @@ __global__ void __launch_bounds__(kSeqThreads, 1) policy_kernel(PolicyArgs a) {
             const float x = a.lp_sign * lp[j];
             float h = 0.0f, l = 0.0f;
             if (a.old_lp) exact_diff(x, old[j], h, l);
-            const float hc = clamp_ratio(h), e = expf(hc);
+            const float hc = clamp_ratio(h), e = expf(hc), k = exp_m1_mx(hc, e);
             dl[j] = 0.0f;
             if (by_seq) {
-              if (counts) f[4] += h;
+              if (counts) f[2] = f[2] + h;
             } else {
               const float A = a.adv_per_token ? adv[j] : adv_seq;
-              const Ratio r = clip_ratio(a, h, l, e, A);
+              const Ratio r = clip_ratio(a, h, l, hc, e, k, A);
               const float ra = r.value * A;
               dl[j] = r.live ? -ra : 0.0f;
               if (counts) {
-                f[0] -= ra;
+                f[0] = f[0] + -ra;
+                f[0].l -= fmaf(r.value, A, -ra) + r.low * A;
                 c[1] += r.clipped;
                 c[2] += r.dual;
               }
@@ -188,12 +205,12 @@ __global__ void __launch_bounds__(kSeqThreads, 1) policy_kernel(PolicyArgs a) {
             if (a.ref) {
               float kl, dkl;
               kl_term(a.kl, x, ref[j], kl, dkl);
-              if (counts) f[1] += kl;
+              if (counts) f[1] = f[1] + kl;
               dl[j] = fmaf(a.kl_coef, dkl, dl[j]);
             }
             if (!grad && counts) {
-              f[3] += exp_m1_mx(hc, e);
-              f[2] += ent[j];
+              pos[1] += k;
+              pos[0] += ent[j];
             }
           }
           c[0] += __popc(on);
@@ -216,10 +233,10 @@ __global__ void __launch_bounds__(kSeqThreads, 1) policy_kernel(PolicyArgs a) {
         }
       }
       if (!grad) {
-        warp_sums(f);
+        warp_sums(f, pos);
 #pragma unroll
         for (int k = 0; k < 3; ++k) c[k] = warp_sum(c[k]);
-        if (lane == 0) a.piece[u] = {f[0], f[1], f[2], f[3], f[4], c[0], c[1], c[2]};
+        if (lane == 0) a.piece[u] = {f[0], f[1], f[2], pos[0], pos[1], c[0], c[1], c[2], 0};
       }
     }
     if (grad) break;
@@ -250,14 +267,13 @@ __global__ void __launch_bounds__(kSeqThreads, 1) policy_kernel(PolicyArgs a) {
       if (share.writes()) {
         PolicySeq o{f[0], f[1], f[2], f[3], n, c[1], c[2], 0.0f};
         if (by_seq && n > 0) {
-          // the mean as a pair again: the quotient, and the quotient of what it leaves
           const float fn = static_cast<float>(n);
-          const float h = f[4].value() / fn;
-          const float l = (fmaf(-h, fn, f[4].h) + f[4].l) / fn;
+          const Pair d = f[4] / fn;
           const float adv = __ldg(a.adv + i);
-          const Ratio r = clip_ratio(a, h, l, expf(clamp_ratio(h)), adv);
+          const float hc = clamp_ratio(d.h), e = expf(hc);
+          const Ratio r = clip_ratio(a, d.h, d.l, hc, e, exp_m1_mx(hc, e), adv);
           const float ra = r.value * adv;
-          o.pg = {-fn * ra, fmaf(-fn, ra, fn * ra)};
+          o.pg = Pair{-ra, -(fmaf(r.value, adv, -ra) + r.low * adv)} * fn;
           o.coef = r.live ? -ra : 0.0f;
           o.clipped = r.clipped;
           o.dual = r.dual;
@@ -281,9 +297,9 @@ __global__ void __launch_bounds__(kSeqThreads, 1) policy_kernel(PolicyArgs a) {
     if (first_block && want_loss) {
       for (int64_t i = threadIdx.x; i < q.B; i += kSeqThreads) {
         const PolicySeq& r = a.seq[i];
-        const float w = mean_seq && r.n > 0 ? 1.0f / static_cast<float>(r.n) : 1.0f;
-        f[0] = f[0] + Pair{w * r.pg.h, fmaf(w, r.pg.h, -(w * r.pg.h)) + w * r.pg.l};
-        f[1] = f[1] + w * (a.kl_coef * r.kl.value() - a.ent_coef * r.ent.value());
+        const float n = mean_seq && r.n > 0 ? static_cast<float>(r.n) : 1.0f;
+        f[0] = f[0] + r.pg / n;
+        f[1] = f[1] + (r.kl * a.kl_coef + r.ent * -a.ent_coef) / n;
         f[2] = f[2] + r.kl;
         f[3] = f[3] + r.ent;
         f[4] = f[4] + r.old_kl;
@@ -306,7 +322,7 @@ __global__ void __launch_bounds__(kSeqThreads, 1) policy_kernel(PolicyArgs a) {
         if (!ok) atomicOr(a.err, FLCE_DEVERR_SEQS);
         if (want_loss) {
           const float nan = __int_as_float(0x7fc00000);
-          a.loss[0] = ok ? w_all * (f[0] + f[1]).value() : nan;
+          a.loss[0] = ok ? ((f[0] + f[1]) * w_all).value() : nan;
           a.stats[0] = ok ? w_all * f[0].value() : nan;
           a.stats[1] = one_token * f[2].value();
           a.stats[2] = one_token * f[3].value();
@@ -391,9 +407,9 @@ int policy_args(const flce_policy_params* p, void* workspace, PolicyArgs* a) {
   split(std::log1p(p->clip_high), &a->hi_h, &a->hi_l);
   split(std::log1p(-p->clip_low), &a->lo_h, &a->lo_l);
   if (p->dual_clip != 0.0) split(std::log(p->dual_clip), &a->dual_h, &a->dual_l);
-  a->r_hi = static_cast<float>(1.0 + p->clip_high);
-  a->r_lo = static_cast<float>(1.0 - p->clip_low);
-  a->r_dual = static_cast<float>(p->dual_clip);
+  split(1.0 + p->clip_high, &a->r_hi, &a->r_hi_l);
+  split(1.0 - p->clip_low, &a->r_lo, &a->r_lo_l);
+  split(p->dual_clip, &a->r_dual, &a->r_dual_l);
   a->kl_coef = static_cast<float>(p->kl_coef);
   a->ent_coef = static_cast<float>(p->entropy_coef);
   a->scale = static_cast<float>(p->scale);

@@ -17,8 +17,9 @@ struct PolicySeq {
 
 // A piece's sums.
 struct PolicyPiece {
-  float pg, kl, ent, old_kl, d;
-  int n, clipped, dual;
+  Pair pg, kl, d;  // of both signs
+  float ent, old_kl;
+  int n, clipped, dual, pad;
 };
 
 // What a launch is for.
@@ -36,7 +37,8 @@ struct PolicyArgs {
   float lp_sign;  // -1: lp holds negative log-probabilities, as does the gradient
   // clipping borders of the log-ratio, as unevaluated sums of two floats
   float hi_h, hi_l, lo_h, lo_l, dual_h, dual_l;
-  float r_hi, r_lo, r_dual;  // the ratio beyond the borders; r_dual 0: no dual clip
+  // the ratio beyond the borders, as sums of two floats; r_dual 0: no dual clip
+  float r_hi, r_hi_l, r_lo, r_lo_l, r_dual, r_dual_l;
   float kl_coef, ent_coef;
   float scale;
   int kl, ratio, aggregate, what;

@@ -153,12 +153,7 @@ __global__ void __launch_bounds__(kSeqThreads, 1) preference_kernel(PrefArgs a) 
       const float per[2] = {n[0] > 0 ? 1.0f / static_cast<float>(n[0]) : 0.0f,
                             n[1] > 0 ? 1.0f / static_cast<float>(n[1]) : 0.0f};
       for (int side = 0; side < 2; ++side) {
-        if (a.norm) {
-          // a pair again: the quotient, and the quotient of what it leaves
-          const float fn = n[side] > 0 ? static_cast<float>(n[side]) : 1.0f;
-          const float x = score[side].value() / fn;
-          score[side] = {x, (fmaf(-x, fn, score[side].h) + score[side].l) / fn};
-        }
+        if (a.norm && n[side] > 0) score[side] = score[side] / static_cast<float>(n[side]);
         if (a.ref_scores) score[side] = score[side] + -__ldg(a.ref_scores + id[side]);
         if (n[side] == 0) score[side] = {};
       }

@@ -249,6 +249,15 @@ __device__ __forceinline__ Pair operator+(Pair a, Pair b) {
   return s;
 }
 __device__ __forceinline__ Pair operator-(Pair a) { return {-a.h, -a.l}; }
+__device__ __forceinline__ Pair operator*(Pair a, float s) {
+  const float x = __fmul_rn(a.h, s);
+  return {x, fmaf(a.h, s, -x) + a.l * s};
+}
+// The quotient, and the quotient of what it leaves.
+__device__ __forceinline__ Pair operator/(Pair a, float s) {
+  const float x = a.value() / s;
+  return {x, (fmaf(-x, s, a.h) + a.l) / s};
+}
 
 // Sums over a warp or a block.  Their loops stay rolled: a launch finds the instruction
 // caches cold, and with every SM fetching the same lines at once straight-line code cost
@@ -260,6 +269,19 @@ __device__ __forceinline__ void warp_sums(float (&v)[N]) {
   for (int o = 16; o > 0; o >>= 1) {
 #pragma unroll
     for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(~0u, v[k], o);
+  }
+}
+
+// Pairs and floats in one loop.
+template <int N, int M>
+__device__ __forceinline__ void warp_sums(Pair (&p)[N], float (&v)[M]) {
+#pragma unroll 1
+  for (int o = 16; o > 0; o >>= 1) {
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      p[k] = p[k] + Pair{__shfl_xor_sync(~0u, p[k].h, o), __shfl_xor_sync(~0u, p[k].l, o)};
+#pragma unroll
+    for (int k = 0; k < M; ++k) v[k] += __shfl_xor_sync(~0u, v[k], o);
   }
 }
 
