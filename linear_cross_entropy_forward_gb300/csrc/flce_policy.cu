@@ -34,11 +34,12 @@ __device__ __forceinline__ bool pair_above(float h, float l, float bh, float bl)
   return __fadd_rn(__fadd_rn(h, -bh), __fadd_rn(l, -bl)) > 0.0f;
 }
 
-// a - b as an unevaluated sum h + l (exact).
+// a - b as an unevaluated sum h + l (exact; an infinite one is h alone).
 __device__ __forceinline__ void exact_diff(float a, float b, float& h, float& l) {
   h = __fadd_rn(a, -b);
   const float z = __fadd_rn(h, -a);
   l = __fadd_rn(__fadd_rn(a, -__fadd_rn(h, -z)), __fadd_rn(-b, -z));
+  if (!(fabsf(h) <= 3.4028235e38f)) l = 0.0f;
 }
 
 // A NaN stays one (fmaxf alone would drop it).

@@ -256,7 +256,7 @@ __device__ __forceinline__ Pair operator*(Pair a, float s) {
 // The quotient, and the quotient of what it leaves.
 __device__ __forceinline__ Pair operator/(Pair a, float s) {
   const float x = a.value() / s;
-  return {x, (fmaf(-x, s, a.h) + a.l) / s};
+  return {x, fabsf(x) <= 3.4028235e38f ? (fmaf(-x, s, a.h) + a.l) / s : 0.0f};
 }
 
 // Sums over a warp or a block.  Their loops stay rolled: a launch finds the instruction

@@ -524,3 +524,21 @@ def test_more_tokens_than_warps_keep(F, ratio):
 def test_few_long_sequences(F, ratio):
     """Sequences whose sums a block adds up."""
     run(F, [200000, 0, 150001], seed=99, kw=dict(KW, ratio=ratio, aggregate="seq_mean_token_mean"))
+
+
+@pytest.mark.parametrize("ratio", ["token", "sequence"])
+def test_counted_infinities_follow_the_formula(F, ratio):
+    """A token of probability zero under the policy, or under the old one: the clamped ratio where
+    it is not clipped, the border where it is, and no gradient either way."""
+    n = 40
+    lp = -torch.rand(n, generator=torch.Generator().manual_seed(4))
+    old = lp + 0.01
+    lp[3], lp[13], old[23], old[33] = -math.inf, -math.inf, -math.inf, -math.inf
+    adv = torch.tensor([1.0, -1.0, 1.0, -1.0])
+    cu = torch.tensor([0, 10, 20, 30, 40], dtype=torch.int32)
+    mask = torch.ones(n, dtype=torch.bool)
+    for kw in (dict(ratio=ratio), dict(ratio=ratio, dual_clip=3.0)):
+        got = F.flce_policy_loss(lp.cuda(), old.cuda(), adv.cuda(), cu_seqlens=cu.cuda(), **kw)
+        want = reference(lp.double(), old.double(), None, None, adv.repeat_interleave(10).double(),
+                         mask, [(i * 10, (i + 1) * 10) for i in range(4)], kw)
+        check(want, *got[:4], None, torch.float32)
