@@ -287,7 +287,8 @@ int flce_forward_noalloc(const flce_params* params, const void* hidden, const vo
 
 enum { FLCE_F32 = 0, FLCE_BF16 = 1, FLCE_F16 = 2 };
 
-/* A batch of B sequences of tokens.
+/* A batch of B sequences of tokens, B * S at most 2^38 (S, where packed), and about 2^31
+ * pieces of 256 tokens, no two sequences in one.
  *   padded (cu_kind 0): arrays [B, S], each with its own row stride ld_* in elements
  *     (>= 0; the last dimension dense);
  *   packed: arrays [S] (S tokens in all), sequence i owning [cu_seqlens[i],

@@ -34,6 +34,11 @@ constexpr int kGroup4 = 32 * kVec;  // a warp's
 constexpr int kGroups = 2;
 constexpr int kTile = kGroups * kGroup4;
 constexpr int kClusterBlocks = 8;   // the portable cluster size
+// Piece numbers are 32-bit, and a loop over them looks one step past the last: a step is a
+// grid's warps at most (or a block's threads, which are fewer).
+constexpr int kMaxBlocks = 1024;
+constexpr int64_t kMaxPieces = (int64_t(1) << 31) - 1 - int64_t(kMaxBlocks) * kSeqWarps;
+static_assert(kMaxBlocks * kSeqWarps >= kSeqThreads, "the longest step");
 
 // How the blocks of a grid meet between the phases of a kernel.
 enum : int { MEET_BLOCK = 0, MEET_CLUSTER = 1, MEET_GRID = 2 };
@@ -490,7 +495,7 @@ inline int make_seqs(const flce_seqs* a, Seqs* q) {
   q->mask_skip = a->cu_kind ? 0 : a->ld_mask - a->S;
   const int64_t per_row = a->S > 0 ? (a->S + kTile - 1) / kTile : 1;
   const int64_t pieces = a->cu_kind ? q->total / kTile + q->B + 1 : q->B * per_row;
-  if (pieces > lim - kTile) return FLCE_ERR_BAD_SHAPE;
+  if (pieces > kMaxPieces) return FLCE_ERR_BAD_SHAPE;
   q->per_row = a->cu_kind ? 0 : static_cast<int>(per_row);
   q->pieces = static_cast<int>(pieces);
   return FLCE_OK;
@@ -541,6 +546,7 @@ inline cudaError_t launch_seq(void (*kernel)(Args), const Args& args, int kept, 
   a.q.meet = blocks == 1 ? MEET_BLOCK : blocks <= kClusterBlocks ? MEET_CLUSTER : MEET_GRID;
   if (a.q.meet == MEET_CLUSTER) blocks = blocks <= 2 ? 2 : blocks <= 4 ? 4 : 8;
   if (blocks > sms) blocks = sms;
+  if (blocks > kMaxBlocks) blocks = kMaxBlocks;
   const int64_t rounds = (a.q.pieces + blocks * kSeqWarps - 1) / (blocks * kSeqWarps);
   a.q.kept = static_cast<int>(rounds < kKept ? rounds : kKept);
   const int smem = kept * kSeqWarps * a.q.kept;
