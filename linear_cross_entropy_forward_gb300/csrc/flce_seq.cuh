@@ -552,8 +552,10 @@ inline cudaError_t launch_seq(void (*kernel)(Args), const Args& args, int kept, 
   const int smem = kept * kSeqWarps * a.q.kept;
   const void* k = reinterpret_cast<const void*>(kernel);
   if (smem > 40 * 1024) {  // more than the default, beside the kernel's static arrays
-    const cudaError_t e =
-        cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // the most that any launch takes, not this one's: the limit is the kernel's own, and
+    // another thread may set it between here and the launch
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               kept * kSeqWarps * kKept);
     if (e != cudaSuccess) {
       cudaGetLastError();
       return e;
