@@ -295,8 +295,8 @@ enum { FLCE_F32 = 0, FLCE_BF16 = 1, FLCE_F16 = 2 };
  *     cu_seqlens[i + 1]), cu_seqlens [B + 1] int32 (cu_kind 1) or int64 (cu_kind 2), rising,
  *     inside [0, S].  Tokens before the first or behind the last sequence do not count
  *     and have zero gradients.  Offsets out of order or out of range are reported as
- *     FLCE_ERR_BAD_SHAPE by flce_status (or with validate), the loss is then NaN; no
- *     access leaves the arrays.
+ *     FLCE_ERR_BAD_SHAPE by flce_status (or with validate); the loss, its means or
+ *     rewards, and all gradients are then NaN, and no access leaves the arrays.
  *   mask_kind 0: every token counts; 1: bytes, non-zero counts; 2: int64 labels, those
  *     other than ignore_index count.  What does not count is not looked at: it may hold
  *     anything, infinities and NaN included.

@@ -126,8 +126,10 @@ __global__ void __launch_bounds__(kSeqThreads, 1) policy_kernel(PolicyArgs a) {
     // the first pass of a launch without the loss counts tokens, no more
     // (and a second pass of a sequence's ratio without a reference knows the gradient)
     const bool values = grad ? !by_seq || a.ref : want_loss || by_seq;
+    // (a weight of NaN, from bad offsets: no pieces to go by, the gradients are written already)
 #pragma unroll 1
-    for (int u = warp, round = 0; u < q.pieces; u += warps, ++round) {
+    for (int u = wg_all == wg_all ? warp : q.pieces, round = 0; u < q.pieces;
+         u += warps, ++round) {
       const Piece pc = find_piece(q, u);
       int t0 = 0, t1 = pc.len;
       float wg = wg_all, coef = 0.0f;
@@ -249,7 +251,7 @@ __global__ void __launch_bounds__(kSeqThreads, 1) policy_kernel(PolicyArgs a) {
     const SeqShare share(q, q.B);
     for (int64_t i = share.first; i < q.B; i += share.stride) {
       int first, last;
-      seq_pieces(q, i, first, last);
+      if (!seq_pieces(q, i, first, last)) atomicOr(&a.totals->live, kBadSeqs);
       Pair f[5] = {};
       long long c[3] = {0, 0, 0};
       for (int u = first + share.offset; u < last; u += share.step) {
@@ -310,42 +312,40 @@ __global__ void __launch_bounds__(kSeqThreads, 1) policy_kernel(PolicyArgs a) {
       block_counts(c);
       block_sums(f, q.B);
     }
-    const float one_token = tokens > 0 ? 1.0f / static_cast<float>(tokens) : 0.0f;
+    float one_token = tokens > 0 ? 1.0f / static_cast<float>(tokens) : 0.0f;
     const float one_seq = live > 0 ? 1.0f / static_cast<float>(live) : 0.0f;
-    const float w_all = a.aggregate == FLCE_AGG_TOKEN_MEAN ? one_token
-                        : a.aggregate == FLCE_AGG_SUM      ? a.scale
-                                                           : one_seq;
+    float w_all = a.aggregate == FLCE_AGG_TOKEN_MEAN ? one_token
+                  : a.aggregate == FLCE_AGG_SUM      ? a.scale
+                                                     : one_seq;
+    // no result where the offsets are bad: NaN in the place of loss, means and gradients
+    const bool bad = live & kBadSeqs;
+    if (bad) w_all = one_token = __int_as_float(0x7fc00000);
     wg_all = w_all;
     if (a.g_loss) g_up = __ldg(a.g_loss);
-    if (first_block) {
-      const bool ok = seqs_ok(q);
-      if (threadIdx.x == 0) {
-        if (!ok) atomicOr(a.err, FLCE_DEVERR_SEQS);
-        if (want_loss) {
-          const float nan = __int_as_float(0x7fc00000);
-          a.loss[0] = ok ? ((f[0] + f[1]) * w_all).value() : nan;
-          a.stats[0] = ok ? w_all * f[0].value() : nan;
-          a.stats[1] = one_token * f[2].value();
-          a.stats[2] = one_token * f[3].value();
-          a.stats[3] = one_token * f[4].value();
-          a.counts[0] = static_cast<long long>(tokens);
-          a.counts[1] = live;
-          a.counts[2] = c[0];
-          a.counts[3] = c[1];
-        }
-      }
+    if (first_block && threadIdx.x == 0 && bad) atomicOr(a.err, FLCE_DEVERR_SEQS);
+    if (first_block && want_loss && threadIdx.x == 0) {
+      a.loss[0] = ((f[0] + f[1]) * w_all).value();
+      a.stats[0] = w_all * f[0].value();
+      a.stats[1] = one_token * f[2].value();
+      a.stats[2] = one_token * f[3].value();
+      a.stats[3] = one_token * f[4].value();
+      a.counts[0] = static_cast<long long>(tokens);
+      a.counts[1] = live & ~kBadSeqs;
+      a.counts[2] = c[0];
+      a.counts[3] = c[1];
     }
     const int64_t thread = warp * int64_t(32) + lane, threads = warps * int64_t(32);
     if (a.lp_out)  // the head's tokens: a packed axis
       for (int64_t p = thread; p < q.total; p += threads)
         a.lp_out[p] = 0.0f + a.lp_sign * load_f(static_cast<const T*>(a.lp) + p);
     if (q.cu && (a.what & POLICY_GRAD)) {
-      // positions outside every sequence
-      const int64_t begin = seq_start(q, 0), end = seq_start(q, q.B);
+      // positions outside every sequence: all of them where the offsets are bad
+      const int64_t begin = bad ? a.g_end : seq_start(q, 0), end = seq_start(q, q.B);
+      const float fill = bad ? w_all : 0.0f;
       for (int64_t p = a.g_begin + thread; p < a.g_end; p += threads)
         if (p < begin || p >= end) {
-          if (a.dlp) store_f(static_cast<T*>(a.dlp) + p, 0.0f);
-          if (a.dent) store_f(static_cast<T*>(a.dent) + p, 0.0f);
+          if (a.dlp) store_f(static_cast<T*>(a.dlp) + p, fill);
+          if (a.dent) store_f(static_cast<T*>(a.dent) + p, fill);
         }
     }
   }

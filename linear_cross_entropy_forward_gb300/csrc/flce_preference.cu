@@ -75,6 +75,25 @@ __device__ void pair_value(const PrefArgs& a, float h, float& l, float& dh) {
   }
 }
 
+// In the place of the losses and the gradient where the sums mean nothing: NaN, and the reason.
+template <typename T>
+__device__ __noinline__ void poison(const PrefArgs& a, uint32_t why) {
+  const float nan = __int_as_float(0x7fc00000);
+  const int64_t thread = blockIdx.x * int64_t(kSeqThreads) + threadIdx.x;
+  const int64_t threads = gridDim.x * int64_t(kSeqThreads);
+  if (thread == 0) atomicOr(a.err, why);
+  if (a.want_loss) {
+    // by the threads that wrote them
+    const int64_t losses = a.reduction == FLCE_RED_NONE ? a.q.B / 2 : 1;
+    if (blockIdx.x == 0) {
+      for (int64_t i = threadIdx.x; i < losses; i += kSeqThreads) a.loss[i] = nan;
+      for (int64_t i = threadIdx.x; i < a.q.B; i += kSeqThreads) a.rewards[i] = nan;
+    }
+  }
+  if (a.dlp)
+    for (int64_t p = thread; p < a.q.total; p += threads) store_f(static_cast<T*>(a.dlp) + p, nan);
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kSeqThreads, 1) preference_kernel(PrefArgs a) {
   const Seqs& q = a.q;
@@ -133,7 +152,7 @@ __global__ void __launch_bounds__(kSeqThreads, 1) preference_kernel(PrefArgs a) 
 #pragma unroll 1
     for (int side = 1; side >= 0; --side) {
       int first, last;
-      seq_pieces(q, id[side], first, last);
+      if (!seq_pieces(q, id[side], first, last)) atomicOr(&a.totals->live, kBadSeqs);
       Pair f[2] = {};
       long long c[1] = {0};
       for (int u = first + share.offset; u < last; u += share.step) {
@@ -180,12 +199,10 @@ __global__ void __launch_bounds__(kSeqThreads, 1) preference_kernel(PrefArgs a) 
   meet_sequences(q, a.totals, 0, my_live, my_pairs, static_cast<unsigned int>(pairs), a.err);
 
   const unsigned int live = __ldcg(&a.totals->live);
-  const bool ok = blockIdx.x == 0 ? seqs_ok(q) : true;
-  const float nan = __int_as_float(0x7fc00000);
   Pair l[1] = {};
   if (blockIdx.x == 0 && a.want_loss) {
     for (int64_t i = threadIdx.x; i < pairs; i += kSeqThreads) {
-      const float v = ok ? a.pair_loss[i] : nan;
+      const float v = a.pair_loss[i];
       if (a.reduction == FLCE_RED_NONE) a.loss[i] = v;
       l[0] = l[0] + v;
     }
@@ -194,10 +211,11 @@ __global__ void __launch_bounds__(kSeqThreads, 1) preference_kernel(PrefArgs a) 
   const float scale =
       a.reduction == FLCE_RED_MEAN ? (live > 0 ? 1.0f / static_cast<float>(live) : 0.0f)
                                    : 1.0f;
-  if (blockIdx.x == 0 && threadIdx.x == 0) {
-    if (!ok) atomicOr(a.err, FLCE_DEVERR_SEQS);
-    if (a.want_loss && a.reduction != FLCE_RED_NONE)
-      a.loss[0] = ok ? l[0].value() * scale : nan;
+  if (blockIdx.x == 0 && threadIdx.x == 0 && a.want_loss && a.reduction != FLCE_RED_NONE)
+    a.loss[0] = l[0].value() * scale;
+  if (live & kBadSeqs) {
+    poison<T>(a, FLCE_DEVERR_SEQS);
+    return;
   }
   T* dlp_ = static_cast<T*>(a.dlp);
   if (!dlp_) return;

@@ -61,25 +61,31 @@ __device__ __forceinline__ int64_t clamp64(int64_t x, int64_t lo, int64_t hi) {
   return x < lo ? lo : (x > hi ? hi : x);
 }
 
+// What a packed batch says of the start of sequence i.
+__device__ __forceinline__ int64_t raw_start(const Seqs& q, int64_t i) {
+  return q.cu64 ? __ldg(static_cast<const long long*>(q.cu) + i)
+                : __ldg(static_cast<const int*>(q.cu) + i);
+}
+
 // Start of sequence i (i = B: the end of the last), inside [0, total] whatever the
 // array holds, so that no offset built from it leaves the arrays.
 __device__ __forceinline__ int64_t seq_start(const Seqs& q, int64_t i) {
-  if (!q.cu) return i * q.S;
-  const int64_t v = q.cu64 ? __ldg(static_cast<const long long*>(q.cu) + i)
-                           : __ldg(static_cast<const int*>(q.cu) + i);
-  return clamp64(v, 0, q.total);
+  return q.cu ? clamp64(raw_start(q, i), 0, q.total) : i * q.S;
 }
 
-// The pieces of sequence i: [first, last), the empty ones left out of a packed axis.
-__device__ __forceinline__ void seq_pieces(const Seqs& q, int64_t i, int& first, int& last) {
+// The pieces of sequence i: [first, last), the empty ones left out of a packed axis.  False
+// where its offsets are out of order or outside the axis: pieces may then cover a token twice
+// or not at all, and no result is to be had.
+__device__ __forceinline__ bool seq_pieces(const Seqs& q, int64_t i, int& first, int& last) {
   if (!q.cu) {
     first = static_cast<int>(i) * q.per_row;
     last = first + q.per_row;
-    return;
+    return true;
   }
   const int64_t a = seq_start(q, i), b = seq_start(q, i + 1);
   first = static_cast<int>(a / kTile + i);
   last = b > a ? static_cast<int>((b - 1) / kTile + i + 1) : first;
+  return a <= b && a == raw_start(q, i) && b == raw_start(q, i + 1);
 }
 
 struct Piece {
@@ -396,9 +402,12 @@ struct SeqShare {
 // first meeting.
 struct SeqTotals {
   unsigned long long tokens;  // counted tokens
-  unsigned int live;          // sequences (pairs) that count
+  unsigned int live;          // sequences (pairs) that count, and kBadSeqs
   unsigned int done;          // sequences (pairs) summed up
 };
+// Whether the offsets of a sequence are out of order or out of range: in a word that is read
+// anyway (a load of its own after the second meeting takes the losses 0.5 us).
+constexpr unsigned int kBadSeqs = 1u << 31;
 
 // The second meeting, by a warp that has summed up `mine` sequences.  Most blocks of a grid
 // have nothing left to do there: polled at full speed by all of them, the barrier's word kept
@@ -436,20 +445,6 @@ __device__ __forceinline__ void meet_sequences(const Seqs& q, SeqTotals* t,
     }
   }
   __syncthreads();
-}
-
-// Whether cu is in order and inside the axis (by a whole block).
-__device__ __forceinline__ bool seqs_ok(const Seqs& q) {
-  if (!q.cu) return true;
-  int bad = 0;
-  for (int64_t i = threadIdx.x; i < q.B; i += kSeqThreads) {
-    const int64_t a = q.cu64 ? __ldg(static_cast<const long long*>(q.cu) + i)
-                             : __ldg(static_cast<const int*>(q.cu) + i);
-    const int64_t b = q.cu64 ? __ldg(static_cast<const long long*>(q.cu) + i + 1)
-                             : __ldg(static_cast<const int*>(q.cu) + i + 1);
-    bad |= a < 0 || b < a || b > q.total;
-  }
-  return __syncthreads_or(bad) == 0;
 }
 
 // exp(x) - 1 - x given e = exp(x), |x| <= 20: near 0 the series x^2 (1/2! + x/3! + x^2/4! +

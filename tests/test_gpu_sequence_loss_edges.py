@@ -50,3 +50,50 @@ def test_threads_whose_launches_keep_different_amounts(F):
     for t in threads:
         t.join()
     assert not wrong, wrong
+
+
+BAD_OFFSETS = [[0, 5000, 100, 5100], [0, 50, 6000], [-5, 50, 5100], [5100, 0], [0, 2000, 1000, 5100]]
+
+
+def stale(*shape, dtype=torch.float32):
+    """Leaves 7s in memory that the next tensor of this size is likely to get."""
+    for _ in range(4):
+        torch.full(shape, 7.0, dtype=dtype, device="cuda")
+
+
+@pytest.mark.parametrize("cu", BAD_OFFSETS)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_offsets_out_of_order_leave_no_result(F, cu, dtype):
+    """Neither a finite one nor what the memory held before."""
+    T = 5100
+    x, ent = torch.zeros(T, dtype=dtype).cuda(), torch.ones(T, dtype=dtype).cuda()
+    c = torch.tensor(cu, dtype=torch.int32).cuda()
+    adv = torch.ones(len(cu) - 1).cuda()
+    stale(T, dtype=dtype)
+    loss, stats, _, dl, de = F.flce_policy_loss(x, x, adv, entropy=ent, entropy_coef=0.1, cu_seqlens=c)
+    for t in (loss, stats, dl, de):
+        assert bool(t.isnan().all())
+    g = torch.ones(1).cuda()
+    dl = F.flce_policy_loss(x, x, adv, cu_seqlens=c, g_loss=g, need_loss=False)[3]
+    assert bool(dl.isnan().all())
+    if len(adv) % 2 == 0:
+        stale(T, dtype=dtype)
+        for reduction in ("mean", "none"):
+            loss, rewards, dl = F.flce_preference_loss(x, cu_seqlens=c, reduction=reduction)
+            for t in (loss, rewards, dl):
+                assert bool(t.isnan().all())
+
+
+@pytest.mark.parametrize("chunk_n", [0, 512])
+def test_offsets_out_of_order_leave_no_result_of_the_head(F, chunk_n):
+    N, H, V = 1300, 64, 512
+    g = torch.Generator().manual_seed(3)
+    hidden = torch.randn(N, H, generator=g).to(torch.bfloat16).cuda()
+    weight = torch.randn(H, V, generator=g).to(torch.bfloat16).cuda()
+    labels = torch.randint(0, V, (N,), generator=g).cuda()
+    c = torch.tensor([0, 1300, 10, 1300], dtype=torch.int64).cuda()
+    loss, stats, _, _, _, dh, dw = F.flce_policy_forward_backward(
+        hidden, weight, labels, torch.zeros(N).cuda(), torch.ones(3).cuda(), cu_seqlens=c,
+        chunk_n=chunk_n)
+    for t in (loss, stats, dh, dw):
+        assert bool(t.isnan().all())
