@@ -218,8 +218,8 @@ int flce_combine_shards(const flce_params* params, const float* stats, int32_t n
 
 /* Synchronises `stream` and returns the device-side status recorded in the
  * workspace header by the last call that used this workspace (FLCE_OK,
- * FLCE_ERR_LABEL, FLCE_ERR_TIMEOUT or, with libflce_debug.so, FLCE_ERR_BOUNDS), or
- * FLCE_ERR_CUDA. */
+ * FLCE_ERR_LABEL, FLCE_ERR_BAD_SHAPE for cu_seqlens out of order, FLCE_ERR_TIMEOUT or, with
+ * libflce_debug.so, FLCE_ERR_BOUNDS), or FLCE_ERR_CUDA. */
 int flce_status(const void* workspace, void* stream);
 
 /* Number of kernels one call with these parameters enqueues (memsets not counted):
@@ -411,6 +411,18 @@ int flce_preference_loss(const flce_preference_params* params, const void* logp,
                          const void* ref_logp, const float* ref_scores, const float* g_loss,
                          float* loss, float* rewards, void* dlogp, void* workspace,
                          size_t ws_bytes, void* stream);
+
+/* Self-tests of the bounded wait between the blocks of these two losses: the call with one
+ * sequence (pair) awaited that never comes.  A batch of more than 256 pieces takes a grid whose
+ * blocks give up after 2 s: loss, means and the gradients of counted tokens are then NaN, and
+ * flce_status (or validate) reports FLCE_ERR_TIMEOUT.  Smaller batches do not wait that way. */
+int flce_selftest_policy_timeout(const flce_policy_params* params, const void* logp,
+                                 const float* advantages, float* loss, float* stats,
+                                 int64_t* counts, void* dlogp, void* workspace, size_t ws_bytes,
+                                 void* stream);
+int flce_selftest_preference_timeout(const flce_preference_params* params, const void* logp,
+                                     float* loss, float* rewards, void* dlogp, void* workspace,
+                                     size_t ws_bytes, void* stream);
 
 /* Embedding lookup out[n] = scale * weight[ids[n]] and its gradient. */
 typedef struct {

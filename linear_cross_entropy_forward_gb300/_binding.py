@@ -99,6 +99,7 @@ EXPORTED = ("flce_workspace_size", "flce_forward", "flce_backward", "flce_status
             "flce_policy_loss", "flce_policy_head_workspace_size",
             "flce_policy_forward_backward", "flce_preference_check_params",
             "flce_preference_workspace_size", "flce_preference_loss",
+            "flce_selftest_policy_timeout", "flce_selftest_preference_timeout",
             "flce_embedding_check_params", "flce_embedding_workspace_size", "flce_embedding",
             "flce_embedding_backward")
 
@@ -185,6 +186,11 @@ def _open(path: str) -> ctypes.CDLL:
     lib.flce_policy_forward_backward.restype = ctypes.c_int
     lib.flce_preference_loss.argtypes = [ctypes.POINTER(FlcePreferenceParams)] + [vp] * 8 + [sz, vp]
     lib.flce_preference_loss.restype = ctypes.c_int
+    lib.flce_selftest_policy_timeout.argtypes = [Q] + [vp] * 7 + [sz, vp]
+    lib.flce_selftest_policy_timeout.restype = ctypes.c_int
+    lib.flce_selftest_preference_timeout.argtypes = [ctypes.POINTER(FlcePreferenceParams)] \
+        + [vp] * 5 + [sz, vp]
+    lib.flce_selftest_preference_timeout.restype = ctypes.c_int
     E = ctypes.POINTER(FlceEmbeddingParams)
     lib.flce_embedding.argtypes = [E, vp, vp, vp, vp, sz, vp]
     lib.flce_embedding.restype = ctypes.c_int

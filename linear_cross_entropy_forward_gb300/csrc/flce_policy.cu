@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(kSeqThreads, 1) policy_kernel(PolicyArgs a) {
         ++my_seqs;
       }
     }
-    meet_sequences(q, a.totals, my_tokens, my_live, my_seqs, static_cast<unsigned int>(q.B), a.err);
+    const bool late = meet_sequences(q, a.totals, my_tokens, my_live, my_seqs, a.err);
 
     // ---- totals and the loss
     const bool first_block = blockIdx.x == 0;
@@ -317,11 +317,14 @@ __global__ void __launch_bounds__(kSeqThreads, 1) policy_kernel(PolicyArgs a) {
     float w_all = a.aggregate == FLCE_AGG_TOKEN_MEAN ? one_token
                   : a.aggregate == FLCE_AGG_SUM      ? a.scale
                                                      : one_seq;
-    // no result where the offsets are bad: NaN in the place of loss, means and gradients
-    const bool bad = live & kBadSeqs;
-    if (bad) w_all = one_token = __int_as_float(0x7fc00000);
-    wg_all = w_all;
     if (a.g_loss) g_up = __ldg(a.g_loss);
+    wg_all = w_all;
+    // no result where the offsets are bad, or the totals of a wait that ran out: NaN in the place
+    // of loss, means and gradients (with the latter, those of this block's pieces)
+    const bool bad = live & kBadSeqs;
+    if (bad || late) w_all = one_token = __int_as_float(0x7fc00000);
+    if (bad) wg_all = w_all;
+    if (late) g_up = w_all;
     if (first_block && threadIdx.x == 0 && bad) atomicOr(a.err, FLCE_DEVERR_SEQS);
     if (first_block && want_loss && threadIdx.x == 0) {
       a.loss[0] = ((f[0] + f[1]) * w_all).value();
@@ -452,11 +455,16 @@ size_t flce_policy_workspace_size(const flce_policy_params* p) {
   return policy_check(p) == FLCE_OK ? policy_workspace(p) : 0;
 }
 
-int flce_policy_loss(const flce_policy_params* p, const void* logp, const void* old_logp,
-                     const void* ref_logp, const void* entropy, const float* advantages,
-                     const float* g_loss, float* loss, float* stats, int64_t* counts,
-                     void* dlogp, void* dentropy, void* workspace, size_t ws_bytes,
-                     void* stream) {
+}  // extern "C"
+
+namespace {
+
+// `missing`: sequences that the second meeting waits for in vain (the self-test's).
+int policy_loss(const flce_policy_params* p, const void* logp, const void* old_logp,
+                const void* ref_logp, const void* entropy, const float* advantages,
+                const float* g_loss, float* loss, float* stats, int64_t* counts, void* dlogp,
+                void* dentropy, void* workspace, size_t ws_bytes, void* stream,
+                unsigned int missing) {
   int rc = policy_check(p);
   if (rc) return rc;
   if (!workspace || (loss == nullptr) != (stats == nullptr) ||
@@ -480,6 +488,7 @@ int flce_policy_loss(const flce_policy_params* p, const void* logp, const void* 
   if (ws_bytes < policy_workspace(p)) return FLCE_ERR_WS_TOO_SMALL;
   int sms;
   if ((rc = require_device(&sms))) return rc;
+  a.q.awaited += missing;
   a.lp = logp;
   a.old_lp = old_logp;
   a.ref = ref_logp;
@@ -495,6 +504,27 @@ int flce_policy_loss(const flce_policy_params* p, const void* logp, const void* 
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if ((rc = launch_policy(a, dt, sms, st))) return rc;
   return p->validate ? read_status(workspace, st) : FLCE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int flce_policy_loss(const flce_policy_params* p, const void* logp, const void* old_logp,
+                     const void* ref_logp, const void* entropy, const float* advantages,
+                     const float* g_loss, float* loss, float* stats, int64_t* counts,
+                     void* dlogp, void* dentropy, void* workspace, size_t ws_bytes,
+                     void* stream) {
+  return policy_loss(p, logp, old_logp, ref_logp, entropy, advantages, g_loss, loss, stats, counts,
+                     dlogp, dentropy, workspace, ws_bytes, stream, 0);
+}
+
+int flce_selftest_policy_timeout(const flce_policy_params* p, const void* logp,
+                                 const float* advantages, float* loss, float* stats,
+                                 int64_t* counts, void* dlogp, void* workspace, size_t ws_bytes,
+                                 void* stream) {
+  return policy_loss(p, logp, nullptr, nullptr, nullptr, advantages, nullptr, loss, stats, counts,
+                     dlogp, nullptr, workspace, ws_bytes, stream, 1);
 }
 
 }  // extern "C"

@@ -83,7 +83,7 @@ __device__ __noinline__ void poison(const PrefArgs& a, uint32_t why) {
   const int64_t threads = gridDim.x * int64_t(kSeqThreads);
   if (thread == 0) atomicOr(a.err, why);
   if (a.want_loss) {
-    // by the threads that wrote them
+    // the losses by the threads that wrote them; the rewards are there since the meeting
     const int64_t losses = a.reduction == FLCE_RED_NONE ? a.q.B / 2 : 1;
     if (blockIdx.x == 0) {
       for (int64_t i = threadIdx.x; i < losses; i += kSeqThreads) a.loss[i] = nan;
@@ -196,21 +196,23 @@ __global__ void __launch_bounds__(kSeqThreads, 1) preference_kernel(PrefArgs a) 
       ++my_pairs;
     }
   }
-  meet_sequences(q, a.totals, 0, my_live, my_pairs, static_cast<unsigned int>(pairs), a.err);
+  const bool late = meet_sequences(q, a.totals, 0, my_live, my_pairs, a.err);
+  const float nan = __int_as_float(0x7fc00000);
 
   const unsigned int live = __ldcg(&a.totals->live);
   Pair l[1] = {};
   if (blockIdx.x == 0 && a.want_loss) {
     for (int64_t i = threadIdx.x; i < pairs; i += kSeqThreads) {
-      const float v = a.pair_loss[i];
+      const float v = late ? nan : a.pair_loss[i];
       if (a.reduction == FLCE_RED_NONE) a.loss[i] = v;
       l[0] = l[0] + v;
     }
     block_sums(l, pairs);
   }
-  const float scale =
-      a.reduction == FLCE_RED_MEAN ? (live > 0 ? 1.0f / static_cast<float>(live) : 0.0f)
-                                   : 1.0f;
+  float scale = a.reduction == FLCE_RED_MEAN
+                    ? (live > 0 ? 1.0f / static_cast<float>(live) : 0.0f)
+                    : 1.0f;
+  if (late) scale = nan;  // totals of a wait that ran out: no loss, no gradients of this block's pieces
   if (blockIdx.x == 0 && threadIdx.x == 0 && a.want_loss && a.reduction != FLCE_RED_NONE)
     a.loss[0] = l[0].value() * scale;
   if (live & kBadSeqs) {
@@ -304,10 +306,15 @@ size_t flce_preference_workspace_size(const flce_preference_params* p) {
   return pref_check(p, &q) == FLCE_OK ? pref_layout(q).total : 0;
 }
 
-int flce_preference_loss(const flce_preference_params* p, const void* logp, const void* ref_logp,
-                         const float* ref_scores, const float* g_loss, float* loss,
-                         float* rewards, void* dlogp, void* workspace, size_t ws_bytes,
-                         void* stream) {
+}  // extern "C"
+
+namespace {
+
+// `missing`: pairs that the second meeting waits for in vain (the self-test's).
+int preference_loss(const flce_preference_params* p, const void* logp, const void* ref_logp,
+                    const float* ref_scores, const float* g_loss, float* loss, float* rewards,
+                    void* dlogp, void* workspace, size_t ws_bytes, void* stream,
+                    unsigned int missing) {
   PrefArgs a{};
   int rc = pref_check(p, &a.q);
   if (rc) return rc;
@@ -324,6 +331,7 @@ int flce_preference_loss(const flce_preference_params* p, const void* logp, cons
   if ((rc = require_device(&sms))) return rc;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const bool packed = p->seqs.cu_kind != 0;
+  a.q.awaited = static_cast<unsigned int>(a.q.B / 2) + missing;
   a.lp = logp;
   a.ref = ref_logp;
   a.lp_skip = packed ? 0 : p->ld_logp - p->seqs.S;
@@ -357,6 +365,25 @@ int flce_preference_loss(const flce_preference_params* p, const void* logp, cons
     e = launch_seq(preference_kernel<__half>, a, 0, sms, st);
   if (e != cudaSuccess) return FLCE_ERR_CUDA;
   return p->validate ? read_status(workspace, st) : FLCE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int flce_preference_loss(const flce_preference_params* p, const void* logp, const void* ref_logp,
+                         const float* ref_scores, const float* g_loss, float* loss,
+                         float* rewards, void* dlogp, void* workspace, size_t ws_bytes,
+                         void* stream) {
+  return preference_loss(p, logp, ref_logp, ref_scores, g_loss, loss, rewards, dlogp, workspace,
+                         ws_bytes, stream, 0);
+}
+
+int flce_selftest_preference_timeout(const flce_preference_params* p, const void* logp,
+                                     float* loss, float* rewards, void* dlogp, void* workspace,
+                                     size_t ws_bytes, void* stream) {
+  return preference_loss(p, logp, nullptr, nullptr, nullptr, loss, rewards, dlogp, workspace,
+                         ws_bytes, stream, 1);
 }
 
 }  // extern "C"

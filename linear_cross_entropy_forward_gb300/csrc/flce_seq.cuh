@@ -55,6 +55,7 @@ struct Seqs {
   int pieces;
   int meet;
   int kept;             // pieces per warp that shared memory holds values of
+  unsigned int awaited; // sequences (pairs) that the second meeting waits for
 };
 
 __device__ __forceinline__ int64_t clamp64(int64_t x, int64_t lo, int64_t hi) {
@@ -413,11 +414,11 @@ constexpr unsigned int kBadSeqs = 1u << 31;
 // have nothing left to do there: polled at full speed by all of them, the barrier's word kept
 // its part of L2 from the few that still read (their sums took 15000 cycles instead of
 // 1700).  So a grid's blocks wait for the count of finished sequences, and sleep between
-// looks.  A wait ends after 2 s at the latest, with the time-out bit set.
-__device__ __forceinline__ void meet_sequences(const Seqs& q, SeqTotals* t,
+// looks.  A wait ends after 2 s at the latest, with the time-out bit set; true (in the whole
+// block) says so: the totals are not to be trusted then.
+__device__ __forceinline__ bool meet_sequences(const Seqs& q, SeqTotals* t,
                                                unsigned long long tokens, unsigned int live,
-                                               unsigned int mine, unsigned int expected,
-                                               uint32_t* err) {
+                                               unsigned int mine, uint32_t* err) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0 && mine > 0) {
     if (tokens) atomicAdd(&t->tokens, tokens);
@@ -429,22 +430,24 @@ __device__ __forceinline__ void meet_sequences(const Seqs& q, SeqTotals* t,
   }
   if (q.meet != MEET_GRID) {
     meet(q.meet);
-    return;
+    return false;
   }
+  int late = 0;
   if (threadIdx.x == 0) {
     const uint64_t t0 = global_timer_ns();
     unsigned int n;
     while (true) {
       asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(n) : "l"(&t->done) : "memory");
-      if (n >= expected) break;
+      if (n >= q.awaited) break;
       if (global_timer_ns() - t0 > FLCE_WAIT_LIMIT_NS) {
         atomicOr(err, FLCE_DEVERR_TIMEOUT);
+        late = 1;
         break;
       }
       __nanosleep(100);
     }
   }
-  __syncthreads();
+  return __syncthreads_or(late) != 0;
 }
 
 // exp(x) - 1 - x given e = exp(x), |x| <= 20: near 0 the series x^2 (1/2! + x/3! + x^2/4! +
@@ -493,6 +496,7 @@ inline int make_seqs(const flce_seqs* a, Seqs* q) {
   if (pieces > kMaxPieces) return FLCE_ERR_BAD_SHAPE;
   q->per_row = a->cu_kind ? 0 : static_cast<int>(per_row);
   q->pieces = static_cast<int>(pieces);
+  q->awaited = static_cast<unsigned int>(a->B);
   return FLCE_OK;
 }
 
