@@ -192,7 +192,10 @@ __global__ void __launch_bounds__(kSeqThreads, 1) policy_kernel(PolicyArgs a) {
             const float hc = clamp_ratio(h), e = expf(hc), k = exp_m1_mx(hc, e);
             dl[j] = 0.0f;
             if (by_seq) {
-              if (counts) f[2] = f[2] + h;
+              if (counts) {
+                f[2] = f[2] + h;
+                f[2].l += l;
+              }
             } else {
               const float A = a.adv_per_token ? adv[j] : adv_seq;
               const Ratio r = clip_ratio(a, h, l, hc, e, k, A);

@@ -1,8 +1,12 @@
-"""Edges of the losses over sequences."""
+"""Edges of the losses over sequences.  Tolerances are those that test_gpu_policy_loss.py derives,
+where nothing else is said."""
+import math
 import threading
 
 import pytest
 import torch
+
+from test_gpu_policy_loss import check, reference
 
 pytestmark = pytest.mark.gpu
 
@@ -97,3 +101,27 @@ def test_offsets_out_of_order_leave_no_result_of_the_head(F, chunk_n):
         chunk_n=chunk_n)
     for t in (loss, stats, dh, dw):
         assert bool(t.isnan().all())
+
+
+@pytest.mark.parametrize("n", [1, 2, 4, 7, 300, 1025])
+def test_sequence_ratios_at_the_borders(F, n):
+    """Means of log-ratios that lie within rounding of a border: logp is the border's fp32 value,
+    old_logp the few bits that the border has beyond it, a little more or less."""
+    spans, lps, olds, advs = [], [], [], []
+    kw = dict(clip_low=0.2, clip_high=0.28, dual_clip=3.0, ratio="sequence")
+    for border, a in ((math.log1p(0.28), 1.0), (math.log1p(-0.2), -1.0), (math.log(3.0), -1.0)):
+        h = torch.tensor(border, dtype=torch.float32)
+        low = border - float(h)
+        for off in (0.5, 0.9, 1.1, 1.5, -0.5, 2.5):
+            spans.append((len(lps), len(lps) + n))
+            lps += [float(h)] * n
+            olds += [-low * off] * n
+            advs.append(a)
+    lp, old, adv = (torch.tensor(v, dtype=torch.float32) for v in (lps, olds, advs))
+    mask = torch.ones(len(lps), dtype=torch.bool)
+    cu = torch.arange(0, len(lps) + 1, n, dtype=torch.int32)
+    got = F.flce_policy_loss(lp.cuda(), old.cuda(), adv.cuda(), cu_seqlens=cu.cuda(), **kw)
+    want = reference(lp.double(), old.double(), None, None, adv.repeat_interleave(n).double(), mask,
+                     spans, kw)
+    assert 0 < want[2][2] and 0 < want[2][3]
+    check(want, *got[:4], None, torch.float32)
