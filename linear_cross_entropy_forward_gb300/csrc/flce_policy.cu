@@ -19,7 +19,8 @@
 //
 // Clipping tests compare d, not r, with log(1 + hi), log(1 - lo), log c: d is formed as
 // an exact sum of two floats and the borders are given the same way, so a token at a
-// border falls on the side that the exact difference falls on.
+// border falls on the side that the exact difference falls on.  (A border beyond +-20, which
+// the clamped d does not reach, clips nothing.)
 #include <cmath>
 
 #include "flce_policy.cuh"
@@ -357,10 +358,16 @@ __global__ void __launch_bounds__(kSeqThreads, 1) policy_kernel(PolicyArgs a) {
   }
 }
 
-// A border b as a sum of two floats (an infinite one as its high part alone).
+// A number as a sum of two floats (an infinite one as its high part alone).
 void split(double b, float* h, float* l) {
   *h = static_cast<float>(b);
   *l = std::isfinite(*h) ? static_cast<float>(b - *h) : 0.0f;
+}
+
+// A border of the log-ratio likewise.  The clamped log-ratio reaches no border at or beyond the
+// limit, whatever the log-ratio itself: such a border is put where nothing reaches it.
+void split_border(double b, float* h, float* l) {
+  split(std::fabs(b) < kLogRatioLimit ? b : std::copysign(HUGE_VAL, b), h, l);
 }
 
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -411,9 +418,9 @@ int policy_args(const flce_policy_params* p, void* workspace, PolicyArgs* a) {
   a->adv_skip = packed ? 0 : p->ld_adv - S;
   a->adv_per_token = p->adv_per_token;
   a->lp_sign = 1.0f;
-  split(std::log1p(p->clip_high), &a->hi_h, &a->hi_l);
-  split(std::log1p(-p->clip_low), &a->lo_h, &a->lo_l);
-  if (p->dual_clip != 0.0) split(std::log(p->dual_clip), &a->dual_h, &a->dual_l);
+  split_border(std::log1p(p->clip_high), &a->hi_h, &a->hi_l);
+  split_border(std::log1p(-p->clip_low), &a->lo_h, &a->lo_l);
+  if (p->dual_clip != 0.0) split_border(std::log(p->dual_clip), &a->dual_h, &a->dual_l);
   split(1.0 + p->clip_high, &a->r_hi, &a->r_hi_l);
   split(1.0 - p->clip_low, &a->r_lo, &a->r_lo_l);
   split(p->dual_clip, &a->r_dual, &a->r_dual_l);

@@ -125,3 +125,36 @@ def test_sequence_ratios_at_the_borders(F, n):
                      spans, kw)
     assert 0 < want[2][2] and 0 < want[2][3]
     check(want, *got[:4], None, torch.float32)
+
+
+@pytest.mark.parametrize("kw,a,d", [(dict(clip_high=1e9), 1.0, 25.0),
+                                    (dict(clip_low=1 - 1e-10), -1.0, -25.0),
+                                    (dict(dual_clip=1e9), -1.0, 25.0),
+                                    (dict(clip_high=1e9, dual_clip=2e9), -1.0, 25.0),
+                                    (dict(clip_high=4e8), 1.0, 25.0),
+                                    (dict(clip_low=1 - 1e-8), -1.0, -25.0),
+                                    (dict(dual_clip=4e8), -1.0, 25.0),
+                                    (dict(clip_high=math.inf), 1.0, math.inf)])
+@pytest.mark.parametrize("ratio", ["token", "sequence"])
+def test_borders_beyond_the_clamp(F, kw, a, d, ratio):
+    """The definition itself: r is the exponential of the clamped log-ratio, and the objective is
+    clipped where clip(r) makes it smaller.  A ratio of e^20 in fp32 is off by a few steps of
+    expf, as the tolerance of 2^-19 covers."""
+    lp = torch.tensor([0.0, d], dtype=torch.float32)
+    lo, hi, c = kw.get("clip_low", 0.2), kw.get("clip_high", 0.2), kw.get("dual_clip", 0.0)
+    want, clipped, dual = 0.0, 0, 0
+    for x in lp.tolist():
+        r = math.exp(max(-20.0, min(20.0, x)))
+        rc = max(1 - lo, min(1 + hi, r))
+        obj = min(r * a, rc * a)
+        clipped += rc * a < r * a
+        if c and a < 0 and c * a > obj:
+            obj, dual = c * a, dual + 1
+        want -= obj
+    cu = torch.tensor([0, 1, 2], dtype=torch.int32).cuda()
+    adv = torch.full((2,), a).cuda()
+    loss, _, counts, dl, _ = F.flce_policy_loss(lp.cuda(), torch.zeros(2).cuda(), adv, cu_seqlens=cu,
+                                                aggregate="sum", ratio=ratio, **kw)
+    assert abs(float(loss) - want) <= 2.0 ** -19 * abs(want)
+    assert counts.tolist() == [2, 2, clipped, dual]
+    assert dl.tolist() == [-a, 0.0]
