@@ -126,7 +126,7 @@ def _scalar_grad(g, n, index):
 def policy_params(logp, old_logp=None, advantages=None, ref_logp=None, entropy=None, mask=None,
                   cu_seqlens=None, clip_low=0.2, clip_high=0.2, dual_clip=0.0, kl_coef=0.0,
                   kl="k3", entropy_coef=0.0, ratio="token", aggregate="token_mean", scale=1.0,
-                  ignore_index=IGNORE_INDEX, validate=False):
+                  ignore_index=IGNORE_INDEX, validate=False, adv_per_token=None):
     """(FlcePolicyParams, device index) of a flce_policy_loss call, its tensors checked."""
     seqs, index, n_seq = _batch(logp, mask, cu_seqlens, ignore_index)
     shape, dt = logp.shape, logp.dtype
@@ -144,9 +144,12 @@ def policy_params(logp, old_logp=None, advantages=None, ref_logp=None, entropy=N
         raise ValueError("entropy_coef needs entropy")
     if not isinstance(advantages, torch.Tensor):
         raise TypeError("advantages must be a CUDA tensor")
-    # one per sequence, unless the shape is the tokens' and that reading is the only one
     per_seq = torch.Size((n_seq,))
-    per_token = advantages.shape != per_seq and ratio != "sequence"
+    if adv_per_token is None:
+        # one per sequence, unless the shape is the tokens' and that reading is the only one
+        per_token = advantages.shape != per_seq and ratio != "sequence"
+    else:
+        per_token = bool(adv_per_token)
     ld_adv = _rows(advantages, "advantages", torch.float32, shape if per_token else per_seq, index)
     if not per_token and not advantages.is_contiguous():
         raise ValueError("advantages must be contiguous")
@@ -187,7 +190,8 @@ def flce_policy_loss(logp, old_logp, advantages, ref_logp=None, entropy=None, ma
                      cu_seqlens=None, clip_low=0.2, clip_high=0.2, dual_clip=0.0, kl_coef=0.0,
                      kl="k3", entropy_coef=0.0, ratio="token", aggregate="token_mean", scale=1.0,
                      ignore_index=IGNORE_INDEX, g_loss=None, need_loss=True, need_grad=True,
-                     need_entropy_grad=True, validate=False, workspace=None, stream=None):
+                     need_entropy_grad=True, validate=False, workspace=None, stream=None,
+                     adv_per_token=None):
     """Clipped policy loss and its gradients, in one launch.
 
     Per counted token, with d = logp - old_logp, r = exp(d) and A its advantage:
@@ -196,7 +200,8 @@ def flce_policy_loss(logp, old_logp, advantages, ref_logp=None, entropy=None, ma
     d = 0 (the policy itself).  kl: 'k1' logp - ref, 'k2' its half square, 'k3'
     exp(-k1) - 1 + k1.  Log-ratios are clamped to +-20, with zero gradient beyond.
     ratio 'sequence' takes the mean of d over each sequence's counted tokens.
-    advantages: fp32 [B], one per sequence, or one per token (logp's shape).
+    advantages: fp32 [B], one per sequence, or one per token (logp's shape); adv_per_token says
+    which where a packed batch has as many tokens as sequences (None: one per sequence there).
     aggregate: 'token_mean', 'seq_mean_token_mean', 'seq_mean_token_sum', or 'sum' (times
     scale); sequences without a counted token do not count.
 
@@ -211,11 +216,11 @@ def flce_policy_loss(logp, old_logp, advantages, ref_logp=None, entropy=None, ma
         return _on(stream, flce_policy_loss, logp, old_logp, advantages, ref_logp, entropy, mask,
                    cu_seqlens, clip_low, clip_high, dual_clip, kl_coef, kl, entropy_coef, ratio,
                    aggregate, scale, ignore_index, g_loss, need_loss, need_grad,
-                   need_entropy_grad, validate, workspace)
+                   need_entropy_grad, validate, workspace, adv_per_token=adv_per_token)
     lib = B._lib or B.load_library()
     p, dev = policy_params(logp, old_logp, advantages, ref_logp, entropy, mask, cu_seqlens,
                            clip_low, clip_high, dual_clip, kl_coef, kl, entropy_coef, ratio,
-                           aggregate, scale, ignore_index, validate)
+                           aggregate, scale, ignore_index, validate, adv_per_token)
     if not need_loss and not need_grad:
         raise ValueError("neither the loss nor the gradients are wanted")
     _scalar_grad(g_loss, 1, dev)
@@ -288,7 +293,7 @@ class _PolicyLoss(torch.autograd.Function):
 def policy_loss(logp, old_logp, advantages, ref_logp=None, entropy=None, mask=None,
                 cu_seqlens=None, clip_low=0.2, clip_high=0.2, dual_clip=0.0, kl_coef=0.0, kl="k3",
                 entropy_coef=0.0, ratio="token", aggregate="token_mean", scale=1.0,
-                ignore_index=IGNORE_INDEX):
+                ignore_index=IGNORE_INDEX, adv_per_token=None):
     """loss, stats, counts = policy_loss(logp, old_logp, advantages, ...)
 
     flce_policy_loss as a differentiable function of logp and entropy (the other tensors are
@@ -302,7 +307,7 @@ def policy_loss(logp, old_logp, advantages, ref_logp=None, entropy=None, mask=No
     """
     kw = dict(clip_low=clip_low, clip_high=clip_high, dual_clip=dual_clip, kl_coef=kl_coef, kl=kl,
               entropy_coef=entropy_coef, ratio=ratio, aggregate=aggregate, scale=scale,
-              ignore_index=ignore_index)
+              ignore_index=ignore_index, adv_per_token=adv_per_token)
     return _PolicyLoss.apply(logp, entropy, old_logp, advantages, ref_logp, mask, cu_seqlens, kw)
 
 
@@ -311,12 +316,13 @@ def flce_policy_forward_backward(hidden, weight, labels, old_logp, advantages, r
                                  kl_coef=0.0, kl="k3", entropy_coef=0.0, ratio="token",
                                  aggregate="token_mean", scale=1.0, ignore_index=IGNORE_INDEX,
                                  softcap=0.0, weight_layout="hv", chunk_n=0, dhidden_fp32=False,
-                                 g_loss=None, validate=False, workspace=None, stream=None):
+                                 g_loss=None, validate=False, workspace=None, stream=None,
+                                 adv_per_token=None):
     """The policy loss on top of the LM head, with dhidden and dweight, in one call.
 
     hidden [N, H], weight and labels as in flce_forward_backward; old_logp, ref_logp fp32 [N];
-    advantages fp32 [B] or [N]; cu_seqlens [B + 1] cuts the N tokens into sequences (None:
-    one).  Tokens whose label is ignore_index do not count.  ratio 'sequence' needs all
+    advantages fp32 [B] or [N] (adv_per_token as in flce_policy_loss); cu_seqlens [B + 1] cuts
+    the N tokens into sequences (None: one).  Tokens whose label is ignore_index do not count.  ratio 'sequence' needs all
     tokens in one chunk (chunk_n >= N).
     Returns (loss [1], stats [4], counts [4], logp [N], entropy [N], dhidden, dweight);
     the gradients are times g_loss ([1] fp32, None: 1).
@@ -325,7 +331,7 @@ def flce_policy_forward_backward(hidden, weight, labels, old_logp, advantages, r
         return _on(stream, flce_policy_forward_backward, hidden, weight, labels, old_logp,
                    advantages, ref_logp, cu_seqlens, clip_low, clip_high, dual_clip, kl_coef, kl,
                    entropy_coef, ratio, aggregate, scale, ignore_index, softcap, weight_layout,
-                   chunk_n, dhidden_fp32, g_loss, validate, workspace)
+                   chunk_n, dhidden_fp32, g_loss, validate, workspace, adv_per_token=adv_per_token)
     lib = B._lib or B.load_library()
     N, H, V, wshape = B._dims(hidden, weight, weight_layout)
     B._need(hidden, "hidden", torch.bfloat16, (N, H))
@@ -338,7 +344,7 @@ def flce_policy_forward_backward(hidden, weight, labels, old_logp, advantages, r
     entropy = torch.empty(N, dtype=torch.float32, device=dev)
     q, index = policy_params(logp, old_logp, advantages, ref_logp, entropy, None, cu_seqlens,
                              clip_low, clip_high, dual_clip, kl_coef, kl, entropy_coef, ratio,
-                             aggregate, scale, ignore_index, validate)
+                             aggregate, scale, ignore_index, validate, adv_per_token)
     _scalar_grad(g_loss, 1, index)
     size = lib.flce_policy_head_workspace_size(ctypes.byref(p), ctypes.byref(q))
     if size == 0:
@@ -386,7 +392,7 @@ def linear_policy_loss(hidden, weight, labels, old_logp, advantages, ref_logp=No
                        cu_seqlens=None, clip_low=0.2, clip_high=0.2, dual_clip=0.0, kl_coef=0.0,
                        kl="k3", entropy_coef=0.0, ratio="token", aggregate="token_mean",
                        scale=1.0, ignore_index=IGNORE_INDEX, softcap=0.0, weight_layout="hv",
-                       chunk_n=0):
+                       chunk_n=0, adv_per_token=None):
     """loss, stats, counts, logp, entropy = linear_policy_loss(hidden, weight, labels, ...)
 
     policy_loss(-nll, ...) of linear_cross_entropy's per-token nll and entropy, with the
@@ -396,7 +402,7 @@ def linear_policy_loss(hidden, weight, labels, old_logp, advantages, ref_logp=No
     kw = dict(clip_low=clip_low, clip_high=clip_high, dual_clip=dual_clip, kl_coef=kl_coef, kl=kl,
               entropy_coef=entropy_coef, ratio=ratio, aggregate=aggregate, scale=scale,
               ignore_index=ignore_index, softcap=softcap, weight_layout=weight_layout,
-              chunk_n=chunk_n)
+              chunk_n=chunk_n, adv_per_token=adv_per_token)
     return _LinearPolicyLoss.apply(hidden, weight, labels, old_logp, advantages, ref_logp,
                                    cu_seqlens, kw)
 

@@ -6,7 +6,7 @@ import threading
 import pytest
 import torch
 
-from test_gpu_policy_loss import check, reference
+from test_gpu_policy_loss import check, make, reference
 
 pytestmark = pytest.mark.gpu
 
@@ -158,3 +158,42 @@ def test_borders_beyond_the_clamp(F, kw, a, d, ratio):
     assert abs(float(loss) - want) <= 2.0 ** -19 * abs(want)
     assert counts.tolist() == [2, 2, clipped, dual]
     assert dl.tolist() == [-a, 0.0]
+
+
+def test_advantages_of_as_many_sequences_as_tokens(F):
+    """A packed batch of three sequences, two of them empty, with three tokens: an advantage per
+    token has the shape of one per sequence, and the call says which it is."""
+    lp, old, ref, ent, adv, mask = make([0, 3, 0], 3, adv_token=True, mask_rate=1.0)
+    cu = torch.tensor([0, 0, 3, 3], dtype=torch.int32).cuda()
+    for per_token, a in ((True, adv), (False, adv[[1, 1, 1]]), (None, adv[[1, 1, 1]])):
+        got = F.flce_policy_loss(lp.cuda(), old.cuda(), adv.cuda(), cu_seqlens=cu,
+                                 adv_per_token=per_token)
+        want = reference(lp.double(), old.double(), None, None, a.double(), mask, [(0, 3)], {})
+        check(want, *got[:4], None, torch.float32)
+        x = lp.cuda().requires_grad_(True)
+        loss = F.policy_loss(x, old.cuda(), adv.cuda(), cu_seqlens=cu, adv_per_token=per_token)[0]
+        assert torch.equal(loss.detach(), got[0][0])
+    with pytest.raises(ValueError, match="advantages"):
+        F.flce_policy_loss(lp.cuda(), old.cuda(), adv.cuda()[:2], cu_seqlens=cu, adv_per_token=True)
+    with pytest.raises(ValueError, match="advantages"):
+        F.flce_policy_loss(lp.cuda().view(1, 3), None, adv.cuda().view(1, 3), adv_per_token=False)
+    with pytest.raises(F.FlceError):
+        F.flce_policy_loss(lp.cuda(), old.cuda(), adv.cuda(), cu_seqlens=cu, ratio="sequence",
+                           adv_per_token=True)
+
+
+def test_advantages_of_as_many_sequences_as_tokens_at_the_head(F):
+    g = torch.Generator().manual_seed(4)
+    hidden = torch.randn(3, 64, generator=g).to(torch.bfloat16).cuda()
+    weight = torch.randn(64, 512, generator=g).to(torch.bfloat16).cuda()
+    labels = torch.randint(0, 512, (3,), generator=g).cuda()
+    adv, old = torch.tensor([1.0, -2.0, 3.0]).cuda(), torch.zeros(3).cuda()
+    cu = torch.tensor([0, 0, 3, 3], dtype=torch.int32).cuda()
+    for per_token in (True, False, None):
+        got = F.flce_policy_forward_backward(hidden, weight, labels, old, adv, cu_seqlens=cu,
+                                             adv_per_token=per_token)
+        want = F.flce_policy_loss(got[3], old, adv, mask=labels, cu_seqlens=cu,
+                                  adv_per_token=per_token)
+        auto = F.linear_policy_loss(hidden, weight, labels, old, adv, cu_seqlens=cu,
+                                    adv_per_token=per_token)
+        assert torch.equal(got[0], want[0]) and torch.equal(auto[0], want[0][0])
