@@ -483,7 +483,9 @@ int policy_loss(const flce_policy_params* p, const void* logp, const void* old_l
   if (!loss && !dlogp && !dentropy) return FLCE_ERR_BAD_ARG;
   PolicyArgs a;
   if ((rc = policy_args(p, workspace, &a))) return rc;
-  if (a.q.total > 0 && (!logp || !advantages)) return FLCE_ERR_BAD_ARG;
+  // (no sequences, no advantages: an empty array has no address)
+  if (a.q.total > 0 && (!logp || (!advantages && (a.q.B > 0 || a.adv_per_token))))
+    return FLCE_ERR_BAD_ARG;
   if (a.q.total > 0 && ((p->kl_coef != 0.0 && !ref_logp) ||
                         ((p->entropy_coef != 0.0 || dentropy) && !entropy)))
     return FLCE_ERR_BAD_ARG;

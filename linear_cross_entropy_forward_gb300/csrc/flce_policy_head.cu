@@ -93,7 +93,8 @@ int flce_policy_forward_backward(const flce_params* p, const flce_policy_params*
   int rc = head_check(p, q);
   if (rc) return rc;
   if (!workspace || !loss || !stats || !counts) return FLCE_ERR_BAD_ARG;
-  if (p->N > 0 && (!advantages || !entropy || !logp || !labels || (q->kl_coef != 0.0 && !ref_logp)))
+  const bool no_adv = !advantages && (q->seqs.B > 0 || q->adv_per_token);
+  if (p->N > 0 && (no_adv || !entropy || !logp || !labels || (q->kl_coef != 0.0 && !ref_logp)))
     return FLCE_ERR_BAD_ARG;
   const uintptr_t f4 = reinterpret_cast<uintptr_t>(old_logp) |
                        reinterpret_cast<uintptr_t>(ref_logp) |

@@ -197,3 +197,21 @@ def test_advantages_of_as_many_sequences_as_tokens_at_the_head(F):
         auto = F.linear_policy_loss(hidden, weight, labels, old, adv, cu_seqlens=cu,
                                     adv_per_token=per_token)
         assert torch.equal(got[0], want[0]) and torch.equal(auto[0], want[0][0])
+
+
+def test_no_sequences_at_all(F):
+    """Tokens that no sequence owns: nothing counts."""
+    x = torch.zeros(300).cuda()
+    cu = torch.zeros(1, dtype=torch.int32).cuda()
+    loss, stats, counts, dl, de = F.flce_policy_loss(x, x, torch.empty(0).cuda(), entropy=x,
+                                                     entropy_coef=0.1, cu_seqlens=cu, validate=True)
+    assert float(loss) == 0 and stats.tolist() == [0] * 4 and counts.tolist() == [0] * 4
+    assert bool((dl == 0).all()) and bool((de == 0).all())
+    loss, rewards, dl = F.flce_preference_loss(x, cu_seqlens=cu, validate=True)
+    assert float(loss) == 0 and rewards.numel() == 0 and bool((dl == 0).all())
+    w = torch.zeros(64, 128, dtype=torch.bfloat16).cuda()
+    h = torch.ones(10, 64, dtype=torch.bfloat16).cuda()
+    got = F.flce_policy_forward_backward(h, w, torch.zeros(10, dtype=torch.int64).cuda(), x[:10],
+                                         torch.empty(0).cuda(), cu_seqlens=cu, validate=True)
+    assert float(got[0]) == 0 and got[2].tolist() == [0] * 4
+    assert bool((got[5] == 0).all()) and bool((got[6] == 0).all())
