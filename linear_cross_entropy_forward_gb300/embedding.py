@@ -17,7 +17,9 @@ from .losses import _DTYPES, _current_device, _on, _raw_stream, _workspace
 
 def embedding_params(N, H, V, scale=1.0, dtype=torch.bfloat16, grad_dtype=None, ids_int64=True,
                      accumulate=False, padding_idx=None, v_offset=0, v_total=0, validate=False):
-    """FlceEmbeddingParams; padding_idx None: none."""
+    """FlceEmbeddingParams; padding_idx None: none (the C struct's -1; no row counts from the end)."""
+    if padding_idx is not None and padding_idx < 0:
+        raise ValueError(f"padding_idx must be a row of the table or None, got {padding_idx}")
     try:
         dt, gdt = _DTYPES[dtype], _DTYPES[grad_dtype or dtype]
     except KeyError as e:
@@ -110,8 +112,8 @@ def flce_embedding_backward(dout, ids, V, scale=1.0, padding_idx=None, dweight=N
     dout's rows whose id is v, summed in fp32 in the tokens' order and rounded once.
 
     dweight: where it goes (dout's type, or fp32), a new tensor if None; accumulate=True adds
-    to it and touches no other row.  Ids equal to padding_idx have no gradient, nor have
-    those of other shards.
+    to it and touches no other row.  Ids equal to padding_idx (a row of the whole table) have
+    no gradient, nor have those of other shards.
     """
     if stream is not None:
         return _on(stream, flce_embedding_backward, dout, ids, V, scale, padding_idx, dweight,
@@ -152,9 +154,15 @@ def flce_embedding_backward(dout, ids, V, scale=1.0, padding_idx=None, dweight=N
 class _Embedding(torch.autograd.Function):
     @staticmethod
     def forward(ctx, ids, weight, scale, padding_idx, v_offset, v_total):
+        out = flce_embedding(ids, weight, scale, v_offset, v_total)
+        V, H = weight.shape
+        if padding_idx is not None:  # the lookup has no use for it: refused here, not in the backward
+            p = embedding_params(ids.numel(), H, V, scale, weight.dtype, None, True, False,
+                                 padding_idx, v_offset, v_total)
+            B._check(B.load_library().flce_embedding_check_params(ctypes.byref(p)))
         ctx.save_for_backward(ids)
-        ctx.cfg = (weight.shape[0], scale, padding_idx, v_offset, v_total)
-        return flce_embedding(ids, weight, scale, v_offset, v_total)
+        ctx.cfg = (V, scale, padding_idx, v_offset, v_total)
+        return out
 
     @staticmethod
     @once_differentiable

@@ -36,3 +36,13 @@ def test_piece_numbers_do_not_wrap(lib, pieces):
         want = 0 if n - 1 + 32 * 1024 <= INT_MAX - 1 else BAD_SHAPE
         assert lib.flce_policy_check_params(ctypes.byref(pol)) == want, n
         assert lib.flce_preference_check_params(ctypes.byref(pre)) == want, n
+
+
+def test_a_negative_padding_row_is_refused():
+    """The C struct's -1 means none; in Python that is None, and -1 is neither that nor the last
+    row."""
+    assert flce.embedding_params(4, 8, 10).padding_idx == -1
+    assert flce.embedding_params(4, 8, 10, padding_idx=9).padding_idx == 9
+    for padding in (-1, -2, -10):
+        with pytest.raises(ValueError, match="padding_idx"):
+            flce.embedding_params(4, 8, 10, padding_idx=padding)
