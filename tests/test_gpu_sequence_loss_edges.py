@@ -6,7 +6,7 @@ import threading
 import pytest
 import torch
 
-from test_gpu_policy_loss import check, make, reference
+from test_gpu_policy_loss import KW, check, make, reference, run
 
 pytestmark = pytest.mark.gpu
 
@@ -215,3 +215,15 @@ def test_no_sequences_at_all(F):
                                          torch.empty(0).cuda(), cu_seqlens=cu, validate=True)
     assert float(got[0]) == 0 and got[2].tolist() == [0] * 4
     assert bool((got[5] == 0).all()) and bool((got[6] == 0).all())
+
+
+@pytest.mark.parametrize("ratio", ["token", "sequence"])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("rounds", [3.4, 4.5])
+def test_several_pieces_per_warp(F, ratio, dtype, rounds):
+    """Three and four pieces per warp whose gradients are kept; beyond four, kept and recomputed
+    ones in one launch."""
+    per = round_tokens()
+    lens = [int(1.2 * per) + 7, 5, int((rounds - 1.3) * per) + 13, int(0.1 * per)]
+    run(F, lens, seed=int(10 * rounds), dtype=dtype,
+        kw=dict(KW, ratio=ratio, aggregate="seq_mean_token_mean"))
