@@ -282,7 +282,8 @@ int flce_forward_noalloc(const flce_params* params, const void* hidden, const vo
  * behind the head in a fine-tuning step.  Conventions as above; these calls use one
  * launch each for the losses (loss and gradients together), and three for the
  * embedding's gradient.  Their sums have a fixed order: results repeat bit for bit.
- * Grids of more than one block are cooperative launches.
+ * Grids of up to eight blocks are clusters, the losses' and the sort's larger ones cooperative
+ * launches.
  * ---------------------------------------------------------------------------------- */
 
 enum { FLCE_F32 = 0, FLCE_BF16 = 1, FLCE_F16 = 2 };

@@ -1,7 +1,7 @@
 // Embedding lookup with scaling, and its gradient by sorted tokens.
 //
 //   out[n] = scale * weight[ids[n]]
-//   dweight[v] (+)= scale * sum over { n : ids[n] = v }, in the order of n, of dout[n]
+//   dweight[v] (+)= scale * sum over { n : ids[n] = v } of dout[n]
 //
 // The gradient sorts the tokens by id first: a stable radix sort with digits of at most
 // 9 bits (18-bit ids: two passes), all passes in one launch: one block up to 512 tokens, a
@@ -11,7 +11,8 @@
 // lies inside the unit at once, rounded once.  A run that crosses a unit's border leaves
 // its part in fp32, and a last launch joins each such run's parts in order.  Frequent ids
 // (padding, the commonest words) are thus spread over many warps; no atomics add anything,
-// so results do not change from run to run.
+// so results do not change from run to run: rows are added in the order of n inside a unit, and
+// the units' sums in order (those of a run over more than nine units in 32 groups first).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

@@ -9,13 +9,19 @@
 //
 // One launch does all of it, loss and gradients:
 //   1  a warp per piece of at most 256 tokens: its sums;
-//   2  a warp per sequence: its pieces' sums, added in a fixed order in pairs of floats;
-//   3  the totals (each block for itself, over the sequences' records), the loss (block
-//      0), and the gradients: of a warp's first four pieces from what pass 1 left in shared
-//      memory, of further ones (beyond 5M tokens) by a second pass over the tokens,
+//   2  a warp per sequence (a block, where they are few and long): its pieces' sums, added in
+//      a fixed order in pairs of floats, and the counts of tokens and sequences by atomics;
+//   3  the loss (block 0, over the sequences' records) and the gradients: of a warp's first
+//      four pieces from what pass 1 left in shared memory, of further ones (beyond 5M tokens) by
+//      a second pass over the tokens,
 // between which the blocks meet.  The sums have a fixed order: results do not change from
 // run to run.  The two passes over the tokens share one body of code: a launch finds the
 // instruction cache cold, and a second copy would be fetched while nothing else runs.
+//
+// What bounds it: up to a piece per warp, latency (4 x 64 tokens 9.6 us in one block, 16 x 1024 20
+// in a cluster, 256 x 4096 22.8 in a grid, whose bytes need 4.5); beyond, that a warp loads a
+// piece, waits, computes and sums it before the next one's loads: 13 us for each further million
+// tokens (1024 x 4096 62 us, 29 % of the copy rate).
 //
 // Clipping tests compare d, not r, with log(1 + hi), log(1 - lo), log c: d is formed as
 // an exact sum of two floats and the borders are given the same way, so a token at a

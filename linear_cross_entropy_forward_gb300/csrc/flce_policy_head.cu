@@ -4,6 +4,12 @@
 // chunk's dlogits need; their weights depend on the labels alone, so no later chunk is
 // waited for.  With one chunk (the usual case) that launch also forms the loss; with
 // several, a last one does.
+//
+// The dlogits are bf16, as in flce_backward and flce_forward_backward: both gradient products
+// take them as tensor-core operands, and a second operand for their low bits would double the
+// products.  At 4096 x 4096 x 32000 the gradients are off by 2.3e-3 (2-norm, relative), by
+// 1.7e-3 where only the outputs are rounded.  The loss of the head's log-probabilities is within
+// 3e-7; these are themselves some 4e-6 too large there, from the tensor cores' accumulation.
 #include "flce_policy.cuh"
 
 namespace flce {

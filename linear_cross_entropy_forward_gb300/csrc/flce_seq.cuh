@@ -13,8 +13,10 @@
 // next tile or to the next sequence), so the first piece of sequence i is
 // f(i) = start(i) / kTile + i, which rises strictly, and piece u belongs to the last i with
 // f(i) <= u.  The numbers that no piece has (a sequence that ends at a cut) are empty
-// pieces.  One long sequence is spread over the GPU as well as many short ones, whatever
-// their lengths, and nothing about them is read on the host.
+// pieces.  The tokens of one long sequence are spread over the GPU as well as those of many,
+// and nothing about their lengths is read on the host.  What a piece costs beside its tokens (a
+// search of cu, the sums) is not: 100000 sequences of 10 tokens take the policy loss 585 us, as
+// many tokens in 256 sequences 23.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -240,8 +242,8 @@ __device__ __forceinline__ unsigned int tokens_in(int t, int t0, int t1) {
 
 // A sum as an unevaluated pair of floats (h + l, about 48 bits): the sums over pieces and
 // sequences, whose terms have both signs.  fp64 adds run at a small fraction of the
-// fp32 rate here: with fp64 sums the policy kernel took 58 us at a million tokens, with
-// pairs 44.
+// fp32 rate here: when the sums became pairs, the policy kernel went from 58 us at a million
+// tokens to 44.
 struct Pair {
   float h, l;
   __device__ __forceinline__ float value() const {
@@ -273,8 +275,8 @@ __device__ __forceinline__ Pair operator/(Pair a, float s) {
 
 // Sums over a warp or a block.  Their loops stay rolled: a launch finds the instruction
 // caches cold, and with every SM fetching the same lines at once straight-line code cost
-// some 60 cycles an instruction (the unrolled forms of these sums took 40000 cycles of the
-// policy kernel's 88000 at a million tokens).
+// some 60 cycles an instruction (when these loops were rolled, the sums' unrolled forms took 40000
+// of the policy kernel's 88000 cycles at a million tokens).
 template <int N>
 __device__ __forceinline__ void warp_sums(float (&v)[N]) {
 #pragma unroll 1
@@ -370,8 +372,10 @@ __device__ __forceinline__ void meet(int how) {
 
 // How the sums of `items` sequences (or pairs) are shared out: a warp each, or, where there
 // are few and long ones, a block each.  The policy loss of one sequence of a million tokens
-// takes 22 us with a block and 57 with a warp; the preference loss of a pair of 16384 tokens
-// each, whose 128 pieces a warp goes through four times, 11.0 with a block and 9.4 with a warp.
+// takes 27 us with a block and 64 with a warp, of four such 64 and 102; the preference loss of a
+// pair of 16384 tokens each, whose 128 pieces a warp goes through four times, 11.9 with a block
+// and 11.2 with a warp.  The rule looks at the average length: a sequence of a million tokens
+// beside 60 of 100 is a warp's, 66 us where a block would take 27.
 struct SeqShare {
   bool wide;
   int64_t first, stride;
@@ -529,11 +533,11 @@ inline cudaError_t launch_meeting(const void* kernel, void* args, int64_t blocks
 }
 
 // A warp per piece: one block where its warps suffice, else a cluster of at most eight
-// (whose hardware barrier is faster: the policy loss of 16 x 1024 tokens takes 14.6 us with
-// a cluster and 15.8 with a grid, of 64 x 1024 15.8 and 17.1), else a cooperative grid of at
+// (whose hardware barrier is faster: the policy loss of 16 x 1024 tokens takes 20.0 us with
+// a cluster and 20.9 with a grid, of 64 x 1024 21.2 and 22.2), else a cooperative grid of at
 // most one block per SM, whose warps take several pieces each.
 // `kept` bytes of dynamic shared memory per warp's piece, for at most kKept of them (the
-// policy loss of 4 x 1M tokens took 81 us with four pieces kept and 91 with one).
+// policy loss of 4 x 1M tokens takes 64 us with four pieces kept and 82 with one).
 constexpr int kKept = 4;
 
 template <typename Args>

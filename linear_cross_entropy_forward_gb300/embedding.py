@@ -109,7 +109,8 @@ def flce_embedding_backward(dout, ids, V, scale=1.0, padding_idx=None, dweight=N
                             accumulate=False, grad_dtype=None, v_offset=0, v_total=0,
                             validate=False, workspace=None, stream=None):
     """The gradient [V, H] of flce_embedding by weight: row v is scale times the sum of
-    dout's rows whose id is v, summed in fp32 in the tokens' order and rounded once.
+    dout's rows whose id is v, summed in fp32 in a fixed order (the tokens', in groups of up
+    to 32 that are then added) and rounded once.
 
     dweight: where it goes (dout's type, or fp32), a new tensor if None; accumulate=True adds
     to it and touches no other row.  Ids equal to padding_idx (a row of the whole table) have

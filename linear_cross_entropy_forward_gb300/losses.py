@@ -325,7 +325,8 @@ def flce_policy_forward_backward(hidden, weight, labels, old_logp, advantages, r
     the N tokens into sequences (None: one).  Tokens whose label is ignore_index do not count.  ratio 'sequence' needs all
     tokens in one chunk (chunk_n >= N).
     Returns (loss [1], stats [4], counts [4], logp [N], entropy [N], dhidden, dweight);
-    the gradients are times g_loss ([1] fp32, None: 1).
+    the gradients are times g_loss ([1] fp32, None: 1).  As in flce_forward_backward, the
+    gradients of the logits are rounded to bf16 before the products with weight and hidden.
     """
     if stream is not None:
         return _on(stream, flce_policy_forward_backward, hidden, weight, labels, old_logp,
@@ -368,7 +369,8 @@ def flce_policy_forward_backward(hidden, weight, labels, old_logp, advantages, r
 
 class _LinearPolicyLoss(torch.autograd.Function):
     """The gradients are formed in the forward, for an upstream gradient of 1, and scaled in
-    the backward (a copy: the saved ones serve another backward pass)."""
+    the backward (a copy: the saved ones serve another backward pass).  Scaled by anything but
+    a power of two, a bf16 gradient is rounded a second time, as with grad_in_forward."""
 
     @staticmethod
     def forward(ctx, hidden, weight, labels, old_logp, advantages, ref_logp, cu_seqlens, kw):
@@ -397,7 +399,9 @@ def linear_policy_loss(hidden, weight, labels, old_logp, advantages, ref_logp=No
 
     policy_loss(-nll, ...) of linear_cross_entropy's per-token nll and entropy, with the
     gradients by hidden and weight formed in the forward: the logits are computed once.
-    Differentiable by hidden and weight through loss alone.
+    Differentiable by hidden and weight through loss alone.  An upstream gradient that is no
+    power of two costs the bf16 gradients a second rounding (flce_policy_forward_backward's
+    g_loss does not).
     """
     kw = dict(clip_low=clip_low, clip_high=clip_high, dual_clip=dual_clip, kl_coef=kl_coef, kl=kl,
               entropy_coef=entropy_coef, ratio=ratio, aggregate=aggregate, scale=scale,
