@@ -455,6 +455,149 @@ int flce_embedding_backward(const flce_embedding_params* params, const void* dou
                             const void* ids, void* dweight, void* workspace, size_t ws_bytes,
                             void* stream);
 
+/* ------------------------------------------------------------------------------------
+ * What stands around the head in a rollout and behind it in a training step: a dense layer,
+ * the distribution that a sampler sees, and the optimizer.  Conventions as above.
+ * ---------------------------------------------------------------------------------- */
+
+enum {
+  FLCE_ACT_NONE = 0,
+  FLCE_ACT_RELU = 1,
+  FLCE_ACT_GELU = 2,      /* z Phi(z) */
+  FLCE_ACT_GELU_TANH = 3, /* z / 2 (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) */
+  FLCE_ACT_SILU = 4       /* z / (1 + e^-z) */
+};
+
+/* Dense layer  y[M,N] = act(z) + residual,  z = x[M,K] @ W + bias.
+ *   x, weight, bias: bf16; weight [K,N] (FLCE_WEIGHT_HV: N % 8 == 0) or [N,K] (FLCE_WEIGHT_VH);
+ *   K % 8 == 0.  residual and y: out_dtype, bf16 or fp32, sums in fp32, rounded once. */
+typedef struct {
+  int64_t M, N, K;
+  int32_t weight_layout;
+  int32_t activation;
+  int32_t out_dtype; /* FLCE_BF16 or FLCE_F32 */
+  int32_t validate;
+} flce_linear_params;
+
+int flce_linear_check_params(const flce_linear_params* params);
+/* backward 0: flce_linear, 1: flce_linear_backward */
+size_t flce_linear_workspace_size(const flce_linear_params* params, int backward);
+
+/* bias, residual: or NULL.  preact: [M,N] bf16, z for the backward, or NULL.  x, weight, y,
+ * residual and preact 16-byte aligned, bias 2-byte. */
+int flce_linear(const flce_linear_params* params, const void* x, const void* weight,
+                const void* bias, const void* residual, void* y, void* preact, void* workspace,
+                size_t ws_bytes, void* stream);
+
+/* Gradients by x [M,K], weight and bias, bf16, each or NULL (that by the residual is dout):
+ *   dz = dout act'(preact), in bf16;  dx = dz W^T,  dweight = x^T dz,  dbias = sum_m of the
+ *   unrounded dz, in fp32.  dout: out_dtype.  preact: or NULL without an activation.  x (weight) may
+ *   be NULL where dweight (dx) is. */
+int flce_linear_backward(const flce_linear_params* params, const void* dout, const void* x,
+                         const void* weight, const void* preact, void* dx, void* dweight,
+                         void* dbias, void* workspace, size_t ws_bytes, void* stream);
+
+/* Rows of logits as a sampler sees them, per row in fp32:
+ *   l = seen ? (l > 0 ? l / repetition : l * repetition) : l
+ *   l = l - frequency * n - presence * [n > 0] + the sum of its biases
+ *   l = -inf where not allowed;  z = l / temperature  (temperature 0: z = l)
+ * with n its occurrences among the row's generated tokens, seen whether it is among its prompt
+ * or generated tokens.  An array of flce_logits_rows takes the place of the value here. */
+typedef struct {
+  int64_t R, V, T;          /* rows, columns (<= 2^30), tokens per row (< 2^30) */
+  int64_t ld_logits, ld_out, ld_tokens;      /* row strides in elements */
+  int64_t n_bias, ld_bias_ids, ld_bias_values; /* entries of a row's list (<= 2048) */
+  int64_t ld_allowed;       /* in bytes (mask_kind 1) or words (2); 0: one mask for all rows */
+  int64_t ignore_index;
+  double repetition_penalty, frequency_penalty, presence_penalty, temperature;
+  int32_t dtype, out_dtype; /* of the logits, and of z: dtype or FLCE_F32 */
+  int32_t tokens_int64, lens_int64, bias_int64; /* 1: int64, 0: int32 */
+  int32_t mask_kind;        /* 0: none, 1: bytes, non-zero allows, 2: bits, v % 32 of word v / 32 */
+  int32_t validate;
+} flce_logits_params;
+
+/* Of each row, or NULL.  tokens [R, T]: the first lengths[r] count (NULL: all), of them the first
+ * prompt_lens[r] are the prompt's (NULL: none).  Tokens and bias ids outside [0, V) are left out;
+ * an id that comes twice in a list has both biases. */
+typedef struct {
+  const void* tokens;
+  const void* prompt_lens;
+  const void* lengths;
+  const float* repetition_penalty;
+  const float* frequency_penalty;
+  const float* presence_penalty;
+  const float* temperature;
+  const void* bias_ids;
+  const float* bias_values;
+  const void* allowed;
+} flce_logits_rows;
+
+int flce_logits_check_params(const flce_logits_params* params);
+
+/* out [R, V]: z (may be logits itself where the types are the same); lse [R]; logp [R], of
+ * labels[r] under softmax(z); entropy [R].  Each or NULL, one at least.  A row whose label is
+ * ignore_index has logp = entropy = 0, one whose label is outside [0, V) NaN, reported as
+ * FLCE_ERR_LABEL with validate, which needs a workspace of 256 bytes (else NULL, 0); labels NULL:
+ * every row counts.  A row with nothing left has lse = logp = -inf and entropy 0; one with a NaN or
+ * +inf left, NaN. */
+int flce_logits(const flce_logits_params* params, const flce_logits_rows* rows,
+                const void* logits, const int64_t* labels, void* out, float* lse, float* logp,
+                float* entropy, void* workspace, size_t ws_bytes, void* stream);
+
+/* dlogits [R, V] (out_dtype, ld_out) = g_logp * d logp / d logits + g_entropy * d entropy / d logits
+ * (NULL: 0), with lse and entropy (or NULL without g_entropy) of flce_logits.  Rows that are
+ * ignored or have nothing left get zeros. */
+int flce_logits_backward(const flce_logits_params* params, const flce_logits_rows* rows,
+                         const void* logits, const int64_t* labels, const float* lse,
+                         const float* entropy, const float* g_logp, const float* g_entropy,
+                         void* dlogits, void* workspace, size_t ws_bytes, void* stream);
+
+/* AdamW over many tensors.  With c = grad_scale * min(1, max_norm / (norm + 1e-6)) (max_norm 0:
+ * no clipping), t the steps so far plus one:
+ *   g = c * grad;  m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2
+ *   p = p (1 - lr weight_decay) - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps)
+ * States, of numel elements for all tensors together, each tensor's at a multiple of 128:
+ *   state_bits 32: m and v in fp32;
+ *   state_bits 8: m and sqrt(v) as e4m3 codes with an fp32 scale per 128 elements, the largest of
+ *     them / 448 (zero where that is below 2^-110).  A magnitude in units of the scale goes to a
+ *     neighbouring code, up where the upper 20 of 32 random bits, a mixing of (seed, t, element),
+ *     carry; a root that isn't 0 is not rounded to 0.
+ * master: fp32 weights in the same layout, or NULL: the parameters themselves are updated, and
+ * rounded, in their own type.  Elements of the states behind a tensor's last stay 0. */
+typedef struct {
+  void* param;
+  const void* grad;   /* dense, as param */
+  int64_t n, offset;  /* elements; where its states begin (a multiple of 128) */
+  float weight_decay;
+  int32_t dtype;      /* of param */
+  int32_t grad_dtype; /* dtype or FLCE_F32 */
+} flce_adamw_tensor;
+
+typedef struct {
+  int64_t n_tensors, numel;
+  double lr, beta1, beta2, eps, grad_scale, max_norm;
+  int32_t state_bits;
+  uint32_t seed;
+  int32_t skip_nonfinite; /* a norm that is not finite: nothing changes, t neither */
+} flce_adamw_params;
+
+int flce_adamw_check_params(const flce_adamw_params* params);
+/* Of both calls below.  The first 256 bytes are zero before the first call that uses the
+ * workspace and after each. */
+size_t flce_adamw_workspace_size(const flce_adamw_params* params);
+
+/* norm [1] = 2-norm of grad_scale * (all gradients); `tensors` is read on the host. */
+int flce_grad_norm(const flce_adamw_params* params, const flce_adamw_tensor* tensors, float* norm,
+                   void* workspace, size_t ws_bytes, void* stream);
+
+/* exp_avg_sq: v, or the codes of sqrt(v).  lr: a device value in the place of params->lr, or
+ * NULL.  norm: of flce_grad_norm, where max_norm or skip_nonfinite asks for it.  step [1]: t,
+ * counted up by the call. */
+int flce_adamw_step(const flce_adamw_params* params, const flce_adamw_tensor* tensors,
+                    float* master, void* exp_avg, void* exp_avg_sq, float* exp_avg_scale,
+                    float* exp_rms_scale, const float* lr, const float* norm, int64_t* step,
+                    void* workspace, size_t ws_bytes, void* stream);
+
 /* Library version as MAJOR*10000 + MINOR*100 + PATCH. */
 int flce_version(void);
 

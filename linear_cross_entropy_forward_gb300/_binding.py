@@ -40,6 +40,46 @@ class FlceParams(ctypes.Structure):
                 ("dhidden_fp32", ctypes.c_int32)]
 
 
+class FlceLinearParams(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
+                ("weight_layout", ctypes.c_int32), ("activation", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32), ("validate", ctypes.c_int32)]
+
+
+class FlceLogitsParams(ctypes.Structure):
+    _fields_ = [("R", ctypes.c_int64), ("V", ctypes.c_int64), ("T", ctypes.c_int64),
+                ("ld_logits", ctypes.c_int64), ("ld_out", ctypes.c_int64),
+                ("ld_tokens", ctypes.c_int64), ("n_bias", ctypes.c_int64),
+                ("ld_bias_ids", ctypes.c_int64), ("ld_bias_values", ctypes.c_int64),
+                ("ld_allowed", ctypes.c_int64), ("ignore_index", ctypes.c_int64),
+                ("repetition_penalty", ctypes.c_double),
+                ("frequency_penalty", ctypes.c_double), ("presence_penalty", ctypes.c_double),
+                ("temperature", ctypes.c_double), ("dtype", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32), ("tokens_int64", ctypes.c_int32),
+                ("lens_int64", ctypes.c_int32), ("bias_int64", ctypes.c_int32),
+                ("mask_kind", ctypes.c_int32), ("validate", ctypes.c_int32)]
+
+
+class FlceLogitsRows(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_void_p) for name in
+                ("tokens", "prompt_lens", "lengths", "repetition_penalty", "frequency_penalty",
+                 "presence_penalty", "temperature", "bias_ids", "bias_values", "allowed")]
+
+
+class FlceAdamwTensor(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("offset", ctypes.c_int64), ("weight_decay", ctypes.c_float),
+                ("dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32)]
+
+
+class FlceAdamwParams(ctypes.Structure):
+    _fields_ = [("n_tensors", ctypes.c_int64), ("numel", ctypes.c_int64),
+                ("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("grad_scale", ctypes.c_double),
+                ("max_norm", ctypes.c_double), ("state_bits", ctypes.c_int32),
+                ("seed", ctypes.c_uint32), ("skip_nonfinite", ctypes.c_int32)]
+
+
 class FlceSeqs(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int64), ("S", ctypes.c_int64), ("cu_seqlens", ctypes.c_void_p),
                 ("mask", ctypes.c_void_p), ("ld_mask", ctypes.c_int64),
@@ -101,7 +141,10 @@ EXPORTED = ("flce_workspace_size", "flce_forward", "flce_backward", "flce_status
             "flce_preference_workspace_size", "flce_preference_loss",
             "flce_selftest_policy_timeout", "flce_selftest_preference_timeout",
             "flce_embedding_check_params", "flce_embedding_workspace_size", "flce_embedding",
-            "flce_embedding_backward")
+            "flce_embedding_backward", "flce_linear_check_params", "flce_linear_workspace_size",
+            "flce_linear", "flce_linear_backward", "flce_logits_check_params", "flce_logits",
+            "flce_logits_backward", "flce_adamw_check_params", "flce_adamw_workspace_size",
+            "flce_grad_norm", "flce_adamw_step")
 
 
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
@@ -196,6 +239,20 @@ def _open(path: str) -> ctypes.CDLL:
     lib.flce_embedding.restype = ctypes.c_int
     lib.flce_embedding_backward.argtypes = [E, vp, vp, vp, vp, sz, vp]
     lib.flce_embedding_backward.restype = ctypes.c_int
+    D, G = ctypes.POINTER(FlceLinearParams), ctypes.POINTER(FlceLogitsParams)
+    A, W = ctypes.POINTER(FlceAdamwParams), ctypes.POINTER(FlceLogitsRows)
+    lib.flce_linear_workspace_size.argtypes = [D, ctypes.c_int]
+    lib.flce_linear_workspace_size.restype = sz
+    lib.flce_adamw_workspace_size.argtypes = [A]
+    lib.flce_adamw_workspace_size.restype = sz
+    for name, args in (("linear_check_params", [D]), ("linear", [D] + [vp] * 7 + [sz, vp]),
+                       ("linear_backward", [D] + [vp] * 8 + [sz, vp]),
+                       ("logits_check_params", [G]), ("logits", [G, W] + [vp] * 7 + [sz, vp]),
+                       ("logits_backward", [G, W] + [vp] * 8 + [sz, vp]),
+                       ("adamw_check_params", [A]), ("grad_norm", [A, vp, vp, vp, sz, vp]),
+                       ("adamw_step", [A] + [vp] * 10 + [sz, vp])):
+        call = getattr(lib, f"flce_{name}")
+        call.argtypes, call.restype = args, ctypes.c_int
     lib.flce_version.argtypes = []
     lib.flce_version.restype = ctypes.c_int
     return lib

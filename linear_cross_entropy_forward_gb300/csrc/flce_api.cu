@@ -439,6 +439,33 @@ GemmShape base_shape(int a_hint, int b_hint) {
 }
 
 }  // namespace
+
+bool tensor_map(CUtensorMap* map, const void* base, int64_t inner, int64_t outer,
+                int64_t row_elems, int box_inner, int box_outer) {
+  Map m;
+  if (!make_map(&m, base, inner, outer, row_elems, box_inner, box_outer)) return false;
+  *map = m.m;
+  return true;
+}
+
+int side_fork(cudaStream_t st, cudaStream_t* side) {
+  SideStream* ss = nullptr;
+  const int rc = side_stream(&ss);
+  if (rc) return rc;
+  *side = ss->stream;
+  return fork_side(*ss, st);
+}
+
+int side_join(cudaStream_t st) {
+  SideStream* ss = nullptr;
+  const int rc = side_stream(&ss);
+  return rc ? rc : join_side(*ss, st);
+}
+
+GemmShape pair_shape(int a_hint, int b_hint) { return base_shape(a_hint, b_hint); }
+
+void plan_pair(GemmShape* sh, int64_t panel_bytes) { plan_tiles(sh, panel_bytes); }
+
 }  // namespace flce
 
 using namespace flce;

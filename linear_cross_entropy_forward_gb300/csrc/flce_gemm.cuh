@@ -49,6 +49,7 @@
 
 #include <atomic>
 
+#include "flce_act.cuh"
 #include "flce_check.cuh"
 #include "flce_device.cuh"
 
@@ -57,19 +58,21 @@ namespace flce {
 constexpr int BK = 64;  // one 128-byte swizzle row of bf16
 constexpr int UK = 16;  // K of one kind::f16 UMMA
 constexpr int PAIR_BM = 256;  // rows of a pair tile (128 per CTA)
-enum EpiKind { EPI_FWD_STATS = 0, EPI_DLOGITS = 1, EPI_STORE_BF16 = 2, EPI_ACCUM = 3 };
+enum EpiKind { EPI_FWD_STATS = 0, EPI_DLOGITS = 1, EPI_STORE_BF16 = 2, EPI_ACCUM = 3,
+               EPI_LINEAR = 4 };
 
 // Epilogue warps per CTA: 4 (one per TMEM lane quadrant, all of a tile's columns)
 // or 8 (two per quadrant, half the columns each).  Epilogue arithmetic costs the
 // UMMA issuer issue slots, so fewer warps are better where the epilogue of a tile
 // stays well inside the next tile's mainloop; the dlogits epilogue (with the
-// soft-cap, on tiles of only H/64 k-steps) needs 8 to stay hidden.
+// soft-cap, on tiles of only H/64 k-steps) needs 8 to stay hidden, and so does a dense
+// layer's with an error function per element.
 #ifndef FLCE_EPI_WARPS
 #define FLCE_EPI_WARPS 0  // 0: per epilogue kind as below; 4 or 8: every kind
 #endif
 template <int EPI>
 __host__ __device__ constexpr int epi_warps() {
-  return FLCE_EPI_WARPS ? FLCE_EPI_WARPS : (EPI == EPI_DLOGITS ? 8 : 4);
+  return FLCE_EPI_WARPS ? FLCE_EPI_WARPS : (EPI == EPI_DLOGITS || EPI == EPI_LINEAR ? 8 : 4);
 }
 template <int EPI>
 __host__ __device__ constexpr int pair_threads() {
@@ -183,6 +186,8 @@ struct EpiArgs {
   int acc_mode;
   uint32_t* err;
   int64_t n_parts;      // EPI_FWD_STATS: column parts of pm / pd / ps (bounds checks)
+  // EPI_LINEAR
+  LinearOut lin;
 };
 
 // A bounds check of the FLCE_DEBUG build: true in the regular build; in the debug
@@ -576,6 +581,34 @@ struct Epilogue<EPI_ACCUM> {
   }
 };
 
+// A dense layer's output: 8 columns at a time (N is a multiple of 8 here), the residual read
+// and the output written in the accumulator's layout, 16 bytes (fp32: 2 x 16) per thread.
+template <>
+struct Epilogue<EPI_LINEAR> {
+  template <int CH>
+  static __device__ __forceinline__ void run(const EpiArgs& ea, uint32_t tbase, int row,
+                                             int col0) {
+    const bool row_ok = row < ea.rows;
+    const LinearOut& o = ea.lin;
+    const int64_t base = static_cast<int64_t>(row) * o.ld;
+#pragma unroll 1
+    for (int c = 0; c < CH; ++c) {
+      float x[32];
+      tmem_ld32(tbase + c * 32, x);
+      if (!row_ok) continue;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int col = col0 + c * 32 + q * 8;
+        if (col >= ea.cols || !FLCE_CHECK(row_run_ok(col, 8, o.ld), ea.err)) continue;
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = x[q * 8 + i];
+        linear_store8(o, base, col, v);
+      }
+    }
+  }
+};
+
 // ------------------------------------------------------------------ pair kernel
 // Both producers of a pair load their halves; completion is counted on the pair
 // leader's full barrier, which expects the bytes landing in both CTAs.  The leader's
@@ -903,6 +936,11 @@ cudaError_t launch_pair_cached(const CUtensorMap& tmA, const CUtensorMap& tmB,
 // whole SM's shared memory, so one query serves them all.  0 if the query fails.
 int pair_capacity();
 
+// A GEMM's shape with the L2 policies wanted for its operands, and its schedule (raster group and
+// policies) for panels of the revisited operand of panel_bytes per tile.
+GemmShape pair_shape(int a_hint, int b_hint);
+void plan_pair(GemmShape* sh, int64_t panel_bytes);
+
 // Launchers of the instantiations the path uses (one translation unit each).
 #define FLCE_DECLARE_LAUNCHER(name)                                                  \
   cudaError_t name(const CUtensorMap& tmA, const CUtensorMap& tmB, const GemmShape& sh, \
@@ -922,5 +960,8 @@ FLCE_DECLARE_LAUNCHER(launch_bwd_dhidden);   // dlogits (K) x weight (K)
 FLCE_DECLARE_LAUNCHER(launch_fwd_stats_vh);    // hidden (K) x weight (K)
 FLCE_DECLARE_LAUNCHER(launch_bwd_dlogits_vh);  // hidden (K) x weight (K)
 FLCE_DECLARE_LAUNCHER(launch_bwd_dhidden_vh);  // dlogits (K) x weight (MN)
+// a dense layer's forward
+FLCE_DECLARE_LAUNCHER(launch_linear);     // x (K) x weight [K,N] (MN)
+FLCE_DECLARE_LAUNCHER(launch_linear_vh);  // x (K) x weight [N,K] (K)
 
 }  // namespace flce

@@ -1,6 +1,7 @@
 // Host helpers shared by the library's entry points.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -34,5 +35,15 @@ int forward_backward(const flce_params* p, const void* hidden, const void* weigh
 
 // Token chunks flce_forward_backward takes.
 int64_t fused_chunks(const flce_params* p);
+
+// Tensor map over a row-major [outer, inner] bf16 array (rows row_elems long) with boxes of
+// box_inner x box_outer, 128-byte swizzle, zeros out of bounds.
+bool tensor_map(CUtensorMap* map, const void* base, int64_t inner, int64_t outer,
+                int64_t row_elems, int box_inner, int box_outer);
+
+// A stream beside `st` (one per thread and device) that waits for the work on it so far; side_join
+// makes `st` wait for the work on that stream.
+int side_fork(cudaStream_t st, cudaStream_t* side);
+int side_join(cudaStream_t st);
 
 }  // namespace flce

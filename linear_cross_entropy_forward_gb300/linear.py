@@ -1,0 +1,175 @@
+"""A dense layer with bias, activation and residual in its epilogue, and its gradients.
+
+    y = act(x W + bias) + residual
+
+for the layers below the head and, with fp32 out, the head's own logits for a sampler.  x, W and
+bias are bf16; W is [K, N] (weight_layout 'hv') or [N, K] ('vh', nn.Linear), as the head's.
+Argument marshalling only; the library's kernels do the work.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from . import _binding as B
+from .losses import _addr, _on, _raw_stream, _workspace
+
+_ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+_OUT = {torch.bfloat16: 1, torch.float32: 0}
+
+
+def linear_params(M, N, K, activation=None, weight_layout="hv", out_dtype=torch.bfloat16,
+                  validate=False):
+    """FlceLinearParams of a flce_linear call."""
+    if out_dtype not in _OUT:
+        raise TypeError(f"out_dtype must be bfloat16 or float32, got {out_dtype}")
+    if activation not in _ACTIVATIONS:
+        raise ValueError("activation must be one of relu/gelu/gelu_tanh/silu or None, got "
+                         f"{activation!r}")
+    return B.FlceLinearParams(M, N, K, B.layout_code(weight_layout), _ACTIVATIONS[activation],
+                              _OUT[out_dtype], bool(validate))
+
+
+def linear_workspace_size(params: "B.FlceLinearParams", backward: bool = False) -> int:
+    """Bytes of workspace a flce_linear (flce_linear_backward) call with these parameters needs."""
+    lib = B._lib or B.load_library()
+    size = lib.flce_linear_workspace_size(ctypes.byref(params), int(backward))
+    if size == 0:
+        B._check(lib.flce_linear_check_params(ctypes.byref(params)))
+    return size
+
+
+def _shapes(x, weight, weight_layout):
+    """(M, N, K, device) of x [..., K] and the weight, checked."""
+    for t, name in ((x, "x"), (weight, "weight")):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA tensor")
+        if t.dtype is not torch.bfloat16:
+            raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    if x.dim() < 1 or weight.dim() != 2:
+        raise ValueError(f"x must be [..., K] and weight 2-D, got {tuple(x.shape)} and "
+                         f"{tuple(weight.shape)}")
+    dev = B._on_current_device(x)
+    if weight.device != dev:
+        raise ValueError(f"weight is on {weight.device}, the other tensors on {dev}")
+    N, K = weight.shape if B.layout_code(weight_layout) == B.WEIGHT_VH else weight.shape[::-1]
+    if x.shape[-1] != K:
+        raise ValueError(f"x has rows of {x.shape[-1]}, the weight takes {K}")
+    M = 1
+    for n in x.shape[:-1]:
+        M *= n
+    return M, N, K, dev
+
+
+def flce_linear(x, weight, bias=None, activation=None, residual=None, weight_layout="hv",
+                out_dtype=torch.bfloat16, need_preact=False, validate=False, workspace=None,
+                stream=None, out=None):
+    """y [..., N] = act(x W + bias) + residual, in bf16 or (out_dtype) fp32.
+
+    x [..., K] and weight bf16, K a multiple of 8, and N too for a [K, N] weight; bias bf16 [N];
+    activation: None, 'relu', 'gelu', 'gelu_tanh' or 'silu'; residual of y's shape and type (out
+    may be the residual itself).  Sums are fp32, rounded once.  With need_preact returns (y, z): z =
+    x W + bias in bf16, as the backward takes it.
+    """
+    if stream is not None:
+        return _on(stream, flce_linear, x, weight, bias, activation, residual, weight_layout,
+                   out_dtype, need_preact, validate, workspace, out=out)
+    lib = B._lib or B.load_library()
+    M, N, K, dev = _shapes(x, weight, weight_layout)
+    shape = (*x.shape[:-1], N)
+    p = linear_params(M, N, K, activation, weight_layout, out_dtype, validate)
+    if bias is not None:
+        B._need(bias, "bias", torch.bfloat16, (N,), dev)
+    if residual is not None:
+        B._need(residual, "residual", out_dtype, shape, dev)
+    size = linear_workspace_size(p)
+    if out is None:
+        out = torch.empty(shape, dtype=out_dtype, device=dev)
+    else:
+        B._need(out, "out", out_dtype, shape, dev)
+    z = torch.empty(shape, dtype=torch.bfloat16, device=dev) if need_preact else None
+    ws = _workspace(size, dev.index, workspace)
+    code = lib.flce_linear(ctypes.byref(p), x.data_ptr(), weight.data_ptr(), _addr(bias),
+                           _addr(residual), out.data_ptr(), _addr(z), ws.data_ptr(), ws.numel(),
+                           _raw_stream(dev.index))
+    if code:
+        B._check(code)
+    return (out, z) if need_preact else out
+
+
+def flce_linear_backward(dout, x, weight, preact=None, activation=None, weight_layout="hv",
+                         need_dx=True, need_dweight=True, need_dbias=True, validate=False,
+                         workspace=None, stream=None, out=None):
+    """(dx, dweight, dbias) of flce_linear, bf16, shaped like x, weight and [N]; None where not
+    wanted.  dout: of y's shape and type (bf16 or fp32); it is the residual's gradient as it is.
+    preact: z of the forward, where there is an activation.  dz = dout act'(z) is rounded to bf16
+    for the products; dbias sums it unrounded.  out: (dx, dweight, dbias) to write into."""
+    if stream is not None:
+        return _on(stream, flce_linear_backward, dout, x, weight, preact, activation,
+                   weight_layout, need_dx, need_dweight, need_dbias, validate, workspace, out=out)
+    lib = B._lib or B.load_library()
+    M, N, K, dev = _shapes(x, weight, weight_layout)
+    shape = (*x.shape[:-1], N)
+    if not isinstance(dout, torch.Tensor):
+        raise TypeError("dout must be a CUDA tensor")
+    p = linear_params(M, N, K, activation, weight_layout, dout.dtype, validate)
+    B._need(dout, "dout", dout.dtype, shape, dev)
+    if p.activation:
+        if preact is None:
+            raise ValueError("an activation's gradient needs preact")
+        B._need(preact, "preact", torch.bfloat16, shape, dev)
+    size = linear_workspace_size(p, True)
+    wanted = (("dx", need_dx, x.shape), ("dweight", need_dweight, weight.shape),
+              ("dbias", need_dbias, (N,)))
+    if out is None:
+        out = [torch.empty(s, dtype=torch.bfloat16, device=dev) if need else None
+               for _, need, s in wanted]
+    else:
+        if len(out) != 3:
+            raise ValueError("out must hold dx, dweight and dbias")
+        out = [t if need else None for t, (_, need, _) in zip(out, wanted)]
+        for t, (name, need, s) in zip(out, wanted):
+            if need:
+                B._need(t, name, torch.bfloat16, s, dev)
+    dx, dw, db = out
+    ws = _workspace(size, dev.index, workspace)
+    code = lib.flce_linear_backward(
+        ctypes.byref(p), dout.data_ptr(), x.data_ptr(), weight.data_ptr(),
+        preact.data_ptr() if p.activation else None, _addr(dx), _addr(dw), _addr(db),
+        ws.data_ptr(), ws.numel(), _raw_stream(dev.index))
+    if code:
+        B._check(code)
+    return dx, dw, db
+
+
+class _Linear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, residual, activation, weight_layout, out_dtype):
+        needs = any(ctx.needs_input_grad[:3])
+        keep = needs and _ACTIVATIONS.get(activation, 0) != 0
+        y = flce_linear(x, weight, bias, activation, residual, weight_layout, out_dtype, keep)
+        y, z = y if keep else (y, None)
+        ctx.save_for_backward(x, weight, z)
+        ctx.cfg = activation, weight_layout
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, g):
+        x, weight, z = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        dx = dw = db = None
+        if any(need[:3]):
+            dx, dw, db = flce_linear_backward(g.contiguous(), x, weight, z, *ctx.cfg, *need[:3])
+        return dx, dw, db, g if need[3] else None, None, None, None
+
+
+def linear(x, weight, bias=None, activation=None, residual=None, weight_layout="hv",
+           out_dtype=torch.bfloat16):
+    """act(x W + bias) + residual, differentiable by x, weight, bias and residual; see
+    flce_linear."""
+    return _Linear.apply(x, weight, bias, residual, activation, weight_layout, out_dtype)
