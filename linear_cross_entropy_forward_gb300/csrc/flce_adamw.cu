@@ -65,7 +65,7 @@ struct StepArgs {
   const float* norm;
   int64_t* step;
   uint32_t* ticket;
-  float lr, beta1, omb1, beta2, omb2, eps, grad_scale, max_norm;
+  float lr, beta1, omb1, beta2, rb2, romb2, eps, grad_scale, max_norm;  // r: root of
   double ln1, ln2;  // logarithms of the betas
   uint32_t seed;
   int32_t skip, last;
@@ -93,10 +93,23 @@ __device__ __forceinline__ T narrow(float x) {
   else return __float2half_rn(x);
 }
 
+__device__ __forceinline__ void ld_cs_v8(const float* p, float (&x)[kPer]) {
+  asm volatile("ld.global.cs.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]),
+                 "=f"(x[6]), "=f"(x[7])
+               : "l"(p));
+}
+
 // 8 elements from p, `n` of them there (the others 0)
 template <typename T>
 __device__ __forceinline__ void load8(const T* p, int64_t n, float (&x)[kPer]) {
   if (n >= kPer && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+    if constexpr (sizeof(T) == 4) {
+      if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {
+        ld_cs_v8(reinterpret_cast<const float*>(p), x);
+        return;
+      }
+    }
     alignas(16) T t[kPer];
     uint4* q = reinterpret_cast<uint4*>(t);
 #pragma unroll
@@ -112,6 +125,12 @@ __device__ __forceinline__ void load8(const T* p, int64_t n, float (&x)[kPer]) {
 template <typename T>
 __device__ __forceinline__ void store8(T* p, int64_t n, const float (&x)[kPer]) {
   if (n >= kPer && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+    if constexpr (sizeof(T) == 4) {
+      if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {
+        st_global_cs_v8f(reinterpret_cast<float*>(p), x);
+        return;
+      }
+    }
     alignas(16) T t[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) t[i] = narrow<T>(x[i]);
@@ -148,14 +167,11 @@ __device__ __forceinline__ void from_e4m3_pair(uint16_t c, float& lo, float& hi)
   hi = __high2float(v);
 }
 
-__device__ __forceinline__ void unpack8(uint2 c, float scale, float (&x)[kPer]) {
+__device__ __forceinline__ void unpack8(uint2 c, float (&x)[kPer]) {
   const uint32_t w[2] = {c.x, c.y};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 4; ++i)
     from_e4m3_pair(static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1))), x[2 * i], x[2 * i + 1]);
-    x[2 * i] *= scale;
-    x[2 * i + 1] *= scale;
-  }
 }
 
 // |x| unit to an e4m3 value, the upper neighbour where the 20 random bits carry into the
@@ -187,8 +203,8 @@ __device__ __forceinline__ uint2 pack8(const float (&x)[kPer], const uint32_t (&
   float y[kPer];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    float a = fabsf(x[i]) * unit;
-    a = a > 448.0f ? 448.0f : a;  // not a minimum: NaN stays
+    // a quotient just above 448, carried up to 480, is 448 again as a code
+    const float a = fabsf(x[i]) * unit;
     float q = round_up_or_down(a, r[i]);
     if (ROOT) {
       if (a > 0.0f && q == 0.0f) q = 0.001953125f;  // 2^-9, the smallest code
@@ -204,8 +220,10 @@ __device__ __forceinline__ uint2 pack8(const float (&x)[kPer], const uint32_t (&
 }
 
 // ------------------------------------------------------------------ the step
+// m = b1 m + cm grad;  v = (rb2 s)^2 + (cs grad)^2 (8 bits) or b2 v + (cs grad)^2, with the root
+// s = sqrt(v);  p = p (1 - lr wd) - step_size m / (root_c2 s + eps)
 struct Coef {
-  float c, beta1, omb1, beta2, omb2, eps, lr, step_size, rc2;
+  float beta1, beta2, rb2, cm, cs, eps, lr, step_size, root_c2;
   uint32_t key;
 };
 
@@ -243,19 +261,33 @@ __device__ __forceinline__ void update8(const Slot& s, const StepArgs& a, const 
     for (int i = 0; i < kPer; ++i) g[i] = w[i] = m[i] = v[i] = 0.0f;
   }
   if constexpr (STATE8) {
-    unpack8(cm, scale_m, m);
-    unpack8(cs, scale_s, v);
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) v[i] *= v[i];
+    unpack8(cm, m);
+    unpack8(cs, v);
   }
   const float shrink = 1.0f - k.lr * s.decay;
+  const uint64_t shrink2 = f2_pack(shrink, shrink), minus = f2_pack(-k.step_size, -k.step_size),
+                 eps2 = f2_pack(k.eps, k.eps), cm2 = f2_pack(k.cm, k.cm), cs2 = f2_pack(k.cs, k.cs),
+                 root2 = f2_pack(k.root_c2, k.root_c2);
+  const float keep_m = STATE8 ? k.beta1 * scale_m : k.beta1;
+  const float keep_v = STATE8 ? k.rb2 * scale_s : k.beta2;
+  const uint64_t keep_m2 = f2_pack(keep_m, keep_m), keep_v2 = f2_pack(keep_v, keep_v);
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const float x = k.c * g[i];
-    m[i] = fmaf(k.beta1, m[i], k.omb1 * x);
-    v[i] = fmaf(k.beta2, v[i], k.omb2 * (x * x));
-    const float d = sqrt_approx(v[i] * k.rc2) + k.eps;
-    w[i] = fmaf(w[i], shrink, -k.step_size * __fdividef(m[i], d));
+  for (int i = 0; i < kPer; i += 2) {
+    const uint64_t x = f2_pack(g[i], g[i + 1]);
+    const uint64_t m2 = f2_fma(x, cm2, f2_mul(f2_pack(m[i], m[i + 1]), keep_m2));
+    const uint64_t y = f2_mul(x, cs2);
+    uint64_t old = f2_mul(f2_pack(v[i], v[i + 1]), keep_v2);
+    if constexpr (STATE8) old = f2_mul(old, old);
+    const uint64_t v2 = f2_fma(y, y, old);
+    float v0, v1, d0, d1;
+    f2_unpack(v2, v0, v1);
+    const float s0 = sqrt_approx(v0), s1 = sqrt_approx(v1);
+    f2_unpack(f2_fma(f2_pack(s0, s1), root2, eps2), d0, d1);
+    const uint64_t u = f2_mul(m2, f2_pack(fast_rcp(d0), fast_rcp(d1)));
+    f2_unpack(f2_fma(u, minus, f2_mul(f2_pack(w[i], w[i + 1]), shrink2)), w[i], w[i + 1]);
+    f2_unpack(m2, m[i], m[i + 1]);
+    v[i] = STATE8 ? s0 : v0;
+    v[i + 1] = STATE8 ? s1 : v1;
   }
   if constexpr (STATE8) {
     uint32_t r1[kPer], r2[kPer];
@@ -265,7 +297,6 @@ __device__ __forceinline__ void update8(const Slot& s, const StepArgs& a, const 
       const uint32_t h = mix((static_cast<uint32_t>(at) + i) ^ key);
       r1[i] = h >> 12;
       r2[i] = (h * 0x9E3779B1u) >> 12;
-      v[i] = sqrtf(v[i]);
     }
     cm = pack8<false>(m, r1, scale_m);
     cs = pack8<true>(v, r2, scale_s);
@@ -321,17 +352,17 @@ __global__ void __launch_bounds__(kThreads)
   }
   if (!skip) {
     Coef k;
-    k.c = c;
     k.beta1 = a.beta1;
-    k.omb1 = a.omb1;
     k.beta2 = a.beta2;
-    k.omb2 = a.omb2;
+    k.rb2 = a.rb2;
+    k.cm = c * a.omb1;
+    k.cs = c * a.romb2;
     k.eps = a.eps;
     k.lr = a.lr_ptr ? *a.lr_ptr : a.lr;
     // 1 - b^t = -(e^{t ln b} - 1): exact to fp32 for small t ln b too
     const double ts = static_cast<double>(step);
     k.step_size = k.lr / -expm1f(static_cast<float>(ts * a.ln1));
-    k.rc2 = 1.0f / -expm1f(static_cast<float>(ts * a.ln2));
+    k.root_c2 = sqrtf(1.0f / -expm1f(static_cast<float>(ts * a.ln2)));
     k.key = mix(a.seed + 0x9E3779B9u * static_cast<uint32_t>(step));
     uint32_t u, end;
     int i = find_run(t, u, end);
@@ -368,14 +399,12 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // ------------------------------------------------------------------ the norm
-// Sum of (scale g)^2: 8 squares in fp32, from there on in 64 bits, in a fixed order.
-template <typename G>
-__device__ __forceinline__ float squares(const void* grad, int64_t n, int64_t e0, float scale) {
-  float x[kPer];
-  const int64_t left = n - e0;
-  if (left <= 0) return 0.0f;
-  const G* p = static_cast<const G*>(grad) + e0;
-  load8(p, left, x);
+// Sum of (scale g)^2: up to 512 squares in fp32, from there on in 64 bits (whose units are few:
+// one addition per 8 squares took longer than the bytes), in a fixed order.
+constexpr int kNormDepth = 4;  // units in flight
+constexpr int kNormFold = 64;  // units whose squares a thread sums in fp32
+
+__device__ __forceinline__ float squares(const float (&x)[kPer], float scale) {
   float sum = 0.0f;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
@@ -383,6 +412,30 @@ __device__ __forceinline__ float squares(const void* grad, int64_t n, int64_t e0
     sum = fmaf(y, y, sum);
   }
   return sum;
+}
+
+// `units` units of one tensor from element e0 on (this thread's first)
+template <typename G>
+__device__ __forceinline__ double sum_units(const void* grad, int64_t n, int64_t e0, int64_t units,
+                                            float scale) {
+  const G* p = static_cast<const G*>(grad);
+  double total = 0.0;
+  for (int64_t u = 0; u < units; u += kNormFold) {
+    const int64_t end = u + kNormFold < units ? u + kNormFold : units;
+    float part[kNormDepth] = {};
+    for (int64_t v = u; v < end; v += kNormDepth) {
+      float x[kNormDepth][kPer];
+#pragma unroll
+      for (int d = 0; d < kNormDepth; ++d) {
+        const int64_t e = e0 + (v + d) * kUnit;
+        load8(p + e, v + d < end ? n - e : 0, x[d]);
+      }
+#pragma unroll
+      for (int d = 0; d < kNormDepth; ++d) part[d] += squares(x[d], scale);
+    }
+    total += (part[0] + part[1]) + (part[2] + part[3]);
+  }
+  return total;
 }
 
 __device__ __forceinline__ double block_sum(double x) {
@@ -403,14 +456,17 @@ __global__ void __launch_bounds__(kThreads)
   uint32_t u, end;
   int i = find_run(t, u, end);
   double total = 0.0;
-  for (; u < end; ++u) {
+  while (u < end) {
     while (i + 1 < t.count && t.first[i + 1] <= u) ++i;
     const Slot& s = t.slot[i];
+    const uint32_t stop = i + 1 < t.count && t.first[i + 1] < end ? t.first[i + 1] : end;
     const int64_t e0 = static_cast<int64_t>(u - t.first[i]) * kUnit + threadIdx.x * kPer;
     const bool f32 = (s.kind & 1) || s.kind == 2 * FLCE_F32;
-    total += f32 ? squares<float>(s.grad, s.n, e0, a.scale)
-             : s.kind == 2 * FLCE_BF16 ? squares<__nv_bfloat16>(s.grad, s.n, e0, a.scale)
-                                       : squares<__half>(s.grad, s.n, e0, a.scale);
+    total += f32 ? sum_units<float>(s.grad, s.n, e0, stop - u, a.scale)
+             : s.kind == 2 * FLCE_BF16
+                 ? sum_units<__nv_bfloat16>(s.grad, s.n, e0, stop - u, a.scale)
+                 : sum_units<__half>(s.grad, s.n, e0, stop - u, a.scale);
+    u = stop;
   }
   total = block_sum(total);
   __shared__ bool is_last;
@@ -646,7 +702,8 @@ int flce_adamw_step(const flce_adamw_params* p, const flce_adamw_tensor* tensors
   a.beta1 = static_cast<float>(p->beta1);
   a.omb1 = static_cast<float>(1.0 - p->beta1);
   a.beta2 = static_cast<float>(p->beta2);
-  a.omb2 = static_cast<float>(1.0 - p->beta2);
+  a.rb2 = static_cast<float>(sqrt(p->beta2));
+  a.romb2 = static_cast<float>(sqrt(1.0 - p->beta2));
   a.eps = static_cast<float>(p->eps);
   a.grad_scale = static_cast<float>(p->grad_scale);
   a.max_norm = static_cast<float>(p->max_norm);

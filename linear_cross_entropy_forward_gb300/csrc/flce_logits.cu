@@ -28,13 +28,34 @@
 namespace flce {
 namespace {
 
-constexpr int kThreads = 512;
+#ifndef FLCE_LOGITS_THREADS
+#define FLCE_LOGITS_THREADS 256
+#endif
+#ifndef FLCE_LOGITS_FILL
+#define FLCE_LOGITS_FILL 4
+#endif
+#ifndef FLCE_LOGITS_ROOM
+#define FLCE_LOGITS_ROOM 65536
+#endif
+constexpr int kThreads = FLCE_LOGITS_THREADS;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBatch = 4;            // vectors in flight per thread
 constexpr int kMaxCluster = 16;
-constexpr int kMaxColumns = 16384;   // counters per block: 64 KB
+constexpr int kRoom = FLCE_LOGITS_ROOM;  // bytes of counters per block
 constexpr int kMaxBias = 2048;       // entries of a row's list: 16 KB of shared memory
-constexpr uint32_t kSeen = 0x80000000u, kBiased = 0x40000000u, kCount = 0x3fffffffu;
+
+// Counters: occurrences among the generated tokens, and flags of the prompt's tokens and of
+// columns with a bias.  16 bits hold the count of histories below 2^14 tokens.
+struct NoCounter {
+  using Word = uint16_t;
+};
+template <typename W>
+struct Counter {
+  using Word = W;
+  static constexpr int kBits = sizeof(W) * 8;
+  static constexpr uint32_t kSeen = 1u << (kBits - 1), kBiased = 1u << (kBits - 2),
+                            kCount = kBiased - 1;
+};
 
 struct Args {
   const void* logits;
@@ -135,24 +156,78 @@ __device__ __forceinline__ uint32_t cluster_size() {
   return r;
 }
 
+// VEC mask bytes at p (that of logit l of a row of V) as bits: bit i set where byte i is not 0.
+template <int VEC>
+__device__ __forceinline__ uint32_t byte_mask(const uint8_t* p, int64_t l, int64_t V) {
+  uint32_t w[VEC / 4];
+  const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 3);
+  if (off == 0 || (l >= 4 && l + VEC + 4 <= V)) {  // whole words inside the row
+    const uint32_t* q = reinterpret_cast<const uint32_t*>(p - off);
+    uint32_t lo = __ldg(q);
+#pragma unroll
+    for (int j = 0; j < VEC / 4; ++j) {
+      const uint32_t hi = j + 1 < VEC / 4 || off ? __ldg(q + j + 1) : 0u;
+      w[j] = __funnelshift_r(lo, hi, 8 * off);
+      lo = hi;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < VEC / 4; ++j)
+      w[j] = p[4 * j] | p[4 * j + 1] << 8 | p[4 * j + 2] << 16 | uint32_t(p[4 * j + 3]) << 24;
+  }
+  uint32_t bits = 0;
+#pragma unroll
+  for (int j = 0; j < VEC / 4; ++j) {
+    // bit 7 of each byte that is not 0, then the four of them side by side
+    const uint32_t t = ((((w[j] & 0x7f7f7f7fu) + 0x7f7f7f7fu) | w[j]) >> 7) & 0x01010101u;
+    bits |= ((t * 0x01020408u) >> 24 & 15u) << (4 * j);
+  }
+  return bits;
+}
+
 // Columns are numbered from the row's last 16-byte boundary at or before its first logit, so
 // that vectors of VEC columns are aligned in every row; `pre` columns before the row are not
 // there.  Column c of that numbering is logit c - pre.
-template <typename T, bool COUNT, int MODE>
-__global__ void __launch_bounds__(kThreads) logits_kernel(const __grid_constant__ Args a) {
+template <typename T, typename COUNTER, int MODE>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads)
+    logits_kernel(const __grid_constant__ Args a) {
   constexpr int VEC = 16 / sizeof(T);
-  extern __shared__ uint32_t counters[];  // [columns], then the biases' columns and values
+  constexpr bool COUNT = !std::is_same_v<COUNTER, NoCounter>;
+  using Word = typename COUNTER::Word;
+  extern __shared__ __align__(16) uint8_t shared[];  // counters, then the biases' columns and values
   __shared__ Stats part[kWarps];
   __shared__ Stats from[kMaxCluster];
   __shared__ float label_z;
+  Word* counters = reinterpret_cast<Word*>(shared);
   const uint32_t rank = cluster_ctarank(), size = cluster_size();
   const int64_t row = blockIdx.x / size;
   const T* x = static_cast<const T*>(a.logits) + row * a.ld;
   const int pre = static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
   const int64_t span = a.V + pre;
   const int64_t per_pass = a.columns * size;
-  int* bias_col = reinterpret_cast<int*>(counters + a.columns);
+  int* bias_col = reinterpret_cast<int*>(shared + a.columns * sizeof(Word));
   float* bias_val = reinterpret_cast<float*>(bias_col + a.n_bias);
+
+  // the first vectors are asked for before anything is waited for
+  alignas(16) T in[kBatch][VEC];
+  auto load = [&](int64_t v0, int64_t c1) {
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int64_t c = v0 + int64_t(b) * kThreads * VEC, l = c - pre;
+      if (c >= c1) continue;
+      if (l >= 0 && l + VEC <= a.V) {
+        *reinterpret_cast<uint4*>(in[b]) = __ldcs(reinterpret_cast<const uint4*>(x + l));
+      } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+          in[b][i] = l + i >= 0 && l + i < a.V ? x[l + i] : narrow<T>(0.0f);
+      }
+    }
+  };
+  {
+    const int64_t c0 = rank * a.columns;
+    load(c0 + threadIdx.x * VEC, c0 + a.columns < span ? c0 + a.columns : span);
+  }
 
   int64_t label = -1;
   bool ignored = false, bad = false;
@@ -188,9 +263,8 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(const __grid_constant_
     length = a.lengths ? whole(a.lengths, row, a.lens64) : a.T;
     length = length < a.T ? length : a.T;
     prompt = a.prompt_lens ? whole(a.prompt_lens, row, a.lens64) : 0;
+    if (p.rep == 1.0f && p.freq == 0.0f && p.pres == 0.0f) length = 0;
   }
-  const bool penal = p.rep != 1.0f || p.freq != 0.0f || p.pres != 0.0f;
-  if (!penal) length = 0;
   if (COUNT && !zero) {
     for (int64_t j = threadIdx.x; j < a.n_bias; j += kThreads) {
       const int64_t id = whole(a.bias_ids, row * a.ld_bias_ids + j, a.bias64);
@@ -209,98 +283,129 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(const __grid_constant_
     if (COUNT && !zero) {
       // every block of the cluster clears its counters before any adds to them
       if (pass > 0) __syncthreads();
-      for (int i = threadIdx.x; i < a.columns; i += kThreads) counters[i] = 0;
+      uint4* clear = reinterpret_cast<uint4*>(shared);
+      for (int i = threadIdx.x; i < a.columns * int(sizeof(Word)) / 16; i += kThreads)
+        clear[i] = make_uint4(0, 0, 0, 0);
       meet();
-      const int64_t share = (length + size - 1) / size;
-      const int64_t t0 = rank * share;
-      const int64_t t1 = t0 + share < length ? t0 + share : length;
-      const uint32_t columns = static_cast<uint32_t>(a.columns);
-      for (int64_t t = t0 + threadIdx.x; t < t1; t += kThreads) {
-        const int64_t id = whole(a.tokens, row * a.ld_tokens + t, a.ids64);
-        const int64_t c = id + pre - base;
-        if (id < 0 || id >= a.V || c < 0 || c >= per_pass) continue;
-        const uint32_t owner = static_cast<uint32_t>(c) / columns;
-        const uint32_t at = remote(counters + (static_cast<uint32_t>(c) - owner * columns), owner);
-        if (t < prompt) red_or(at, kSeen);
-        else red_add(at, 1u);
-      }
-      for (int j = threadIdx.x; j < a.n_bias; j += kThreads) {
-        const int64_t c = bias_col[j];  // every block marks its own columns
-        if (c >= c0 && c < c1) atomicOr(counters + (c - c0), kBiased);
+      if constexpr (COUNT) {
+        const int64_t share = (length + size - 1) / size;
+        const int64_t t0 = rank * share;
+        const int64_t t1 = t0 + share < length ? t0 + share : length;
+        const uint32_t columns = static_cast<uint32_t>(a.columns);
+        for (int64_t t = t0 + threadIdx.x; t < t1; t += kThreads) {
+          const int64_t id = whole(a.tokens, row * a.ld_tokens + t, a.ids64);
+          const int64_t c = id + pre - base;
+          if (id < 0 || id >= a.V || c < 0 || c >= per_pass) continue;
+          const uint32_t owner = static_cast<uint32_t>(c) / columns;
+          const uint32_t byte = (static_cast<uint32_t>(c) - owner * columns) * sizeof(Word);
+          const uint32_t at = remote(shared + (byte & ~3u), owner), shift = 8 * (byte & 3u);
+          if (t < prompt) red_or(at, COUNTER::kSeen << shift);
+          else red_add(at, 1u << shift);
+        }
+        for (int j = threadIdx.x; j < a.n_bias; j += kThreads) {
+          const int64_t c = bias_col[j];  // every block marks its own columns
+          if (c < c0 || c >= c1) continue;
+          const uint32_t byte = static_cast<uint32_t>(c - c0) * sizeof(Word);
+          atomicOr(reinterpret_cast<uint32_t*>(shared + (byte & ~3u)),
+                   COUNTER::kBiased << (8 * (byte & 3u)));
+        }
       }
       meet();
     } else if (MODE == MODE_FORWARD && a.stats && pass == 0) {
       meet();  // label_z of the first block is there, and cleared
     }
     for (int64_t v0 = c0 + threadIdx.x * VEC; v0 < c1; v0 += int64_t(kThreads) * VEC * kBatch) {
-      alignas(16) T in[kBatch][VEC];
-#pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        const int64_t c = v0 + int64_t(b) * kThreads * VEC;
-        if (c >= c1 || zero) continue;
-        const int64_t l = c - pre;
-        if (l >= 0 && l + VEC <= a.V) {
-          *reinterpret_cast<uint4*>(in[b]) = __ldcs(reinterpret_cast<const uint4*>(x + l));
-        } else {
-#pragma unroll
-          for (int i = 0; i < VEC; ++i)
-            in[b][i] = l + i >= 0 && l + i < a.V ? x[l + i] : narrow<T>(0.0f);
-        }
-      }
+      if ((pass > 0 || v0 >= c0 + int64_t(kThreads) * VEC) && !zero) load(v0, c1);
 #pragma unroll
       for (int b = 0; b < kBatch; ++b) {
         const int64_t c = v0 + int64_t(b) * kThreads * VEC;
         if (c >= c1) continue;
         const int64_t l = c - pre;
-        float z[VEC], slope[VEC];
-        uint32_t there = 0;  // bit i: column c + i is a logit and allowed
-        if (l >= 0 && l + VEC <= a.V) {
-          there = (1u << VEC) - 1;
-        } else {
+        const bool inside = l >= 0 && l + VEC <= a.V;
+        constexpr uint32_t kAll = (1u << VEC) - 1;
+        uint32_t real = kAll;  // bit i: column c + i is a logit
+        if (!inside) {
+          real = 0;
 #pragma unroll
           for (int i = 0; i < VEC; ++i)
-            if (l + i >= 0 && l + i < a.V) there |= 1u << i;
+            if (l + i >= 0 && l + i < a.V) real |= 1u << i;
         }
-        const uint32_t real = there;
+        uint32_t there = real;  // and allowed
         if (a.mask_kind == 2) {
           const uint32_t* w = reinterpret_cast<const uint32_t*>(p.mask);
-          uint32_t bits = 0;
           if (l >= 0) {
             const uint32_t lo = __ldg(w + (l >> 5));
             const uint32_t hi = (l & 31) + VEC > 32 && ((l >> 5) + 1) * 32 < a.V
                                     ? __ldg(w + (l >> 5) + 1) : 0u;
-            bits = __funnelshift_r(lo, hi, static_cast<uint32_t>(l & 31));
+            there &= __funnelshift_r(lo, hi, static_cast<uint32_t>(l & 31));
           } else {
-            bits = __ldg(w) << static_cast<uint32_t>(-l);
+            there &= __ldg(w) << static_cast<uint32_t>(-l);
           }
-          there &= bits;
         } else if (a.mask_kind == 1) {
+          if (inside) {
+            there = byte_mask<VEC>(p.mask + l, l, a.V);
+          } else {
 #pragma unroll
-          for (int i = 0; i < VEC; ++i)
-            if ((real >> i & 1) && p.mask[l + i] == 0) there &= ~(1u << i);
+            for (int i = 0; i < VEC; ++i)
+              if ((real >> i & 1) && p.mask[l + i] == 0) there &= ~(1u << i);
+          }
         }
+        float z[VEC], slope[VEC];
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-          float y = zero ? 0.0f : widen(in[b][i]);
-          float k = 1.0f;
-          if (COUNT && !zero) {
-            const uint32_t n = counters[c - c0 + i];
-            if (n) {
-              if (n & (kSeen | kCount)) {
-                k = y > 0.0f ? p.inv_rep : p.rep;
+          z[i] = widen(in[b][i]);
+          slope[i] = p.inv_temp;
+        }
+        if constexpr (COUNT) {
+          constexpr int WORDS = VEC * sizeof(Word) / 4;
+          uint32_t n32[WORDS];
+          uint32_t any = 0;
+          if (!zero) {
+            const uint32_t* src = reinterpret_cast<const uint32_t*>(counters + (c - c0));
+            if constexpr (WORDS == 2) {
+              *reinterpret_cast<uint2*>(n32) = *reinterpret_cast<const uint2*>(src);
+            } else {
+#pragma unroll
+              for (int j = 0; j < WORDS; j += 4)
+                *reinterpret_cast<uint4*>(n32 + j) = *reinterpret_cast<const uint4*>(src + j);
+            }
+#pragma unroll
+            for (int j = 0; j < WORDS; ++j) any |= n32[j];
+          }
+          if (any) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+              const uint32_t n = sizeof(Word) == 4
+                                     ? n32[i % WORDS] : n32[i / 2 % WORDS] >> (16 * (i & 1)) & 0xffffu;
+              if (n == 0) continue;
+              float y = z[i];
+              if (n & (COUNTER::kSeen | COUNTER::kCount)) {
+                const float k = y > 0.0f ? p.inv_rep : p.rep;
                 y *= k;
+                slope[i] *= k;
               }
-              if (n & kCount) y = fmaf(-p.freq, static_cast<float>(n & kCount), y) - p.pres;
-              if (n & kBiased) {
+              if (n & COUNTER::kCount)
+                y = fmaf(-p.freq, static_cast<float>(n & COUNTER::kCount), y) - p.pres;
+              if (n & COUNTER::kBiased) {
                 float sum = 0.0f;
+#pragma unroll 1
                 for (int j = 0; j < a.n_bias; ++j)
                   if (bias_col[j] == static_cast<int>(c) + i) sum += bias_val[j];
                 y += sum;
               }
+              z[i] = y;
             }
           }
-          z[i] = there >> i & 1 ? y * p.inv_temp : -INFINITY;
-          slope[i] = there >> i & 1 ? k * p.inv_temp : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) z[i] *= p.inv_temp;
+        if (there != kAll) {
+#pragma unroll
+          for (int i = 0; i < VEC; ++i)
+            if (!(there >> i & 1)) {
+              z[i] = -INFINITY;
+              slope[i] = 0.0f;
+            }
         }
         const int64_t yl = label - l;  // the label's place in this vector
         if (MODE == MODE_FORWARD) {
@@ -348,7 +453,7 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(const __grid_constant_
         if (a.out) {
           if (a.out_f32) {
             float* o = static_cast<float*>(a.out) + row * a.ld_out + l;
-            if (real == (1u << VEC) - 1 && (reinterpret_cast<uintptr_t>(o) & 15) == 0) {
+            if (inside && (reinterpret_cast<uintptr_t>(o) & 15) == 0) {
 #pragma unroll
               for (int i = 0; i < VEC / 4; ++i)
                 __stcs(reinterpret_cast<float4*>(o) + i,
@@ -360,7 +465,7 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(const __grid_constant_
             }
           } else {
             T* o = static_cast<T*>(a.out) + row * a.ld_out + l;
-            if (real == (1u << VEC) - 1 && (reinterpret_cast<uintptr_t>(o) & 15) == 0) {
+            if (inside && (reinterpret_cast<uintptr_t>(o) & 15) == 0) {
               alignas(16) T t[VEC];
 #pragma unroll
               for (int i = 0; i < VEC; ++i) t[i] = narrow<T>(z[i]);
@@ -376,9 +481,11 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(const __grid_constant_
     }
   }
   if (MODE == MODE_FORWARD && a.stats) {
+    __syncwarp();
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) {
-      const Stats o{__shfl_down_sync(0xffffffffu, mine.m, d), __shfl_down_sync(0xffffffffu, mine.d, d),
+      const Stats o{__shfl_down_sync(0xffffffffu, mine.m, d),
+                    __shfl_down_sync(0xffffffffu, mine.d, d),
                     __shfl_down_sync(0xffffffffu, mine.s, d)};
       mine = join(mine, o);
     }
@@ -398,7 +505,10 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(const __grid_constant_
       const float log_d = logf(r.d);
       const float all = r.m == -INFINITY && r.d == 0.0f ? -INFINITY : r.m + log_d;
       if (a.lse) a.lse[row] = all;
-      if (a.logp) a.logp[row] = ignored ? 0.0f : bad ? NAN : label_z == -INFINITY ? -INFINITY : label_z - all;
+      if (a.logp)
+        a.logp[row] = ignored ? 0.0f
+                      : bad   ? NAN
+                              : label_z == -INFINITY ? -INFINITY : label_z - all;
       if (a.entropy) {
         const float H = all == -INFINITY ? 0.0f : log_d - kLn2 * __fdiv_rn(r.s, r.d);
         a.entropy[row] = ignored ? 0.0f : bad ? NAN : H;
@@ -439,25 +549,30 @@ int check(const flce_logits_params* p) {
   return FLCE_OK;
 }
 
-template <typename T, bool COUNT, int MODE>
+template <typename T, typename COUNTER, int MODE>
 int run(Args a, int sms, cudaStream_t st) {
-  auto kernel = logits_kernel<T, COUNT, MODE>;
+  auto kernel = logits_kernel<T, COUNTER, MODE>;
+  constexpr bool COUNT = !std::is_same_v<COUNTER, NoCounter>;
   constexpr int VEC = 16 / sizeof(T);
   constexpr int64_t wide = int64_t(kThreads) * VEC;
+  // whole 16-byte words of counters, whole vectors
+  constexpr int64_t unit = 16 / sizeof(typename COUNTER::Word) > VEC
+                               ? 16 / sizeof(typename COUNTER::Word) : VEC;
+  constexpr int64_t most = kRoom / sizeof(typename COUNTER::Word);
   const int64_t span = a.V + VEC - 1;  // with what may stand before a row
-  // As few blocks per row as fill the GPU three times over, but no more than have a vector for
-  // half of their threads; the counters' room asks for more.
+  // As few blocks per row as fill the GPU's block slots, but no more than have a vector for half
+  // of their threads; the counters' room asks for more.
   int size = 1;
-  while (size < kMaxCluster && ((a.R * size < 3 * sms && span > size * wide / 2) ||
-                                (COUNT && span > int64_t(size) * kMaxColumns)))
+  while (size < kMaxCluster && ((a.R * size < FLCE_LOGITS_FILL * sms && span > size * wide / 2) ||
+                                (COUNT && span > size * most)))
     size *= 2;
-  a.columns = cdiv(cdiv(span, size), VEC) * VEC;
+  a.columns = cdiv(cdiv(span, size), unit) * unit;
   a.passes = 1;
-  if (COUNT && a.columns > kMaxColumns) {
-    a.columns = kMaxColumns;
-    a.passes = cdiv(span, int64_t(size) * kMaxColumns);
+  if (COUNT && a.columns > most) {
+    a.columns = most;
+    a.passes = cdiv(span, size * most);
   }
-  const size_t smem = COUNT ? a.columns * 4 + a.n_bias * 8 : 0;
+  const size_t smem = COUNT ? a.columns * sizeof(typename COUNTER::Word) + a.n_bias * 8 : 0;
   // the same values from every thread that gets here, once per device
   static std::atomic<uint64_t> ready{0};
   int dev = 0;
@@ -465,7 +580,7 @@ int run(Args a, int sms, cudaStream_t st) {
   if (rc) return rc;
   if (!(ready.load() >> (dev & 63) & 1)) {
     if ((rc = rc_of(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kMaxColumns * 4 + kMaxBias * 8))) ||
+                                         kRoom + kMaxBias * 8))) ||
         (rc = rc_of(cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed,
                                          1))))
       return rc;
@@ -485,11 +600,17 @@ int run(Args a, int sms, cudaStream_t st) {
   return rc_of(cudaLaunchKernelEx(&cfg, kernel, a));
 }
 
+// count 0: no counters, else their bits
 template <typename T>
-int run_type(const Args& a, bool count, bool backward, int sms, cudaStream_t st) {
-  if (backward)
-    return count ? run<T, true, MODE_BACKWARD>(a, sms, st) : run<T, false, MODE_BACKWARD>(a, sms, st);
-  return count ? run<T, true, MODE_FORWARD>(a, sms, st) : run<T, false, MODE_FORWARD>(a, sms, st);
+int run_type(const Args& a, int count, bool backward, int sms, cudaStream_t st) {
+  if (count == 16)
+    return backward ? run<T, Counter<uint16_t>, MODE_BACKWARD>(a, sms, st)
+                    : run<T, Counter<uint16_t>, MODE_FORWARD>(a, sms, st);
+  if (count == 32)
+    return backward ? run<T, Counter<uint32_t>, MODE_BACKWARD>(a, sms, st)
+                    : run<T, Counter<uint32_t>, MODE_FORWARD>(a, sms, st);
+  return backward ? run<T, NoCounter, MODE_BACKWARD>(a, sms, st)
+                  : run<T, NoCounter, MODE_FORWARD>(a, sms, st);
 }
 
 // What both calls have in common: the checks and the kernel's arguments.
@@ -560,7 +681,8 @@ int launch(const flce_logits_params* p, Args a, bool backward, void* workspace, 
   if (p->R > 0) {
     const bool penalties = a.rep || a.freq || a.pres || a.rep1 != 1.0f || a.freq1 != 0.0f ||
                            a.pres1 != 0.0f;
-    const bool count = (a.tokens && penalties) || a.n_bias > 0;
+    if (!penalties) a.tokens = nullptr;
+    const int count = a.tokens && a.T >= 1 << 14 ? 32 : a.tokens || a.n_bias > 0 ? 16 : 0;
     rc = p->dtype == FLCE_F32    ? run_type<float>(a, count, backward, sms, st)
          : p->dtype == FLCE_BF16 ? run_type<__nv_bfloat16>(a, count, backward, sms, st)
                                  : run_type<__half>(a, count, backward, sms, st);
