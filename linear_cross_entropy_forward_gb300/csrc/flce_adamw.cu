@@ -44,7 +44,7 @@ struct Slot {
   const void* grad;
   int64_t n, offset;
   float decay;
-  int32_t kind;  // dtype * 2 + (gradient in fp32 beside a 16-bit parameter)
+  int16_t dtype, grad_dtype;
 };
 
 template <int CAP>
@@ -80,19 +80,6 @@ struct NormArgs {
 };
 
 // ------------------------------------------------------------------ elements
-template <typename T>
-__device__ __forceinline__ float widen(T x) {
-  if constexpr (std::is_same_v<T, float>) return x;
-  else if constexpr (std::is_same_v<T, __nv_bfloat16>) return __bfloat162float(x);
-  else return __half2float(x);
-}
-template <typename T>
-__device__ __forceinline__ T narrow(float x) {
-  if constexpr (std::is_same_v<T, float>) return x;
-  else if constexpr (std::is_same_v<T, __nv_bfloat16>) return __float2bfloat16_rn(x);
-  else return __float2half_rn(x);
-}
-
 __device__ __forceinline__ void ld_cs_v8(const float* p, float (&x)[kPer]) {
   asm volatile("ld.global.cs.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]),
@@ -100,48 +87,83 @@ __device__ __forceinline__ void ld_cs_v8(const float* p, float (&x)[kPer]) {
                : "l"(p));
 }
 
-// 8 elements from p, `n` of them there (the others 0)
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, int64_t n, float (&x)[kPer]) {
-  if (n >= kPer && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
-    if constexpr (sizeof(T) == 4) {
-      if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {
-        ld_cs_v8(reinterpret_cast<const float*>(p), x);
-        return;
-      }
-    }
-    alignas(16) T t[kPer];
-    uint4* q = reinterpret_cast<uint4*>(t);
-#pragma unroll
-    for (int i = 0; i < int(sizeof(T) * kPer / 16); ++i)
-      q[i] = __ldcs(reinterpret_cast<const uint4*>(p) + i);
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) x[i] = widen(t[i]);
+// Eight elements of any type as they are in memory (16-bit ones in q[0]).  The type is looked at
+// when they are converted, by branches that a warp takes together, so that there is one copy of
+// the rest of the code for all types.
+struct Raw {
+  uint4 q[2];
+};
+
+// `left` elements are there; what is not aligned, and a tensor's last, goes element by element
+// through memory of the thread's own, in rolled loops that take no registers from the rest.
+__device__ __forceinline__ void load_raw(const void* base, int64_t e, int64_t left, int dtype, Raw& r) {
+  const bool wide = dtype == FLCE_F32;
+  const uint8_t* p = static_cast<const uint8_t*>(base) + e * (wide ? 4 : 2);
+  if (left >= kPer && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+    r.q[0] = __ldcs(reinterpret_cast<const uint4*>(p));
+    if (wide) r.q[1] = __ldcs(reinterpret_cast<const uint4*>(p) + 1);
   } else {
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) x[i] = i < n ? widen(p[i]) : 0.0f;
+    Raw own;
+    own.q[0] = own.q[1] = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+    for (int i = 0; i < kPer && i < left; ++i) {
+      if (wide) reinterpret_cast<uint32_t*>(&own)[i] = reinterpret_cast<const uint32_t*>(p)[i];
+      else reinterpret_cast<uint16_t*>(&own)[i] = reinterpret_cast<const uint16_t*>(p)[i];
+    }
+    r = own;
   }
 }
-template <typename T>
-__device__ __forceinline__ void store8(T* p, int64_t n, const float (&x)[kPer]) {
-  if (n >= kPer && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
-    if constexpr (sizeof(T) == 4) {
-      if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {
-        st_global_cs_v8f(reinterpret_cast<float*>(p), x);
-        return;
-      }
+__device__ __forceinline__ void widen(const Raw& r, int dtype, float (&x)[kPer]) {
+  const uint32_t w[8] = {r.q[0].x, r.q[0].y, r.q[0].z, r.q[0].w,
+                         r.q[1].x, r.q[1].y, r.q[1].z, r.q[1].w};
+  if (dtype == FLCE_F32) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) x[i] = __uint_as_float(w[i]);
+  } else if (dtype == FLCE_BF16) {
+#pragma unroll
+    for (int i = 0; i < kPer; i += 2) {
+      x[i] = __uint_as_float(w[i / 2] << 16);
+      x[i + 1] = __uint_as_float(w[i / 2] & 0xffff0000u);
     }
-    alignas(16) T t[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) t[i] = narrow<T>(x[i]);
-    const uint4* q = reinterpret_cast<const uint4*>(t);
-#pragma unroll
-    for (int i = 0; i < int(sizeof(T) * kPer / 16); ++i)
-      __stcs(reinterpret_cast<uint4*>(p) + i, q[i]);
   } else {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (i < n) p[i] = narrow<T>(x[i]);
+    for (int i = 0; i < kPer; i += 2) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i / 2]));
+      x[i] = f.x;
+      x[i + 1] = f.y;
+    }
+  }
+}
+__device__ __forceinline__ void store_raw(void* base, int64_t e, int64_t left, int dtype,
+                                          const float (&x)[kPer]) {
+  const bool wide = dtype == FLCE_F32;
+  uint8_t* p = static_cast<uint8_t*>(base) + e * (wide ? 4 : 2);
+  uint32_t w[8] = {};
+  if (wide) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) w[i] = __float_as_uint(x[i]);
+  } else if (dtype == FLCE_BF16) {
+#pragma unroll
+    for (int i = 0; i < kPer; i += 2) w[i / 2] = pack_bf16x2(x[i], x[i + 1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kPer; i += 2) {
+      const __half2 h = __floats2half2_rn(x[i], x[i + 1]);
+      w[i / 2] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+  Raw r;
+  r.q[0] = make_uint4(w[0], w[1], w[2], w[3]);
+  r.q[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  if (left >= kPer && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+    __stcs(reinterpret_cast<uint4*>(p), r.q[0]);
+    if (wide) __stcs(reinterpret_cast<uint4*>(p) + 1, r.q[1]);
+  } else {
+#pragma unroll 1
+    for (int i = 0; i < kPer && i < left; ++i) {
+      if (wide) reinterpret_cast<uint32_t*>(p)[i] = reinterpret_cast<const uint32_t*>(&r)[i];
+      else reinterpret_cast<uint16_t*>(p)[i] = reinterpret_cast<const uint16_t*>(&r)[i];
+    }
   }
 }
 
@@ -198,8 +220,8 @@ __device__ __forceinline__ uint2 pack8(const float (&x)[kPer], const uint32_t (&
   for (int i = 0; i < kPer; ++i) top = fmaxf(top, fabsf(x[i]));
   top = block_max(top);
   const bool none = top < kTiny;
-  const float unit = none ? 0.0f : __fdiv_rn(448.0f, top);
-  scale = none ? 0.0f : __fdiv_rn(top, 448.0f);
+  const float unit = none ? 0.0f : 448.0f * fast_rcp(top);
+  scale = none ? 0.0f : top * (1.0f / 448.0f);
   float y[kPer];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
@@ -227,42 +249,77 @@ struct Coef {
   uint32_t key;
 };
 
-__device__ __forceinline__ float sqrt_approx(float x) {
+template <bool FTZ>
+__device__ __forceinline__ float root(float x) {
   float y;
-  asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));  // subnormals are kept
+  if constexpr (FTZ) asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  else asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
-// One thread's 8 elements: element e0 of the tensor on, the state's offset `at`.
-template <typename P, typename G, bool STATE8, bool MASTER>
-__device__ __forceinline__ void update8(const Slot& s, const StepArgs& a, const Coef& k,
-                                        int64_t e0) {
+// One thread's 8 elements as they are in memory.
+template <bool STATE8, bool MASTER>
+struct Fetched {
+  Raw g, w;
+  float master[MASTER ? kPer : 1], m[STATE8 ? 1 : kPer], v[STATE8 ? 1 : kPer];
+  uint2 cm, cs;
+  float scale_m, scale_s;
+};
+
+// Elements e0 on of the tensor, the states' (32-byte aligned) from s.offset + e0 on.  Past the
+// tensor's last block of 128 there is no state; the 16 lanes of a block leave or stay together.
+__device__ __forceinline__ bool has_state(const Slot& s, int64_t e0) {
+  return (e0 & ~int64_t(kBlockElems - 1)) < s.n;
+}
+
+template <bool STATE8, bool MASTER>
+__device__ __forceinline__ void fetch(const Slot& s, const StepArgs& a, int64_t e0,
+                                      Fetched<STATE8, MASTER>& f) {
+  if (!has_state(s, e0)) return;
   const int64_t left = s.n - e0, at = s.offset + e0;
-  // past the tensor's last block of 128 there is no state; 16 lanes leave or stay together
-  const bool in = (e0 & ~int64_t(kBlockElems - 1)) < s.n;
+  load_raw(s.grad, e0, left, s.grad_dtype, f.g);
+  if constexpr (MASTER) ld_cs_v8(a.master + at, f.master);
+  else load_raw(s.param, e0, left, s.dtype, f.w);
+  if constexpr (STATE8) {
+    f.cm = __ldcs(reinterpret_cast<const uint2*>(static_cast<uint8_t*>(a.m) + at));
+    f.cs = __ldcs(reinterpret_cast<const uint2*>(static_cast<uint8_t*>(a.v) + at));
+    f.scale_m = a.m_scale[at / kBlockElems];
+    f.scale_s = a.s_scale[at / kBlockElems];
+  } else {
+    ld_cs_v8(static_cast<const float*>(a.m) + at, f.m);
+    ld_cs_v8(static_cast<const float*>(a.v) + at, f.v);
+  }
+}
+
+template <bool STATE8, bool MASTER>
+__device__ __forceinline__ void update8(const Slot& s, const StepArgs& a, const Coef& k,
+                                        int64_t e0, const Fetched<STATE8, MASTER>& f) {
+  const int64_t left = s.n - e0, at = s.offset + e0;
+  const bool in = has_state(s, e0);
+  if (!STATE8 && !in) return;
   float g[kPer], w[kPer], m[kPer], v[kPer];
-  float scale_m = 0.0f, scale_s = 0.0f;
-  uint2 cm = make_uint2(0, 0), cs = make_uint2(0, 0);
-  if (in) {
-    load8(static_cast<const G*>(s.grad) + e0, left, g);
-    if constexpr (MASTER) load8(a.master + at, kPer, w);
-    else load8(static_cast<const P*>(s.param) + e0, left, w);
-    if constexpr (STATE8) {
-      cm = __ldcs(reinterpret_cast<const uint2*>(static_cast<uint8_t*>(a.m) + at));
-      cs = __ldcs(reinterpret_cast<const uint2*>(static_cast<uint8_t*>(a.v) + at));
-      scale_m = a.m_scale[at / kBlockElems];
-      scale_s = a.s_scale[at / kBlockElems];
-    } else {
-      load8(static_cast<const float*>(a.m) + at, kPer, m);
-      load8(static_cast<const float*>(a.v) + at, kPer, v);
+  float scale_m = f.scale_m, scale_s = f.scale_s;
+  widen(f.g, s.grad_dtype, g);
+  if constexpr (MASTER) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) w[i] = f.master[i];
+  } else {
+    widen(f.w, s.dtype, w);
+  }
+  if constexpr (STATE8) {
+    unpack8(f.cm, m);
+    unpack8(f.cs, v);
+    if (!in) {  // no part in another block's largest: zeros throughout
+      scale_m = scale_s = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) g[i] = m[i] = v[i] = 0.0f;
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) g[i] = w[i] = m[i] = v[i] = 0.0f;
-  }
-  if constexpr (STATE8) {
-    unpack8(cm, m);
-    unpack8(cs, v);
+    for (int i = 0; i < kPer; ++i) {
+      m[i] = f.m[i];
+      v[i] = f.v[i];
+    }
   }
   const float shrink = 1.0f - k.lr * s.decay;
   const uint64_t shrink2 = f2_pack(shrink, shrink), minus = f2_pack(-k.step_size, -k.step_size),
@@ -281,7 +338,8 @@ __device__ __forceinline__ void update8(const Slot& s, const StepArgs& a, const 
     const uint64_t v2 = f2_fma(y, y, old);
     float v0, v1, d0, d1;
     f2_unpack(v2, v0, v1);
-    const float s0 = sqrt_approx(v0), s1 = sqrt_approx(v1);
+    // 8 bits: a root below 2^-63 is 0 (v is below fp32's normal range there)
+    const float s0 = root<STATE8>(v0), s1 = root<STATE8>(v1);
     f2_unpack(f2_fma(f2_pack(s0, s1), root2, eps2), d0, d1);
     const uint64_t u = f2_mul(m2, f2_pack(fast_rcp(d0), fast_rcp(d1)));
     f2_unpack(f2_fma(u, minus, f2_mul(f2_pack(w[i], w[i + 1]), shrink2)), w[i], w[i + 1]);
@@ -289,6 +347,7 @@ __device__ __forceinline__ void update8(const Slot& s, const StepArgs& a, const 
     v[i] = STATE8 ? s0 : v0;
     v[i + 1] = STATE8 ? s1 : v1;
   }
+  uint2 cm, cs;
   if constexpr (STATE8) {
     uint32_t r1[kPer], r2[kPer];
     const uint32_t key = mix(k.key + static_cast<uint32_t>(static_cast<uint64_t>(at) >> 32));
@@ -302,13 +361,8 @@ __device__ __forceinline__ void update8(const Slot& s, const StepArgs& a, const 
     cs = pack8<true>(v, r2, scale_s);
   }
   if (!in) return;
-  if constexpr (MASTER) {
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (i >= left) w[i] = 0.0f;  // the padding of the states stays zero
-    store8(a.master + at, kPer, w);
-  }
-  store8(static_cast<P*>(s.param) + e0, left, w);
+  if constexpr (MASTER) st_global_cs_v8f(a.master + at, w);
+  store_raw(s.param, e0, left, s.dtype, w);
   if constexpr (STATE8) {
     __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.m) + at), cm);
     __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.v) + at), cs);
@@ -317,8 +371,8 @@ __device__ __forceinline__ void update8(const Slot& s, const StepArgs& a, const 
       a.s_scale[at / kBlockElems] = scale_s;
     }
   } else {
-    store8(static_cast<float*>(a.m) + at, kPer, m);
-    store8(static_cast<float*>(a.v) + at, kPer, v);
+    st_global_cs_v8f(static_cast<float*>(a.m) + at, m);
+    st_global_cs_v8f(static_cast<float*>(a.v) + at, v);
   }
 }
 
@@ -337,8 +391,14 @@ __device__ __forceinline__ int find_run(const Table<CAP>& t, uint32_t& u, uint32
   return lo;
 }
 
+#ifndef FLCE_ADAMW_B8
+#define FLCE_ADAMW_B8 4
+#endif
+#ifndef FLCE_ADAMW_B32
+#define FLCE_ADAMW_B32 4
+#endif
 template <bool STATE8, bool MASTER, int CAP>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, STATE8 ? FLCE_ADAMW_B8 : FLCE_ADAMW_B32)
     adamw_kernel(const __grid_constant__ Table<CAP> t, const __grid_constant__ StepArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t step = *a.step + 1;
@@ -366,25 +426,24 @@ __global__ void __launch_bounds__(kThreads)
     k.key = mix(a.seed + 0x9E3779B9u * static_cast<uint32_t>(step));
     uint32_t u, end;
     int i = find_run(t, u, end);
-    for (; u < end; ++u) {
+    while (u < end) {
       while (i + 1 < t.count && t.first[i + 1] <= u) ++i;
       const Slot& s = t.slot[i];
-      const int64_t e0 = static_cast<int64_t>(u - t.first[i]) * kUnit + threadIdx.x * kPer;
-      switch (s.kind) {
-        case 2 * FLCE_BF16:
-          update8<__nv_bfloat16, __nv_bfloat16, STATE8, MASTER>(s, a, k, e0);
-          break;
-        case 2 * FLCE_BF16 + 1:
-          update8<__nv_bfloat16, float, STATE8, MASTER>(s, a, k, e0);
-          break;
-        case 2 * FLCE_F16:
-          update8<__half, __half, STATE8, MASTER>(s, a, k, e0);
-          break;
-        case 2 * FLCE_F16 + 1:
-          update8<__half, float, STATE8, MASTER>(s, a, k, e0);
-          break;
-        default:
-          update8<float, float, STATE8, MASTER>(s, a, k, e0);
+      const uint32_t stop = i + 1 < t.count && t.first[i + 1] < end ? t.first[i + 1] : end;
+      int64_t e0 = static_cast<int64_t>(u - t.first[i]) * kUnit + threadIdx.x * kPer;
+      Fetched<STATE8, MASTER> f;
+      if (STATE8) fetch(s, a, e0, f);
+#pragma unroll 1
+      for (; u < stop; ++u, e0 += kUnit) {
+        if constexpr (STATE8) {
+          // the next unit is asked for ahead of the arithmetic, which is as long as the bytes take
+          const Fetched<STATE8, MASTER> now = f;
+          if (u + 1 < stop) fetch(s, a, e0 + kUnit, f);
+          update8(s, a, k, e0, now);
+        } else {
+          fetch(s, a, e0, f);
+          update8(s, a, k, e0, f);
+        }
       }
     }
   }
@@ -415,23 +474,26 @@ __device__ __forceinline__ float squares(const float (&x)[kPer], float scale) {
 }
 
 // `units` units of one tensor from element e0 on (this thread's first)
-template <typename G>
-__device__ __forceinline__ double sum_units(const void* grad, int64_t n, int64_t e0, int64_t units,
-                                            float scale) {
-  const G* p = static_cast<const G*>(grad);
+__device__ __forceinline__ double sum_units(const Slot& s, int64_t e0, int64_t units, float scale) {
   double total = 0.0;
   for (int64_t u = 0; u < units; u += kNormFold) {
     const int64_t end = u + kNormFold < units ? u + kNormFold : units;
     float part[kNormDepth] = {};
+#pragma unroll 1
     for (int64_t v = u; v < end; v += kNormDepth) {
-      float x[kNormDepth][kPer];
+      Raw r[kNormDepth];
 #pragma unroll
       for (int d = 0; d < kNormDepth; ++d) {
         const int64_t e = e0 + (v + d) * kUnit;
-        load8(p + e, v + d < end ? n - e : 0, x[d]);
+        r[d].q[0] = r[d].q[1] = make_uint4(0, 0, 0, 0);
+        if (v + d < end && e < s.n) load_raw(s.grad, e, s.n - e, s.grad_dtype, r[d]);
       }
 #pragma unroll
-      for (int d = 0; d < kNormDepth; ++d) part[d] += squares(x[d], scale);
+      for (int d = 0; d < kNormDepth; ++d) {
+        float x[kPer];
+        widen(r[d], s.grad_dtype, x);
+        part[d] += squares(x, scale);
+      }
     }
     total += (part[0] + part[1]) + (part[2] + part[3]);
   }
@@ -461,11 +523,7 @@ __global__ void __launch_bounds__(kThreads)
     const Slot& s = t.slot[i];
     const uint32_t stop = i + 1 < t.count && t.first[i + 1] < end ? t.first[i + 1] : end;
     const int64_t e0 = static_cast<int64_t>(u - t.first[i]) * kUnit + threadIdx.x * kPer;
-    const bool f32 = (s.kind & 1) || s.kind == 2 * FLCE_F32;
-    total += f32 ? sum_units<float>(s.grad, s.n, e0, stop - u, a.scale)
-             : s.kind == 2 * FLCE_BF16
-                 ? sum_units<__nv_bfloat16>(s.grad, s.n, e0, stop - u, a.scale)
-                 : sum_units<__half>(s.grad, s.n, e0, stop - u, a.scale);
+    total += sum_units(s, e0, stop - u, a.scale);
     u = stop;
   }
   total = block_sum(total);
@@ -546,7 +604,7 @@ int fill(Table<CAP>* out, const flce_adamw_params* p, const flce_adamw_tensor* t
     if (units + more >= kMaxUnits) return FLCE_ERR_BAD_SHAPE;
     out->first[out->count] = static_cast<uint32_t>(units);
     out->slot[out->count] = Slot{x.param, x.grad, x.n, x.offset, x.weight_decay,
-                                 2 * x.dtype + (x.grad_dtype != x.dtype)};
+                                 static_cast<int16_t>(x.dtype), static_cast<int16_t>(x.grad_dtype)};
     units += more;
     ++out->count;
   }
@@ -679,7 +737,7 @@ int flce_adamw_step(const flce_adamw_params* p, const flce_adamw_tensor* tensors
   const bool state8 = p->state_bits == 8;
   if (state8 && (!exp_avg_scale || !exp_rms_scale)) return FLCE_ERR_BAD_ARG;
   if ((p->max_norm > 0.0 || p->skip_nonfinite) && !norm) return FLCE_ERR_BAD_ARG;
-  if ((addr(master) | addr(exp_avg) | addr(exp_avg_sq)) & 15 ||
+  if ((addr(master) | addr(exp_avg) | addr(exp_avg_sq)) & 31 ||
       (addr(exp_avg_scale) | addr(exp_rms_scale) | addr(lr) | addr(norm)) & 3 || addr(step) & 7 ||
       addr(workspace) & 255)
     return FLCE_ERR_ALIGN;

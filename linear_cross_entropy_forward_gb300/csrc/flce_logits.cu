@@ -7,13 +7,18 @@
 // n counts a token among the row's generated tokens, seen says whether it is among prompt or
 // generated ones.  One pass over the logits, so bound by their bytes, in and out.
 //
-// A row is shared by a cluster of blocks, each with a run of columns and a 32-bit counter per
-// column in its shared memory.  The row's tokens are read once: each block takes a share of
-// them and adds into the counter of the block that has the column, over distributed shared
-// memory.  Biases only mark their columns' counters; a marked column sums its biases from the
-// row's list, in the list's order.  The running maximum m, d = sum 2^u and s = sum 2^u u with
-// u = log2(e) (z - m) stay in registers, are joined in the block and then in the cluster, in a
-// fixed order:  lse = m + ln d,  H = ln d - ln 2 s / d.
+// A row is shared by a cluster of blocks, each with a run of columns and a counter per column in its
+// shared memory.  Each block reads all of the row's tokens, which come from L2, and counts those of
+// its own columns.  (Reading each token once and adding into the other blocks' counters over
+// distributed shared memory took 5 to 8 cycles of an SM per token; laying the tokens out by owner
+// and fetching them, three meetings of the cluster: 384 x 256000 in bf16 after 1 and after 8192
+// tokens 114 and 250 us, against 79 and 174.  A list of the changed columns, worked off by a thread per
+// entry beside the pass over all logits: 87 and 240.)  Biases only mark their columns' counters; a
+// marked column sums its biases from the row's list, in the list's order.
+//
+// The running maximum m, d = sum 2^u and s = sum 2^u u with u = log2(e) (z - m) stay in registers, are
+// joined in the block and then in the cluster, in a fixed order:  lse = m + ln d,
+// H = ln d - ln 2 s / d.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -28,26 +33,36 @@
 namespace flce {
 namespace {
 
-#ifndef FLCE_LOGITS_THREADS
-#define FLCE_LOGITS_THREADS 256
-#endif
 #ifndef FLCE_LOGITS_FILL
-#define FLCE_LOGITS_FILL 4
+#define FLCE_LOGITS_FILL 6
+#endif
+#ifndef FLCE_LOGITS_STAGE
+#define FLCE_LOGITS_STAGE 16384
 #endif
 #ifndef FLCE_LOGITS_ROOM
-#define FLCE_LOGITS_ROOM 65536
+#define FLCE_LOGITS_ROOM 32768
 #endif
-constexpr int kThreads = FLCE_LOGITS_THREADS;
+#ifndef FLCE_LOGITS_B
+#define FLCE_LOGITS_B 3
+#endif
+#ifndef FLCE_LOGITS_DEEP
+#define FLCE_LOGITS_DEEP 4
+#endif
+#ifndef FLCE_LOGITS_T
+#define FLCE_LOGITS_T 256
+#endif
+constexpr int kThreads = FLCE_LOGITS_T;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBatch = 4;            // vectors in flight per thread
 constexpr int kMaxCluster = 16;
-constexpr int kRoom = FLCE_LOGITS_ROOM;  // bytes of counters per block
+constexpr int kStage = FLCE_LOGITS_STAGE;  // bytes of logits per copy into shared memory, two in flight
+constexpr int kRoom = FLCE_LOGITS_ROOM;    // bytes of counters per block
 constexpr int kMaxBias = 2048;       // entries of a row's list: 16 KB of shared memory
 
 // Counters: occurrences among the generated tokens, and flags of the prompt's tokens and of
 // columns with a bias.  16 bits hold the count of histories below 2^14 tokens.
 struct NoCounter {
   using Word = uint16_t;
+  static constexpr uint32_t kSeen = 0, kBiased = 0, kCount = 0;
 };
 template <typename W>
 struct Counter {
@@ -83,20 +98,55 @@ struct Args {
   const float* g_logp;
   const float* g_entropy;
   uint32_t* err;
-  int64_t columns, passes;  // per block and pass; runs of whole vectors
+  int64_t columns, room;  // per block, and of them at a time (whole vectors)
+  int32_t passes, stage_bytes;
   int32_t ids64, lens64, bias64, mask_kind, out_f32, stats;
 };
 
 enum { MODE_FORWARD = 0, MODE_BACKWARD = 1 };
 
+// The 4 or 8 values of 16 bytes.
 template <typename T>
-__device__ __forceinline__ float widen(T x) {
+__device__ __forceinline__ void widen(const uint4& q, float (&x)[16 / sizeof(T)]) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (std::is_same_v<T, float>) {
+      x[i] = __uint_as_float(w[i]);
+    } else if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    } else {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      x[2 * i] = f.x;
+      x[2 * i + 1] = f.y;
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ uint4 narrow(const float (&x)[16 / sizeof(T)]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (std::is_same_v<T, float>) {
+      w[i] = __float_as_uint(x[i]);
+    } else if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+      w[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+    } else {
+      const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <typename T>
+__device__ __forceinline__ float widen1(T x) {
   if constexpr (std::is_same_v<T, float>) return x;
   else if constexpr (std::is_same_v<T, __nv_bfloat16>) return __bfloat162float(x);
   else return __half2float(x);
 }
 template <typename T>
-__device__ __forceinline__ T narrow(float x) {
+__device__ __forceinline__ T narrow1(float x) {
   if constexpr (std::is_same_v<T, float>) return x;
   else if constexpr (std::is_same_v<T, __nv_bfloat16>) return __float2bfloat16_rn(x);
   else return __float2half_rn(x);
@@ -112,408 +162,599 @@ struct Stats {
   float m, d, s;
 };
 
-__device__ __forceinline__ Stats join(const Stats& a, const Stats& b) {
-  const float m = fmaxf(a.m, b.m);
-  Stats r{m, a.d + b.d, a.s + b.s};
-  if (m == -INFINITY) return r;
-  // a part without anything has d = s = 0: its exponent may be anything finite
-  const float ta = a.m == -INFINITY ? 0.0f : (a.m - m) * kLog2e;
-  const float tb = b.m == -INFINITY ? 0.0f : (b.m - m) * kLog2e;
-  const float ea = fast_ex2(ta), eb = fast_ex2(tb);
-  r.d = fmaf(ea, a.d, eb * b.d);
-  r.s = (ea != 0.0f ? ea * fmaf(ta, a.d, a.s) : 0.0f) +
-        (eb != 0.0f ? eb * fmaf(tb, b.d, b.s) : 0.0f);
-  return r;
-}
-
-// What a row's columns are changed by.
-struct Row {
-  float rep, inv_rep, freq, pres, inv_temp;
-  const uint8_t* mask;
-};
-
-// Address of a shared variable of this block's in block `rank` of the cluster.
-__device__ __forceinline__ uint32_t remote(const void* p, uint32_t rank) {
-  return mapa_shared(smem_u32(p), rank);
-}
-__device__ __forceinline__ void red_add(uint32_t a, uint32_t v) {
-  asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
-}
-__device__ __forceinline__ void red_or(uint32_t a, uint32_t v) {
-  asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+// The join of lanes 0 to n - 1 (a power of two; the others' are not looked at by them), in every one
+// of them: first the largest m, then sums in its units.
+__device__ __forceinline__ Stats join_warp(Stats x, int n) {
+  float m = x.m;
+  for (int j = n / 2; j > 0; j >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, j));
+  if (m != -INFINITY) {
+    const float t = x.m == -INFINITY ? 0.0f : (x.m - m) * kLog2e;
+    const float e = fast_ex2(t);
+    x.s = e != 0.0f ? e * fmaf(t, x.d, x.s) : 0.0f;
+    x.d *= e;
+  }
+  for (int j = n / 2; j > 0; j >>= 1) {
+    x.d += __shfl_xor_sync(0xffffffffu, x.d, j);
+    x.s += __shfl_xor_sync(0xffffffffu, x.s, j);
+  }
+  return Stats{m, x.d, x.s};
 }
 __device__ __forceinline__ void st_remote(uint32_t a, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
-}
-// All blocks of the cluster, whatever paths the threads of a warp came by.
-__device__ __forceinline__ void meet() {
-  __syncwarp();
-  cluster_sync();
 }
 __device__ __forceinline__ uint32_t cluster_size() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
   return r;
 }
-
-// VEC mask bytes at p (that of logit l of a row of V) as bits: bit i set where byte i is not 0.
-template <int VEC>
-__device__ __forceinline__ uint32_t byte_mask(const uint8_t* p, int64_t l, int64_t V) {
-  uint32_t w[VEC / 4];
-  const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 3);
-  if (off == 0 || (l >= 4 && l + VEC + 4 <= V)) {  // whole words inside the row
-    const uint32_t* q = reinterpret_cast<const uint32_t*>(p - off);
-    uint32_t lo = __ldg(q);
-#pragma unroll
-    for (int j = 0; j < VEC / 4; ++j) {
-      const uint32_t hi = j + 1 < VEC / 4 || off ? __ldg(q + j + 1) : 0u;
-      w[j] = __funnelshift_r(lo, hi, 8 * off);
-      lo = hi;
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < VEC / 4; ++j)
-      w[j] = p[4 * j] | p[4 * j + 1] << 8 | p[4 * j + 2] << 16 | uint32_t(p[4 * j + 3]) << 24;
-  }
-  uint32_t bits = 0;
-#pragma unroll
-  for (int j = 0; j < VEC / 4; ++j) {
-    // bit 7 of each byte that is not 0, then the four of them side by side
-    const uint32_t t = ((((w[j] & 0x7f7f7f7fu) + 0x7f7f7f7fu) | w[j]) >> 7) & 0x01010101u;
-    bits |= ((t * 0x01020408u) >> 24 & 15u) << (4 * j);
-  }
-  return bits;
+// The cluster's barrier in two halves (every thread of every block, in warps).
+__device__ __forceinline__ void cluster_arrive() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
+__device__ __forceinline__ void cluster_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// One more (FLAG: seen) at the counter of column `at` where there is one; without a branch, as some
+// lane of a warp nearly always has a column here.
+template <typename COUNTER, bool FLAG>
+__device__ __forceinline__ void bump(uint32_t at, uint32_t columns, uint32_t counters) {
+  constexpr bool WIDE = sizeof(typename COUNTER::Word) == 4;
+  const uint32_t to = counters + (WIDE ? at * 4 : (at >> 1) * 4);
+  const uint32_t one = FLAG ? COUNTER::kSeen : 1u, value = !WIDE && (at & 1) ? one << 16 : one;
+  if (FLAG)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.lt.u32 p, %0, %1;\n\t"
+        "@p red.shared::cta.or.b32 [%2], %3;\n\t}" ::"r"(at), "r"(columns), "r"(to), "r"(value)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.lt.u32 p, %0, %1;\n\t"
+        "@p red.shared::cta.add.u32 [%2], %3;\n\t}" ::"r"(at), "r"(columns), "r"(to), "r"(value)
+        : "memory");
+}
+
+// Counts tokens [t0, t1) of a row that fall on the `columns` columns from id `first` on (FLAG: marks
+// them as seen), 16 bytes of tokens at a time, the next ones asked for ahead.  The counter of an id
+// outside the row is never looked at.
+template <typename COUNTER, bool FLAG, typename ID>
+__device__ __forceinline__ void count(const ID* tokens, int t0, int t1, int first, uint32_t columns,
+                                      uint32_t counters) {
+  constexpr int kIds = 16 / sizeof(ID), kDeep = FLCE_LOGITS_DEEP;
+  const uint32_t none = 0xffffffffu;  // no column
+  auto add = [&](const uint4& q) {
+    if constexpr (sizeof(ID) == 8) {  // the upper half of an id of the row is 0
+      bump<COUNTER, FLAG>(q.y ? none : q.x - first, columns, counters);
+      bump<COUNTER, FLAG>(q.w ? none : q.z - first, columns, counters);
+    } else {
+      bump<COUNTER, FLAG>(q.x - first, columns, counters);
+      bump<COUNTER, FLAG>(q.y - first, columns, counters);
+      bump<COUNTER, FLAG>(q.z - first, columns, counters);
+      bump<COUNTER, FLAG>(q.w - first, columns, counters);
+    }
+  };
+  if (t1 <= t0) return;
+  // whole 16-byte words from a to b, a few tokens before and behind them
+  const int skew = static_cast<int>((reinterpret_cast<uintptr_t>(tokens + t0) & 15) / sizeof(ID));
+  const int a = min(skew ? t0 + kIds - skew : t0, t1), words = (t1 - a) / kIds, b = a + words * kIds;
+  const int tid = threadIdx.x;
+  if (tid < 2 * kIds) {
+    const int t = tid < kIds ? t0 + tid : b + tid - kIds;
+    if (tid < kIds ? t < a : t < t1) {
+      const int64_t id = tokens[t];
+      bump<COUNTER, FLAG>(id < 0 || id >> 31 ? none : static_cast<uint32_t>(id) - first, columns,
+                          counters);
+    }
+  }
+  const uint4* from = reinterpret_cast<const uint4*>(tokens + a);
+  const uint4 nothing = make_uint4(none, none, none, none);
+  uint4 next[kDeep];
+#pragma unroll
+  for (int j = 0; j < kDeep; ++j)
+    next[j] = tid + j * kThreads < words ? __ldg(from + tid + j * kThreads) : nothing;
+#pragma unroll 1
+  for (int i = 0; i < words; i += kDeep * kThreads) {
+    uint4 q[kDeep];
+#pragma unroll
+    for (int j = 0; j < kDeep; ++j) q[j] = next[j];
+    const int n = i + kDeep * kThreads + tid;
+#pragma unroll
+    for (int j = 0; j < kDeep; ++j)
+      next[j] = n + j * kThreads < words ? __ldg(from + n + j * kThreads) : nothing;
+#pragma unroll
+    for (int j = 0; j < kDeep; ++j) add(q[j]);
+  }
+}
+
+// Four mask bytes as bits: bit i set where byte i is not 0.
+__device__ __forceinline__ uint32_t byte_bits(uint32_t w) {
+  // bit 0 of each byte that is not 0, then the four of them side by side
+  const uint32_t t = ((((w & 0x7f7f7f7fu) + 0x7f7f7f7fu) | w) >> 7) & 0x01010101u;
+  return (t * 0x01020408u) >> 24 & 15u;
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          dst),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// What all of a block needs to know of its row, found out by one thread.
+struct RowArgs {
+  float rep, inv_rep, freq, pres, inv_temp;
+  float lse, g, h, ent;      // the gradient: -p (g + h (ln p + H)) + g [label]
+  int label, length, prompt;
+  int ignored, bad, zero;    // zero: a gradient of zeros
+};
+
+template <bool COUNT, bool BACKWARD>
+__device__ __forceinline__ void read_row(const Args& a, int64_t row, RowArgs& r) {
+  const int64_t y = a.labels ? a.labels[row] : -1;
+  const float temp = a.temp ? a.temp[row] : a.temp1;
+  if (COUNT) {
+    r.rep = a.rep ? a.rep[row] : a.rep1;
+    r.freq = a.freq ? a.freq[row] : a.freq1;
+    r.pres = a.pres ? a.pres[row] : a.pres1;
+    const int64_t n = !a.tokens ? 0 : a.lengths ? whole(a.lengths, row, a.lens64) : a.T;
+    const int64_t q = a.prompt_lens ? whole(a.prompt_lens, row, a.lens64) : 0;
+    r.inv_rep = __fdiv_rn(1.0f, r.rep);
+    r.length = static_cast<int>(n < 0 ? 0 : n < a.T ? n : a.T);
+    if (r.rep == 1.0f && r.freq == 0.0f && r.pres == 0.0f) r.length = 0;
+    r.prompt = static_cast<int>(q < 0 ? 0 : q < r.length ? q : r.length);
+  }
+  r.ignored = a.labels && y == a.ignore_index;
+  r.label = y >= 0 && y < a.V ? static_cast<int>(y) : -1;
+  r.bad = a.labels && !r.ignored && r.label < 0;
+  r.inv_temp = temp > 0.0f ? __fdiv_rn(1.0f, temp) : 1.0f;
+  r.zero = 0;
+  if (BACKWARD) {
+    r.lse = a.lse[row];
+    r.g = a.g_logp ? a.g_logp[row] : 0.0f;
+    r.h = a.g_entropy ? a.g_entropy[row] : 0.0f;
+    r.ent = a.entropy ? a.entropy[row] : 0.0f;
+    r.zero = r.ignored || r.lse == -INFINITY;
+  }
+}
+
+// A running maximum and the sums below it, of one thread.
+struct Running {
+  float top = -INFINITY, d = 0.0f, s = 0.0f;
+
+  template <int N>
+  __device__ __forceinline__ void add(const float (&z)[N], bool entropy) {
+    float m = z[0];
+    if constexpr (N > 1) {
+      m = fmaxf(z[0], z[1]);
+#pragma unroll
+      for (int i = 2; i + 1 < N; i += 2) m = fmax3(m, z[i], z[i + 1]);
+    }
+    if (m > top) {
+      const float t = (top - m) * kLog2e;  // -inf before the first
+      const float e = fast_ex2(t);
+      s = e != 0.0f ? e * fmaf(t, d, s) : 0.0f;
+      d *= e;
+      top = m;
+    }
+    // nothing yet: -inf alone, or NaN, which makes d NaN
+    const float base = top == -INFINITY ? 0.0f : top;
+    if constexpr (N == 1) {
+      const float u = (z[0] - base) * kLog2e, e = fast_ex2(u);
+      d += e;
+      s = fmaf(e, fmaxf(u, -200.0f), s);
+    } else {
+      const uint64_t base2 = f2_pack(-base, -base), log2 = f2_pack(kLog2e, kLog2e);
+      uint64_t sum = 0, dot = 0;
+#pragma unroll
+      for (int i = 0; i < N; i += 2) {
+        float u0, u1;
+        f2_unpack(f2_mul(f2_add(f2_pack(z[i], z[i + 1]), base2), log2), u0, u1);
+        const uint64_t e = f2_pack(fast_ex2(u0), fast_ex2(u1));
+        sum = f2_add(sum, e);
+        if (entropy)  // 2^u is 0 below, and u may be -inf
+          dot = f2_fma(e, f2_pack(fmaxf(u0, -200.0f), fmaxf(u1, -200.0f)), dot);
+      }
+      float a0, a1;
+      f2_unpack(sum, a0, a1);
+      d += a0 + a1;
+      if (entropy) {
+        f2_unpack(dot, a0, a1);
+        s += a0 + a1;
+      }
+    }
+  }
+};
 
 // Columns are numbered from the row's last 16-byte boundary at or before its first logit, so
 // that vectors of VEC columns are aligned in every row; `pre` columns before the row are not
-// there.  Column c of that numbering is logit c - pre.
+// there.  Column c of that numbering is logit c - pre.  A block's columns go by passes of as many
+// as it has counters for, a pass by copies of kStage bytes, two on their way at a time; the vectors
+// at a row's ends that are not whole are done element by element.
 template <typename T, typename COUNTER, int MODE>
-__global__ void __launch_bounds__(kThreads, 1024 / kThreads)
+__global__ void __launch_bounds__(kThreads, FLCE_LOGITS_B)
     logits_kernel(const __grid_constant__ Args a) {
   constexpr int VEC = 16 / sizeof(T);
-  constexpr bool COUNT = !std::is_same_v<COUNTER, NoCounter>;
+  constexpr uint32_t kAll = (1u << VEC) - 1;
+  constexpr int kColumns = kStage / sizeof(T);  // per copy
+  constexpr bool COUNT = !std::is_same_v<COUNTER, NoCounter>, BACKWARD = MODE == MODE_BACKWARD;
   using Word = typename COUNTER::Word;
-  extern __shared__ __align__(16) uint8_t shared[];  // counters, then the biases' columns and values
+  // two copies of logits, counters, the biases' columns and values
+  extern __shared__ __align__(16) uint8_t shared[];
+  __shared__ uint64_t landed[2];
+  __shared__ int gave_up;
+  __shared__ RowArgs r;
   __shared__ Stats part[kWarps];
-  __shared__ Stats from[kMaxCluster];
+  __shared__ float4 from[kMaxCluster];  // each block's statistics and, if it has it, the label's z
   __shared__ float label_z;
-  Word* counters = reinterpret_cast<Word*>(shared);
+  __shared__ uint32_t mask_bits[2][kColumns / 32];  // of two copies, a bit per column
   const uint32_t rank = cluster_ctarank(), size = cluster_size();
   const int64_t row = blockIdx.x / size;
+  const int V = static_cast<int>(a.V), tid = threadIdx.x;
   const T* x = static_cast<const T*>(a.logits) + row * a.ld;
   const int pre = static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
-  const int64_t span = a.V + pre;
-  const int64_t per_pass = a.columns * size;
-  int* bias_col = reinterpret_cast<int*>(shared + a.columns * sizeof(Word));
-  float* bias_val = reinterpret_cast<float*>(bias_col + a.n_bias);
+  const int span = V + pre, columns = static_cast<int>(a.columns), room = static_cast<int>(a.room);
+  const int n_bias = static_cast<int>(a.n_bias);
+  uint8_t* counters = shared + a.stage_bytes;
+  int* bias_col = reinterpret_cast<int*>(counters + (COUNT ? room * sizeof(Word) : 0));
+  float* bias_val = reinterpret_cast<float*>(bias_col + n_bias);
+  const uint8_t* mask = static_cast<const uint8_t*>(a.allowed) +
+                        row * a.ld_allowed * (a.mask_kind == 2 ? 4 : 1);
+  uint8_t* out = static_cast<uint8_t*>(a.out);
+  if (out) out += row * a.ld_out * (a.out_f32 ? 4 : sizeof(T));
+  const int begin = static_cast<int>(rank) * columns, end = min(begin + columns, span);
+  // whole vectors of the row among the block's columns
+  const int in0 = max(begin, pre ? VEC : 0), in1 = max(in0, min(end, span / VEC * VEC));
+  const int copies = (in1 - in0 + kColumns - 1) / kColumns;
 
-  // the first vectors are asked for before anything is waited for
-  alignas(16) T in[kBatch][VEC];
-  auto load = [&](int64_t v0, int64_t c1) {
+  auto copy = [&](int k) {  // by one thread
+    const int c = in0 + k * kColumns;
+    const uint32_t bytes = static_cast<uint32_t>(min(kColumns, in1 - c)) * sizeof(T);
+    mbar_arrive_expect_tx(&landed[k & 1], bytes);
+    bulk_load(smem_u32(shared) + (k & 1) * kStage, x + (c - pre), bytes, &landed[k & 1]);
+  };
+  if (tid == 0) {
+    mbar_init(&landed[0], 1);
+    mbar_init(&landed[1], 1);
+    gave_up = 0;
+    label_z = -INFINITY;
+    fence_mbar_init();
+    if (copies > 0) copy(0);
+    if (copies > 1) copy(1);
+  }
+  // The mask of a copy's columns: a thread's 32 of them are asked for a copy ahead, and made bits of
+  // when the copy before is done.
+  static_assert(kColumns / 32 <= kThreads, "a word of mask bits per thread");
+  uint32_t raw[9];
+  int raw_off = 0;  // bytes: where they begin in raw; -1: raw[0] is the bits already
+  auto load_mask = [&](int k) {
+    const int c = in0 + k * kColumns + 32 * tid, l = c - pre;
+    if (k >= copies || c >= min(in0 + (k + 1) * kColumns, in1)) return;
+    if (a.mask_kind == 2) {
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(mask) + (l >> 5);
+      raw[0] = __ldg(w);
+      raw[1] = (l & 31) && ((l >> 5) + 1) * 32 < V ? __ldg(w + 1) : 0u;
+    } else {
+      const uint8_t* p = mask + l;
+      raw_off = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 3);
+      if (l + 32 <= V && (raw_off == 0 || (l >= 4 && l + 36 <= V))) {  // whole words inside the row
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(p - raw_off);
+        if ((reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+          const uint4 u = __ldcs(reinterpret_cast<const uint4*>(w)),
+                      v = __ldcs(reinterpret_cast<const uint4*>(w) + 1);
+          raw[0] = u.x; raw[1] = u.y; raw[2] = u.z; raw[3] = u.w;
+          raw[4] = v.x; raw[5] = v.y; raw[6] = v.z; raw[7] = v.w;
+          raw[8] = 0;
+        } else {
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      const int64_t c = v0 + int64_t(b) * kThreads * VEC, l = c - pre;
-      if (c >= c1) continue;
-      if (l >= 0 && l + VEC <= a.V) {
-        *reinterpret_cast<uint4*>(in[b]) = __ldcs(reinterpret_cast<const uint4*>(x + l));
+          for (int j = 0; j < 8; ++j) raw[j] = __ldcs(w + j);
+          raw[8] = raw_off ? __ldcs(w + 8) : 0u;
+        }
       } else {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i)
-          in[b][i] = l + i >= 0 && l + i < a.V ? x[l + i] : narrow<T>(0.0f);
+        uint32_t bits = 0;
+#pragma unroll 1
+        for (int i = 0; i < 32 && l + i < V; ++i) bits |= (p[i] != 0 ? 1u : 0u) << i;
+        raw[0] = bits;
+        raw_off = -1;
       }
     }
   };
-  {
-    const int64_t c0 = rank * a.columns;
-    load(c0 + threadIdx.x * VEC, c0 + a.columns < span ? c0 + a.columns : span);
-  }
-
-  int64_t label = -1;
-  bool ignored = false, bad = false;
-  if (a.labels) {
-    const int64_t y = a.labels[row];
-    ignored = y == a.ignore_index;
-    if (y >= 0 && y < a.V) label = y;
-    else bad = !ignored;
-  }
-  // the gradient's constants: -p (g + h (ln p + H)) + g [label]
-  float lse = 0.0f, g = 0.0f, h = 0.0f, ent = 0.0f;
-  bool zero = false;
-  if (MODE == MODE_BACKWARD) {
-    lse = a.lse[row];
-    if (!ignored) {
-      g = a.g_logp ? a.g_logp[row] : 0.0f;
-      h = a.g_entropy ? a.g_entropy[row] : 0.0f;
+  auto store_mask = [&](int k) {
+    const int c = in0 + k * kColumns + 32 * tid;
+    if (k >= copies || c >= min(in0 + (k + 1) * kColumns, in1)) return;
+    uint32_t bits;
+    if (a.mask_kind == 2) {
+      bits = __funnelshift_r(raw[0], raw[1], static_cast<uint32_t>(c - pre));
+    } else if (raw_off < 0) {
+      bits = raw[0];
+    } else {
+      bits = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        bits |= byte_bits(__funnelshift_r(raw[j], raw[j + 1], 8 * raw_off)) << (4 * j);
     }
-    ent = a.entropy ? a.entropy[row] : 0.0f;
-    zero = ignored || lse == -INFINITY;
-  }
-  Row p;
-  p.rep = a.rep ? a.rep[row] : a.rep1;
-  p.inv_rep = __fdiv_rn(1.0f, p.rep);
-  p.freq = a.freq ? a.freq[row] : a.freq1;
-  p.pres = a.pres ? a.pres[row] : a.pres1;
-  const float temp = a.temp ? a.temp[row] : a.temp1;
-  p.inv_temp = temp > 0.0f ? __fdiv_rn(1.0f, temp) : 1.0f;
-  p.mask = static_cast<const uint8_t*>(a.allowed) +
-           row * a.ld_allowed * (a.mask_kind == 2 ? 4 : 1);
-  int64_t length = 0, prompt = 0;
-  if (COUNT && a.tokens) {
-    length = a.lengths ? whole(a.lengths, row, a.lens64) : a.T;
-    length = length < a.T ? length : a.T;
-    prompt = a.prompt_lens ? whole(a.prompt_lens, row, a.lens64) : 0;
-    if (p.rep == 1.0f && p.freq == 0.0f && p.pres == 0.0f) length = 0;
-  }
-  if (COUNT && !zero) {
-    for (int64_t j = threadIdx.x; j < a.n_bias; j += kThreads) {
+    mask_bits[k & 1][tid] = bits;
+  };
+  if (a.mask_kind) load_mask(0);
+  if (tid == kThreads - 1) read_row<COUNT, BACKWARD>(a, row, r);
+  auto clear = [&] {
+    for (int i = tid; i < room * int(sizeof(Word)) / 16; i += kThreads)
+      reinterpret_cast<uint4*>(counters)[i] = make_uint4(0, 0, 0, 0);
+  };
+  if (COUNT) clear();
+  if (COUNT) {
+    for (int j = tid; j < n_bias; j += kThreads) {
       const int64_t id = whole(a.bias_ids, row * a.ld_bias_ids + j, a.bias64);
-      // columns are below 2^31; -1 is no column
-      bias_col[j] = id >= 0 && id < a.V ? static_cast<int>(id + pre) : -1;
+      bias_col[j] = id >= 0 && id < V ? static_cast<int>(id) + pre : -1;
       bias_val[j] = a.bias_values[row * a.ld_bias_values + j];
     }
   }
-  if (a.stats && threadIdx.x == 0 && rank == 0) label_z = -INFINITY;
+  if (!BACKWARD && a.stats) cluster_arrive();  // waited for before another block's memory is written
+  if (a.mask_kind) store_mask(0);
+  __syncthreads();
+  const bool zero = BACKWARD && r.zero;
 
-  Stats mine{-INFINITY, 0.0f, 0.0f};
-  for (int64_t pass = 0; pass < a.passes; ++pass) {
-    const int64_t base = pass * per_pass;  // of the pass's columns
-    const int64_t c0 = base + rank * a.columns;
-    const int64_t c1 = c0 + a.columns < span ? c0 + a.columns : span;
-    if (COUNT && !zero) {
-      // every block of the cluster clears its counters before any adds to them
-      if (pass > 0) __syncthreads();
-      uint4* clear = reinterpret_cast<uint4*>(shared);
-      for (int i = threadIdx.x; i < a.columns * int(sizeof(Word)) / 16; i += kThreads)
-        clear[i] = make_uint4(0, 0, 0, 0);
-      meet();
-      if constexpr (COUNT) {
-        const int64_t share = (length + size - 1) / size;
-        const int64_t t0 = rank * share;
-        const int64_t t1 = t0 + share < length ? t0 + share : length;
-        const uint32_t columns = static_cast<uint32_t>(a.columns);
-        for (int64_t t = t0 + threadIdx.x; t < t1; t += kThreads) {
-          const int64_t id = whole(a.tokens, row * a.ld_tokens + t, a.ids64);
-          const int64_t c = id + pre - base;
-          if (id < 0 || id >= a.V || c < 0 || c >= per_pass) continue;
-          const uint32_t owner = static_cast<uint32_t>(c) / columns;
-          const uint32_t byte = (static_cast<uint32_t>(c) - owner * columns) * sizeof(Word);
-          const uint32_t at = remote(shared + (byte & ~3u), owner), shift = 8 * (byte & 3u);
-          if (t < prompt) red_or(at, COUNTER::kSeen << shift);
-          else red_add(at, 1u << shift);
+  // z of the sum so far, by its counter; the slope by its logit goes into k
+  auto change = [&](float y, uint32_t n, int c, float& k) {
+    if (n & (COUNTER::kSeen | COUNTER::kCount)) {
+      k = y > 0.0f ? r.inv_rep : r.rep;
+      y *= k;
+      if (n & COUNTER::kCount) y = fmaf(-r.freq, static_cast<float>(n & COUNTER::kCount), y) - r.pres;
+    }
+    if (n & COUNTER::kBiased) {
+      float sum = 0.0f;
+#pragma unroll 1
+      for (int j = 0; j < n_bias; ++j)
+        if (bias_col[j] == c) sum += bias_val[j];
+      y += sum;
+    }
+    return y;
+  };
+  auto gradient = [&](float z, float slope, bool label) {
+    const float q = z - r.lse;
+    const float e = fast_ex2(q * kLog2e);
+    float dz = e != 0.0f ? -e * fmaf(r.h, q + r.ent, r.g) : 0.0f;
+    if (label) dz += r.g;
+    return slope * dz;
+  };
+  Running run;
+  float inv_temp = r.inv_temp;
+  const float rep = COUNT ? r.rep : 1.0f, inv_rep = COUNT ? r.inv_rep : 1.0f;
+  const float freq = COUNT ? r.freq : 0.0f, pres = COUNT ? r.pres : 0.0f;
+  const bool stats = !BACKWARD && a.stats, entropy = a.entropy != nullptr;
+  const int label = r.label;
+  int copied = 0;
+  for (int pass = 0; pass < a.passes; ++pass) {
+    const int c0 = begin + pass * room, c1 = min(c0 + room, end);
+    if (c0 >= c1) break;
+    if constexpr (COUNT) {
+      if (!zero) {
+        if (pass > 0) {
+          __syncthreads();  // the last pass's counters are done with
+          clear();
+          __syncthreads();
         }
-        for (int j = threadIdx.x; j < a.n_bias; j += kThreads) {
-          const int64_t c = bias_col[j];  // every block marks its own columns
+        if (r.length > 0) {
+          const uint32_t at = smem_u32(counters);
+          if (a.ids64) {
+            const auto* t = static_cast<const int64_t*>(a.tokens) + row * a.ld_tokens;
+            count<COUNTER, true>(t, 0, r.prompt, c0 - pre, c1 - c0, at);
+            count<COUNTER, false>(t, r.prompt, r.length, c0 - pre, c1 - c0, at);
+          } else {
+            const auto* t = static_cast<const int32_t*>(a.tokens) + row * a.ld_tokens;
+            count<COUNTER, true>(t, 0, r.prompt, c0 - pre, c1 - c0, at);
+            count<COUNTER, false>(t, r.prompt, r.length, c0 - pre, c1 - c0, at);
+          }
+        }
+        for (int j = tid; j < n_bias; j += kThreads) {
+          const int c = bias_col[j];
           if (c < c0 || c >= c1) continue;
-          const uint32_t byte = static_cast<uint32_t>(c - c0) * sizeof(Word);
-          atomicOr(reinterpret_cast<uint32_t*>(shared + (byte & ~3u)),
+          const uint32_t byte = (c - c0) * sizeof(Word);
+          atomicOr(reinterpret_cast<uint32_t*>(counters + (byte & ~3u)),
                    COUNTER::kBiased << (8 * (byte & 3u)));
         }
+        __syncthreads();
       }
-      meet();
-    } else if (MODE == MODE_FORWARD && a.stats && pass == 0) {
-      meet();  // label_z of the first block is there, and cleared
     }
-    for (int64_t v0 = c0 + threadIdx.x * VEC; v0 < c1; v0 += int64_t(kThreads) * VEC * kBatch) {
-      if ((pass > 0 || v0 >= c0 + int64_t(kThreads) * VEC) && !zero) load(v0, c1);
-#pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        const int64_t c = v0 + int64_t(b) * kThreads * VEC;
-        if (c >= c1) continue;
-        const int64_t l = c - pre;
-        const bool inside = l >= 0 && l + VEC <= a.V;
-        constexpr uint32_t kAll = (1u << VEC) - 1;
-        uint32_t real = kAll;  // bit i: column c + i is a logit
-        if (!inside) {
-          real = 0;
-#pragma unroll
-          for (int i = 0; i < VEC; ++i)
-            if (l + i >= 0 && l + i < a.V) real |= 1u << i;
-        }
-        uint32_t there = real;  // and allowed
-        if (a.mask_kind == 2) {
-          const uint32_t* w = reinterpret_cast<const uint32_t*>(p.mask);
-          if (l >= 0) {
-            const uint32_t lo = __ldg(w + (l >> 5));
-            const uint32_t hi = (l & 31) + VEC > 32 && ((l >> 5) + 1) * 32 < a.V
-                                    ? __ldg(w + (l >> 5) + 1) : 0u;
-            there &= __funnelshift_r(lo, hi, static_cast<uint32_t>(l & 31));
-          } else {
-            there &= __ldg(w) << static_cast<uint32_t>(-l);
-          }
-        } else if (a.mask_kind == 1) {
-          if (inside) {
-            there = byte_mask<VEC>(p.mask + l, l, a.V);
-          } else {
-#pragma unroll
-            for (int i = 0; i < VEC; ++i)
-              if ((real >> i & 1) && p.mask[l + i] == 0) there &= ~(1u << i);
+    // a row's first and last columns where they are no whole vector
+    for (int edge = 0; edge < 2; ++edge) {
+      const int c = edge == 0 ? (pre ? 0 : -1) : (span % VEC ? span / VEC * VEC : -1);
+      if (c < c0 || c >= c1 || (edge == 1 && pre && c == 0) || tid != edge * 32) continue;
+#pragma unroll 1
+      for (int i = 0; i < VEC; ++i) {
+        const int l = c + i - pre;
+        if (l < 0 || l >= V) continue;
+        bool ok = true;
+        if (a.mask_kind == 2)
+          ok = reinterpret_cast<const uint32_t*>(mask)[l >> 5] >> (l & 31) & 1;
+        else if (a.mask_kind == 1)
+          ok = mask[l] != 0;
+        float z = widen1(x[l]), k = 1.0f;
+        if constexpr (COUNT) {
+          if (!zero) {
+            const uint32_t n = reinterpret_cast<const Word*>(counters)[c + i - c0];
+            if (n) z = change(z, n, c + i, k);
           }
         }
-        float z[VEC], slope[VEC];
+        z = ok ? z * inv_temp : -INFINITY;
+        if (stats) {
+          const float one[1] = {z};
+          run.add(one, entropy);
+          if (l == label) label_z = z;
+        }
+        if (BACKWARD) z = zero ? 0.0f : gradient(z, ok ? k * inv_temp : 0.0f, l == label);
+        if (out) {
+          if (a.out_f32) reinterpret_cast<float*>(out)[l] = z;
+          else reinterpret_cast<T*>(out)[l] = narrow1<T>(z);
+        }
+      }
+    }
+    // the pass's whole vectors, copy by copy
+    const int p1 = min(c1, in1);
+    for (int c = max(c0, in0); c < p1;) {
+      const int k = (c - in0) / kColumns, base = in0 + k * kColumns;
+      const int stop = min(base + kColumns, p1);  // of this pass and copy
+      if (k >= copied) {
+        // a wait that runs out leaves NaN in the outputs; every thread goes the same way on
+        if (!mbar_wait(&landed[k & 1], (k >> 1) & 1, &gave_up, a.err)) inv_temp = NAN;
+        copied = k + 1;
+      }
+      const uint8_t* staged = shared + (k & 1) * kStage;
+      const bool ends = stop == min(base + kColumns, in1);  // the copy, not just the pass
+      if (a.mask_kind && ends) load_mask(k + 1);
+#pragma unroll 1
+      for (int cv = c + tid * VEC; cv < stop; cv += kThreads * VEC) {
+        const int l = cv - pre;
+        float z[VEC], slope[BACKWARD ? VEC : 1];
+        widen<T>(*reinterpret_cast<const uint4*>(staged + (cv - base) * sizeof(T)), z);
+        if constexpr (BACKWARD) {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          z[i] = widen(in[b][i]);
-          slope[i] = p.inv_temp;
+          for (int i = 0; i < VEC; ++i) slope[i] = inv_temp;
         }
         if constexpr (COUNT) {
           constexpr int WORDS = VEC * sizeof(Word) / 4;
           uint32_t n32[WORDS];
           uint32_t any = 0;
-          if (!zero) {
-            const uint32_t* src = reinterpret_cast<const uint32_t*>(counters + (c - c0));
-            if constexpr (WORDS == 2) {
-              *reinterpret_cast<uint2*>(n32) = *reinterpret_cast<const uint2*>(src);
-            } else {
+          const uint8_t* src = counters + (cv - c0) * sizeof(Word);
+          if constexpr (WORDS == 2) {
+            *reinterpret_cast<uint2*>(n32) = *reinterpret_cast<const uint2*>(src);
+          } else {
 #pragma unroll
-              for (int j = 0; j < WORDS; j += 4)
-                *reinterpret_cast<uint4*>(n32 + j) = *reinterpret_cast<const uint4*>(src + j);
-            }
-#pragma unroll
-            for (int j = 0; j < WORDS; ++j) any |= n32[j];
+            for (int j = 0; j < WORDS; j += 4)
+              *reinterpret_cast<uint4*>(n32 + j) = *reinterpret_cast<const uint4*>(src + 4 * j);
           }
-          if (any) {
+#pragma unroll
+          for (int j = 0; j < WORDS; ++j) any |= n32[j];
+          if (any && !zero) {
+            // without branches, as lanes differ; biases, which are few, behind it
+            uint32_t biased = 0;
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
               const uint32_t n = sizeof(Word) == 4
                                      ? n32[i % WORDS] : n32[i / 2 % WORDS] >> (16 * (i & 1)) & 0xffffu;
-              if (n == 0) continue;
-              float y = z[i];
-              if (n & (COUNTER::kSeen | COUNTER::kCount)) {
-                const float k = y > 0.0f ? p.inv_rep : p.rep;
-                y *= k;
-                slope[i] *= k;
-              }
-              if (n & COUNTER::kCount)
-                y = fmaf(-p.freq, static_cast<float>(n & COUNTER::kCount), y) - p.pres;
-              if (n & COUNTER::kBiased) {
-                float sum = 0.0f;
+              const float times = z[i] > 0.0f ? inv_rep : rep;
+              const float k1 = n & (COUNTER::kSeen | COUNTER::kCount) ? times : 1.0f;
+              const float made = static_cast<float>(n & COUNTER::kCount);
+              z[i] = fmaf(-freq, made, z[i] * k1) - (n & COUNTER::kCount ? pres : 0.0f);
+              if constexpr (BACKWARD) slope[i] *= k1;
+              biased |= n & COUNTER::kBiased;
+            }
+            if (biased) {
 #pragma unroll 1
-                for (int j = 0; j < a.n_bias; ++j)
-                  if (bias_col[j] == static_cast<int>(c) + i) sum += bias_val[j];
-                y += sum;
+              for (int j = 0; j < n_bias; ++j) {
+                const int i = bias_col[j] - cv;
+                if (i < 0 || i >= VEC) continue;
+#pragma unroll
+                for (int q = 0; q < VEC; ++q) z[q] += q == i ? bias_val[j] : 0.0f;
               }
-              z[i] = y;
             }
           }
         }
+        const uint64_t inv2 = f2_pack(inv_temp, inv_temp);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) z[i] *= p.inv_temp;
-        if (there != kAll) {
+        for (int i = 0; i < VEC; i += 2)
+          f2_unpack(f2_mul(f2_pack(z[i], z[i + 1]), inv2), z[i], z[i + 1]);
+        if (a.mask_kind) {
+          const int at = cv - base;
+          const uint32_t there = mask_bits[k & 1][at >> 5] >> (at & 31) & kAll;
+          if (there != kAll) {
 #pragma unroll
-          for (int i = 0; i < VEC; ++i)
-            if (!(there >> i & 1)) {
-              z[i] = -INFINITY;
-              slope[i] = 0.0f;
-            }
-        }
-        const int64_t yl = label - l;  // the label's place in this vector
-        if (MODE == MODE_FORWARD) {
-          if (a.stats) {
-            float top = z[0];
-#pragma unroll
-            for (int i = 1; i < VEC; ++i) top = fmaxf(top, z[i]);
-            if (top > mine.m) {
-              const float t = (mine.m - top) * kLog2e;  // -inf before the first
-              const float e = fast_ex2(t);
-              mine.s = e != 0.0f ? e * fmaf(t, mine.d, mine.s) : 0.0f;
-              mine.d *= e;
-              mine.m = top;
-            }
-            if (mine.m != -INFINITY) {
-#pragma unroll
-              for (int i = 0; i < VEC; ++i) {
-                const float t = (z[i] - mine.m) * kLog2e;
-                const float e = fast_ex2(t);
-                mine.d += e;
-                mine.s += e != 0.0f ? e * t : 0.0f;
+            for (int i = 0; i < VEC; ++i)
+              if (!(there >> i & 1)) {
+                z[i] = -INFINITY;
+                if constexpr (BACKWARD) slope[i] = 0.0f;
               }
-            } else {
-#pragma unroll
-              for (int i = 0; i < VEC; ++i) mine.d += z[i] != z[i] ? z[i] : 0.0f;  // NaN alone
-            }
-            if (yl >= 0 && yl < VEC) {
+          }
+        }
+        if constexpr (!BACKWARD) {
+          if (stats) {
+            run.add(z, entropy);
+            if (static_cast<uint32_t>(label - l) < VEC) {
               float zy = z[0];
 #pragma unroll
               for (int i = 1; i < VEC; ++i)
-                if (i == yl) zy = z[i];
-              st_remote(remote(&label_z, 0), zy);
+                if (i == label - l) zy = z[i];
+              label_z = zy;
             }
           }
+          if (!out) continue;
         } else {
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) {
-            const float q = z[i] - lse;
-            const float e = fast_ex2(q * kLog2e);
-            float d = e != 0.0f ? -e * fmaf(h, q + ent, g) : 0.0f;
-            if (i == yl) d += g;
-            z[i] = zero ? 0.0f : slope[i] * d;
+          for (int i = 0; i < VEC; ++i) z[i] = zero ? 0.0f : gradient(z[i], slope[i], i == label - l);
+        }
+        if (a.out_f32) {
+          float* o = reinterpret_cast<float*>(out) + l;
+          if ((reinterpret_cast<uintptr_t>(o) & 15) == 0) {
+#pragma unroll
+            for (int i = 0; i < VEC / 4; ++i)
+              __stcs(reinterpret_cast<float4*>(o) + i,
+                     make_float4(z[4 * i], z[4 * i + 1], z[4 * i + 2], z[4 * i + 3]));
+          } else {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) o[i] = z[i];
+          }
+        } else {
+          T* o = reinterpret_cast<T*>(out) + l;
+          if ((reinterpret_cast<uintptr_t>(o) & 15) == 0) {
+            __stcs(reinterpret_cast<uint4*>(o), narrow<T>(z));
+          } else {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) o[i] = narrow1<T>(z[i]);
           }
         }
-        if (a.out) {
-          if (a.out_f32) {
-            float* o = static_cast<float*>(a.out) + row * a.ld_out + l;
-            if (inside && (reinterpret_cast<uintptr_t>(o) & 15) == 0) {
-#pragma unroll
-              for (int i = 0; i < VEC / 4; ++i)
-                __stcs(reinterpret_cast<float4*>(o) + i,
-                       make_float4(z[4 * i], z[4 * i + 1], z[4 * i + 2], z[4 * i + 3]));
-            } else {
-#pragma unroll
-              for (int i = 0; i < VEC; ++i)
-                if (real >> i & 1) o[i] = z[i];
-            }
-          } else {
-            T* o = static_cast<T*>(a.out) + row * a.ld_out + l;
-            if (inside && (reinterpret_cast<uintptr_t>(o) & 15) == 0) {
-              alignas(16) T t[VEC];
-#pragma unroll
-              for (int i = 0; i < VEC; ++i) t[i] = narrow<T>(z[i]);
-              __stcs(reinterpret_cast<uint4*>(o), *reinterpret_cast<uint4*>(t));
-            } else {
-#pragma unroll
-              for (int i = 0; i < VEC; ++i)
-                if (real >> i & 1) o[i] = narrow<T>(z[i]);
-            }
-          }
+      }
+      c = stop;
+      if (ends && k + 1 < copies && (a.mask_kind || k + 2 < copies)) {
+        if (a.mask_kind) store_mask(k + 1);
+        __syncthreads();  // the copy is done with, the next one's mask is there
+        if (tid == 0 && k + 2 < copies) {
+          asm volatile("fence.proxy.async;" ::: "memory");
+          copy(k + 2);
         }
       }
     }
   }
-  if (MODE == MODE_FORWARD && a.stats) {
+  if (stats) {
     __syncwarp();
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-      const Stats o{__shfl_down_sync(0xffffffffu, mine.m, d),
-                    __shfl_down_sync(0xffffffffu, mine.d, d),
-                    __shfl_down_sync(0xffffffffu, mine.s, d)};
-      mine = join(mine, o);
-    }
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = mine;
+    Stats mine = join_warp(Stats{run.top, run.d, run.s}, 32);
+    if ((tid & 31) == 0) part[tid >> 5] = mine;
     __syncthreads();
-    if (threadIdx.x == 0) {
-      for (int w = 1; w < kWarps; ++w) mine = join(mine, part[w]);
-      const uint32_t at = remote(&from[rank], 0);
-      st_remote(at, mine.m);
-      st_remote(at + 4, mine.d);
-      st_remote(at + 8, mine.s);
-    }
-    meet();
-    if (rank == 0 && threadIdx.x == 0) {
-      Stats r = from[0];
-      for (uint32_t i = 1; i < size; ++i) r = join(r, from[i]);
-      const float log_d = logf(r.d);
-      const float all = r.m == -INFINITY && r.d == 0.0f ? -INFINITY : r.m + log_d;
-      if (a.lse) a.lse[row] = all;
-      if (a.logp)
-        a.logp[row] = ignored ? 0.0f
-                      : bad   ? NAN
-                              : label_z == -INFINITY ? -INFINITY : label_z - all;
-      if (a.entropy) {
-        const float H = all == -INFINITY ? 0.0f : log_d - kLn2 * __fdiv_rn(r.s, r.d);
-        a.entropy[row] = ignored ? 0.0f : bad ? NAN : H;
+    cluster_wait();
+    if (tid < 32) {
+      mine = join_warp(tid < kWarps ? part[tid] : Stats{-INFINITY, 0.0f, 0.0f}, kWarps);
+      if (tid == 0) {
+        const uint32_t at = mapa_shared(smem_u32(&from[rank]), 0);
+        st_remote(at, mine.m);
+        st_remote(at + 4, mine.d);
+        st_remote(at + 8, mine.s);
+        st_remote(at + 12, label_z);
       }
-      if (bad && a.err) atomicOr(a.err, FLCE_DEVERR_LABEL);
+    }
+    cluster_arrive();  // the other blocks are done; their memory is not written by any
+    if (rank != 0) return;
+    cluster_wait();
+    if (tid < 32) {
+      const float4 one = tid < size ? from[tid] : make_float4(-INFINITY, 0.0f, 0.0f, -INFINITY);
+      const Stats all = join_warp(Stats{one.x, one.y, one.z}, kMaxCluster);
+      float zy = one.w;  // a NaN there is in all.d too
+#pragma unroll
+      for (int j = kMaxCluster / 2; j > 0; j >>= 1)
+        zy = fmaxf(zy, __shfl_xor_sync(0xffffffffu, zy, j));
+      if (tid != 0) return;
+      const float log_d = logf(all.d);
+      const bool none = all.m == -INFINITY && all.d == 0.0f;  // nothing is left
+      if (a.lse) a.lse[row] = none ? -INFINITY : all.m + log_d;
+      if (a.logp)
+        a.logp[row] = r.ignored ? 0.0f
+                      : r.bad   ? NAN
+                                : none || zy == -INFINITY ? -INFINITY : (zy - all.m) - log_d;
+      if (a.entropy) {
+        const float H = none ? 0.0f : log_d - kLn2 * __fdiv_rn(all.s, all.d);
+        a.entropy[row] = r.ignored ? 0.0f : r.bad ? NAN : H;
+      }
+      if (r.bad && a.err) atomicOr(a.err, FLCE_DEVERR_LABEL);
     }
   }
 }
@@ -556,23 +797,21 @@ int run(Args a, int sms, cudaStream_t st) {
   constexpr int VEC = 16 / sizeof(T);
   constexpr int64_t wide = int64_t(kThreads) * VEC;
   // whole 16-byte words of counters, whole vectors
-  constexpr int64_t unit = 16 / sizeof(typename COUNTER::Word) > VEC
-                               ? 16 / sizeof(typename COUNTER::Word) : VEC;
-  constexpr int64_t most = kRoom / sizeof(typename COUNTER::Word);
+  using Word = typename COUNTER::Word;
+  constexpr int64_t unit = 16 / sizeof(Word) > VEC ? 16 / sizeof(Word) : VEC;
+  constexpr int64_t most = kRoom / sizeof(Word);
   const int64_t span = a.V + VEC - 1;  // with what may stand before a row
-  // As few blocks per row as fill the GPU's block slots, but no more than have a vector for half
-  // of their threads; the counters' room asks for more.
+  // As few blocks per row as fill the GPU several times over, so that its last round is a small
+  // part, but no more than have a vector for half of their threads.
   int size = 1;
-  while (size < kMaxCluster && ((a.R * size < FLCE_LOGITS_FILL * sms && span > size * wide / 2) ||
-                                (COUNT && span > size * most)))
-    size *= 2;
+  while (size < kMaxCluster && a.R * size < FLCE_LOGITS_FILL * sms && span > size * wide / 2) size *= 2;
   a.columns = cdiv(cdiv(span, size), unit) * unit;
-  a.passes = 1;
-  if (COUNT && a.columns > most) {
-    a.columns = most;
-    a.passes = cdiv(span, size * most);
-  }
-  const size_t smem = COUNT ? a.columns * sizeof(typename COUNTER::Word) + a.n_bias * 8 : 0;
+  a.passes = static_cast<int32_t>(COUNT ? cdiv(a.columns, most) : 1);
+  a.room = cdiv(cdiv(a.columns, a.passes), unit) * unit;
+  const int64_t bytes = a.columns * static_cast<int64_t>(sizeof(T));
+  a.stage_bytes = bytes < 2 * kStage ? static_cast<int32_t>(cdiv(bytes, 16) * 16) : 2 * kStage;
+  const size_t smem = a.stage_bytes + (COUNT ? a.room * sizeof(Word) : 0) + a.n_bias * 8;
+  constexpr int kMostShared = 2 * kStage + (COUNT ? kRoom : 0) + kMaxBias * 8;
   // the same values from every thread that gets here, once per device
   static std::atomic<uint64_t> ready{0};
   int dev = 0;
@@ -580,7 +819,7 @@ int run(Args a, int sms, cudaStream_t st) {
   if (rc) return rc;
   if (!(ready.load() >> (dev & 63) & 1)) {
     if ((rc = rc_of(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kRoom + kMaxBias * 8))) ||
+                                         kMostShared))) ||
         (rc = rc_of(cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed,
                                          1))))
       return rc;
@@ -682,7 +921,8 @@ int launch(const flce_logits_params* p, Args a, bool backward, void* workspace, 
     const bool penalties = a.rep || a.freq || a.pres || a.rep1 != 1.0f || a.freq1 != 0.0f ||
                            a.pres1 != 0.0f;
     if (!penalties) a.tokens = nullptr;
-    const int count = a.tokens && a.T >= 1 << 14 ? 32 : a.tokens || a.n_bias > 0 ? 16 : 0;
+    if (!a.tokens) a.T = 0;
+    const int count = !a.tokens && a.n_bias == 0 ? 0 : a.T >= 1 << 14 ? 32 : 16;
     rc = p->dtype == FLCE_F32    ? run_type<float>(a, count, backward, sms, st)
          : p->dtype == FLCE_BF16 ? run_type<__nv_bfloat16>(a, count, backward, sms, st)
                                  : run_type<__half>(a, count, backward, sms, st);
