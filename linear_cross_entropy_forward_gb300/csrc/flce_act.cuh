@@ -19,6 +19,7 @@ struct LinearOut {
   int64_t ld;
   int32_t act;
   int32_t out_f32;
+  int32_t wide;  // rows and arrays are 32-byte aligned, 16 columns at a time
 };
 
 __device__ __forceinline__ float sigmoid_fast(float x) {
@@ -30,10 +31,32 @@ __device__ __forceinline__ float sigmoid_fast(float x) {
 constexpr float kGeluK = 0.7978845608028654f;  // sqrt(2 / pi)
 constexpr float kGeluA = 0.044715f;
 
+// The lower tail Phi(-|z|) and e = exp(-z^2 / 2):  with x = |z| / sqrt(2),
+// erfc(x) = exp(-x^2) g(1 / (1 + x / 3)) for a polynomial g, least squares reweighted towards the
+// largest relative error of exp(x^2) erfc(x) on [0, 9]: 1.3e-7, 4e-7 with fp32's roundings.  One exponential and one
+// reciprocal, no branch, and no cancellation where the tail is small.
+__device__ __forceinline__ float normal_tail(float z, float& e) {
+  const float t = fast_rcp(fmaf(fabsf(z), 0.7071067811865476f / 3.0f, 1.0f));
+  e = fast_ex2(-0.5f * kLog2e * z * z);
+  float g = -0.12484309822320938f;
+  g = fmaf(g, t, 0.401925265789032f);
+  g = fmaf(g, t, -0.26398417353630066f);
+  g = fmaf(g, t, 0.33701184391975403f);
+  g = fmaf(g, t, 0.08211106061935425f);
+  g = fmaf(g, t, 0.19337718188762665f);
+  g = fmaf(g, t, 0.1862521916627884f);
+  g = fmaf(g, t, 0.1881496012210846f);
+  return 0.5f * g * t * e;
+}
+
 __device__ __forceinline__ float activate(float z, int act) {
   switch (act) {
     case FLCE_ACT_RELU: return z < 0.0f ? 0.0f : z;  // NaN stays
-    case FLCE_ACT_GELU: return 0.5f * z * (1.0f + erff(z * 0.7071067811865476f));
+    case FLCE_ACT_GELU: {
+      float e;
+      const float tail = normal_tail(z, e);
+      return z * (z > 0.0f ? 1.0f - tail : tail);
+    }
     case FLCE_ACT_GELU_TANH: return z * sigmoid_fast(2.0f * kGeluK * fmaf(kGeluA * z, z * z, z));
     case FLCE_ACT_SILU: return z * sigmoid_fast(z);
     default: return z;
@@ -44,8 +67,9 @@ __device__ __forceinline__ float activate_slope(float z, int act) {
   switch (act) {
     case FLCE_ACT_RELU: return z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
     case FLCE_ACT_GELU: {
-      const float cdf = 0.5f * (1.0f + erff(z * 0.7071067811865476f));
-      return fmaf(z, 0.3989422804014327f * fast_ex2(-0.5f * kLog2e * z * z), cdf);
+      float e;
+      const float tail = normal_tail(z, e);
+      return fmaf(z, 0.3989422804014327f * e, z > 0.0f ? 1.0f - tail : tail);
     }
     case FLCE_ACT_GELU_TANH: {
       const float s = sigmoid_fast(2.0f * kGeluK * fmaf(kGeluA * z, z * z, z));
@@ -76,62 +100,109 @@ __device__ __forceinline__ uint4 pack_bf16x8(const float (&x)[8]) {
                     pack_bf16x2(x[6], x[7]));
 }
 
-// Eight neighbouring sums of a row that starts at element `base`, all arrays 16-byte aligned there.
-__device__ __forceinline__ void linear_store8(const LinearOut& o, int64_t base, int col,
-                                              float (&v)[8]) {
-  if (o.bias) {
-    float b[8];
-    if (reinterpret_cast<uintptr_t>(o.bias) & 15) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) b[i] = __bfloat162float(o.bias[col + i]);
-    } else {
-      unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(o.bias + col)), b);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += b[i];
-  }
-  if (o.preact) *reinterpret_cast<uint4*>(o.preact + base + col) = pack_bf16x8(v);
-  switch (o.act) {  // outside the loops: one copy of each activation's code
+template <int N>
+__device__ __forceinline__ void activate_all(float (&v)[N], int act) {
+  switch (act) {  // outside the loops: one copy of each activation's code
     case FLCE_ACT_NONE: break;
     case FLCE_ACT_RELU:
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = activate(v[i], FLCE_ACT_RELU);
+      for (int i = 0; i < N; ++i) v[i] = activate(v[i], FLCE_ACT_RELU);
       break;
     case FLCE_ACT_GELU:
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = activate(v[i], FLCE_ACT_GELU);
+      for (int i = 0; i < N; ++i) v[i] = activate(v[i], FLCE_ACT_GELU);
       break;
     case FLCE_ACT_GELU_TANH:
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = activate(v[i], FLCE_ACT_GELU_TANH);
+      for (int i = 0; i < N; ++i) v[i] = activate(v[i], FLCE_ACT_GELU_TANH);
       break;
     default:
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = activate(v[i], FLCE_ACT_SILU);
-  }
-  if (o.out_f32) {
-    float* y = static_cast<float*>(o.y) + base + col;
-    if (o.residual) {
-      const float4* r = reinterpret_cast<const float4*>(static_cast<const float*>(o.residual) + base + col);
-      const float4 r0 = r[0], r1 = r[1];
-      v[0] += r0.x; v[1] += r0.y; v[2] += r0.z; v[3] += r0.w;
-      v[4] += r1.x; v[5] += r1.y; v[6] += r1.z; v[7] += r1.w;
-    }
-    reinterpret_cast<float4*>(y)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4*>(y)[1] = make_float4(v[4], v[5], v[6], v[7]);
-  } else {
-    if (o.residual) {
-      float r[8];
-      unpack_bf16x8(*reinterpret_cast<const uint4*>(
-                        static_cast<const __nv_bfloat16*>(o.residual) + base + col), r);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] += r[i];
-    }
-    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(o.y) + base + col) = pack_bf16x8(v);
+      for (int i = 0; i < N; ++i) v[i] = activate(v[i], FLCE_ACT_SILU);
   }
 }
 
-// One sum, of row `base` and column col.
+// Sixteen bf16 values to 32 aligned bytes: one full sector of L2.  (16 bytes at a time are two half
+// sectors, and L2's traffic is what the tensor cores' operands need.)
+__device__ __forceinline__ void store_sector(__nv_bfloat16* p, const float (&v)[16]) {
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+  st_global_v8(p, w);
+}
+
+// Sixteen neighbouring sums of a row that starts at element `base`, of which the first `cols` are
+// the row's (16 or 8), all arrays 16-byte aligned there.
+__device__ __forceinline__ void linear_store16(const LinearOut& o, int64_t base, int col, int cols,
+                                               float (&v)[16]) {
+  const bool all = cols >= 16;
+  if (o.bias) {
+    const __nv_bfloat16* p = o.bias + col;
+    float b[8];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (h == 1 && !all) break;
+      if (reinterpret_cast<uintptr_t>(p) & 15) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) b[i] = __bfloat162float(p[8 * h + i]);
+      } else {
+        unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(p) + h), b);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[8 * h + i] += b[i];
+    }
+  }
+  auto put = [&](__nv_bfloat16* p) {
+    if (all && o.wide) {
+      store_sector(p, v);
+    } else {
+      reinterpret_cast<uint4*>(p)[0] =
+          make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                     pack_bf16x2(v[6], v[7]));
+      if (all)
+        reinterpret_cast<uint4*>(p)[1] =
+            make_uint4(pack_bf16x2(v[8], v[9]), pack_bf16x2(v[10], v[11]),
+                       pack_bf16x2(v[12], v[13]), pack_bf16x2(v[14], v[15]));
+    }
+  };
+  if (o.preact) put(o.preact + base + col);
+  activate_all(v, o.act);
+  if (o.out_f32) {
+    float* y = static_cast<float*>(o.y) + base + col;
+    const float* r = static_cast<const float*>(o.residual) + base + col;
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      if (h >= 2 && !all) break;
+      float4 u = make_float4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
+      if (o.residual) {
+        const float4 t = reinterpret_cast<const float4*>(r)[h];
+        u.x += t.x; u.y += t.y; u.z += t.z; u.w += t.w;
+      }
+      v[4 * h] = u.x; v[4 * h + 1] = u.y; v[4 * h + 2] = u.z; v[4 * h + 3] = u.w;
+      if (!(all && o.wide)) reinterpret_cast<float4*>(y)[h] = u;
+    }
+    if (all && o.wide) {
+      st_global_v8f(y, v);
+      st_global_v8f(y + 8, v + 8);
+    }
+  } else {
+    if (o.residual) {
+      const uint4* r = reinterpret_cast<const uint4*>(
+          static_cast<const __nv_bfloat16*>(o.residual) + base + col);
+      float t[8];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (h == 1 && !all) break;
+        unpack_bf16x8(r[h], t);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[8 * h + i] += t[i];
+      }
+    }
+    put(static_cast<__nv_bfloat16*>(o.y) + base + col);
+  }
+}
+
+// One sum, element `at` of the output.
 __device__ __forceinline__ void linear_store1(const LinearOut& o, int64_t at, float bias, float v) {
   v += bias;
   if (o.preact) o.preact[at] = __float2bfloat16_rn(v);

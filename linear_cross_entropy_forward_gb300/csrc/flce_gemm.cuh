@@ -144,6 +144,8 @@ struct GemmShape {
   // sched[1] the pairs that finished; both zero at launch, and zero again when the
   // kernel ends (the last pair to finish resets them)
   unsigned int* sched;
+  // every pair has one tile at most: the counters are not looked at, and may hold anything
+  int one_round;
   // extents (inner, outer) of the arrays behind the A and B tensor maps: the
   // FLCE_DEBUG build checks every TMA box against them
   int64_t a_inner, a_outer, b_inner, b_outer;
@@ -188,6 +190,7 @@ struct EpiArgs {
   int64_t n_parts;      // EPI_FWD_STATS: column parts of pm / pd / ps (bounds checks)
   // EPI_LINEAR
   LinearOut lin;
+  int clear;            // the error word is cleared by the kernel itself
 };
 
 // A bounds check of the FLCE_DEBUG build: true in the regular build; in the debug
@@ -581,8 +584,8 @@ struct Epilogue<EPI_ACCUM> {
   }
 };
 
-// A dense layer's output: 8 columns at a time (N is a multiple of 8 here), the residual read
-// and the output written in the accumulator's layout, 16 bytes (fp32: 2 x 16) per thread.
+// A dense layer's output: 16 columns at a time (N is a multiple of 8 here), the residual read and
+// the output written in the accumulator's layout.
 template <>
 struct Epilogue<EPI_LINEAR> {
   template <int CH>
@@ -594,16 +597,17 @@ struct Epilogue<EPI_LINEAR> {
 #pragma unroll 1
     for (int c = 0; c < CH; ++c) {
       float x[32];
+      __syncwarp();
       tmem_ld32(tbase + c * 32, x);
       if (!row_ok) continue;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int col = col0 + c * 32 + q * 8;
-        if (col >= ea.cols || !FLCE_CHECK(row_run_ok(col, 8, o.ld), ea.err)) continue;
-        float v[8];
+      for (int q = 0; q < 2; ++q) {
+        const int col = col0 + c * 32 + q * 16, left = ea.cols - col;
+        if (left <= 0 || !FLCE_CHECK(row_run_ok(col, left < 16 ? left : 16, o.ld), ea.err)) continue;
+        float v[16];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = x[q * 8 + i];
-        linear_store8(o, base, col, v);
+        for (int i = 0; i < 16; ++i) v[i] = x[q * 16 + i];
+        linear_store16(o, base, col, left, v);
       }
     }
   }
@@ -673,6 +677,8 @@ __global__ void __launch_bounds__(pair_threads<EPI>(), 1)
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
+  // (a wait that runs out does so seconds later)
+  if (EPI == EPI_LINEAR && ea.clear && blockIdx.x == 0 && threadIdx.x == 0) *ea.err = 0;
   const int total = sh.m_tiles * sh.n_tiles;
   constexpr uint32_t kSched = 1;  // the CTA whose warp 1 schedules the pair's tiles
   const uint32_t rempty_sched = mapa_shared(smem_u32(&rempty[0]), kSched);
@@ -761,12 +767,12 @@ __global__ void __launch_bounds__(pair_threads<EPI>(), 1)
         mbar_arrive_local(&rfull[slot]);
         mbar_arrive_cluster(rfull_lead + slot * 8);
         if (t >= total) break;
-        t = ncl + static_cast<int>(atomicAdd(sh.sched, 1u));
+        t = sh.one_round ? total : ncl + static_cast<int>(atomicAdd(sh.sched, 1u));
       }
       // this pair draws no more tiles; the last pair to get here resets the counters
       // (every other pair's draws happened before its increment)
       __threadfence();
-      if (atomicAdd(sh.sched + 1, 1u) == static_cast<unsigned int>(ncl - 1)) {
+      if (!sh.one_round && atomicAdd(sh.sched + 1, 1u) == static_cast<unsigned int>(ncl - 1)) {
         __threadfence();
         atomicExch(sh.sched, 0u);
         atomicExch(sh.sched + 1, 0u);
@@ -963,5 +969,11 @@ FLCE_DECLARE_LAUNCHER(launch_bwd_dhidden_vh);  // dlogits (K) x weight (MN)
 // a dense layer's forward
 FLCE_DECLARE_LAUNCHER(launch_linear);     // x (K) x weight [K,N] (MN)
 FLCE_DECLARE_LAUNCHER(launch_linear_vh);  // x (K) x weight [N,K] (K)
+// tiles of 128 columns, for a layer with few: its forward, dx (as dhidden) and dweight
+FLCE_DECLARE_LAUNCHER(launch_linear_128);
+FLCE_DECLARE_LAUNCHER(launch_linear_vh_128);
+FLCE_DECLARE_LAUNCHER(launch_linear_dx_128);
+FLCE_DECLARE_LAUNCHER(launch_linear_dx_vh_128);
+FLCE_DECLARE_LAUNCHER(launch_linear_dweight_128);
 
 }  // namespace flce
