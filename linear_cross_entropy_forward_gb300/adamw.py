@@ -132,6 +132,8 @@ class AdamW:
         self._wanted = [(p.dtype,) if p.dtype is torch.float32 else (p.dtype, torch.float32)
                         for p in self.params]
         self._table = np.zeros(n, _TENSOR)
+        self._table_at = self._table.ctypes.data
+        self._columns = [self._table[name] for name in ("param", "grad", "grad_dtype")]
         self._table["n"] = [p.numel() for p in self.params]
         self._table["dtype"] = [_DTYPES[p.dtype] for p in self.params]
         self._table["weight_decay"] = decay
@@ -199,16 +201,17 @@ class AdamW:
         if index != _current_device():
             B._on_current_device(self.params[0])
         grads = [p.grad for p in self.params] if grads is None else list(grads)
-        table = self._table
         if len(grads) != len(self.params):
             raise ValueError(f"{len(grads)} gradients for {len(self.params)} tensors")
         for i, (g, shape, dtypes) in enumerate(zip(grads, self._shapes, self._wanted)):
             if not (isinstance(g, torch.Tensor) and g.dtype in dtypes and g.shape == shape
                     and g.get_device() == index and g.is_contiguous()):
                 _refuse_grad(g, f"gradient {i}", shape, dtypes, index)
-        table["param"] = [p.data_ptr() for p in self.params]
-        table["grad"] = [g.data_ptr() for g in grads]
-        table["grad_dtype"] = [_DTYPES[g.dtype] for g in grads]
+        param, grad, grad_dtype = self._columns
+        param[:] = [p.data_ptr() for p in self.params]
+        grad[:] = [g.data_ptr() for g in grads]
+        grad_dtype[:] = [_DTYPES[g.dtype] for g in grads]
+        table = self._table_at
         lr_ptr = None
         if isinstance(self.lr, torch.Tensor):
             B._need(self.lr.reshape(1), "lr", torch.float32, (1,), self.step_count.device)
@@ -220,7 +223,7 @@ class AdamW:
         norm = None
         if self._need_norm:
             norm = torch.empty(1, dtype=torch.float32, device=index)
-            code = lib.flce_grad_norm(self._ref, table.ctypes.data, norm.data_ptr(),
+            code = lib.flce_grad_norm(self._ref, table, norm.data_ptr(),
                                       ws.data_ptr(), ws.numel(), stream)
             if code:
                 B._check(code)
@@ -231,7 +234,7 @@ class AdamW:
             states = (s["exp_avg"].data_ptr(), s["exp_rms"].data_ptr(),
                       s["exp_avg_scale"].data_ptr(), s["exp_rms_scale"].data_ptr())
         code = lib.flce_adamw_step(
-            self._ref, table.ctypes.data, None if self.master is None else self.master.data_ptr(),
+            self._ref, table, None if self.master is None else self.master.data_ptr(),
             *states, lr_ptr, None if norm is None else norm.data_ptr(),
             self.step_count.data_ptr(), ws.data_ptr(), ws.numel(), stream)
         if code:

@@ -201,7 +201,9 @@ __device__ __forceinline__ void unpack8(uint2 c, float (&x)[kPer]) {
 // [2^-6, 2^-5), so adding 2^-6 first makes the same 20 bits the ones cut off.
 __device__ __forceinline__ float round_up_or_down(float a, uint32_t r20) {
   const float low = a < 0.015625f ? 0.015625f : 0.0f;
-  return __uint_as_float((__float_as_uint(a + low) + r20) & 0xFFF00000u) - low;
+  // (a NaN of larger bits would become 0 by the addition)
+  const uint32_t bits = min(__float_as_uint(a + low), 0x7FC00000u);
+  return __uint_as_float((bits + r20) & 0xFFF00000u) - low;
 }
 
 // The largest of 16 lanes' x (lanes 0-15 and 16-31 of a warp hold a block each).
@@ -733,9 +735,10 @@ int flce_adamw_step(const flce_adamw_params* p, const flce_adamw_tensor* tensors
                     size_t ws_bytes, void* stream) {
   int rc = check(p);
   if (rc || (rc = check_tensors(p, tensors, true))) return rc;
-  if (!exp_avg || !exp_avg_sq || !step || !workspace) return FLCE_ERR_BAD_ARG;
   const bool state8 = p->state_bits == 8;
-  if (state8 && (!exp_avg_scale || !exp_rms_scale)) return FLCE_ERR_BAD_ARG;
+  if (!step || !workspace) return FLCE_ERR_BAD_ARG;
+  if (p->numel > 0 && (!exp_avg || !exp_avg_sq || (state8 && (!exp_avg_scale || !exp_rms_scale))))
+    return FLCE_ERR_BAD_ARG;
   if ((p->max_norm > 0.0 || p->skip_nonfinite) && !norm) return FLCE_ERR_BAD_ARG;
   if ((addr(master) | addr(exp_avg) | addr(exp_avg_sq)) & 31 ||
       (addr(exp_avg_scale) | addr(exp_rms_scale) | addr(lr) | addr(norm)) & 3 || addr(step) & 7 ||

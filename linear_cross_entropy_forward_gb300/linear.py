@@ -14,10 +14,12 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _binding as B
-from .losses import _addr, _on, _raw_stream, _workspace
+from .losses import _addr, _current_device, _on, _raw_stream, _workspace
 
 _ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 _OUT = {torch.bfloat16: 1, torch.float32: 0}
+_LAYOUTS = {"hv": 0, "vh": 1, 0: 0, 1: 1}
+_HEADER = 256  # bytes of workspace of the forward, whatever the shape
 
 
 def linear_params(M, N, K, activation=None, weight_layout="hv", out_dtype=torch.bfloat16,
@@ -79,26 +81,47 @@ def flce_linear(x, weight, bias=None, activation=None, residual=None, weight_lay
         return _on(stream, flce_linear, x, weight, bias, activation, residual, weight_layout,
                    out_dtype, need_preact, validate, workspace, out=out)
     lib = B._lib or B.load_library()
-    M, N, K, dev = _shapes(x, weight, weight_layout)
-    shape = (*x.shape[:-1], N)
-    p = linear_params(M, N, K, activation, weight_layout, out_dtype, validate)
-    if bias is not None:
-        B._need(bias, "bias", torch.bfloat16, (N,), dev)
-    if residual is not None:
-        B._need(residual, "residual", out_dtype, shape, dev)
-    size = linear_workspace_size(p)
+    # one pass over what is right, as a small layer's time is these checks; _refuse says what is
+    # wrong
+    try:
+        bf16, dev = torch.bfloat16, x.get_device()
+        layout, act, out_code = _LAYOUTS[weight_layout], _ACTIVATIONS[activation], _OUT[out_dtype]
+        N, K = weight.shape if layout else weight.shape[::-1]
+        shape = (*x.shape[:-1], N)
+        if not (dev >= 0 and x.dtype is bf16 and weight.dtype is bf16 and x.shape[-1] == K
+                and weight.get_device() == dev == _current_device() and x.is_contiguous() and weight.is_contiguous()):
+            raise ValueError
+        for t, dtype, size in ((bias, bf16, (N,)), (residual, out_dtype, shape), (out, out_dtype, shape)):
+            if t is not None and not (t.dtype is dtype and t.shape == size
+                                      and t.get_device() == dev and t.is_contiguous()):
+                raise ValueError
+    except (AttributeError, IndexError, KeyError, TypeError, ValueError):
+        _refuse(x, weight, bias, activation, residual, weight_layout, out_dtype, out)
+        raise
+    p = B.FlceLinearParams(x.numel() // K if K else 0, N, K, layout, act, out_code, bool(validate))
     if out is None:
-        out = torch.empty(shape, dtype=out_dtype, device=dev)
-    else:
-        B._need(out, "out", out_dtype, shape, dev)
-    z = torch.empty(shape, dtype=torch.bfloat16, device=dev) if need_preact else None
-    ws = _workspace(size, dev.index, workspace)
+        out = torch.empty(shape, dtype=out_dtype, device=x.device)
+    z = torch.empty(shape, dtype=bf16, device=x.device) if need_preact else None
+    ws = torch.empty(_HEADER, dtype=torch.uint8, device=x.device) if workspace is None \
+        else _workspace(linear_workspace_size(p), dev, workspace)
     code = lib.flce_linear(ctypes.byref(p), x.data_ptr(), weight.data_ptr(), _addr(bias),
                            _addr(residual), out.data_ptr(), _addr(z), ws.data_ptr(), ws.numel(),
-                           _raw_stream(dev.index))
+                           _raw_stream(dev))
     if code:
         B._check(code)
     return (out, z) if need_preact else out
+
+
+def _refuse(x, weight, bias, activation, residual, weight_layout, out_dtype, out):
+    """Says what is wrong with flce_linear's arguments."""
+    M, N, K, dev = _shapes(x, weight, weight_layout)
+    linear_params(M, N, K, activation, weight_layout, out_dtype)
+    shape = (*x.shape[:-1], N)
+    if bias is not None:
+        B._need(bias, "bias", torch.bfloat16, (N,), dev)
+    for t, name in ((residual, "residual"), (out, "out")):
+        if t is not None:
+            B._need(t, name, out_dtype, shape, dev)
 
 
 def flce_linear_backward(dout, x, weight, preact=None, activation=None, weight_layout="hv",

@@ -26,15 +26,15 @@ from .workloads import IGNORE_INDEX
 _WHOLE = {torch.int64: 1, torch.int32: 0}
 
 
-def _per_row(value, name, R, index):
-    """(value, tensor or None) of a number or a [R] fp32 tensor."""
+def _per_row(value, name, R, index, none):
+    """(number, address) of a number or a [R] fp32 tensor."""
     if not isinstance(value, torch.Tensor):
         return float(value), None
     if value.dtype is not torch.float32 or value.shape != (R,) or value.get_device() != index \
             or not value.is_contiguous():
         raise TypeError(f"{name} must be a number or a contiguous fp32 [{R}] tensor on "
                         f"cuda:{index}, got {value.dtype} {tuple(value.shape)} on {value.device}")
-    return None, value
+    return none, value.data_ptr()
 
 
 def _lists(t, name, R, index, dtypes):
@@ -79,32 +79,27 @@ class _Call:
         out_dtype = out_dtype or logits.dtype
         if out_dtype not in (logits.dtype, torch.float32):
             raise TypeError(f"out must be {logits.dtype} or float32, got {out_dtype}")
-        p = B.FlceLogitsParams(R=R, V=V, ld_logits=logits.stride(0), ld_out=V,
-                               ignore_index=ignore_index, dtype=_DTYPES[logits.dtype],
-                               out_dtype=_DTYPES[out_dtype], validate=bool(validate))
-        rows = B.FlceLogitsRows()
-        for name, value in (("repetition_penalty", repetition_penalty),
-                            ("frequency_penalty", frequency_penalty),
-                            ("presence_penalty", presence_penalty), ("temperature", temperature)):
-            number, t = _per_row(value, name, R, index)
-            if t is None:
-                setattr(p, name, number)
-            else:
-                # the number that stands for no change, where the array says what is changed
-                setattr(p, name, 0.0 if name[0] in "fp" else 1.0)
-                setattr(rows, name, t.data_ptr())
+        # where an array says what is changed, the number stands for no change
+        rep, rep_at = _per_row(repetition_penalty, "repetition_penalty", R, index, 1.0)
+        freq, freq_at = _per_row(frequency_penalty, "frequency_penalty", R, index, 0.0)
+        pres, pres_at = _per_row(presence_penalty, "presence_penalty", R, index, 0.0)
+        temp, temp_at = _per_row(temperature, "temperature", R, index, 1.0)
+        p = B.FlceLogitsParams(R, V, 0, logits.stride(0), V, 0, 0, 0, 0, 0, ignore_index, rep, freq,
+                               pres, temp, _DTYPES[logits.dtype], _DTYPES[out_dtype], 0, 0, 0, 0,
+                               bool(validate))
+        rows = B.FlceLogitsRows(None, None, None, rep_at, freq_at, pres_at, temp_at)
         if tokens is not None:
             p.ld_tokens = _lists(tokens, "tokens", R, index, tuple(_WHOLE))
             p.tokens_int64, p.T = _WHOLE[tokens.dtype], tokens.shape[1]
             rows.tokens = tokens.data_ptr()
-            kinds = set()
-            for name, t in (("prompt_lens", prompt_lens), ("lengths", lengths)):
-                if t is not None:
-                    kinds.add(_lens(t, name, R, index))
-                    setattr(rows, name, t.data_ptr())
-            if len(kinds) > 1:
-                raise TypeError("prompt_lens and lengths must have the same type")
-            p.lens_int64 = kinds.pop() if kinds else 0
+            if prompt_lens is not None:
+                p.lens_int64 = _lens(prompt_lens, "prompt_lens", R, index)
+                rows.prompt_lens = prompt_lens.data_ptr()
+            if lengths is not None:
+                if prompt_lens is not None and lengths.dtype is not prompt_lens.dtype:
+                    raise TypeError("prompt_lens and lengths must have the same type")
+                p.lens_int64 = _lens(lengths, "lengths", R, index)
+                rows.lengths = lengths.data_ptr()
         elif prompt_lens is not None or lengths is not None:
             raise ValueError("prompt_lens and lengths need tokens")
         if (bias_ids is None) != (bias_values is None):
