@@ -561,7 +561,9 @@ int flce_logits_backward(const flce_logits_params* params, const flce_logits_row
  *   state_bits 8: m and sqrt(v) as e4m3 codes with an fp32 scale per 128 elements, the largest of
  *     them / 448 (zero where that is below 2^-110).  A magnitude in units of the scale goes to a
  *     neighbouring code, up where the upper 20 of 32 random bits, a mixing of (seed, t, element),
- *     carry; a root that isn't 0 is not rounded to 0.
+ *     carry; a root that isn't 0 is not rounded to 0.  What a code is made of is rounded to fp32
+ *     after every operation, in the order of the formulas; a magnitude in units is that times
+ *     448 * (1 / largest).
  * master: fp32 weights in the same layout, or NULL: the parameters themselves are updated, and
  * rounded, in their own type.  Elements of the states behind a tensor's last stay 0. */
 typedef struct {

@@ -15,7 +15,10 @@
 // A magnitude goes to one of its two neighbouring codes, the upper one with the probability
 // that keeps the mean: rounded to nearest, a decay of 0.1 % a step would never leave a code
 // whose neighbours are 6 to 12 % away.  The random bits are a mixing of (seed, step, element),
-// so a step repeats bit for bit.  s > 0 is never rounded to 0 (m / eps would follow).
+// so a step repeats bit for bit.  s > 0 is never rounded to 0 (m / eps would follow).  What a code is
+// made of is rounded after every operation, in the order of the formulas, so that the codes are the
+// definition's and not this kernel's; the weights, which no code depends on, take fused and
+// approximate operations.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -65,7 +68,7 @@ struct StepArgs {
   const float* norm;
   int64_t* step;
   uint32_t* ticket;
-  float lr, beta1, omb1, beta2, rb2, romb2, eps, grad_scale, max_norm;  // r: root of
+  float lr, beta1, omb1, beta2, omb2, eps, grad_scale, max_norm;
   double ln1, ln2;  // logarithms of the betas
   uint32_t seed;
   int32_t skip, last;
@@ -80,11 +83,17 @@ struct NormArgs {
 };
 
 // ------------------------------------------------------------------ elements
-__device__ __forceinline__ void ld_cs_v8(const float* p, float (&x)[kPer]) {
-  asm volatile("ld.global.cs.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+__device__ __forceinline__ void ld_v8(const float* p, float (&x)[kPer]) {
+  asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]),
                  "=f"(x[6]), "=f"(x[7])
                : "l"(p));
+}
+
+__device__ __forceinline__ void st_v8(float* p, const float* v) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p),
+               "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
 }
 
 // Eight elements of any type as they are in memory (16-bit ones in q[0]).  The type is looked at
@@ -222,7 +231,7 @@ __device__ __forceinline__ uint2 pack8(const float (&x)[kPer], const uint32_t (&
   for (int i = 0; i < kPer; ++i) top = fmaxf(top, fabsf(x[i]));
   top = block_max(top);
   const bool none = top < kTiny;
-  const float unit = none ? 0.0f : 448.0f * fast_rcp(top);
+  const float unit = none ? 0.0f : 448.0f * __frcp_rn(top);
   scale = none ? 0.0f : top * (1.0f / 448.0f);
   float y[kPer];
 #pragma unroll
@@ -244,19 +253,26 @@ __device__ __forceinline__ uint2 pack8(const float (&x)[kPer], const uint32_t (&
 }
 
 // ------------------------------------------------------------------ the step
-// m = b1 m + cm grad;  v = (rb2 s)^2 + (cs grad)^2 (8 bits) or b2 v + (cs grad)^2, with the root
-// s = sqrt(v);  p = p (1 - lr wd) - step_size m / (root_c2 s + eps)
+// g = c grad;  m = beta1 m + omb1 g;  v = beta2 v + omb2 g^2;
+// p = p (1 - lr wd) - step_size m / (root_c2 sqrt(v) + eps)
 struct Coef {
-  float beta1, beta2, rb2, cm, cs, eps, lr, step_size, root_c2;
+  float c, beta1, omb1, beta2, omb2, eps, lr, step_size, root_c2;
   uint32_t key;
 };
 
-template <bool FTZ>
+// fp32 states: to a unit in the last place or two, subnormals kept; 8-bit states: rounded.
+template <bool STATE8>
 __device__ __forceinline__ float root(float x) {
+  if constexpr (STATE8) return __fsqrt_rn(x);
   float y;
-  if constexpr (FTZ) asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  else asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// a b + c d, rounded after each product and the sum: not by the packed operations, of which a
+// multiplication is fused with the addition behind it even where both say .rn.
+__device__ __forceinline__ float sum_of_products(float a, float b, float c, float d) {
+  return __fadd_rn(__fmul_rn(a, b), __fmul_rn(c, d));
 }
 
 // One thread's 8 elements as they are in memory.
@@ -280,7 +296,7 @@ __device__ __forceinline__ void fetch(const Slot& s, const StepArgs& a, int64_t 
   if (!has_state(s, e0)) return;
   const int64_t left = s.n - e0, at = s.offset + e0;
   load_raw(s.grad, e0, left, s.grad_dtype, f.g);
-  if constexpr (MASTER) ld_cs_v8(a.master + at, f.master);
+  if constexpr (MASTER) ld_v8(a.master + at, f.master);
   else load_raw(s.param, e0, left, s.dtype, f.w);
   if constexpr (STATE8) {
     f.cm = __ldcs(reinterpret_cast<const uint2*>(static_cast<uint8_t*>(a.m) + at));
@@ -288,8 +304,8 @@ __device__ __forceinline__ void fetch(const Slot& s, const StepArgs& a, int64_t 
     f.scale_m = a.m_scale[at / kBlockElems];
     f.scale_s = a.s_scale[at / kBlockElems];
   } else {
-    ld_cs_v8(static_cast<const float*>(a.m) + at, f.m);
-    ld_cs_v8(static_cast<const float*>(a.v) + at, f.v);
+    ld_v8(static_cast<const float*>(a.m) + at, f.m);
+    ld_v8(static_cast<const float*>(a.v) + at, f.v);
   }
 }
 
@@ -325,22 +341,32 @@ __device__ __forceinline__ void update8(const Slot& s, const StepArgs& a, const 
   }
   const float shrink = 1.0f - k.lr * s.decay;
   const uint64_t shrink2 = f2_pack(shrink, shrink), minus = f2_pack(-k.step_size, -k.step_size),
-                 eps2 = f2_pack(k.eps, k.eps), cm2 = f2_pack(k.cm, k.cm), cs2 = f2_pack(k.cs, k.cs),
+                 eps2 = f2_pack(k.eps, k.eps), c2 = f2_pack(k.c, k.c),
+                 beta1 = f2_pack(k.beta1, k.beta1), omb1 = f2_pack(k.omb1, k.omb1),
+                 beta2 = f2_pack(k.beta2, k.beta2), omb2 = f2_pack(k.omb2, k.omb2),
                  root2 = f2_pack(k.root_c2, k.root_c2);
-  const float keep_m = STATE8 ? k.beta1 * scale_m : k.beta1;
-  const float keep_v = STATE8 ? k.rb2 * scale_s : k.beta2;
-  const uint64_t keep_m2 = f2_pack(keep_m, keep_m), keep_v2 = f2_pack(keep_v, keep_v);
+  const uint64_t unit_m = f2_pack(scale_m, scale_m), unit_s = f2_pack(scale_s, scale_s);
 #pragma unroll
   for (int i = 0; i < kPer; i += 2) {
-    const uint64_t x = f2_pack(g[i], g[i + 1]);
-    const uint64_t m2 = f2_fma(x, cm2, f2_mul(f2_pack(m[i], m[i + 1]), keep_m2));
-    const uint64_t y = f2_mul(x, cs2);
-    uint64_t old = f2_mul(f2_pack(v[i], v[i + 1]), keep_v2);
-    if constexpr (STATE8) old = f2_mul(old, old);
-    const uint64_t v2 = f2_fma(y, y, old);
+    const uint64_t x = f2_mul(f2_pack(g[i], g[i + 1]), c2);
+    uint64_t m2 = f2_pack(m[i], m[i + 1]), v2 = f2_pack(v[i], v[i + 1]);
+    if constexpr (STATE8) {
+      m2 = f2_mul(m2, unit_m);
+      v2 = f2_mul(v2, unit_s);
+      v2 = f2_mul(v2, v2);
+      float x0, x1, y0, y1, p0, p1, q0, q1;
+      f2_unpack(x, x0, x1);
+      f2_unpack(f2_mul(x, x), y0, y1);
+      f2_unpack(m2, p0, p1);
+      f2_unpack(v2, q0, q1);
+      m2 = f2_pack(sum_of_products(p0, k.beta1, x0, k.omb1), sum_of_products(p1, k.beta1, x1, k.omb1));
+      v2 = f2_pack(sum_of_products(q0, k.beta2, y0, k.omb2), sum_of_products(q1, k.beta2, y1, k.omb2));
+    } else {
+      m2 = f2_fma(m2, beta1, f2_mul(x, omb1));
+      v2 = f2_fma(v2, beta2, f2_mul(f2_mul(x, x), omb2));
+    }
     float v0, v1, d0, d1;
     f2_unpack(v2, v0, v1);
-    // 8 bits: a root below 2^-63 is 0 (v is below fp32's normal range there)
     const float s0 = root<STATE8>(v0), s1 = root<STATE8>(v1);
     f2_unpack(f2_fma(f2_pack(s0, s1), root2, eps2), d0, d1);
     const uint64_t u = f2_mul(m2, f2_pack(fast_rcp(d0), fast_rcp(d1)));
@@ -363,7 +389,7 @@ __device__ __forceinline__ void update8(const Slot& s, const StepArgs& a, const 
     cs = pack8<true>(v, r2, scale_s);
   }
   if (!in) return;
-  if constexpr (MASTER) st_global_cs_v8f(a.master + at, w);
+  if constexpr (MASTER) st_v8(a.master + at, w);
   store_raw(s.param, e0, left, s.dtype, w);
   if constexpr (STATE8) {
     __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.m) + at), cm);
@@ -373,8 +399,8 @@ __device__ __forceinline__ void update8(const Slot& s, const StepArgs& a, const 
       a.s_scale[at / kBlockElems] = scale_s;
     }
   } else {
-    st_global_cs_v8f(static_cast<float*>(a.m) + at, m);
-    st_global_cs_v8f(static_cast<float*>(a.v) + at, v);
+    st_v8(static_cast<float*>(a.m) + at, m);
+    st_v8(static_cast<float*>(a.v) + at, v);
   }
 }
 
@@ -393,14 +419,11 @@ __device__ __forceinline__ int find_run(const Table<CAP>& t, uint32_t& u, uint32
   return lo;
 }
 
-#ifndef FLCE_ADAMW_B8
-#define FLCE_ADAMW_B8 4
-#endif
-#ifndef FLCE_ADAMW_B32
-#define FLCE_ADAMW_B32 4
-#endif
+// Two blocks per SM's worth of registers for fp32 states, whose loads are all of a unit's bytes (600M
+// with masters 2.96 ms; for four blocks 3.02), four for 8 bits, bound by their arithmetic (300M: 1.09 ms
+// against 1.16).
 template <bool STATE8, bool MASTER, int CAP>
-__global__ void __launch_bounds__(kThreads, STATE8 ? FLCE_ADAMW_B8 : FLCE_ADAMW_B32)
+__global__ void __launch_bounds__(kThreads, STATE8 ? 4 : 2)
     adamw_kernel(const __grid_constant__ Table<CAP> t, const __grid_constant__ StepArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t step = *a.step + 1;
@@ -414,11 +437,11 @@ __global__ void __launch_bounds__(kThreads, STATE8 ? FLCE_ADAMW_B8 : FLCE_ADAMW_
   }
   if (!skip) {
     Coef k;
+    k.c = c;
     k.beta1 = a.beta1;
+    k.omb1 = a.omb1;
     k.beta2 = a.beta2;
-    k.rb2 = a.rb2;
-    k.cm = c * a.omb1;
-    k.cs = c * a.romb2;
+    k.omb2 = a.omb2;
     k.eps = a.eps;
     k.lr = a.lr_ptr ? *a.lr_ptr : a.lr;
     // 1 - b^t = -(e^{t ln b} - 1): exact to fp32 for small t ln b too
@@ -460,46 +483,58 @@ __global__ void __launch_bounds__(kThreads, STATE8 ? FLCE_ADAMW_B8 : FLCE_ADAMW_
 }
 
 // ------------------------------------------------------------------ the norm
-// Sum of (scale g)^2: up to 512 squares in fp32, from there on in 64 bits (whose units are few:
-// one addition per 8 squares took longer than the bytes), in a fixed order.
+// Sum of (scale g)^2, each square rounded to fp32, their sum exact to 2^-45 or so: a pair of floats per
+// lane of a packed addition, whose rounding errors are added up beside it (two 64-bit additions per
+// 16 squares took longer than their bytes do).
 constexpr int kNormDepth = 4;  // units in flight
-constexpr int kNormFold = 64;  // units whose squares a thread sums in fp32
 
-__device__ __forceinline__ float squares(const float (&x)[kPer], float scale) {
-  float sum = 0.0f;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const float y = scale * x[i];
-    sum = fmaf(y, y, sum);
+struct PairSum {
+  uint64_t hi = 0, lo = 0;  // two lanes each
+
+  // (a + b and what it lost: the two-sum of Knuth)
+  __device__ __forceinline__ void add(uint64_t x) {
+    const uint64_t sign = 0x8000000080000000ull;
+    const uint64_t sum = f2_add(hi, x), part = f2_add(sum, hi ^ sign);
+    const uint64_t lost = f2_add(f2_add(hi, f2_add(sum, part ^ sign) ^ sign), f2_add(x, part ^ sign));
+    hi = sum;
+    lo = f2_add(lo, lost);
   }
-  return sum;
-}
+  __device__ __forceinline__ double value() const {
+    float h0, h1, l0, l1;
+    f2_unpack(hi, h0, h1);
+    f2_unpack(lo, l0, l1);
+    // an infinity's lost part is NaN
+    if (!isfinite(h0) || !isfinite(h1)) return static_cast<double>(h0) + h1;
+    return (static_cast<double>(h0) + l0) + (static_cast<double>(h1) + l1);
+  }
+};
 
 // `units` units of one tensor from element e0 on (this thread's first)
-__device__ __forceinline__ double sum_units(const Slot& s, int64_t e0, int64_t units, float scale) {
-  double total = 0.0;
-  for (int64_t u = 0; u < units; u += kNormFold) {
-    const int64_t end = u + kNormFold < units ? u + kNormFold : units;
-    float part[kNormDepth] = {};
+__device__ __forceinline__ void sum_units(const Slot& s, int64_t e0, int64_t units, float scale,
+                                          PairSum& sum) {
+  const uint64_t scale2 = f2_pack(scale, scale);
 #pragma unroll 1
-    for (int64_t v = u; v < end; v += kNormDepth) {
-      Raw r[kNormDepth];
+  for (int64_t v = 0; v < units; v += kNormDepth) {
+    Raw r[kNormDepth];
 #pragma unroll
-      for (int d = 0; d < kNormDepth; ++d) {
-        const int64_t e = e0 + (v + d) * kUnit;
-        r[d].q[0] = r[d].q[1] = make_uint4(0, 0, 0, 0);
-        if (v + d < end && e < s.n) load_raw(s.grad, e, s.n - e, s.grad_dtype, r[d]);
-      }
+    for (int d = 0; d < kNormDepth; ++d) {
+      const int64_t e = e0 + (v + d) * kUnit;
+      r[d].q[0] = r[d].q[1] = make_uint4(0, 0, 0, 0);
+      if (v + d < units && e < s.n) load_raw(s.grad, e, s.n - e, s.grad_dtype, r[d]);
+    }
 #pragma unroll
-      for (int d = 0; d < kNormDepth; ++d) {
-        float x[kPer];
-        widen(r[d], s.grad_dtype, x);
-        part[d] += squares(x, scale);
+    for (int d = 0; d < kNormDepth; ++d) {
+      float x[kPer];
+      widen(r[d], s.grad_dtype, x);
+#pragma unroll
+      for (int i = 0; i < kPer; i += 2) {
+        const uint64_t y = f2_mul(f2_pack(x[i], x[i + 1]), scale2);
+        float y0, y1;
+        f2_unpack(y, y0, y1);
+        sum.add(f2_pack(__fmul_rn(y0, y0), __fmul_rn(y1, y1)));
       }
     }
-    total += (part[0] + part[1]) + (part[2] + part[3]);
   }
-  return total;
 }
 
 __device__ __forceinline__ double block_sum(double x) {
@@ -519,16 +554,16 @@ __global__ void __launch_bounds__(kThreads)
     norm_kernel(const __grid_constant__ Table<CAP> t, const __grid_constant__ NormArgs a) {
   uint32_t u, end;
   int i = find_run(t, u, end);
-  double total = 0.0;
+  PairSum sum_of;
   while (u < end) {
     while (i + 1 < t.count && t.first[i + 1] <= u) ++i;
     const Slot& s = t.slot[i];
     const uint32_t stop = i + 1 < t.count && t.first[i + 1] < end ? t.first[i + 1] : end;
     const int64_t e0 = static_cast<int64_t>(u - t.first[i]) * kUnit + threadIdx.x * kPer;
-    total += sum_units(s, e0, stop - u, a.scale);
+    sum_units(s, e0, stop - u, a.scale, sum_of);
     u = stop;
   }
-  total = block_sum(total);
+  const double total = block_sum(sum_of.value());
   __shared__ bool is_last;
   if (threadIdx.x == 0) {
     a.partial[a.base + blockIdx.x] = total;
@@ -763,8 +798,7 @@ int flce_adamw_step(const flce_adamw_params* p, const flce_adamw_tensor* tensors
   a.beta1 = static_cast<float>(p->beta1);
   a.omb1 = static_cast<float>(1.0 - p->beta1);
   a.beta2 = static_cast<float>(p->beta2);
-  a.rb2 = static_cast<float>(sqrt(p->beta2));
-  a.romb2 = static_cast<float>(sqrt(1.0 - p->beta2));
+  a.omb2 = static_cast<float>(1.0 - p->beta2);
   a.eps = static_cast<float>(p->eps);
   a.grad_scale = static_cast<float>(p->grad_scale);
   a.max_norm = static_cast<float>(p->max_norm);

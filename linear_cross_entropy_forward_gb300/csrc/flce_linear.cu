@@ -75,9 +75,8 @@ __device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, uint
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "l"(policy)
       : "memory");
 }
-// 16 fp32 columns of this warp's 32 TMEM lanes
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
-  uint32_t r[16];
+// 16 fp32 columns of this warp's 32 TMEM lanes; tmem_wait before they are looked at
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
       "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
@@ -86,9 +85,13 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
         "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr)
       : "memory");
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+// (the registers go through the wait, so that nothing reads them before it)
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
 }
 
 template <bool MN, int ROWS>
@@ -108,9 +111,15 @@ __device__ __forceinline__ void load_rows(uint8_t* dst, const CUtensorMap* map, 
 // A block per tile of 128 columns of y and tt tokens (a multiple of 16) and share of the depth; the
 // blocks of a cluster share a tile's depth, leave their sums in shared memory, and each adds up and
 // finishes a part of the tile's tokens, in the blocks' order.
+//
+// The tensor cores cut off what an addition to an accumulator loses, so that its error grows with the
+// additions: 4.4e-6 of fp32 logits after a depth of 4096.  A block's depth goes to as many accumulators
+// one after the other as TMEM holds beside another block (eight at most: 4.8e-7), whose sums are then
+// added with rounding.  A bf16 output, whose rounding is 2^-8, takes one.
 struct SplitArgs {
   int32_t M, N;
   int32_t tt, m_tiles, k_blocks, stages;
+  int32_t parts;  // accumulators that the depth is spread over
   LinearOut out;
   uint32_t* err;
   int32_t clear;
@@ -148,7 +157,8 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
   const int n0 = tile / a.m_tiles * kRows, m0 = tile % a.m_tiles * a.tt;
   const int kb0 = static_cast<int>(int64_t(a.k_blocks) * rank / size);
   const int kb1 = static_cast<int>(int64_t(a.k_blocks) * (rank + 1) / size);
-  const uint32_t cols = a.tt <= 32 ? 32 : a.tt <= 64 ? 64 : a.tt <= 128 ? 128 : 256;
+  const int width = a.tt * a.parts;
+  const uint32_t cols = width <= 32 ? 32 : width <= 64 ? 64 : width <= 128 ? 128 : 256;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
@@ -213,15 +223,18 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
       const uint64_t b0 = operand_desc<B_MN>(smem_u32(sB), 0, strides);
       constexpr uint64_t kKA = (A_MN ? UK * 128 : UK * 2) >> 4;
       constexpr uint64_t kKB = (B_MN ? UK * 128 : UK * 2) >> 4;
-      int stage = 0;
+      int stage = 0, part = 0, until = kb0;
       uint32_t phase = 0;
       for (int kb = kb0; kb < kb1; ++kb) {
         if (!mbar_wait(&full[stage], phase, abort_flag, a.err)) break;
         tc_fence_after();
+        const bool begin = kb == until;  // of an accumulator
+        if (begin) until = kb0 + (kb1 - kb0) * ++part / a.parts;
+        const uint32_t d = tmem + (part - 1) * a.tt;
         const uint64_t as = a0 + stage * (kABytes >> 4), bs = b0 + stage * (b_bytes >> 4);
 #pragma unroll
         for (int kk = 0; kk < BK / UK; ++kk)
-          umma_bf16(tmem, as + kk * kKA, bs + kk * kKB, idesc, kb == kb0 && kk == 0 ? 0u : 1u);
+          umma_bf16(d, as + kk * kKA, bs + kk * kKB, idesc, begin && kk == 0 ? 0u : 1u);
         umma_commit(&empty[stage]);
         if (++stage == stages) {
           stage = 0;
@@ -245,9 +258,22 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
     const uint32_t tbase = tmem + (static_cast<uint32_t>(q * 32) << 16);
 #pragma unroll 1
     for (int c = half * 16; c < rows; c += 32) {
-      float x[16];
+      float x[16] = {};
       __syncwarp();
-      tmem_ld16(tbase + c, x);
+      // the accumulators' columns, two on their way
+      uint32_t u[16], v[16];
+      for (int p = 0; p < a.parts; p += 2) {
+        tmem_ld16(tbase + p * a.tt + c, u);
+        if (p + 1 < a.parts) tmem_ld16(tbase + (p + 1) * a.tt + c, v);
+        tmem_wait(u);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] += __uint_as_float(u[i]);
+        if (p + 1 < a.parts) {
+          tmem_wait(v);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[i] += __uint_as_float(v[i]);
+        }
+      }
       if (size > 1) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) part[(c + i) * kRows + nl] = x[i];
@@ -534,6 +560,10 @@ int launch_split(const Product& g, const Plan& s, const LinearOut& out, uint32_t
   a.m_tiles = static_cast<int32_t>(cdiv(g.rows, s.tt));
   a.k_blocks = static_cast<int32_t>(cdiv(g.depth, BK));
   a.stages = s.stages;
+  // parts of a block's share of the depth, of one 64-deep block at least
+  const int share = a.k_blocks / s.size;
+  a.parts = !out.out_f32 ? 1 : 256 / s.tt < 8 ? 256 / s.tt : 8;
+  if (a.parts > share) a.parts = share;
   a.out = out;
   a.err = err;
   a.clear = clear;

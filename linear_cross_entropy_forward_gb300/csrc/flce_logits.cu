@@ -33,29 +33,16 @@
 namespace flce {
 namespace {
 
-#ifndef FLCE_LOGITS_FILL
-#define FLCE_LOGITS_FILL 6
-#endif
-#ifndef FLCE_LOGITS_STAGE
-#define FLCE_LOGITS_STAGE 16384
-#endif
-#ifndef FLCE_LOGITS_ROOM
-#define FLCE_LOGITS_ROOM 32768
-#endif
-#ifndef FLCE_LOGITS_B
-#define FLCE_LOGITS_B 3
-#endif
-#ifndef FLCE_LOGITS_DEEP
-#define FLCE_LOGITS_DEEP 4
-#endif
-#ifndef FLCE_LOGITS_T
-#define FLCE_LOGITS_T 256
-#endif
-constexpr int kThreads = FLCE_LOGITS_T;
+// 256 threads and 64 KB (three blocks per SM): 512 threads took 204 us where 256 took 173 (384 x 256000
+// in bf16 after up to 8192 tokens each), 128 threads and half the memory 189.
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kBlocks = 3;           // per SM
+constexpr int kFill = 6;             // blocks per SM that a row's are multiplied up to (12: 200 us, 4: 206)
 constexpr int kMaxCluster = 16;
-constexpr int kStage = FLCE_LOGITS_STAGE;  // bytes of logits per copy into shared memory, two in flight
-constexpr int kRoom = FLCE_LOGITS_ROOM;    // bytes of counters per block
+constexpr int kStage = 16384;        // bytes of logits per copy into shared memory, two on their way
+constexpr int kRoom = 32768;         // bytes of counters
+constexpr int kDeep = 2;             // 16-byte words of tokens on their way per thread
 constexpr int kMaxBias = 2048;       // entries of a row's list: 16 KB of shared memory
 
 // Counters: occurrences among the generated tokens, and flags of the prompt's tokens and of
@@ -222,7 +209,7 @@ __device__ __forceinline__ void bump(uint32_t at, uint32_t columns, uint32_t cou
 template <typename COUNTER, bool FLAG, typename ID>
 __device__ __forceinline__ void count(const ID* tokens, int t0, int t1, int first, uint32_t columns,
                                       uint32_t counters) {
-  constexpr int kIds = 16 / sizeof(ID), kDeep = FLCE_LOGITS_DEEP;
+  constexpr int kIds = 16 / sizeof(ID);
   const uint32_t none = 0xffffffffu;  // no column
   auto add = [&](const uint4& q) {
     if constexpr (sizeof(ID) == 8) {  // the upper half of an id of the row is 0
@@ -281,6 +268,31 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
           dst),
       "l"(src), "r"(bytes), "r"(smem_u32(bar))
       : "memory");
+}
+
+template <typename COUNTER>
+__device__ __forceinline__ float count_of(uint32_t n) {
+  // below 2^23 a whole number is the end of a float of that exponent: no conversion
+  if constexpr (sizeof(typename COUNTER::Word) == 2)
+    return __uint_as_float(0x4B000000u | (n & COUNTER::kCount)) - 8388608.0f;
+  else
+    return static_cast<float>(n & COUNTER::kCount);
+}
+
+// Zeros for logits [l0, l1) of an output row.
+template <typename T>
+__device__ __forceinline__ void zero_columns(const Args& a, uint8_t* out, int l0, int l1) {
+  const int bytes = a.out_f32 ? 4 : sizeof(T);
+  uint8_t* p = out + static_cast<int64_t>(max(l0, 0)) * bytes;
+  uint8_t* end = out + static_cast<int64_t>(l1) * bytes;
+  uint8_t* first = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 15) & ~uintptr_t(15));
+  if (first > end) first = end;
+  uint8_t* last = first + (end - first) / 16 * 16;
+  const int tid = threadIdx.x;
+  for (uint8_t* q = first + tid * 16; q < last; q += kThreads * 16)
+    __stcs(reinterpret_cast<uint4*>(q), make_uint4(0, 0, 0, 0));
+  if (tid < 8 && p + tid * 2 < first) *reinterpret_cast<uint16_t*>(p + tid * 2) = 0;
+  if (tid < 8 && last + tid * 2 < end) *reinterpret_cast<uint16_t*>(last + tid * 2) = 0;
 }
 
 // What all of a block needs to know of its row, found out by one thread.
@@ -374,7 +386,7 @@ struct Running {
 // as it has counters for, a pass by copies of kStage bytes, two on their way at a time; the vectors
 // at a row's ends that are not whole are done element by element.
 template <typename T, typename COUNTER, int MODE>
-__global__ void __launch_bounds__(kThreads, FLCE_LOGITS_B)
+__global__ void __launch_bounds__(kThreads, kBlocks)
     logits_kernel(const __grid_constant__ Args a) {
   constexpr int VEC = 16 / sizeof(T);
   constexpr uint32_t kAll = (1u << VEC) - 1;
@@ -392,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, FLCE_LOGITS_B)
   __shared__ uint32_t mask_bits[2][kColumns / 32];  // of two copies, a bit per column
   const uint32_t rank = cluster_ctarank(), size = cluster_size();
   const int64_t row = blockIdx.x / size;
-  const int V = static_cast<int>(a.V), tid = threadIdx.x;
+  const int V = static_cast<int>(a.V), tid = threadIdx.x, lane = tid & 31;
   const T* x = static_cast<const T*>(a.logits) + row * a.ld;
   const int pre = static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
   const int span = V + pre, columns = static_cast<int>(a.columns), room = static_cast<int>(a.room);
@@ -496,6 +508,12 @@ __global__ void __launch_bounds__(kThreads, FLCE_LOGITS_B)
   __syncthreads();
   const bool zero = BACKWARD && r.zero;
 
+  if (zero) {  // the same columns, without a look at the logits
+    zero_columns<T>(a, out, begin - pre, end - pre);
+    if (copies > 0) mbar_wait(&landed[0], 0, &gave_up, a.err);  // nothing is on its way when it ends
+    if (copies > 1) mbar_wait(&landed[1], 0, &gave_up, a.err);
+    return;
+  }
   // z of the sum so far, by its counter; the slope by its logit goes into k
   auto change = [&](float y, uint32_t n, int c, float& k) {
     if (n & (COUNTER::kSeen | COUNTER::kCount)) {
@@ -513,16 +531,17 @@ __global__ void __launch_bounds__(kThreads, FLCE_LOGITS_B)
     return y;
   };
   auto gradient = [&](float z, float slope, bool label) {
-    const float q = z - r.lse;
-    const float e = fast_ex2(q * kLog2e);
-    float dz = e != 0.0f ? -e * fmaf(r.h, q + r.ent, r.g) : 0.0f;
-    if (label) dz += r.g;
+    const float q = fmaxf(z - r.lse, -200.0f), e = fast_ex2(q * kLog2e);
+    const float dz = -e * (fmaf(r.h, q + r.ent, r.g) + (r.lse - r.lse)) + (label ? r.g : 0.0f);
     return slope * dz;
   };
   Running run;
   float inv_temp = r.inv_temp;
   const float rep = COUNT ? r.rep : 1.0f, inv_rep = COUNT ? r.inv_rep : 1.0f;
   const float freq = COUNT ? r.freq : 0.0f, pres = COUNT ? r.pres : 0.0f;
+  // the gradient of a column that is not the label's: p (down_h ln p + down_g); a row whose lse is NaN has NaN
+  const float down_h = BACKWARD ? -r.h * inv_temp : 0.0f;
+  float down_g = BACKWARD ? -fmaf(r.h, r.ent, r.g) * inv_temp + (r.lse - r.lse) : 0.0f;
   const bool stats = !BACKWARD && a.stats, entropy = a.entropy != nullptr;
   const int label = r.label;
   int copied = 0;
@@ -530,33 +549,31 @@ __global__ void __launch_bounds__(kThreads, FLCE_LOGITS_B)
     const int c0 = begin + pass * room, c1 = min(c0 + room, end);
     if (c0 >= c1) break;
     if constexpr (COUNT) {
-      if (!zero) {
-        if (pass > 0) {
-          __syncthreads();  // the last pass's counters are done with
-          clear();
-          __syncthreads();
-        }
-        if (r.length > 0) {
-          const uint32_t at = smem_u32(counters);
-          if (a.ids64) {
-            const auto* t = static_cast<const int64_t*>(a.tokens) + row * a.ld_tokens;
-            count<COUNTER, true>(t, 0, r.prompt, c0 - pre, c1 - c0, at);
-            count<COUNTER, false>(t, r.prompt, r.length, c0 - pre, c1 - c0, at);
-          } else {
-            const auto* t = static_cast<const int32_t*>(a.tokens) + row * a.ld_tokens;
-            count<COUNTER, true>(t, 0, r.prompt, c0 - pre, c1 - c0, at);
-            count<COUNTER, false>(t, r.prompt, r.length, c0 - pre, c1 - c0, at);
-          }
-        }
-        for (int j = tid; j < n_bias; j += kThreads) {
-          const int c = bias_col[j];
-          if (c < c0 || c >= c1) continue;
-          const uint32_t byte = (c - c0) * sizeof(Word);
-          atomicOr(reinterpret_cast<uint32_t*>(counters + (byte & ~3u)),
-                   COUNTER::kBiased << (8 * (byte & 3u)));
-        }
+      if (pass > 0) {
+        __syncthreads();  // the last pass's counters are done with
+        clear();
         __syncthreads();
       }
+      if (r.length > 0) {
+        const uint32_t at = smem_u32(counters);
+        if (a.ids64) {
+          const auto* t = static_cast<const int64_t*>(a.tokens) + row * a.ld_tokens;
+          count<COUNTER, true>(t, 0, r.prompt, c0 - pre, c1 - c0, at);
+          count<COUNTER, false>(t, r.prompt, r.length, c0 - pre, c1 - c0, at);
+        } else {
+          const auto* t = static_cast<const int32_t*>(a.tokens) + row * a.ld_tokens;
+          count<COUNTER, true>(t, 0, r.prompt, c0 - pre, c1 - c0, at);
+          count<COUNTER, false>(t, r.prompt, r.length, c0 - pre, c1 - c0, at);
+        }
+      }
+      for (int j = tid; j < n_bias; j += kThreads) {
+        const int c = bias_col[j];
+        if (c < c0 || c >= c1) continue;
+        const uint32_t byte = (c - c0) * sizeof(Word);
+        atomicOr(reinterpret_cast<uint32_t*>(counters + (byte & ~3u)),
+                 COUNTER::kBiased << (8 * (byte & 3u)));
+      }
+      __syncthreads();
     }
     // a row's first and last columns where they are no whole vector
     for (int edge = 0; edge < 2; ++edge) {
@@ -573,10 +590,8 @@ __global__ void __launch_bounds__(kThreads, FLCE_LOGITS_B)
           ok = mask[l] != 0;
         float z = widen1(x[l]), k = 1.0f;
         if constexpr (COUNT) {
-          if (!zero) {
-            const uint32_t n = reinterpret_cast<const Word*>(counters)[c + i - c0];
-            if (n) z = change(z, n, c + i, k);
-          }
+          const uint32_t n = reinterpret_cast<const Word*>(counters)[c + i - c0];
+          if (n) z = change(z, n, c + i, k);
         }
         z = ok ? z * inv_temp : -INFINITY;
         if (stats) {
@@ -584,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, FLCE_LOGITS_B)
           run.add(one, entropy);
           if (l == label) label_z = z;
         }
-        if (BACKWARD) z = zero ? 0.0f : gradient(z, ok ? k * inv_temp : 0.0f, l == label);
+        if (BACKWARD) z = gradient(z, ok ? k * inv_temp : 0.0f, l == label);
         if (out) {
           if (a.out_f32) reinterpret_cast<float*>(out)[l] = z;
           else reinterpret_cast<T*>(out)[l] = narrow1<T>(z);
@@ -598,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, FLCE_LOGITS_B)
       const int stop = min(base + kColumns, p1);  // of this pass and copy
       if (k >= copied) {
         // a wait that runs out leaves NaN in the outputs; every thread goes the same way on
-        if (!mbar_wait(&landed[k & 1], (k >> 1) & 1, &gave_up, a.err)) inv_temp = NAN;
+        if (!mbar_wait(&landed[k & 1], (k >> 1) & 1, &gave_up, a.err)) inv_temp = down_g = NAN;
         copied = k + 1;
       }
       const uint8_t* staged = shared + (k & 1) * kStage;
@@ -607,16 +622,13 @@ __global__ void __launch_bounds__(kThreads, FLCE_LOGITS_B)
 #pragma unroll 1
       for (int cv = c + tid * VEC; cv < stop; cv += kThreads * VEC) {
         const int l = cv - pre;
-        float z[VEC], slope[BACKWARD ? VEC : 1];
+        float z[VEC];
+        uint32_t any = 0, biased = 0;    // columns that are changed, and by a bias
+        float times[COUNT ? VEC : 1];    // where any: the slope by the repetition penalty
         widen<T>(*reinterpret_cast<const uint4*>(staged + (cv - base) * sizeof(T)), z);
-        if constexpr (BACKWARD) {
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) slope[i] = inv_temp;
-        }
         if constexpr (COUNT) {
           constexpr int WORDS = VEC * sizeof(Word) / 4;
           uint32_t n32[WORDS];
-          uint32_t any = 0;
           const uint8_t* src = counters + (cv - c0) * sizeof(Word);
           if constexpr (WORDS == 2) {
             *reinterpret_cast<uint2*>(n32) = *reinterpret_cast<const uint2*>(src);
@@ -627,27 +639,38 @@ __global__ void __launch_bounds__(kThreads, FLCE_LOGITS_B)
           }
 #pragma unroll
           for (int j = 0; j < WORDS; ++j) any |= n32[j];
-          if (any && !zero) {
-            // without branches, as lanes differ; biases, which are few, behind it
-            uint32_t biased = 0;
+          if (any) {
+            // without branches, as lanes differ
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
               const uint32_t n = sizeof(Word) == 4
                                      ? n32[i % WORDS] : n32[i / 2 % WORDS] >> (16 * (i & 1)) & 0xffffu;
-              const float times = z[i] > 0.0f ? inv_rep : rep;
-              const float k1 = n & (COUNTER::kSeen | COUNTER::kCount) ? times : 1.0f;
-              const float made = static_cast<float>(n & COUNTER::kCount);
-              z[i] = fmaf(-freq, made, z[i] * k1) - (n & COUNTER::kCount ? pres : 0.0f);
-              if constexpr (BACKWARD) slope[i] *= k1;
+              const float k1 = z[i] > 0.0f ? inv_rep : rep;
+              times[i] = n & (COUNTER::kSeen | COUNTER::kCount) ? k1 : 1.0f;
+              z[i] = fmaf(-freq, count_of<COUNTER>(n), z[i] * times[i]) -
+                     (n & COUNTER::kCount ? pres : 0.0f);
               biased |= n & COUNTER::kBiased;
             }
-            if (biased) {
+          }
+          if (n_bias > 0) {
+            // the lanes of a warp look through 32 entries at a time, for all of its columns
+            const int cw = cv - lane * VEC;
+            const uint32_t lanes = stop - cw >= 32 * VEC ? 0xffffffffu
+                                                         : (1u << ((stop - cw + VEC - 1) / VEC)) - 1u;
+            if (__any_sync(lanes, biased)) {
+              const int width = __popc(lanes);
 #pragma unroll 1
-              for (int j = 0; j < n_bias; ++j) {
-                const int i = bias_col[j] - cv;
-                if (i < 0 || i >= VEC) continue;
+              for (int j0 = 0; j0 < n_bias; j0 += width) {
+                const int at = j0 + lane < n_bias ? bias_col[j0 + lane] - cw : -1;
+                const float value = j0 + lane < n_bias ? bias_val[j0 + lane] : 0.0f;
+                for (uint32_t hits = __ballot_sync(lanes, at >= 0 && at < width * VEC); hits;
+                     hits &= hits - 1) {
+                  const int from_lane = __ffs(hits) - 1;
+                  const int i = __shfl_sync(lanes, at, from_lane) - lane * VEC;
+                  const float v = __shfl_sync(lanes, value, from_lane);
 #pragma unroll
-                for (int q = 0; q < VEC; ++q) z[q] += q == i ? bias_val[j] : 0.0f;
+                  for (int q = 0; q < VEC; ++q) z[q] += q == i ? v : 0.0f;
+                }
               }
             }
           }
@@ -656,16 +679,14 @@ __global__ void __launch_bounds__(kThreads, FLCE_LOGITS_B)
 #pragma unroll
         for (int i = 0; i < VEC; i += 2)
           f2_unpack(f2_mul(f2_pack(z[i], z[i + 1]), inv2), z[i], z[i + 1]);
+        uint32_t there = kAll;
         if (a.mask_kind) {
           const int at = cv - base;
-          const uint32_t there = mask_bits[k & 1][at >> 5] >> (at & 31) & kAll;
+          there = mask_bits[k & 1][at >> 5] >> (at & 31) & kAll;
           if (there != kAll) {
 #pragma unroll
             for (int i = 0; i < VEC; ++i)
-              if (!(there >> i & 1)) {
-                z[i] = -INFINITY;
-                if constexpr (BACKWARD) slope[i] = 0.0f;
-              }
+              if (!(there >> i & 1)) z[i] = -INFINITY;
           }
         }
         if constexpr (!BACKWARD) {
@@ -681,8 +702,29 @@ __global__ void __launch_bounds__(kThreads, FLCE_LOGITS_B)
           }
           if (!out) continue;
         } else {
+          // p and its logarithm from q = max(z - lse, -200): p is 0 there, and -inf stays out of the sums
+          const uint64_t minus = f2_pack(-r.lse, -r.lse), log2 = f2_pack(kLog2e, kLog2e);
+          const uint64_t h2 = f2_pack(down_h, down_h), g2 = f2_pack(down_g, down_g);
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) z[i] = zero ? 0.0f : gradient(z[i], slope[i], i == label - l);
+          for (int i = 0; i < VEC; i += 2) {
+            float q0, q1, t0, t1;
+            f2_unpack(f2_add(f2_pack(z[i], z[i + 1]), minus), q0, q1);
+            const uint64_t q = f2_pack(fmaxf(q0, -200.0f), fmaxf(q1, -200.0f));
+            f2_unpack(f2_mul(q, log2), t0, t1);
+            const uint64_t p = f2_pack(fast_ex2(t0), fast_ex2(t1));
+            f2_unpack(f2_mul(p, f2_fma(h2, q, g2)), z[i], z[i + 1]);
+          }
+          if (static_cast<uint32_t>(label - l) < VEC) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i)
+              if (i == label - l && (there >> i & 1)) z[i] += r.g * inv_temp;
+          }
+          if constexpr (COUNT) {
+            if (any) {
+#pragma unroll
+              for (int i = 0; i < VEC; ++i) z[i] *= times[i];
+            }
+          }
         }
         if (a.out_f32) {
           float* o = reinterpret_cast<float*>(out) + l;
@@ -804,7 +846,7 @@ int run(Args a, int sms, cudaStream_t st) {
   // As few blocks per row as fill the GPU several times over, so that its last round is a small
   // part, but no more than have a vector for half of their threads.
   int size = 1;
-  while (size < kMaxCluster && a.R * size < FLCE_LOGITS_FILL * sms && span > size * wide / 2) size *= 2;
+  while (size < kMaxCluster && a.R * size < kFill * sms && span > size * wide / 2) size *= 2;
   a.columns = cdiv(cdiv(span, size), unit) * unit;
   a.passes = static_cast<int32_t>(COUNT ? cdiv(a.columns, most) : 1);
   a.room = cdiv(cdiv(a.columns, a.passes), unit) * unit;
