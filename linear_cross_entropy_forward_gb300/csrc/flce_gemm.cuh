@@ -59,7 +59,7 @@ constexpr int BK = 64;  // one 128-byte swizzle row of bf16
 constexpr int UK = 16;  // K of one kind::f16 UMMA
 constexpr int PAIR_BM = 256;  // rows of a pair tile (128 per CTA)
 enum EpiKind { EPI_FWD_STATS = 0, EPI_DLOGITS = 1, EPI_STORE_BF16 = 2, EPI_ACCUM = 3,
-               EPI_LINEAR = 4 };
+               EPI_LINEAR = 4, EPI_LINEAR_F32 = 5 };
 
 // Epilogue warps per CTA: 4 (one per TMEM lane quadrant, all of a tile's columns)
 // or 8 (two per quadrant, half the columns each).  Epilogue arithmetic costs the
@@ -72,7 +72,7 @@ enum EpiKind { EPI_FWD_STATS = 0, EPI_DLOGITS = 1, EPI_STORE_BF16 = 2, EPI_ACCUM
 #endif
 template <int EPI>
 __host__ __device__ constexpr int epi_warps() {
-  return FLCE_EPI_WARPS ? FLCE_EPI_WARPS : (EPI == EPI_DLOGITS || EPI == EPI_LINEAR ? 8 : 4);
+  return FLCE_EPI_WARPS ? FLCE_EPI_WARPS : (EPI == EPI_DLOGITS || EPI == EPI_LINEAR || EPI == EPI_LINEAR_F32 ? 8 : 4);
 }
 template <int EPI>
 __host__ __device__ constexpr int pair_threads() {
@@ -613,6 +613,16 @@ struct Epilogue<EPI_LINEAR> {
   }
 };
 
+// The tensor cores cut off what an addition to an accumulator loses: after a depth of 4096 fp32
+// outputs are 4.4e-6 off, where rounding would leave 6e-7.  For these an accumulator takes
+// kDrainBlocks 64-deep blocks, and the epilogue warps add its sums to their own in registers
+// (128 per thread) while the next one fills: 5e-7.
+constexpr int kDrainBlocks = 8;
+template <int EPI>
+__host__ __device__ constexpr bool drained() {
+  return EPI == EPI_LINEAR_F32;
+}
+
 // ------------------------------------------------------------------ pair kernel
 // Both producers of a pair load their halves; completion is counted on the pair
 // leader's full barrier, which expects the bytes landing in both CTAs.  The leader's
@@ -678,7 +688,7 @@ __global__ void __launch_bounds__(pair_threads<EPI>(), 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
   // (a wait that runs out does so seconds later)
-  if (EPI == EPI_LINEAR && ea.clear && blockIdx.x == 0 && threadIdx.x == 0) *ea.err = 0;
+  if ((EPI == EPI_LINEAR || EPI == EPI_LINEAR_F32) && ea.clear && blockIdx.x == 0 && threadIdx.x == 0) *ea.err = 0;
   const int total = sh.m_tiles * sh.n_tiles;
   constexpr uint32_t kSched = 1;  // the CTA whose warp 1 schedules the pair's tiles
   const uint32_t rempty_sched = mapa_shared(smem_u32(&rempty[0]), kSched);
@@ -794,9 +804,44 @@ __global__ void __launch_bounds__(pair_threads<EPI>(), 1)
       constexpr uint64_t kKA = (A_MN ? UK * 128 : UK * 2) >> 4;
       constexpr uint64_t kKB = (B_MN ? UK * 128 : UK * 2) >> 4;
       uint32_t stage = 0, phase = 0;
+      [[maybe_unused]] int unit = 0;  // accumulators filled, where a tile takes several
       bool ok = true;
       for (int it = 0; ok; ++it) {
         if (take_tile(it, true) >= total) break;
+        if constexpr (drained<EPI>()) {
+          for (int kb0 = 0; kb0 < sh.k_blocks && ok; kb0 += kDrainBlocks, ++unit) {
+            const int acc = unit % C::NACC;
+            if (!mbar_wait<true>(&tempty[acc], ((unit / C::NACC) & 1) ^ 1u, abort_flag, ea.err)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const int kb1 = kb0 + kDrainBlocks < sh.k_blocks ? kb0 + kDrainBlocks : sh.k_blocks;
+            for (int kb = kb0; kb < kb1; ++kb) {
+              if (!mbar_wait(&full[stage], phase, abort_flag, ea.err)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              const uint64_t a_st = a_desc0 + stage * (C::A_BYTES >> 4);
+              const uint64_t b_st = b_desc0 + stage * (C::B_BYTES >> 4);
+              uint64_t ad[BK / UK], bd[BK / UK];
+#pragma unroll
+              for (int kk = 0; kk < BK / UK; ++kk) {
+                ad[kk] = a_st + kk * kKA;
+                bd[kk] = b_st + kk * kKB;
+              }
+              umma_bf16_pair_x4(tmem_base + acc * TN, ad, bd, IDESC, kb != kb0 ? 1u : 0u);
+              umma_commit_pair(&empty[stage], kPairMask);
+              if (++stage == C::STAGES) {
+                stage = 0;
+                phase ^= 1u;
+              }
+            }
+            if (ok) umma_commit_pair(&tfull[acc], kPairMask);
+          }
+          continue;
+        }
         const int acc = it % C::NACC;
         const uint32_t aph = (it / C::NACC) & 1;
         // the epilogues of both CTAs arrive here (cluster-scope acquire)
@@ -834,6 +879,7 @@ __global__ void __launch_bounds__(pair_threads<EPI>(), 1)
     const int half = (warp - 2) >> 2;
     const int r = q * 32 + lane;
     const uint32_t tempty_leader = mapa_shared(smem_u32(&tempty[0]), kLead);
+    [[maybe_unused]] int unit = 0;
     for (int it = 0;; ++it) {
       const int t = take_tile(it, false);
       __syncwarp();
@@ -841,6 +887,48 @@ __global__ void __launch_bounds__(pair_threads<EPI>(), 1)
       if (t >= total) break;
       int mt, nt;
       tile_coords(t, sh, mt, nt);
+      if constexpr (drained<EPI>()) {
+        float sum[C::EPI_COLS];
+#pragma unroll
+        for (int j = 0; j < C::EPI_COLS; ++j) sum[j] = 0.0f;
+        bool got = true;
+        for (int kb0 = 0; kb0 < sh.k_blocks; kb0 += kDrainBlocks, ++unit) {
+          const int acc = unit % C::NACC;
+          if (!mbar_wait(&tfull[acc], (unit / C::NACC) & 1, abort_flag, ea.err)) {
+            got = false;
+            break;
+          }
+          __syncwarp();
+          tc_fence_after();
+          const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * TN +
+                              half * C::EPI_COLS;
+#pragma unroll
+          for (int c = 0; c < C::EPI_CHUNKS; ++c) {
+            float x[32];
+            tmem_ld32(tb + c * 32, x);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) sum[c * 32 + j] += x[j];
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(tempty_leader + acc * 8);
+        }
+        if (!got) break;
+        const int row = mt * PAIR_BM + static_cast<int>(prank) * 128 + r;
+        const int col0 = nt * TN + half * C::EPI_COLS;
+#pragma unroll
+        for (int c = 0; c < C::EPI_COLS / 16; ++c) {
+          const int col = col0 + c * 16, left = ea.cols - col;
+          if (row >= ea.rows || left <= 0 ||
+              !FLCE_CHECK(row_run_ok(col, left < 16 ? left : 16, ea.lin.ld), ea.err))
+            continue;
+          float v[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) v[j] = sum[c * 16 + j];
+          linear_store16(ea.lin, static_cast<int64_t>(row) * ea.lin.ld, col, left, v);
+        }
+        continue;
+      }
       const int acc = it % C::NACC;
       const uint32_t aph = (it / C::NACC) & 1;
       if (!mbar_wait(&tfull[acc], aph, abort_flag, ea.err)) break;
@@ -849,7 +937,7 @@ __global__ void __launch_bounds__(pair_threads<EPI>(), 1)
                              half * C::EPI_COLS;
       if (FLCE_CHECK(tmem_ok(acc * TN + half * C::EPI_COLS, C::EPI_CHUNKS * 32, q, warp),
                      ea.err))
-        Epilogue<EPI>::template run<C::EPI_CHUNKS>(
+        Epilogue<drained<EPI>() ? EPI_LINEAR : EPI>::template run<C::EPI_CHUNKS>(
             ea, tbase, mt * PAIR_BM + static_cast<int>(prank) * 128 + r,
             nt * TN + half * C::EPI_COLS);
       tc_fence_before();
@@ -969,6 +1057,8 @@ FLCE_DECLARE_LAUNCHER(launch_bwd_dhidden_vh);  // dlogits (K) x weight (MN)
 // a dense layer's forward
 FLCE_DECLARE_LAUNCHER(launch_linear);     // x (K) x weight [K,N] (MN)
 FLCE_DECLARE_LAUNCHER(launch_linear_vh);  // x (K) x weight [N,K] (K)
+FLCE_DECLARE_LAUNCHER(launch_linear_f32);
+FLCE_DECLARE_LAUNCHER(launch_linear_vh_f32);
 // tiles of 128 columns, for a layer with few: its forward, dx (as dhidden) and dweight
 FLCE_DECLARE_LAUNCHER(launch_linear_128);
 FLCE_DECLARE_LAUNCHER(launch_linear_vh_128);

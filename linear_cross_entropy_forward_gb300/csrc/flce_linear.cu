@@ -21,10 +21,6 @@
 #include <cuda_bf16.h>
 #include <math.h>
 #include <stdint.h>
-#ifdef FLCE_LINEAR_PLAN
-#include <stdio.h>
-#include <stdlib.h>
-#endif
 
 #include <atomic>
 
@@ -483,12 +479,12 @@ struct Plan {
   int tt, size, stages;
 };
 
-Plan choose(const Product& g, int sms) {
+Plan choose(const Product& g, int sms, bool f32 = false) {
   const double kb = static_cast<double>(cdiv(g.depth, BK));
   Plan best{};
   double least = 1e30;
   if (g.cols % 8 == 0) {
-    for (int width = 256; width >= 128; width /= 2) {
+    for (int width = 256; width >= (f32 ? 256 : 128); width /= 2) {
       const int64_t rounds = cdiv(cdiv(g.rows, 256) * cdiv(g.cols, width), sms / 2);
       const double us = rounds * kb * (width == 256 ? 0.33 : 0.27) + (width == 256 ? 8.0 : 7.0) +
                         (rounds > 1 ? 2.0 : 0.0);
@@ -526,11 +522,6 @@ Plan choose(const Product& g, int sms) {
       }
     }
   }
-#ifdef FLCE_LINEAR_PLAN
-  static const char* dbg = getenv("FLCE_LIN");
-  if (dbg && dbg[0] == 'p') best = Plan{atoi(dbg + 1), 0, 0, 0};
-  if (getenv("FLCE_V")) fprintf(stderr, "%ld x %ld x %ld: width %d tt %d size %d stages %d us %.1f\n", (long)g.rows, (long)g.depth, (long)g.cols, best.width, best.tt, best.size, best.stages, least);
-#endif
   return best;
 }
 
@@ -628,6 +619,8 @@ int run_pair(const Product& g, int width, int kind, const LinearOut& out, uint32
   const bool wide = width == 256;
   if (kind == 0) {
     ea.lin = out;
+    if (out.out_f32)
+      return rc_of((g.right_mn ? launch_linear_f32 : launch_linear_vh_f32)(A, B, sh, ea, st));
     return rc_of((g.right_mn ? (wide ? launch_linear : launch_linear_128)
                              : (wide ? launch_linear_vh : launch_linear_vh_128))(A, B, sh, ea, st));
   }
@@ -750,7 +743,7 @@ int flce_linear(const flce_linear_params* p, const void* x, const void* weight, 
   o.out_f32 = p->out_dtype == FLCE_F32;
   o.wide = p->N % 16 == 0 && ((addr(y) | addr(preact)) & 31) == 0;
   const Product g = forward_product(p, x, weight);
-  const Plan plan = choose(g, sms);
+  const Plan plan = choose(g, sms, o.out_f32);
   // The header is cleared ahead where the schedule's counters are needed (and in the bounds-checking
   // build, whose first findings a kernel could wipe out), else by the kernel: a memset is a
   // microsecond or two of a small layer's ten.
