@@ -19,7 +19,6 @@ struct LinearOut {
   int64_t ld;
   int32_t act;
   int32_t out_f32;
-  int32_t wide;  // rows and arrays are 32-byte aligned, 16 columns at a time
 };
 
 __device__ __forceinline__ float sigmoid_fast(float x) {
@@ -122,97 +121,64 @@ __device__ __forceinline__ void activate_all(float (&v)[N], int act) {
   }
 }
 
-// Sixteen bf16 values to 32 aligned bytes: one full sector of L2.  (16 bytes at a time are two half
-// sectors, and L2's traffic is what the tensor cores' operands need.)
-__device__ __forceinline__ void store_sector(__nv_bfloat16* p, const float (&v)[16]) {
-  uint32_t w[8];
+// One column of TOKENS rows, `left` of which are there, element `at` of the output on.  The residual's
+// bits are asked for ahead of the sums that they are added to, and all before any is looked at (a
+// conversion beside its load waits for it, and so does a load behind a store).
+template <int TOKENS>
+__device__ __forceinline__ void linear_residual(const LinearOut& o, int64_t at, int left,
+                                                uint32_t (&r)[TOKENS]) {
+  if (!o.residual) return;
+  if (o.out_f32) {
+    const uint32_t* p = static_cast<const uint32_t*>(o.residual) + at;
+    if (left >= TOKENS) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-  st_global_v8(p, w);
-}
-
-// Sixteen neighbouring sums of a row that starts at element `base`, of which the first `cols` are
-// the row's (16 or 8), all arrays 16-byte aligned there.
-__device__ __forceinline__ void linear_store16(const LinearOut& o, int64_t base, int col, int cols,
-                                               float (&v)[16]) {
-  const bool all = cols >= 16;
-  if (o.bias) {
-    const __nv_bfloat16* p = o.bias + col;
-    float b[8];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (h == 1 && !all) break;
-      if (reinterpret_cast<uintptr_t>(p) & 15) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) b[i] = __bfloat162float(p[8 * h + i]);
-      } else {
-        unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(p) + h), b);
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[8 * h + i] += b[i];
-    }
-  }
-  auto put = [&](__nv_bfloat16* p) {
-    if (all && o.wide) {
-      store_sector(p, v);
+      for (int i = 0; i < TOKENS; ++i) r[i] = p[i * o.ld];
     } else {
-      reinterpret_cast<uint4*>(p)[0] =
-          make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                     pack_bf16x2(v[6], v[7]));
-      if (all)
-        reinterpret_cast<uint4*>(p)[1] =
-            make_uint4(pack_bf16x2(v[8], v[9]), pack_bf16x2(v[10], v[11]),
-                       pack_bf16x2(v[12], v[13]), pack_bf16x2(v[14], v[15]));
-    }
-  };
-  if (o.preact) put(o.preact + base + col);
-  activate_all(v, o.act);
-  if (o.out_f32) {
-    float* y = static_cast<float*>(o.y) + base + col;
-    const float* r = static_cast<const float*>(o.residual) + base + col;
 #pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      if (h >= 2 && !all) break;
-      float4 u = make_float4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
-      if (o.residual) {
-        const float4 t = reinterpret_cast<const float4*>(r)[h];
-        u.x += t.x; u.y += t.y; u.z += t.z; u.w += t.w;
-      }
-      v[4 * h] = u.x; v[4 * h + 1] = u.y; v[4 * h + 2] = u.z; v[4 * h + 3] = u.w;
-      if (!(all && o.wide)) reinterpret_cast<float4*>(y)[h] = u;
-    }
-    if (all && o.wide) {
-      st_global_v8f(y, v);
-      st_global_v8f(y + 8, v + 8);
+      for (int i = 0; i < TOKENS; ++i)
+        if (i < left) r[i] = p[i * o.ld];
     }
   } else {
-    if (o.residual) {
-      const uint4* r = reinterpret_cast<const uint4*>(
-          static_cast<const __nv_bfloat16*>(o.residual) + base + col);
-      float t[8];
+    const uint16_t* p = static_cast<const uint16_t*>(o.residual) + at;
+    if (left >= TOKENS) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (h == 1 && !all) break;
-        unpack_bf16x8(r[h], t);
+      for (int i = 0; i < TOKENS; ++i) r[i] = p[i * o.ld];
+    } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[8 * h + i] += t[i];
-      }
+      for (int i = 0; i < TOKENS; ++i)
+        if (i < left) r[i] = p[i * o.ld];
     }
-    put(static_cast<__nv_bfloat16*>(o.y) + base + col);
   }
 }
-
-// One sum, element `at` of the output.
-__device__ __forceinline__ void linear_store1(const LinearOut& o, int64_t at, float bias, float v) {
-  v += bias;
-  if (o.preact) o.preact[at] = __float2bfloat16_rn(v);
-  v = activate(v, o.act);
+template <int TOKENS>
+__device__ __forceinline__ void linear_store_column(const LinearOut& o, int64_t at, int left,
+                                                    float bias, const uint32_t (&r)[TOKENS],
+                                                    float (&v)[TOKENS]) {
+  if (left <= 0) return;
+#pragma unroll
+  for (int i = 0; i < TOKENS; ++i) v[i] += bias;
+  if (o.preact) {
+    __nv_bfloat16* p = o.preact + at;
+#pragma unroll
+    for (int i = 0; i < TOKENS; ++i)
+      if (i < left) p[i * o.ld] = __float2bfloat16_rn(v[i]);
+  }
+  activate_all(v, o.act);
+  if (o.residual) {
+    const int bits = o.out_f32 ? 0 : 16;
+#pragma unroll
+    for (int i = 0; i < TOKENS; ++i) v[i] += __uint_as_float(r[i] << bits);
+  }
   if (o.out_f32) {
-    if (o.residual) v += static_cast<const float*>(o.residual)[at];
-    static_cast<float*>(o.y)[at] = v;
+    float* p = static_cast<float*>(o.y) + at;
+#pragma unroll
+    for (int i = 0; i < TOKENS; ++i)
+      if (i < left) p[i * o.ld] = v[i];
   } else {
-    if (o.residual) v += __bfloat162float(static_cast<const __nv_bfloat16*>(o.residual)[at]);
-    static_cast<__nv_bfloat16*>(o.y)[at] = __float2bfloat16_rn(v);
+    __nv_bfloat16* p = static_cast<__nv_bfloat16*>(o.y) + at;
+#pragma unroll
+    for (int i = 0; i < TOKENS; ++i)
+      if (i < left) p[i * o.ld] = __float2bfloat16_rn(v[i]);
   }
 }
 

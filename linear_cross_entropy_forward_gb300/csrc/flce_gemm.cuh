@@ -72,7 +72,7 @@ enum EpiKind { EPI_FWD_STATS = 0, EPI_DLOGITS = 1, EPI_STORE_BF16 = 2, EPI_ACCUM
 #endif
 template <int EPI>
 __host__ __device__ constexpr int epi_warps() {
-  return FLCE_EPI_WARPS ? FLCE_EPI_WARPS : (EPI == EPI_DLOGITS || EPI == EPI_LINEAR || EPI == EPI_LINEAR_F32 ? 8 : 4);
+  return FLCE_EPI_WARPS ? FLCE_EPI_WARPS : (EPI == EPI_DLOGITS || EPI >= EPI_LINEAR ? 8 : 4);
 }
 template <int EPI>
 __host__ __device__ constexpr int pair_threads() {
@@ -584,30 +584,61 @@ struct Epilogue<EPI_ACCUM> {
   }
 };
 
-// A dense layer's output: 16 columns at a time (N is a multiple of 8 here), the residual read and
-// the output written in the accumulator's layout.
+// A dense layer's output, the product transposed, y^T = W^T x^T: a lane has a column of y, a register a
+// token, so that a warp's stores run along y's rows, whose length need not be a multiple of anything.
+// (A lane with a row of y and 16 of its columns at a time, whose 32 loads and stores are 32 sectors:
+// 6000 x 256 x 8192 71 us, with a residual 110; so 54 and 94.)
 template <>
 struct Epilogue<EPI_LINEAR> {
+  static __device__ __forceinline__ float bias(const EpiArgs& ea, int n) {
+    return ea.lin.bias && n < ea.rows ? __bfloat162float(ea.lin.bias[n]) : 0.0f;
+  }
+  // Column n's 16-token pieces from `token` on.  AHEAD: the residual of the first is asked for at the
+  // start and the next one's before a piece's output, for 16 registers.
+  template <bool AHEAD>
+  struct Column {
+    const EpiArgs& ea;
+    const int n;
+    int token;
+    const float b;
+    uint32_t next[AHEAD ? 16 : 1];
+    __device__ __forceinline__ Column(const EpiArgs& args, int row, int col0)
+        : ea(args), n(row), token(col0), b(bias(args, row)) {
+      if constexpr (AHEAD) linear_residual(ea.lin, at(), left(), next);
+    }
+    __device__ __forceinline__ int left() const { return n < ea.rows ? ea.cols - token : 0; }
+    __device__ __forceinline__ int64_t at() const {
+      return static_cast<int64_t>(token) * ea.lin.ld + n;
+    }
+    __device__ __forceinline__ void put(float (&v)[16], bool more) {
+      uint32_t res[16];
+      const int64_t to = at();
+      const int rows = left();
+      if constexpr (AHEAD) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) res[i] = next[i];
+      } else {
+        linear_residual(ea.lin, to, rows, res);
+      }
+      token += 16;
+      if constexpr (AHEAD)
+        if (more) linear_residual(ea.lin, at(), left(), next);
+      linear_store_column(ea.lin, to, rows, b, res, v);
+    }
+  };
   template <int CH>
-  static __device__ __forceinline__ void run(const EpiArgs& ea, uint32_t tbase, int row,
-                                             int col0) {
-    const bool row_ok = row < ea.rows;
-    const LinearOut& o = ea.lin;
-    const int64_t base = static_cast<int64_t>(row) * o.ld;
+  static __device__ __forceinline__ void run(uint32_t tbase, Column<true>& column) {
 #pragma unroll 1
     for (int c = 0; c < CH; ++c) {
       float x[32];
       __syncwarp();
       tmem_ld32(tbase + c * 32, x);
-      if (!row_ok) continue;
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        const int col = col0 + c * 32 + q * 16, left = ea.cols - col;
-        if (left <= 0 || !FLCE_CHECK(row_run_ok(col, left < 16 ? left : 16, o.ld), ea.err)) continue;
         float v[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) v[i] = x[q * 16 + i];
-        linear_store16(o, base, col, left, v);
+        column.put(v, q == 0 || c + 1 < CH);
       }
     }
   }
@@ -615,9 +646,11 @@ struct Epilogue<EPI_LINEAR> {
 
 // The tensor cores cut off what an addition to an accumulator loses: after a depth of 4096 fp32
 // outputs are 4.4e-6 off, where rounding would leave 6e-7.  For these an accumulator takes
-// kDrainBlocks 64-deep blocks, and the epilogue warps add its sums to their own in registers
-// (128 per thread) while the next one fills: 5e-7.
-constexpr int kDrainBlocks = 8;
+// kDrainBlocks 64-deep blocks, and the epilogue warps add its sums to their own in registers (128 per
+// thread) while the next one fills: 7e-7, for 190 us instead of bf16's 148 at 8192 x 4096 x 4096.
+// (8 blocks: 4.7e-7 and 199 us; 16: 1.0e-6 and 175.)
+constexpr int kDrainBlocks = 12;
+constexpr int kWholeBlocks = 16;  // what one accumulator may take if it is the only one: 1.0e-6
 template <int EPI>
 __host__ __device__ constexpr bool drained() {
   return EPI == EPI_LINEAR_F32;
@@ -688,7 +721,7 @@ __global__ void __launch_bounds__(pair_threads<EPI>(), 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
   // (a wait that runs out does so seconds later)
-  if ((EPI == EPI_LINEAR || EPI == EPI_LINEAR_F32) && ea.clear && blockIdx.x == 0 && threadIdx.x == 0) *ea.err = 0;
+  if (EPI >= EPI_LINEAR && ea.clear && blockIdx.x == 0 && threadIdx.x == 0) *ea.err = 0;
   const int total = sh.m_tiles * sh.n_tiles;
   constexpr uint32_t kSched = 1;  // the CTA whose warp 1 schedules the pair's tiles
   const uint32_t rempty_sched = mapa_shared(smem_u32(&rempty[0]), kSched);
@@ -887,7 +920,10 @@ __global__ void __launch_bounds__(pair_threads<EPI>(), 1)
       if (t >= total) break;
       int mt, nt;
       tile_coords(t, sh, mt, nt);
+      const int row = mt * PAIR_BM + static_cast<int>(prank) * 128 + r;
+      const int col0 = nt * TN + half * C::EPI_COLS;
       if constexpr (drained<EPI>()) {
+        Epilogue<EPI_LINEAR>::Column<false> column(ea, row, col0);
         float sum[C::EPI_COLS];
 #pragma unroll
         for (int j = 0; j < C::EPI_COLS; ++j) sum[j] = 0.0f;
@@ -914,32 +950,30 @@ __global__ void __launch_bounds__(pair_threads<EPI>(), 1)
           if (lane == 0) mbar_arrive_cluster(tempty_leader + acc * 8);
         }
         if (!got) break;
-        const int row = mt * PAIR_BM + static_cast<int>(prank) * 128 + r;
-        const int col0 = nt * TN + half * C::EPI_COLS;
 #pragma unroll
         for (int c = 0; c < C::EPI_COLS / 16; ++c) {
-          const int col = col0 + c * 16, left = ea.cols - col;
-          if (row >= ea.rows || left <= 0 ||
-              !FLCE_CHECK(row_run_ok(col, left < 16 ? left : 16, ea.lin.ld), ea.err))
-            continue;
           float v[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) v[j] = sum[c * 16 + j];
-          linear_store16(ea.lin, static_cast<int64_t>(row) * ea.lin.ld, col, left, v);
+          column.put(v, c + 1 < C::EPI_COLS / 16);
         }
         continue;
       }
       const int acc = it % C::NACC;
       const uint32_t aph = (it / C::NACC) & 1;
-      if (!mbar_wait(&tfull[acc], aph, abort_flag, ea.err)) break;
-      tc_fence_after();
       const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * TN +
                              half * C::EPI_COLS;
-      if (FLCE_CHECK(tmem_ok(acc * TN + half * C::EPI_COLS, C::EPI_CHUNKS * 32, q, warp),
-                     ea.err))
-        Epilogue<drained<EPI>() ? EPI_LINEAR : EPI>::template run<C::EPI_CHUNKS>(
-            ea, tbase, mt * PAIR_BM + static_cast<int>(prank) * 128 + r,
-            nt * TN + half * C::EPI_COLS);
+      if constexpr (EPI == EPI_LINEAR) {
+        Epilogue<EPI_LINEAR>::Column<true> column(ea, row, col0);
+        if (!mbar_wait(&tfull[acc], aph, abort_flag, ea.err)) break;
+        tc_fence_after();
+        Epilogue<EPI_LINEAR>::run<C::EPI_CHUNKS>(tbase, column);
+      } else if constexpr (!drained<EPI>()) {
+        if (!mbar_wait(&tfull[acc], aph, abort_flag, ea.err)) break;
+        tc_fence_after();
+        if (FLCE_CHECK(tmem_ok(acc * TN + half * C::EPI_COLS, C::EPI_CHUNKS * 32, q, warp), ea.err))
+          Epilogue<EPI>::template run<C::EPI_CHUNKS>(ea, tbase, row, col0);
+      }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(tempty_leader + acc * 8);
@@ -1055,11 +1089,12 @@ FLCE_DECLARE_LAUNCHER(launch_fwd_stats_vh);    // hidden (K) x weight (K)
 FLCE_DECLARE_LAUNCHER(launch_bwd_dlogits_vh);  // hidden (K) x weight (K)
 FLCE_DECLARE_LAUNCHER(launch_bwd_dhidden_vh);  // dlogits (K) x weight (MN)
 // a dense layer's forward
-FLCE_DECLARE_LAUNCHER(launch_linear);     // x (K) x weight [K,N] (MN)
-FLCE_DECLARE_LAUNCHER(launch_linear_vh);  // x (K) x weight [N,K] (K)
+// a dense layer's output, transposed
+FLCE_DECLARE_LAUNCHER(launch_linear);     // weight [K,N] (MN) x x (K)
+FLCE_DECLARE_LAUNCHER(launch_linear_vh);  // weight [N,K] (K) x x (K)
 FLCE_DECLARE_LAUNCHER(launch_linear_f32);
 FLCE_DECLARE_LAUNCHER(launch_linear_vh_f32);
-// tiles of 128 columns, for a layer with few: its forward, dx (as dhidden) and dweight
+// tiles of 128 columns, for a layer with few
 FLCE_DECLARE_LAUNCHER(launch_linear_128);
 FLCE_DECLARE_LAUNCHER(launch_linear_vh_128);
 FLCE_DECLARE_LAUNCHER(launch_linear_dx_128);

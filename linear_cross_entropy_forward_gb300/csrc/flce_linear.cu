@@ -3,16 +3,20 @@
 // Two GEMM kernels, both tcgen05 with operands brought by TMA:
 //
 //   pair     flce_gemm.cuh's CTA pairs on 256 x 256 tiles, for shapes with enough tiles to fill
-//            the GPU in whole rounds: bound by the tensor cores.
-//   split    (here) for all others, above all few tokens, which are bound by the bytes of the
-//            weight.  The product is taken transposed, y^T = W^T x^T: 128 columns of y are the
-//            128 TMEM lanes and up to 256 tokens its columns, so that a tile has no rows for
-//            tokens that are not there, and a warp's stores run along y's rows whatever N is.
-//            Where there are fewer tiles than SMs, the blocks of a cluster share a tile's depth and
-//            add up their sums over distributed shared memory: one launch, no workspace.
-//            (Cutting the line of all tiles' 64-deep blocks into equal pieces per SM, with partial
-//            sums in the workspace and a second launch to join them: one token through 4096 x 4096
-//            11.8 us, against 8.8; 200 tokens 34.7 against 16.5.)
+//            the GPU in whole rounds: bound by the tensor cores (8192 x 4096 x 16384: 565 us, 1.95
+//            PFLOP/s with its operands in L2).
+//   split    (here) for few tokens, which are bound by the bytes of the weight (24 x 4096 x 128256:
+//            161 us, 6.6 TB/s), and for shallow products, bound by their outputs.  Tiles are 128
+//            columns of y by up to 256 tokens, so that a tile has no rows for tokens that are not
+//            there, and two blocks of an SM take turns at the tensor cores and the stores.
+//
+// Both take the product transposed, y^T = W^T x^T: y's columns are the TMEM lanes, and a warp's stores
+// run along y's rows whatever N is (rows of a lane each: 8192 x 4096 x 4097 679 us, so 173).
+//
+// Where there are fewer split tiles than SMs, the blocks of a cluster share a tile's depth and add up
+// their sums over distributed shared memory: one launch, no workspace.  (Cutting the line of all tiles'
+// 64-deep blocks into equal pieces per SM, with partial sums in the workspace and a second launch to
+// join them: one token through 4096 x 4096 11.8 us, against 8.8; 200 tokens 34.7 against 15.9.)
 //
 // Results repeat bit for bit: either adds in a fixed order.
 //
@@ -23,6 +27,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "flce_act.cuh"
 #include "flce_gemm.cuh"
@@ -109,8 +114,8 @@ __device__ __forceinline__ void load_rows(uint8_t* dst, const CUtensorMap* map, 
 // finishes a part of the tile's tokens, in the blocks' order.
 //
 // The tensor cores cut off what an addition to an accumulator loses, so that its error grows with the
-// additions: 4.4e-6 of fp32 logits after a depth of 4096.  A block's depth goes to as many accumulators
-// one after the other as TMEM holds beside another block (eight at most: 4.8e-7), whose sums are then
+// additions: 4.4e-6 of fp32 logits after a depth of 4096.  A block's depth goes to several accumulators
+// one after the other (eight, where TMEM holds them beside another block: 4.8e-7), whose sums are then
 // added with rounding.  A bf16 output, whose rounding is 2^-8, takes one.
 struct SplitArgs {
   int32_t M, N;
@@ -255,6 +260,9 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
 #pragma unroll 1
     for (int c = half * 16; c < rows; c += 32) {
       float x[16] = {};
+      uint32_t res[16];
+      const int64_t at = int64_t(m0 + c) * a.out.ld + n;
+      if (size == 1) linear_residual(a.out, at, n_ok ? rows - c : 0, res);
       __syncwarp();
       // the accumulators' columns, two on their way
       uint32_t u[16], v[16];
@@ -274,9 +282,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
 #pragma unroll
         for (int i = 0; i < 16; ++i) part[(c + i) * kRows + nl] = x[i];
       } else if (n_ok) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (c + i < rows) linear_store1(a.out, int64_t(m0 + c + i) * a.out.ld + n, bias, x[i]);
+        linear_store_column(a.out, at, rows - c, bias, res, x);
       }
     }
   }
@@ -290,15 +296,16 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
       constexpr int kDeep = 4;  // tokens whose sums are on their way
       for (int m = r0 + half * kDeep; m < r1; m += 2 * kDeep) {
         float sum[kDeep] = {};
+        uint32_t res[kDeep];
+        const int64_t at = int64_t(m0 + m) * a.out.ld + n;
+        linear_residual(a.out, at, r1 - m, res);
         for (uint32_t j = 0; j < size; ++j) {
           const uint32_t from = mapa_shared(own, j);
 #pragma unroll
           for (int i = 0; i < kDeep; ++i)
             if (m + i < r1) sum[i] += ld_cluster(from + (m + i) * kRows * 4);
         }
-#pragma unroll
-        for (int i = 0; i < kDeep; ++i)
-          if (m + i < r1) linear_store1(a.out, int64_t(m0 + m + i) * a.out.ld + n, bias, sum[i]);
+        linear_store_column(a.out, at, r1 - m, bias, res, sum);
       }
     }
     __syncwarp();
@@ -322,92 +329,153 @@ struct DzArgs {
   int32_t act, dout_f32;
 };
 
-// A thread takes VEC columns and a strip of rows, a block neighbouring columns: whole kilobytes of a
-// row at a time, four rows on their way, and the columns' sums stay in the thread.
-template <int VEC>
+// Eight neighbouring elements, from element `at` on, of an array of 16-byte aligned beginning and
+// `total` elements.  ALIGNED: at is a multiple of 8.  Else the aligned 16-byte pieces that they lie in
+// are read (neighbouring threads' pieces are the same lines of L1) and shifted; elements behind the
+// array's end are not touched.
+template <bool ALIGNED>
+struct Eight16 {
+  uint4 q[ALIGNED ? 1 : 2];
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, int64_t at, int64_t total) {
+    if constexpr (ALIGNED) {
+      q[0] = __ldcs(reinterpret_cast<const uint4*>(p + at));
+    } else {
+      const int64_t piece = at >> 3;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        q[i] = make_uint4(0, 0, 0, 0);
+        const int64_t first = (piece + i) * 8;
+        if (first + 8 <= total) {
+          q[i] = __ldg(reinterpret_cast<const uint4*>(p) + piece + i);
+        } else if (first < total) {
+          uint32_t w[4];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const uint32_t x = first + j < total
+                                   ? reinterpret_cast<const uint16_t*>(p)[first + j] : 0u;
+            w[j / 2] = j & 1 ? w[j / 2] | x << 16 : x;
+          }
+          q[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void get(int64_t at, float (&x)[8]) const {
+    if constexpr (ALIGNED) {
+      unpack_bf16x8(q[0], x);
+    } else {
+      const uint32_t w[8] = {q[0].x, q[0].y, q[0].z, q[0].w, q[1].x, q[1].y, q[1].z, q[1].w};
+      uint32_t u[6], v[5], o[4];
+#pragma unroll
+      for (int i = 0; i < 6; ++i) u[i] = at & 4 ? w[i + 2] : w[i];
+#pragma unroll
+      for (int i = 0; i < 5; ++i) v[i] = at & 2 ? u[i + 1] : u[i];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = __funnelshift_r(v[i], v[i + 1], (at & 1) * 16);
+      unpack_bf16x8(make_uint4(o[0], o[1], o[2], o[3]), x);
+    }
+  }
+};
+template <bool ALIGNED>
+struct Eight32 {
+  uint4 q[ALIGNED ? 2 : 3];
+  __device__ __forceinline__ void load(const float* p, int64_t at, int64_t total) {
+    const int64_t piece = at >> 2;
+#pragma unroll
+    for (int i = 0; i < (ALIGNED ? 2 : 3); ++i) {
+      const int64_t first = (piece + i) * 4;
+      if (ALIGNED) {
+        q[i] = __ldcs(reinterpret_cast<const uint4*>(p) + piece + i);
+      } else if (first + 4 <= total) {
+        q[i] = __ldg(reinterpret_cast<const uint4*>(p) + piece + i);
+      } else {
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(p);
+        q[i].x = first < total ? w[first] : 0u;
+        q[i].y = first + 1 < total ? w[first + 1] : 0u;
+        q[i].z = first + 2 < total ? w[first + 2] : 0u;
+        q[i].w = 0;
+      }
+    }
+  }
+  __device__ __forceinline__ void get(int64_t at, float (&x)[8]) const {
+    if constexpr (ALIGNED) {
+      const uint32_t w[8] = {q[0].x, q[0].y, q[0].z, q[0].w, q[1].x, q[1].y, q[1].z, q[1].w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
+    } else {
+      const uint32_t w[12] = {q[0].x, q[0].y, q[0].z, q[0].w, q[1].x, q[1].y, q[1].z, q[1].w,
+                              q[2].x, q[2].y, q[2].z, q[2].w};
+      uint32_t u[9];
+#pragma unroll
+      for (int i = 0; i < 9; ++i) u[i] = at & 2 ? w[i + 2] : w[i];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(at & 1 ? u[i + 1] : u[i]);
+    }
+  }
+};
+
+// A thread takes eight columns and a strip of rows, a block neighbouring columns: whole kilobytes of a
+// row at a time, four rows on their way (two where they are not aligned), and the columns' sums stay
+// in the thread.
+template <bool ALIGNED, bool F32>
 __global__ void __launch_bounds__(kDzThreads) dz_kernel(const __grid_constant__ DzArgs a) {
-  const int64_t n = (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) * VEC;
+  const int64_t n = (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) * 8;
   const int64_t m0 = blockIdx.y * a.strip;
   const int64_t m1 = m0 + a.strip < a.M ? m0 + a.strip : a.M;
   if (n >= a.N) return;
-  constexpr int kDeep = VEC == 8 ? 4 : 8;
-  float sum[VEC];
+  constexpr int kDeep = ALIGNED ? 4 : 2;
+  const int64_t total = a.M * a.N;
+  const int left = a.N - n < 8 ? static_cast<int>(a.N - n) : 8;
+  float sum[8];
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) sum[i] = 0.0f;
+  for (int i = 0; i < 8; ++i) sum[i] = 0.0f;
   const bool act = a.act != FLCE_ACT_NONE;
   for (int64_t m = m0; m < m1; m += kDeep) {
-    uint4 graw[kDeep], zraw[kDeep];
-    float4 gwide[kDeep];
-    float g1[kDeep], z1[kDeep];
+    std::conditional_t<F32, Eight32<ALIGNED>, Eight16<ALIGNED>> graw[kDeep];
+    Eight16<ALIGNED> zraw[kDeep];
 #pragma unroll
     for (int d = 0; d < kDeep; ++d) {
       if (m + d >= m1) continue;
       const int64_t at = (m + d) * a.N + n;
-      if constexpr (VEC == 8) {
-        if (a.dout_f32) {
-          const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.dout) + at);
-          gwide[d] = __ldcs(p);
-          const float4 v = __ldcs(p + 1);
-          graw[d] = make_uint4(__float_as_uint(v.x), __float_as_uint(v.y), __float_as_uint(v.z),
-                               __float_as_uint(v.w));
-        } else {
-          graw[d] = __ldcs(reinterpret_cast<const uint4*>(
-              static_cast<const __nv_bfloat16*>(a.dout) + at));
-        }
-        if (act) zraw[d] = __ldcs(reinterpret_cast<const uint4*>(a.preact + at));
-      } else {
-        g1[d] = a.dout_f32 ? static_cast<const float*>(a.dout)[at]
-                           : __bfloat162float(static_cast<const __nv_bfloat16*>(a.dout)[at]);
-        if (act) z1[d] = __bfloat162float(a.preact[at]);
-      }
+      if constexpr (F32) graw[d].load(static_cast<const float*>(a.dout), at, total);
+      else graw[d].load(static_cast<const __nv_bfloat16*>(a.dout), at, total);
+      if (act) zraw[d].load(a.preact, at, total);
     }
 #pragma unroll
     for (int d = 0; d < kDeep; ++d) {
       if (m + d >= m1) continue;
-      float g[VEC], z[VEC];
-      if constexpr (VEC == 8) {
-        if (a.dout_f32) {
-          g[0] = gwide[d].x; g[1] = gwide[d].y; g[2] = gwide[d].z; g[3] = gwide[d].w;
-          g[4] = __uint_as_float(graw[d].x); g[5] = __uint_as_float(graw[d].y);
-          g[6] = __uint_as_float(graw[d].z); g[7] = __uint_as_float(graw[d].w);
-        } else {
-          unpack_bf16x8(graw[d], g);
-        }
-        if (act) unpack_bf16x8(zraw[d], z);
-      } else {
-        g[0] = g1[d];
-        if (act) z[0] = z1[d];
-      }
+      const int64_t at = (m + d) * a.N + n;
+      float g[8], z[8];
+      graw[d].get(at, g);
+      if (act) zraw[d].get(at, z);
       switch (a.act) {
         case FLCE_ACT_NONE: break;
         case FLCE_ACT_RELU:
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) g[i] *= activate_slope(z[i], FLCE_ACT_RELU);
+          for (int i = 0; i < 8; ++i) g[i] *= activate_slope(z[i], FLCE_ACT_RELU);
           break;
         case FLCE_ACT_GELU:
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) g[i] *= activate_slope(z[i], FLCE_ACT_GELU);
+          for (int i = 0; i < 8; ++i) g[i] *= activate_slope(z[i], FLCE_ACT_GELU);
           break;
         case FLCE_ACT_GELU_TANH:
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) g[i] *= activate_slope(z[i], FLCE_ACT_GELU_TANH);
+          for (int i = 0; i < 8; ++i) g[i] *= activate_slope(z[i], FLCE_ACT_GELU_TANH);
           break;
         default:
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) g[i] *= activate_slope(z[i], FLCE_ACT_SILU);
+          for (int i = 0; i < 8; ++i) g[i] *= activate_slope(z[i], FLCE_ACT_SILU);
       }
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) sum[i] += g[i];
-      if (a.dz) {
-        __nv_bfloat16* o = a.dz + (m + d) * a.ld_dz + n;
-        if constexpr (VEC == 8) *reinterpret_cast<uint4*>(o) = pack_bf16x8(g);
-        else *o = __float2bfloat16_rn(g[0]);
-      }
+      for (int i = 0; i < 8; ++i) sum[i] += g[i];
+      // (rows of dz are padded to eight columns; nothing reads the padding)
+      if (a.dz) *reinterpret_cast<uint4*>(a.dz + (m + d) * a.ld_dz + n) = pack_bf16x8(g);
     }
   }
   if (!a.part) return;
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) a.part[blockIdx.y * a.N + n + i] = sum[i];
+  for (int i = 0; i < 8; ++i)
+    if (i < left) a.part[blockIdx.y * a.N + n + i] = sum[i];
 }
 
 // db: the strips' sums, eight groups of strips side by side, then those
@@ -466,35 +534,59 @@ struct Product {
   bool left_mn, right_mn;
 };
 
-// How a product is done: by CTA pairs on tiles of 256 x `width`, or split, with tiles of tt rows and
-// `size` blocks along the depth; whichever should take the fewest microseconds.  What the estimates
-// are made of was measured: a 64-deep block of a pair's 256 x 256 tile takes 0.33 us (the tensor
-// cores' rate), of 256 x 128 0.27 (an SM takes about 100 KB from L2 in a microsecond, which bounds it
-// and the split tiles); 3 to 5 us pass from the launch to the first product, and the last tile's epilogue
-// and the join of a cluster are in nobody's shadow.  512 x 4096 x 4096: 256 x 256 pairs 28.7 us, 128 x
-// 128 split 28.2; 200 x 4096 x 4096: 28.8 and (64 rows, depth in two) 16.5; 24 x 4096 x 128256: split
-// 162, depth in two 174.
+// Tiles of CTA pairs; a layer's output is made transposed.
+int64_t pair_tiles(const Product& g, bool layer, int width) {
+  return layer ? cdiv(g.cols, PAIR_BM) * cdiv(g.rows, width)
+               : cdiv(g.rows, PAIR_BM) * cdiv(g.cols, width);
+}
+
+// fp32 outputs of a depth that one accumulator should not add up.
+bool drained(const Product& g, const LinearOut& o) {
+  return o.out_f32 && cdiv(g.depth, BK) > kWholeBlocks;
+}
+
+// Accumulators of a split block with fp32 output for a share of the depth: eight, or as many more as
+// it takes, and TMEM holds beside another block, but none without a 64-deep block.
+int parts_of(int tt, int share) {
+  int parts = static_cast<int>(cdiv(share, kWholeBlocks));
+  if (parts < 8) parts = 8;
+  if (parts > 256 / tt) parts = 256 / tt;
+  return parts < share ? parts : share;
+}
+
+// How a product is done: by CTA pairs on tiles of 256 x `width`, or split, with tiles of tt rows,
+// `size` blocks along the depth and one or two blocks per SM; whichever should take the fewest
+// microseconds.  What the estimates are made of was measured: a 64-deep block of a pair's 256 x 256
+// tile takes 0.33 us (the tensor cores' rate), of 256 x 128 0.27 (an SM takes about 100 KB from L2 in a
+// microsecond, which bounds it and the split tiles); 3 to 5 us pass from the launch to the first
+// product.  An SM's share of the output, 128 columns of 256 tokens, takes 4.5 us for its stores, and
+// more with an activation, preact and a residual; pairs do it beside the next tile's products, and so do
+// two split blocks of one SM, if less well.  The blocks of a cluster share it.
 struct Plan {
   int width;  // of a pair's tiles; 0: split
   int tt, size, stages;
 };
 
-Plan choose(const Product& g, int sms, bool f32 = false) {
+Plan choose(const Product& g, int sms, bool layer, const LinearOut& o) {
   const double kb = static_cast<double>(cdiv(g.depth, BK));
+  const double output = 4.5 + (o.act != FLCE_ACT_NONE ? 1.7 : 0.0) + (o.preact ? 2.5 : 0.0) +
+                        (o.residual ? 3.5 : 0.0) + (o.out_f32 ? 1.0 : 0.0);
+  const double traffic = (static_cast<double>(g.rows) + g.cols) * g.depth * 2 / 6.2e6 + 4.0;
   Plan best{};
   double least = 1e30;
-  if (g.cols % 8 == 0) {
-    for (int width = 256; width >= (f32 ? 256 : 128); width /= 2) {
-      const int64_t rounds = cdiv(cdiv(g.rows, 256) * cdiv(g.cols, width), sms / 2);
-      const double us = rounds * kb * (width == 256 ? 0.33 : 0.27) + (width == 256 ? 8.0 : 7.0) +
-                        (rounds > 1 ? 2.0 : 0.0);
-      const double dram = (static_cast<double>(g.rows) + g.cols) * g.depth * 2 / 5.8e6 + 6.0;
-      const double t = us > dram ? us : dram;
-      if (t < least) {
-        least = t;
-        best = Plan{width, 0, 0, 0};
-      }
+  auto consider = [&](double us, const Plan& p) {
+    if (us < least) {
+      least = us;
+      best = p;
     }
+  };
+  const bool drain = drained(g, o);
+  for (int width = 256; width >= (drain ? 256 : 128); width /= 2) {
+    const int64_t rounds = cdiv(pair_tiles(g, layer, width), sms / 2);
+    const double feed = kb * (width == 256 ? 0.33 : 0.27), finish = output * width / 256;
+    const double us = rounds * (feed > finish ? feed : finish) + (feed > finish ? finish : feed) +
+                      (drain ? rounds * finish / 2 : 0.0) + 5.0 + (rounds > 1 ? 2.0 : 0.0);
+    consider(us > traffic + 3.0 ? us : traffic + 3.0, Plan{width, 0, 0, 0});
   }
   const int unit = g.left_mn ? 64 : 16;
   const int64_t fewest = cdiv(g.rows, kMaxTokens);
@@ -503,22 +595,23 @@ Plan choose(const Product& g, int sms, bool f32 = false) {
     if (tt > kMaxTokens) continue;
     const int64_t tiles = cdiv(g.cols, kRows) * cdiv(g.rows, tt);
     for (int size = 1; size <= 8 && size <= kb; size *= 2) {
-      const int64_t blocks = tiles * size;
-      const int stage = (kRows + tt) * BK * 2;
-      // two blocks per SM where there are blocks for it and half the memory holds a deep enough ring
-      const bool two = blocks > sms && tt <= 64;
-      int stages = ((two ? SMEM_LIMIT / 2 - 1024 : SMEM_LIMIT) - 1024 - 512) / stage;
-      if (stages > 12) stages = 12;
-      if (size > 1 && stages * stage < tt * kRows * 4) continue;  // a tile's sums do not fit
-      const double mma = 0.34 * tt / 256, bytes = stage / 100e3;
-      const double rounds = !two ? static_cast<double>(cdiv(blocks, sms)) : static_cast<double>(blocks) / sms;
-      const double us = rounds * (kb / size * (mma > bytes ? mma : bytes) + 1.0 + tt * 0.012) + 3.0 +
-                        (size > 1 ? 1.5 + tt * 0.01 : 0.0);
-      const double dram = (static_cast<double>(g.rows) + g.cols) * g.depth * 2 / 6.2e6 + 4.0;
-      const double t = us > dram ? us : dram;
-      if (t < least) {
-        least = t;
-        best = Plan{0, tt, size, stages};
+      for (int per_sm = 1; per_sm <= 2; ++per_sm) {
+        const int64_t blocks = tiles * size;
+        if (per_sm == 2 && blocks <= sms) continue;
+        const int stage = (kRows + tt) * BK * 2;
+        int stages = ((per_sm == 2 ? SMEM_LIMIT / 2 - 1024 : SMEM_LIMIT) - 1024 - 512) / stage;
+        if (stages > 12) stages = 12;
+        if (size > 1 && stages * stage < tt * kRows * 4) continue;  // a tile's sums do not fit
+        const int share = static_cast<int>(kb) / size;
+        if (o.out_f32 && share > kWholeBlocks * parts_of(tt, share)) continue;
+        const double mma = 0.34 * tt / 256, bytes = stage / 100e3;
+        const double feed = kb / size * (mma > bytes ? mma : bytes);
+        const double finish = 1.0 + output * tt / 256 / size + (size > 1 ? 1.5 + tt * 0.01 : 0.0);
+        const double rounds = static_cast<double>(cdiv(blocks, per_sm * sms));
+        const double us = rounds * (per_sm == 2 ? 2 * feed + 1.3 * finish : feed + finish) + 3.0;
+        // the memory rests while an SM's only block finishes
+        const double memory = traffic + (per_sm == 1 ? rounds * finish : 0.0);
+        consider(us > memory ? us : memory, Plan{0, tt, size, stages});
       }
     }
   }
@@ -551,10 +644,7 @@ int launch_split(const Product& g, const Plan& s, const LinearOut& out, uint32_t
   a.m_tiles = static_cast<int32_t>(cdiv(g.rows, s.tt));
   a.k_blocks = static_cast<int32_t>(cdiv(g.depth, BK));
   a.stages = s.stages;
-  // parts of a block's share of the depth, of one 64-deep block at least
-  const int share = a.k_blocks / s.size;
-  a.parts = !out.out_f32 ? 1 : 256 / s.tt < 8 ? 256 / s.tt : 8;
-  if (a.parts > share) a.parts = share;
+  a.parts = out.out_f32 ? parts_of(s.tt, a.k_blocks / s.size) : 1;
   a.out = out;
   a.err = err;
   a.clear = clear;
@@ -586,13 +676,16 @@ int run_split(const Product& g, const Plan& s, const LinearOut& out, uint32_t* e
 }
 
 // Whether every pair has one tile at most, so that the schedule's counters are not needed.
-bool one_round(const Product& g, int width) {
-  return cdiv(g.rows, PAIR_BM) * cdiv(g.cols, width) <= pair_capacity();
+bool one_round(const Product& g, bool layer, int width) {
+  return pair_tiles(g, layer, width) <= pair_capacity();
 }
 
 // The product by CTA pairs; kind 0: a layer's output, 1: dx, 2: dweight.
-int run_pair(const Product& g, int width, int kind, const LinearOut& out, uint32_t* err, int slot,
+int run_pair(const Product& p, int width, int kind, const LinearOut& out, uint32_t* err, int slot,
              bool clear, cudaStream_t st) {
+  const Product g = kind ? p
+                         : Product{p.right, p.left, p.cols, p.rows, p.depth, p.ld_right, p.ld_left,
+                                   p.right_mn, p.left_mn};
   CUtensorMap A, B;
   if (!(g.left_mn ? tensor_map(&A, g.left, g.rows, g.depth, g.ld_left, 64, BK)
                   : tensor_map(&A, g.left, g.depth, g.rows, g.ld_left, BK, 64)) ||
@@ -605,7 +698,7 @@ int run_pair(const Product& g, int width, int kind, const LinearOut& out, uint32
   sh.k_blocks = static_cast<int>(cdiv(g.depth, BK));
   sh.raster = 0;
   sh.sched = reinterpret_cast<unsigned int*>(reinterpret_cast<uint8_t*>(err) + kSched + 8 * slot);
-  sh.one_round = one_round(g, width);
+  sh.one_round = one_round(p, kind == 0, width);
   sh.a_inner = g.left_mn ? g.rows : g.depth;
   sh.a_outer = g.left_mn ? g.depth : g.rows;
   sh.b_inner = g.right_mn ? g.cols : g.depth;
@@ -619,10 +712,10 @@ int run_pair(const Product& g, int width, int kind, const LinearOut& out, uint32
   const bool wide = width == 256;
   if (kind == 0) {
     ea.lin = out;
-    if (out.out_f32)
-      return rc_of((g.right_mn ? launch_linear_f32 : launch_linear_vh_f32)(A, B, sh, ea, st));
-    return rc_of((g.right_mn ? (wide ? launch_linear : launch_linear_128)
-                             : (wide ? launch_linear_vh : launch_linear_vh_128))(A, B, sh, ea, st));
+    if (drained(g, out))
+      return rc_of((g.left_mn ? launch_linear_f32 : launch_linear_vh_f32)(A, B, sh, ea, st));
+    return rc_of((g.left_mn ? (wide ? launch_linear : launch_linear_128)
+                            : (wide ? launch_linear_vh : launch_linear_vh_128))(A, B, sh, ea, st));
   }
   if (kind == 1) {
     ea.acc_out = static_cast<__nv_bfloat16*>(out.y);
@@ -655,7 +748,7 @@ Product dw_product(const flce_linear_params* p, const void* dz, int64_t ld_dz, c
 // Rows per strip of the dz kernel: at most 256 strips, and as short as 16 rows where the columns
 // alone give few threads.
 int64_t dz_strip(const flce_linear_params* p) {
-  const int64_t threads = cdiv(p->N, p->N % 8 == 0 ? 8 : 1);
+  const int64_t threads = cdiv(p->N, 8);
   int64_t strip = cdiv(p->M * threads, int64_t(1) << 18);  // about 2^18 threads
   if (strip < 16) strip = 16;
   const int64_t least = cdiv(p->M, 256);
@@ -678,13 +771,14 @@ BwdLayout bwd_layout(const flce_linear_params* p) {
   return L;
 }
 
-template <int VEC>
 int launch_dz(const DzArgs& a, int64_t strips, cudaStream_t st) {
-  const int64_t lanes = cdiv(a.N, VEC);
+  const int64_t lanes = cdiv(a.N, 8);
   const int threads = lanes >= kDzThreads ? kDzThreads : static_cast<int>(cdiv(lanes, 32) * 32);
   const int64_t cols = cdiv(lanes, threads);
   if (cols > (int64_t(1) << 31) - 1) return FLCE_ERR_BAD_SHAPE;
-  dz_kernel<VEC><<<dim3(static_cast<unsigned>(cols), static_cast<unsigned>(strips)), threads, 0, st>>>(a);
+  auto kernel = a.N % 8 == 0 ? (a.dout_f32 ? dz_kernel<true, true> : dz_kernel<true, false>)
+                             : (a.dout_f32 ? dz_kernel<false, true> : dz_kernel<false, false>);
+  kernel<<<dim3(static_cast<unsigned>(cols), static_cast<unsigned>(strips)), threads, 0, st>>>(a);
   return rc_of(cudaGetLastError());
 }
 
@@ -694,7 +788,7 @@ int run_gradient(const Product& g, int kind, void* out, uint32_t* err, int slot,
   LinearOut o{};
   o.y = out;
   o.ld = g.cols;
-  const Plan plan = choose(g, sms);
+  const Plan plan = choose(g, sms, false, o);
   return plan.width ? run_pair(g, plan.width, kind, o, err, slot, false, st)
                     : run_split(g, plan, o, err, false, st);
 }
@@ -741,13 +835,12 @@ int flce_linear(const flce_linear_params* p, const void* x, const void* weight, 
   o.ld = p->N;
   o.act = p->activation;
   o.out_f32 = p->out_dtype == FLCE_F32;
-  o.wide = p->N % 16 == 0 && ((addr(y) | addr(preact)) & 31) == 0;
   const Product g = forward_product(p, x, weight);
-  const Plan plan = choose(g, sms, o.out_f32);
+  const Plan plan = choose(g, sms, true, o);
   // The header is cleared ahead where the schedule's counters are needed (and in the bounds-checking
   // build, whose first findings a kernel could wipe out), else by the kernel: a memset is a
   // microsecond or two of a small layer's ten.
-  const bool ahead = FLCE_DEBUG || (plan.width && !one_round(g, plan.width));
+  const bool ahead = FLCE_DEBUG || (plan.width && !one_round(g, true, plan.width));
   if (ahead && (rc = rc_of(cudaMemsetAsync(ws, 0, kHeader, st)))) return rc;
   rc = plan.width ? run_pair(g, plan.width, 0, o, err, 0, !ahead, st)
                   : run_split(g, plan, o, err, !ahead, st);
@@ -796,7 +889,7 @@ int flce_linear_backward(const flce_linear_params* p, const void* dout, const vo
     a.strip = dz_strip(p);
     a.act = p->activation;
     a.dout_f32 = f32;
-    rc = p->N % 8 == 0 ? launch_dz<8>(a, L.strips, st) : launch_dz<1>(a, L.strips, st);
+    rc = launch_dz(a, L.strips, st);
     if (rc) return rc;
   }
   if (dbias) {

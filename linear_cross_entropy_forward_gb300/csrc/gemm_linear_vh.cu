@@ -1,4 +1,4 @@
-// Instantiations: a dense layer's output tiles; x K-major, weight [N,K] K-major.
+// Instantiations: a dense layer's output tiles, transposed; weight [N,K] and x both K-major.
 #include "flce_gemm.cuh"
 
 namespace flce {

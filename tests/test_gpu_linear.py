@@ -348,3 +348,32 @@ def test_refusals():
         flce.flce_linear_backward(dy.half(), x, w, weight_layout="vh")
     with pytest.raises(ValueError, match="dout"):
         flce.flce_linear_backward(dy[:2], x, w, weight_layout="vh")
+
+
+@pytest.mark.parametrize("M,K,N,layout", [(2600, 1032, 2301, "vh"), (2600, 1032, 2304, "hv"),
+                                          (1100, 264, 4099, "vh"), (2049, 2048, 2047, "vh")])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+def test_many_tokens_by_odd_widths(M, K, N, layout, out):
+    """Tiles of every kind with rows that 16 bytes do not divide; everything in the output at once, in
+    place of the residual too; and the gradients, dz unaligned."""
+    x, w, b, r = make(M, K, N, layout, 9, residual=out)
+    z, tol = exact(x, w, b, layout)
+    want = act64(z, "silu") + r.double()
+    y, pre = flce.flce_linear(x, w, b, "silu", r, layout, out, need_preact=True, validate=True)
+    rounding = (E8 if out is torch.bfloat16 else E23) * want.abs()
+    close(y, want, 1.13 * tol + 1e-6 * (z.abs() + 1) + rounding)
+    close(pre, z, tol + E8 * z.abs())
+    same = r.clone()
+    flce.flce_linear(x, w, b, "silu", same, layout, out, out=same)
+    assert torch.equal(same, y)
+    dx, dw, db = flce.flce_linear_backward(r, x, w, pre, "silu", layout, validate=True)
+    dz = r.double() * slope64(pre.double(), "silu")
+    off = 1e-6 * (pre.double().abs() + 1) * r.double().abs() + E8 * dz.abs()
+    W = (w if layout == "vh" else w.t()).double()
+    close(dx, dz @ W, off @ W.abs() + (N + 8) * E23 * (dz.abs() @ W.abs()) + E8 * (dz @ W).abs(), "dx")
+    dW = dz.t() @ x.double()
+    close(dw if layout == "vh" else dw.t(), dW, off.t() @ x.double().abs()
+          + (M + 8) * E23 * (dz.abs().t() @ x.double().abs()) + E8 * dW.abs(), "dw")
+    s = dz.sum(0)
+    close(db, s, (1e-6 * (pre.double().abs() + 1) * r.double().abs()).sum(0)
+          + (M + 8) * 2.0 ** -24 * dz.abs().sum(0) + E8 * s.abs(), "db")
