@@ -1,0 +1,10 @@
+// Instantiations: kernels of the processed logits for logits of fp32.
+#include "flce_logits.cuh"
+
+namespace flce {
+namespace logits {
+int run_f32(const Args& a, int count, int mode, int sms, cudaStream_t st) {
+  return run_type<float>(a, count, mode, sms, st);
+}
+}  // namespace logits
+}  // namespace flce

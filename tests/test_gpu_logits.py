@@ -487,3 +487,45 @@ def test_refusals():
     with pytest.raises(ValueError, match="entropy"):
         flce.flce_logits_logprob_backward(x, t[:, 0].contiguous(), x[:, 0].contiguous(), None, None,
                                           torch.zeros(2, device="cuda"))
+
+
+@pytest.mark.parametrize("R,V,T,dtype,ids", [(96, 256000, 12000, torch.bfloat16, torch.int64),
+                                             (40, 128257, 60001, torch.float32, torch.int32),
+                                             (61, 50257, 70000, torch.float16, torch.int64),
+                                             (24, 1000003, 16000, torch.bfloat16, torch.int32)])
+def test_long_histories_of_many_rows(R, V, T, dtype, ids):
+    """In every element what few rows at a time give, whose blocks have fewer columns and passes, and a
+    few rows against 64 bits; ids outside the row, empty and full histories, prompts alone, rows that
+    begin anywhere."""
+    o = options(R, V, T, 11, ids=ids, lens=ids)
+    tok = o["tokens"]
+    tok[:, 5::97] = -1
+    tok[:, 6::89] = V
+    tok[:, 7::83] = 2 ** 31 - 1 if ids is torch.int32 else -2 ** 40
+    tok[:, 8::79] = V + (2 ** 33 if ids is torch.int64 else 5)
+    tok[:, :T // 3] = (tok[:, :T // 3].double() / V).clamp(0, 1).pow(3).mul(1000).to(ids)  # repeated
+    o["lengths"][1], o["prompt_lens"][1] = 0, 0
+    o["lengths"][2], o["prompt_lens"][2] = T, T
+    o["repetition_penalty"][3], o["frequency_penalty"][3], o["presence_penalty"][3] = 1.0, 0.0, 0.0
+    x = rows_of(R, V, dtype, 12, pad=3, skew=1)
+    z, lse = flce.flce_process_logits(x, need_lse=True, **o)
+    labels = torch.randint(0, V, (R,), generator=torch.Generator(device="cuda").manual_seed(13), device="cuda")
+    logp, ent, lse2 = flce.flce_logits_logprob(x, labels, **o)
+    d = flce.flce_logits_logprob_backward(x, labels, lse2, ent, torch.ones_like(lse2), None, **o)
+    assert torch.equal(lse, lse2)
+    few = 3 if V < 200000 else 1
+    for r in range(0, R, few):
+        part = {k: v[r:r + few] for k, v in o.items()}
+        zp = flce.flce_process_logits(x[r:r + few], **part)
+        assert torch.equal(zp, z[r:r + few]), r
+        dp = flce.flce_logits_logprob_backward(x[r:r + few], labels[r:r + few], lse2[r:r + few], ent[r:r + few],
+                                               torch.ones_like(lse2[r:r + few]), None, **part)
+        assert torch.equal(dp, d[r:r + few]), r
+    for r in (0, 1, 2, 3, R - 1):
+        part = {k: v[r:r + 1] for k, v in o.items()}
+        want, _, size = reference(x[r:r + 1], part)
+        tol = 8 * 2.0 ** -24 * size + HALF_STEP[dtype] * want.abs() + (2.0 ** -25 if dtype is torch.float16 else 0)
+        assert bool(((z[r:r + 1].double().cpu() - want).abs() <= tol + 1e-30).all()), r
+        want = torch.logsumexp(want, 1)
+        assert abs(float(lse[r].double().cpu() - want)) <= 2 * 8 * 2.0 ** -24 * float(size.max()) + 2e-6 \
+            + 2.0 ** -23 * abs(float(want)), r
