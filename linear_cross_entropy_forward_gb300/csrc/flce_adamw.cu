@@ -39,7 +39,8 @@ constexpr int kUnit = kThreads * kPer;     // elements per unit
 constexpr int kBlockElems = 128;           // elements per scale of the 8-bit states
 constexpr int kSmall = 40, kLarge = 680;   // tensors in one launch's arguments
 constexpr float kTiny = 7.703719777548943e-34f;  // 2^-110: blocks below are held as zeros
-constexpr int kNormBlocks = 4;             // blocks per SM of the norm
+constexpr int kNormBlocks = 8;             // blocks per SM of the norm, of kNormUnits at least
+constexpr int kNormUnits = 4;               // (2.1M: 9.9 us; of one unit 14.0)
 constexpr int64_t kMaxUnits = int64_t(1) << 31;
 
 struct Slot {
@@ -420,8 +421,8 @@ __device__ __forceinline__ int find_run(const Table<CAP>& t, uint32_t& u, uint32
 }
 
 // Two blocks per SM's worth of registers for fp32 states, whose loads are all of a unit's bytes (600M
-// with masters 2.96 ms; for four blocks 3.02), four for 8 bits, bound by their arithmetic (300M: 1.09 ms
-// against 1.16).
+// with masters 2.64 ms, 5.8 TB/s; for four blocks 2.70), four for 8 bits, bound by their arithmetic, some 85
+// instructions per element (300M: 1.01 ms, 4.6 TB/s; for two 1.08).
 template <bool STATE8, bool MASTER, int CAP>
 __global__ void __launch_bounds__(kThreads, STATE8 ? 4 : 2)
     adamw_kernel(const __grid_constant__ Table<CAP> t, const __grid_constant__ StepArgs a) {
@@ -483,10 +484,12 @@ __global__ void __launch_bounds__(kThreads, STATE8 ? 4 : 2)
 }
 
 // ------------------------------------------------------------------ the norm
-// Sum of (scale g)^2, each square rounded to fp32, their sum exact to 2^-45 or so: a pair of floats per
-// lane of a packed addition, whose rounding errors are added up beside it (two 64-bit additions per
-// 16 squares took longer than their bytes do).
-constexpr int kNormDepth = 4;  // units in flight
+// Sum of (scale g)^2: those of eight elements in fp32, four additions deep, and these sums in a pair of
+// floats per lane of a packed addition, whose rounding errors are added up beside it.  The roundings of
+// many eights cancel: 2^-24 / sqrt(n / 8) or so is left of them.  (Two 64-bit additions per 16 squares
+// took longer than their bytes do, and so did every pair of squares in the pair of floats: 600M in bf16
+// 370 us; so 238, 5.0 TB/s, and in fp32 337, 7.1 TB/s.)
+constexpr int kNormDepth = 2;  // units in flight (four, for half the blocks per SM: 600M in bf16 329 us)
 
 struct PairSum {
   uint64_t hi = 0, lo = 0;  // two lanes each
@@ -526,13 +529,13 @@ __device__ __forceinline__ void sum_units(const Slot& s, int64_t e0, int64_t uni
     for (int d = 0; d < kNormDepth; ++d) {
       float x[kPer];
       widen(r[d], s.grad_dtype, x);
+      uint64_t squares = 0;
 #pragma unroll
       for (int i = 0; i < kPer; i += 2) {
         const uint64_t y = f2_mul(f2_pack(x[i], x[i + 1]), scale2);
-        float y0, y1;
-        f2_unpack(y, y0, y1);
-        sum.add(f2_pack(__fmul_rn(y0, y0), __fmul_rn(y1, y1)));
+        squares = f2_fma(y, y, squares);
       }
+      sum.add(squares);
     }
   }
 }
@@ -550,7 +553,7 @@ __device__ __forceinline__ double block_sum(double x) {
 }
 
 template <int CAP>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kNormBlocks)
     norm_kernel(const __grid_constant__ Table<CAP> t, const __grid_constant__ NormArgs a) {
   uint32_t u, end;
   int i = find_run(t, u, end);
@@ -691,7 +694,8 @@ int run_norm(const flce_adamw_params* p, const flce_adamw_tensor* t, float* norm
     int rc = fill(&table, p, t, &i);
     if (rc) return rc;
     const int64_t cap = static_cast<int64_t>(sms) * kNormBlocks;
-    const unsigned blocks = static_cast<unsigned>(table.units < cap ? table.units : cap);
+    const int64_t enough = cdiv(table.units, kNormUnits);
+    const unsigned blocks = static_cast<unsigned>(enough < cap ? enough : cap);
     a.last = !more_from(p, t, i);
     if ((rc = launch(norm_kernel<CAP>, blocks, false, st, table, a))) return rc;
     a.base += static_cast<int32_t>(blocks);
@@ -716,7 +720,8 @@ int run_step(const flce_adamw_params* p, const flce_adamw_tensor* t, StepArgs a,
     int rc = fill(&table, p, t, &i);
     if (rc) return rc;
     const int64_t cap = static_cast<int64_t>(sms) * per;
-    const unsigned blocks = static_cast<unsigned>(table.units < cap ? table.units : cap);
+    const int64_t enough = cdiv(table.units, kNormUnits);
+    const unsigned blocks = static_cast<unsigned>(enough < cap ? enough : cap);
     a.last = !more_from(p, t, i);
     if ((rc = launch(adamw_kernel<STATE8, MASTER, CAP>, blocks, true, st, table, a))) return rc;
   } while (!a.last);
