@@ -325,6 +325,7 @@ struct DzArgs {
   const __nv_bfloat16* preact;
   __nv_bfloat16* dz;  // NULL: dout serves
   float* part;        // [strips, N], or NULL
+  uint32_t* header;   // the workspace's, cleared for the launches behind
   int64_t M, N, ld_dz, strip;
   int32_t act, dout_f32;
 };
@@ -422,6 +423,8 @@ __global__ void __launch_bounds__(kDzThreads) dz_kernel(const __grid_constant__ 
   const int64_t n = (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) * 8;
   const int64_t m0 = blockIdx.y * a.strip;
   const int64_t m1 = m0 + a.strip < a.M ? m0 + a.strip : a.M;
+  if (blockIdx.x == 0 && blockIdx.y == 0)
+    for (int i = threadIdx.x; i < int(kHeader / 4); i += blockDim.x) a.header[i] = 0;
   if (n >= a.N) return;
   constexpr int kDeep = ALIGNED ? 4 : 2;
   const int64_t total = a.M * a.N;
@@ -565,6 +568,7 @@ int parts_of(int tt, int share) {
 struct Plan {
   int width;  // of a pair's tiles; 0: split
   int tt, size, stages;
+  double us;  // what it should take
 };
 
 Plan choose(const Product& g, int sms, bool layer, const LinearOut& o) {
@@ -572,12 +576,11 @@ Plan choose(const Product& g, int sms, bool layer, const LinearOut& o) {
   const double output = 4.5 + (o.act != FLCE_ACT_NONE ? 1.7 : 0.0) + (o.preact ? 2.5 : 0.0) +
                         (o.residual ? 3.5 : 0.0) + (o.out_f32 ? 1.0 : 0.0);
   const double traffic = (static_cast<double>(g.rows) + g.cols) * g.depth * 2 / 6.2e6 + 4.0;
-  Plan best{};
-  double least = 1e30;
+  Plan best{0, 0, 0, 0, 1e30};
   auto consider = [&](double us, const Plan& p) {
-    if (us < least) {
-      least = us;
+    if (us < best.us) {
       best = p;
+      best.us = us;
     }
   };
   const bool drain = drained(g, o);
@@ -586,7 +589,7 @@ Plan choose(const Product& g, int sms, bool layer, const LinearOut& o) {
     const double feed = kb * (width == 256 ? 0.33 : 0.27), finish = output * width / 256;
     const double us = rounds * (feed > finish ? feed : finish) + (feed > finish ? finish : feed) +
                       (drain ? rounds * finish / 2 : 0.0) + 5.0 + (rounds > 1 ? 2.0 : 0.0);
-    consider(us > traffic + 3.0 ? us : traffic + 3.0, Plan{width, 0, 0, 0});
+    consider(us > traffic + 3.0 ? us : traffic + 3.0, Plan{width, 0, 0, 0, us});
   }
   const int unit = g.left_mn ? 64 : 16;
   const int64_t fewest = cdiv(g.rows, kMaxTokens);
@@ -611,7 +614,7 @@ Plan choose(const Product& g, int sms, bool layer, const LinearOut& o) {
         const double us = rounds * (per_sm == 2 ? 2 * feed + 1.3 * finish : feed + finish) + 3.0;
         // the memory rests while an SM's only block finishes
         const double memory = traffic + (per_sm == 1 ? rounds * finish : 0.0);
-        consider(us > memory ? us : memory, Plan{0, tt, size, stages});
+        consider(us > memory ? us : memory, Plan{0, tt, size, stages, us});
       }
     }
   }
@@ -782,16 +785,19 @@ int launch_dz(const DzArgs& a, int64_t strips, cudaStream_t st) {
   return rc_of(cudaGetLastError());
 }
 
-// One gradient's product, by whichever kernel suits it.
-int run_gradient(const Product& g, int kind, void* out, uint32_t* err, int slot, int sms,
+// One gradient's product.
+int run_gradient(const Product& g, const Plan& plan, int kind, void* out, uint32_t* err, int slot,
                  cudaStream_t st) {
   LinearOut o{};
   o.y = out;
   o.ld = g.cols;
-  const Plan plan = choose(g, sms, false, o);
   return plan.width ? run_pair(g, plan.width, kind, o, err, slot, false, st)
                     : run_split(g, plan, o, err, false, st);
 }
+
+// Below this many microseconds of the smaller of two products, running them side by side costs the host
+// more than it saves the GPU.
+constexpr double kSideBySide = 10.0;
 
 }  // namespace
 }  // namespace flce
@@ -866,8 +872,8 @@ int flce_linear_backward(const flce_linear_params* p, const void* dout, const vo
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   uint32_t* err = static_cast<uint32_t*>(workspace);
-  if ((rc = rc_of(cudaMemsetAsync(ws, 0, kHeader, st)))) return rc;
   if (p->M == 0) {  // sums over no tokens
+    if ((rc = rc_of(cudaMemsetAsync(ws, 0, kHeader, st)))) return rc;
     if (dweight && (rc = rc_of(cudaMemsetAsync(dweight, 0, size_t(p->N) * p->K * 2, st)))) return rc;
     if (dbias && (rc = rc_of(cudaMemsetAsync(dbias, 0, size_t(p->N) * 2, st)))) return rc;
     return p->validate ? read_status(ws, st) : FLCE_OK;
@@ -882,6 +888,7 @@ int flce_linear_backward(const flce_linear_params* p, const void* dout, const vo
     a.dout = dout;
     a.preact = static_cast<const __nv_bfloat16*>(preact);
     a.dz = own_dz && (dx || dweight) ? reinterpret_cast<__nv_bfloat16*>(ws + L.dz) : nullptr;
+    a.header = err;
     a.part = dbias ? reinterpret_cast<float*>(ws + L.db) : nullptr;
     a.M = p->M;
     a.N = p->N;
@@ -891,6 +898,8 @@ int flce_linear_backward(const flce_linear_params* p, const void* dout, const vo
     a.dout_f32 = f32;
     rc = launch_dz(a, L.strips, st);
     if (rc) return rc;
+  } else if ((rc = rc_of(cudaMemsetAsync(ws, 0, kHeader, st)))) {
+    return rc;
   }
   if (dbias) {
     cudaLaunchConfig_t cfg{};
@@ -902,14 +911,15 @@ int flce_linear_backward(const flce_linear_params* p, const void* dout, const vo
       return rc;
   }
   // dx on the caller's stream, dweight beside it, as the head's backward does
+  const Product x_product = dx_product(p, dz, ld_dz, weight), w_product = dw_product(p, dz, ld_dz, x);
+  Plan x_plan{}, w_plan{};
+  if (dx) x_plan = choose(x_product, sms, false, LinearOut{});
+  if (dweight) w_plan = choose(w_product, sms, false, LinearOut{});
   cudaStream_t side = st;
-  const bool both = dx && dweight;
+  const bool both = dx && dweight && x_plan.us >= kSideBySide && w_plan.us >= kSideBySide;
   if (both && (rc = side_fork(st, &side))) return rc;
-  if (dx && (rc = run_gradient(dx_product(p, dz, ld_dz, weight), 1, dx, err, 0, sms, st)))
-    return rc;
-  if (dweight &&
-      (rc = run_gradient(dw_product(p, dz, ld_dz, x), 2, dweight, err, 1, sms, side)))
-    return rc;
+  if (dx && (rc = run_gradient(x_product, x_plan, 1, dx, err, 0, st))) return rc;
+  if (dweight && (rc = run_gradient(w_product, w_plan, 2, dweight, err, 1, side))) return rc;
   if (both && (rc = side_join(st))) return rc;
   return p->validate ? read_status(ws, st) : FLCE_OK;
 }

@@ -135,38 +135,59 @@ def flce_linear_backward(dout, x, weight, preact=None, activation=None, weight_l
         return _on(stream, flce_linear_backward, dout, x, weight, preact, activation,
                    weight_layout, need_dx, need_dweight, need_dbias, validate, workspace, out=out)
     lib = B._lib or B.load_library()
-    M, N, K, dev = _shapes(x, weight, weight_layout)
-    shape = (*x.shape[:-1], N)
-    if not isinstance(dout, torch.Tensor):
-        raise TypeError("dout must be a CUDA tensor")
-    p = linear_params(M, N, K, activation, weight_layout, dout.dtype, validate)
-    B._need(dout, "dout", dout.dtype, shape, dev)
-    if p.activation:
-        if preact is None:
-            raise ValueError("an activation's gradient needs preact")
-        B._need(preact, "preact", torch.bfloat16, shape, dev)
+    try:  # as in flce_linear
+        bf16, dev = torch.bfloat16, x.get_device()
+        layout, act, code = _LAYOUTS[weight_layout], _ACTIVATIONS[activation], _OUT[dout.dtype]
+        N, K = weight.shape if layout else weight.shape[::-1]
+        shape = (*x.shape[:-1], N)
+        if not (dev >= 0 and x.dtype is bf16 and weight.dtype is bf16 and x.shape[-1] == K
+                and weight.get_device() == dev == _current_device() and x.is_contiguous()
+                and weight.is_contiguous()):
+            raise ValueError
+        for t in (dout, preact) if act else (dout,):
+            if not (t.shape == shape and t.get_device() == dev and t.is_contiguous()):
+                raise ValueError
+        if act and preact.dtype is not bf16:
+            raise ValueError
+    except (AttributeError, IndexError, KeyError, TypeError, ValueError):
+        _refuse_backward(dout, x, weight, preact, activation, weight_layout)
+        raise
+    p = B.FlceLinearParams(x.numel() // K if K else 0, N, K, layout, act, code, bool(validate))
     size = linear_workspace_size(p, True)
     wanted = (("dx", need_dx, x.shape), ("dweight", need_dweight, weight.shape),
               ("dbias", need_dbias, (N,)))
     if out is None:
-        out = [torch.empty(s, dtype=torch.bfloat16, device=dev) if need else None
-               for _, need, s in wanted]
+        out = [torch.empty(s, dtype=bf16, device=dev) if need else None for _, need, s in wanted]
     else:
         if len(out) != 3:
             raise ValueError("out must hold dx, dweight and dbias")
         out = [t if need else None for t, (_, need, _) in zip(out, wanted)]
         for t, (name, need, s) in zip(out, wanted):
             if need:
-                B._need(t, name, torch.bfloat16, s, dev)
+                B._need(t, name, bf16, s, x.device)
     dx, dw, db = out
-    ws = _workspace(size, dev.index, workspace)
+    ws = _workspace(size, dev, workspace)
     code = lib.flce_linear_backward(
         ctypes.byref(p), dout.data_ptr(), x.data_ptr(), weight.data_ptr(),
-        preact.data_ptr() if p.activation else None, _addr(dx), _addr(dw), _addr(db),
-        ws.data_ptr(), ws.numel(), _raw_stream(dev.index))
+        preact.data_ptr() if act else None, _addr(dx), _addr(dw), _addr(db),
+        ws.data_ptr(), ws.numel(), _raw_stream(dev))
     if code:
         B._check(code)
     return dx, dw, db
+
+
+def _refuse_backward(dout, x, weight, preact, activation, weight_layout):
+    """Says what is wrong with flce_linear_backward's arguments."""
+    M, N, K, dev = _shapes(x, weight, weight_layout)
+    shape = (*x.shape[:-1], N)
+    if not isinstance(dout, torch.Tensor):
+        raise TypeError("dout must be a CUDA tensor")
+    p = linear_params(M, N, K, activation, weight_layout, dout.dtype)
+    B._need(dout, "dout", dout.dtype, shape, dev)
+    if p.activation:
+        if preact is None:
+            raise ValueError("an activation's gradient needs preact")
+        B._need(preact, "preact", torch.bfloat16, shape, dev)
 
 
 class _Linear(torch.autograd.Function):

@@ -122,7 +122,9 @@ class _Call:
                                  f"{tuple(allowed.shape)}")
             rows.allowed = allowed.data_ptr()
         self.p, self.rows, self.R, self.V, self.out_dtype = p, rows, R, V, out_dtype
-        self.keep = (tokens, prompt_lens, lengths, bias_ids, bias_values, allowed)
+        # whose addresses are in rows
+        self.keep = (tokens, prompt_lens, lengths, repetition_penalty, frequency_penalty,
+                     presence_penalty, bias_ids, bias_values, allowed, temperature)
 
     def workspace(self):
         return torch.empty(256, dtype=torch.uint8, device=self.index) if self.p.validate else None
@@ -214,11 +216,15 @@ def flce_logits_logprob(logits, labels, tokens=None, prompt_lens=None, lengths=N
               presence_penalty, bias_ids, bias_values, allowed, temperature, ignore_index, None,
               validate)
     _labels(labels, c.R, c.index)
+    return _logprob(lib, c, logits, labels)
+
+
+def _logprob(lib, c, logits, labels):
     logp, ent, lse = torch.empty(3, c.R, dtype=torch.float32, device=c.index).unbind(0)
     ws = c.workspace()
     code = lib.flce_logits(ctypes.byref(c.p), ctypes.byref(c.rows), logits.data_ptr(),
                            labels.data_ptr(), None, lse.data_ptr(), logp.data_ptr(),
-                           ent.data_ptr(), _addr(ws), 256 if validate else 0,
+                           ent.data_ptr(), _addr(ws), 256 if c.p.validate else 0,
                            _raw_stream(c.index))
     if code:
         B._check(code)
@@ -254,6 +260,10 @@ def flce_logits_logprob_backward(logits, labels, lse, entropy, g_logp, g_entropy
         _row_grad(t, name, c.R, c.index)
     if lse is None or (g_entropy is not None and entropy is None):
         raise ValueError("the gradient needs lse, and that of the entropy needs entropy")
+    return _logprob_backward(lib, c, logits, labels, lse, entropy, g_logp, g_entropy)
+
+
+def _logprob_backward(lib, c, logits, labels, lse, entropy, g_logp, g_entropy):
     d = torch.empty(c.R, c.V, dtype=c.out_dtype, device=c.index)
     code = lib.flce_logits_backward(ctypes.byref(c.p), ctypes.byref(c.rows), logits.data_ptr(),
                                     labels.data_ptr(), lse.data_ptr(), _addr(entropy),
@@ -267,25 +277,34 @@ def flce_logits_logprob_backward(logits, labels, lse, entropy, g_logp, g_entropy
 class _LogitsLogprob(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, labels, options):
-        logp, ent, lse = flce_logits_logprob(logits, labels, **options)
-        tensors = {k: v for k, v in options.items() if isinstance(v, torch.Tensor)}
-        ctx.rest = {k: v for k, v in options.items() if k not in tensors and k != "validate"}
-        ctx.names = tuple(tensors)
-        ctx.save_for_backward(logits, labels, lse, ent, *tensors.values())
+        lib = B._lib or B.load_library()
+        c = _Call(logits, *options)
+        _labels(labels, c.R, c.index)
+        logp, ent, lse = _logprob(lib, c, logits, labels)
+        # the options' tensors are saved for the check that nothing has changed them since
+        ctx.save_for_backward(logits, labels, lse, ent,
+                              *(t for t in options if isinstance(t, torch.Tensor)))
+        c.p.validate = 0
+        ctx.call = c
         ctx.set_materialize_grads(False)
         return logp, ent
 
     @staticmethod
     @once_differentiable
     def backward(ctx, g_logp, g_ent):
-        logits, labels, lse, ent, *tensors = ctx.saved_tensors
+        logits, labels, lse, ent = ctx.saved_tensors[:4]
         if g_logp is None and g_ent is None:
             return None, None, None
-        d = flce_logits_logprob_backward(
-            logits, labels, lse, ent, None if g_logp is None else g_logp.contiguous(),
-            None if g_ent is None else g_ent.contiguous(), **dict(zip(ctx.names, tensors)),
-            **ctx.rest)
-        return d, None, None
+        g_logp, g_ent = (None if g is None else g.contiguous() for g in (g_logp, g_ent))
+        c = ctx.call
+        if c.index != _current_device():
+            B._on_current_device(logits)
+        if logits.stride(1) != 1:
+            logits = logits.contiguous()
+        c.p.ld_logits = logits.stride(0)  # a saved tensor may come back as a copy
+        for name, g in (("g_logp", g_logp), ("g_entropy", g_ent)):
+            _row_grad(g, name, c.R, c.index)
+        return _logprob_backward(B._lib, c, logits, labels, lse, ent, g_logp, g_ent), None, None
 
 
 def logits_logprob(logits, labels, tokens=None, prompt_lens=None, lengths=None,
@@ -294,8 +313,6 @@ def logits_logprob(logits, labels, tokens=None, prompt_lens=None, lengths=None,
                    ignore_index=IGNORE_INDEX, validate=False):
     """(logp, entropy) of labels under the processed distribution, differentiable by logits (the
     options have no gradient); see flce_logits_logprob."""
-    return _LogitsLogprob.apply(logits, labels, dict(
-        tokens=tokens, prompt_lens=prompt_lens, lengths=lengths,
-        repetition_penalty=repetition_penalty, frequency_penalty=frequency_penalty,
-        presence_penalty=presence_penalty, bias_ids=bias_ids, bias_values=bias_values,
-        allowed=allowed, temperature=temperature, ignore_index=ignore_index, validate=validate))
+    return _LogitsLogprob.apply(logits, labels, (
+        tokens, prompt_lens, lengths, repetition_penalty, frequency_penalty, presence_penalty,
+        bias_ids, bias_values, allowed, temperature, ignore_index, None, validate))

@@ -529,3 +529,26 @@ def test_long_histories_of_many_rows(R, V, T, dtype, ids):
         want = torch.logsumexp(want, 1)
         assert abs(float(lse[r].double().cpu() - want)) <= 2 * 8 * 2.0 ** -24 * float(size.max()) + 2e-6 \
             + 2.0 ** -23 * abs(float(want)), r
+
+
+def test_saved_tensors_that_come_back_as_copies():
+    """Hooks on what is saved hand the gradient copies of the logits, without their row stride; the
+    options' tensors stay where the call found them."""
+    R, V = 5, 1000
+    x = rows_of(R, V, torch.float32, 21, pad=24)
+    labels = torch.arange(R, device="cuda") * 7
+    g = torch.linspace(-1, 1, R, device="cuda")
+
+    def run(hooks):
+        leaf = x.detach().requires_grad_(True)
+        o = options(R, V, 60, 22, mask="bits")
+        with torch.autograd.graph.saved_tensors_hooks(*hooks):
+            logp, ent = flce.logits_logprob(leaf, labels, **o)
+        del o
+        junk = [torch.full((R,), 1e9, device="cuda") for _ in range(20)]
+        (d,) = torch.autograd.grad((logp * g).sum() + ent.sum(), leaf)
+        del junk
+        return d
+
+    assert torch.equal(run((lambda t: t, lambda t: t)),
+                       run((lambda t: t.cpu(), lambda t: t.cuda().contiguous())))
