@@ -967,7 +967,8 @@ __global__ void __launch_bounds__(pair_threads<EPI>(), 1)
         Epilogue<EPI_LINEAR>::Column<true> column(ea, row, col0);
         if (!mbar_wait(&tfull[acc], aph, abort_flag, ea.err)) break;
         tc_fence_after();
-        Epilogue<EPI_LINEAR>::run<C::EPI_CHUNKS>(tbase, column);
+        if (FLCE_CHECK(tmem_ok(acc * TN + half * C::EPI_COLS, C::EPI_CHUNKS * 32, q, warp), ea.err))
+          Epilogue<EPI_LINEAR>::run<C::EPI_CHUNKS>(tbase, column);
       } else if constexpr (!drained<EPI>()) {
         if (!mbar_wait(&tfull[acc], aph, abort_flag, ea.err)) break;
         tc_fence_after();
