@@ -484,7 +484,8 @@ int flce_linear_check_params(const flce_linear_params* params);
 size_t flce_linear_workspace_size(const flce_linear_params* params, int backward);
 
 /* bias, residual: or NULL.  preact: [M,N] bf16, z for the backward, or NULL.  x, weight, y,
- * residual and preact 16-byte aligned, bias 2-byte. */
+ * residual and preact 16-byte aligned, bias 2-byte.  y may be the residual itself; outputs otherwise
+ * share no memory with one another or with what is read, here and in the backward. */
 int flce_linear(const flce_linear_params* params, const void* x, const void* weight,
                 const void* bias, const void* residual, void* y, void* preact, void* workspace,
                 size_t ws_bytes, void* stream);

@@ -67,6 +67,17 @@ def _shapes(x, weight, weight_layout):
     return M, N, K, dev
 
 
+def _apart(outs, inputs):
+    """Refuses outputs (name, tensor or None) that share memory with one another or with an input, which
+    would be read after it is overwritten."""
+    spans = [(t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), name)
+             for name, t in (*outs, *inputs) if t is not None and t.numel()]
+    for i, (a, b, name) in enumerate(spans[:sum(t is not None and t.numel() > 0 for _, t in outs)]):
+        for c, d, other in spans[i + 1:]:
+            if a < d and c < b:
+                raise ValueError(f"{name} shares memory with {other}")
+
+
 def flce_linear(x, weight, bias=None, activation=None, residual=None, weight_layout="hv",
                 out_dtype=torch.bfloat16, need_preact=False, validate=False, workspace=None,
                 stream=None, out=None):
@@ -101,6 +112,10 @@ def flce_linear(x, weight, bias=None, activation=None, residual=None, weight_lay
     p = B.FlceLinearParams(x.numel() // K if K else 0, N, K, layout, act, out_code, bool(validate))
     if out is None:
         out = torch.empty(shape, dtype=out_dtype, device=x.device)
+    else:
+        own = residual is not None and out.data_ptr() == residual.data_ptr()
+        _apart([("out", out)], [("x", x), ("weight", weight), ("bias", bias),
+                                ("residual", None if own else residual)])
     z = torch.empty(shape, dtype=bf16, device=x.device) if need_preact else None
     ws = torch.empty(_HEADER, dtype=torch.uint8, device=x.device) if workspace is None \
         else _workspace(linear_workspace_size(p), dev, workspace)
@@ -165,6 +180,8 @@ def flce_linear_backward(dout, x, weight, preact=None, activation=None, weight_l
         for t, (name, need, s) in zip(out, wanted):
             if need:
                 B._need(t, name, bf16, s, x.device)
+        _apart([(name, t) for (name, _, _), t in zip(wanted, out)],
+               [("dout", dout), ("x", x), ("weight", weight), ("preact", preact if act else None)])
     dx, dw, db = out
     ws = _workspace(size, dev, workspace)
     code = lib.flce_linear_backward(

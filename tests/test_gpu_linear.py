@@ -377,3 +377,28 @@ def test_many_tokens_by_odd_widths(M, K, N, layout, out):
     s = dz.sum(0)
     close(db, s, (1e-6 * (pre.double().abs() + 1) * r.double().abs()).sum(0)
           + (M + 8) * 2.0 ** -24 * dz.abs().sum(0) + E8 * s.abs(), "db")
+
+
+def test_outputs_that_share_memory_are_refused():
+    """Tiles are read while others are written, so an output over an input would be read back."""
+    x, w, b, r = make(16, 16, 16, "vh", residual=torch.bfloat16)
+    big = torch.empty(16 * 16 + 8, device="cuda", dtype=torch.bfloat16)
+    L = lambda **k: flce.flce_linear(x, w, b, weight_layout="vh", **k)  # noqa: E731
+    with pytest.raises(ValueError, match="out shares memory with x"):
+        L(out=x)
+    with pytest.raises(ValueError, match="out shares memory with weight"):
+        L(out=w)
+    with pytest.raises(ValueError, match="out shares memory with residual"):
+        L(residual=big[8:].view(16, 16), out=big[:256].view(16, 16))
+    L(residual=r, out=r)
+    dy = torch.ones_like(r)
+    D = lambda *o: flce.flce_linear_backward(dy, x, w, weight_layout="vh", out=o)  # noqa: E731
+    new = lambda *s: torch.empty(s, device="cuda", dtype=torch.bfloat16)  # noqa: E731
+    same = new(16, 16)
+    with pytest.raises(ValueError, match="dx shares memory with dout"):
+        D(dy, new(16, 16), new(16))
+    with pytest.raises(ValueError, match="dx shares memory with dweight"):
+        D(same, same, new(16))
+    with pytest.raises(ValueError, match="dweight shares memory with x"):
+        D(new(16, 16), x, new(16))
+    D(new(16, 16), new(16, 16), new(16))
