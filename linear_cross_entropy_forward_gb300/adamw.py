@@ -203,10 +203,15 @@ class AdamW:
         grads = [p.grad for p in self.params] if grads is None else list(grads)
         if len(grads) != len(self.params):
             raise ValueError(f"{len(grads)} gradients for {len(self.params)} tensors")
-        for i, (g, shape, dtypes) in enumerate(zip(grads, self._shapes, self._wanted)):
+        for i, (p, g, shape, dtypes) in enumerate(zip(self.params, grads, self._shapes,
+                                                      self._wanted)):
             if not (isinstance(g, torch.Tensor) and g.dtype in dtypes and g.shape == shape
                     and g.get_device() == index and g.is_contiguous()):
                 _refuse_grad(g, f"gradient {i}", shape, dtypes, index)
+            # (a parameter's data may have been exchanged since)
+            if not (p.dtype is dtypes[0] and p.shape == shape and p.get_device() == index
+                    and p.is_contiguous()):
+                _refuse_grad(p, f"parameter {i}", shape, dtypes[:1], index)
         param, grad, grad_dtype = self._columns
         param[:] = [p.data_ptr() for p in self.params]
         grad[:] = [g.data_ptr() for g in grads]

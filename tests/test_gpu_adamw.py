@@ -400,3 +400,24 @@ def test_refusals():
         A([p], lr=torch.ones(1, device="cuda", dtype=torch.float64)).step([p.clone()])
     with pytest.raises(ValueError, match="workspace"):
         flce.flce_grad_norm([p], workspace=torch.zeros(10, dtype=torch.uint8, device="cuda"))
+
+
+def test_exchanged_parameters():
+    """A parameter's data may be exchanged for another tensor of its kind; for one of another size or
+    type the step, whose table holds the old ones, is refused."""
+    p = torch.nn.Parameter(torch.zeros(300, device="cuda"))
+    opt = flce.AdamW([p], lr=0.1, weight_decay=0.0)
+    g = torch.ones(300, device="cuda")
+    opt.step([g])
+    p.data = torch.full((300,), 5.0, device="cuda")
+    opt.step([g])
+    assert bool(((p.detach() - 4.9).abs() < 1e-4).all())
+    for other, error in ((torch.zeros(20, device="cuda"), ValueError),
+                         (torch.zeros(300, device="cuda").half(), TypeError),
+                         (torch.zeros(300), TypeError),
+                         (torch.zeros(600, device="cuda")[::2], ValueError)):
+        kept, p.data = p.data, other
+        with pytest.raises(error, match="parameter 0"):
+            opt.step([g])
+        p.data = kept
+    opt.step([g])
