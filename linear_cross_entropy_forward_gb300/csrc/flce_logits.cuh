@@ -101,6 +101,10 @@ struct Args {
 // PROCESS: z, with or without lse.  FORWARD: whatever is asked for.
 enum { MODE_FORWARD = 0, MODE_BACKWARD = 1, MODE_PROCESS = 2 };
 
+// (one per source: what a source has set up for its kernels is not shared with another build of them in
+// the same process)
+namespace {
+
 // The 4 or 8 values of 16 bytes.
 template <typename T>
 __device__ __forceinline__ void widen(const uint4& q, float (&x)[16 / sizeof(T)]) {
@@ -917,6 +921,8 @@ int run_type(const Args& a, int count, int mode, int sms, cudaStream_t st) {
   return mask ? run_mode<T, NoCounter, true, false>(a, mode, sms, st)
               : run_mode<T, NoCounter, false, false>(a, mode, sms, st);
 }
+
+}  // namespace
 
 // by the logits' type, each in a source of its own
 int run_f32(const Args& a, int count, int mode, int sms, cudaStream_t st);

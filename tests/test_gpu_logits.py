@@ -552,3 +552,21 @@ def test_saved_tensors_that_come_back_as_copies():
 
     assert torch.equal(run((lambda t: t, lambda t: t)),
                        run((lambda t: t.cpu(), lambda t: t.cuda().contiguous())))
+
+
+def test_two_builds_in_one_process(tmp_path):
+    """What a library has set up for its kernels is its own: another build beside it (as the one with
+    bounds checks is) sets up its own."""
+    import shutil
+
+    from linear_cross_entropy_forward_gb300 import _binding as B
+    x = rows_of(4, 128256, torch.bfloat16, 31)
+    o = options(4, 128256, 50, 32)
+    z = flce.flce_process_logits(x, **o)
+    other = tmp_path / "libflce_copy.so"
+    shutil.copy(B.LIB_PATH, other)
+    mine = B.use_library(str(other))
+    try:
+        assert torch.equal(flce.flce_process_logits(x, **o), z)
+    finally:
+        B.restore_library(mine)
