@@ -863,10 +863,16 @@ int run(Args a, int sms, cudaStream_t st) {
   constexpr int64_t unit = 16 / sizeof(Word) > VEC ? 16 / sizeof(Word) : VEC;
   constexpr int64_t most = kRoom / sizeof(Word);
   const int64_t span = a.V + VEC - 1;  // with what may stand before a row
-  // As few blocks per row as fill the GPU several times over, so that its last round is a small
-  // part, but no more than have a vector for half of their threads.
+  // Blocks per row: few rows take as many as are resident at once, as a second round of blocks costs more
+  // than shorter ones save (64 x 128256 in fp32 with a mask: 23.6 us by 4, 30.6 by 16; 200 x 32000: 13.3 by
+  // 2, 19.0 by 8); more rows as few as fill the GPU several times over, so that the last round is a small
+  // part (384 x 256000: 156 us by 4, 161 by 1).  None has less than a vector for half of its threads.
+  const int64_t resident = int64_t(kBlocks) * sms;
+  const bool few = 2 * a.R <= resident;
   int size = 1;
-  while (size < kMaxCluster && a.R * size < kFill * sms && span > size * wide / 2) size *= 2;
+  while (size < kMaxCluster && (few ? 2 * a.R * size <= resident : a.R * size < kFill * sms) &&
+         span > size * wide / 2)
+    size *= 2;
   a.columns = cdiv(cdiv(span, size), unit) * unit;
   a.passes = static_cast<int32_t>(COUNT ? cdiv(a.columns, most) : 1);
   a.room = cdiv(cdiv(a.columns, a.passes), unit) * unit;
