@@ -914,16 +914,17 @@ int run_mode(const Args& a, int mode, int sms, cudaStream_t st) {
                                 : run<T, COUNTER, MODE_BACKWARD, MASK, BIAS>(a, sms, st);
 }
 
-// count 0: no counters, else their bits.  Histories of 2^14 tokens and more, and rows with biases, take
-// the kernels that can do everything.
+// count 0: no counters, else their bits.  Histories of 2^14 tokens and more take the kernels that can do
+// everything.
 template <typename T>
 int run_type(const Args& a, int count, int mode, int sms, cudaStream_t st) {
   const bool mask = a.mask_kind != 0, bias = a.n_bias != 0;
   if (count == 32) return run_mode<T, Counter<uint32_t>, true, true>(a, mode, sms, st);
   if (count == 16)
-    return bias   ? run_mode<T, Counter<uint16_t>, true, true>(a, mode, sms, st)
-           : mask ? run_mode<T, Counter<uint16_t>, true, false>(a, mode, sms, st)
-                  : run_mode<T, Counter<uint16_t>, false, false>(a, mode, sms, st);
+    return bias ? (mask ? run_mode<T, Counter<uint16_t>, true, true>(a, mode, sms, st)
+                        : run_mode<T, Counter<uint16_t>, false, true>(a, mode, sms, st))
+                : (mask ? run_mode<T, Counter<uint16_t>, true, false>(a, mode, sms, st)
+                        : run_mode<T, Counter<uint16_t>, false, false>(a, mode, sms, st));
   return mask ? run_mode<T, NoCounter, true, false>(a, mode, sms, st)
               : run_mode<T, NoCounter, false, false>(a, mode, sms, st);
 }
