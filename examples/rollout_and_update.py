@@ -98,7 +98,7 @@ def main(rounds=3, seed=0, quiet=False):
         for epoch in range(2):
             logp, entropy = score(tokens, table, weight, bias, allowed)
             if epoch == 0:
-                apart = float((logp - old).abs().max())
+                apart = float((logp.detach() - old).abs().max())
             loss, _, _ = flce.policy_loss(logp, old, advantages, entropy=entropy, entropy_coef=0.01)
             loss.sum().backward()
             norm = opt.step()
