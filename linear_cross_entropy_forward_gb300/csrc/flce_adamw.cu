@@ -473,12 +473,16 @@ __global__ void __launch_bounds__(kThreads, STATE8 ? 4 : 2)
       }
     }
   }
-  // the last block to have read the step counts it, and leaves the ticket at 0
-  if (a.last && threadIdx.x == 0 && !skip) {
-    __threadfence();
-    if (atomicAdd(a.ticket, 1u) == gridDim.x - 1) {
-      *a.ticket = 0;
-      *a.step = step;
+  // A block's ticket says that all of its threads have read the step; the last one counts it, and leaves
+  // the ticket at 0.  (a.last and skip are the same for all threads.)
+  if (a.last && !skip) {
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      __threadfence();
+      if (atomicAdd(a.ticket, 1u) == gridDim.x - 1) {
+        *a.ticket = 0;
+        *a.step = step;
+      }
     }
   }
 }
