@@ -14,7 +14,7 @@ import numpy as np
 import torch
 
 from . import _binding as B
-from .losses import _DTYPES, _current_device, _on, _raw_stream
+from .losses import _DTYPES, _current_device, _on, _raw_stream, _written
 
 BLOCK = 128  # elements that share a scale of the 8-bit states
 _TENSOR = np.dtype([("param", np.uint64), ("grad", np.uint64), ("n", np.int64),
@@ -244,4 +244,5 @@ class AdamW:
             self.step_count.data_ptr(), ws.data_ptr(), ws.numel(), stream)
         if code:
             B._check(code)
+        _written(*self.params, self.step_count, self.master, *s.values())
         return norm

@@ -14,7 +14,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _binding as B
-from .losses import _addr, _current_device, _on, _raw_stream, _workspace
+from .losses import _addr, _current_device, _on, _raw_stream, _workspace, _written
 
 _ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 _OUT = {torch.bfloat16: 1, torch.float32: 0}
@@ -110,7 +110,8 @@ def flce_linear(x, weight, bias=None, activation=None, residual=None, weight_lay
         _refuse(x, weight, bias, activation, residual, weight_layout, out_dtype, out)
         raise
     p = B.FlceLinearParams(x.numel() // K if K else 0, N, K, layout, act, out_code, bool(validate))
-    if out is None:
+    given = out is not None
+    if not given:
         out = torch.empty(shape, dtype=out_dtype, device=x.device)
     else:
         own = residual is not None and out.data_ptr() == residual.data_ptr()
@@ -124,6 +125,8 @@ def flce_linear(x, weight, bias=None, activation=None, residual=None, weight_lay
                            _raw_stream(dev))
     if code:
         B._check(code)
+    if given:
+        _written(out)
     return (out, z) if need_preact else out
 
 
@@ -171,7 +174,8 @@ def flce_linear_backward(dout, x, weight, preact=None, activation=None, weight_l
     size = linear_workspace_size(p, True)
     wanted = (("dx", need_dx, x.shape), ("dweight", need_dweight, weight.shape),
               ("dbias", need_dbias, (N,)))
-    if out is None:
+    given = out is not None
+    if not given:
         out = [torch.empty(s, dtype=bf16, device=dev) if need else None for _, need, s in wanted]
     else:
         if len(out) != 3:
@@ -190,6 +194,8 @@ def flce_linear_backward(dout, x, weight, preact=None, activation=None, weight_l
         ws.data_ptr(), ws.numel(), _raw_stream(dev))
     if code:
         B._check(code)
+    if given:
+        _written(dx, dw, db)
     return dx, dw, db
 
 

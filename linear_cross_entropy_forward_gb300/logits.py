@@ -20,7 +20,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _binding as B
-from .losses import _DTYPES, _addr, _current_device, _on, _raw_stream
+from .losses import _DTYPES, _addr, _current_device, _on, _raw_stream, _written
 from .workloads import IGNORE_INDEX
 
 _WHOLE = {torch.int64: 1, torch.int32: 0}
@@ -169,7 +169,8 @@ def flce_process_logits(logits, tokens=None, prompt_lens=None, lengths=None,
     c = _Call(logits, tokens, prompt_lens, lengths, repetition_penalty, frequency_penalty,
               presence_penalty, bias_ids, bias_values, allowed, temperature, IGNORE_INDEX,
               out_dtype, False)
-    if out is None:
+    given = out is not None
+    if not given:
         out = torch.empty(c.R, c.V, dtype=c.out_dtype, device=c.index)
     else:
         if out.shape != (c.R, c.V) or out.get_device() != c.index:
@@ -182,6 +183,8 @@ def flce_process_logits(logits, tokens=None, prompt_lens=None, lengths=None,
                            out.data_ptr(), _addr(lse), None, None, None, 0, _raw_stream(c.index))
     if code:
         B._check(code)
+    if given:
+        _written(out)
     return (out, lse) if need_lse else out
 
 

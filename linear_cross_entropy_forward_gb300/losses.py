@@ -55,6 +55,12 @@ def _on(stream, call, *args, **kw):
         return call(*args, **kw)
 
 
+def _written(*tensors):
+    """Tells autograd that the library has changed these tensors (or None) of the caller's: a backward
+    that saved one of them then raises instead of using the new values."""
+    torch.autograd.graph.increment_version([t for t in tensors if t is not None])
+
+
 def _refuse(t, name, dtype, shape, index):
     """Says what is wrong with one array of a batch."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
