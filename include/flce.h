@@ -515,6 +515,7 @@ typedef struct {
   int32_t tokens_int64, lens_int64, bias_int64; /* 1: int64, 0: int32 */
   int32_t mask_kind;        /* 0: none, 1: bytes, non-zero allows, 2: bits, v % 32 of word v / 32 */
   int32_t validate;
+  int32_t split_lse;        /* lse is [2, R]: behind it what its rounding to fp32 left off */
 } flce_logits_params;
 
 /* Of each row, or NULL.  tokens [R, T]: the first lengths[r] count (NULL: all), of them the first
@@ -546,8 +547,9 @@ int flce_logits(const flce_logits_params* params, const flce_logits_rows* rows,
                 float* entropy, void* workspace, size_t ws_bytes, void* stream);
 
 /* dlogits [R, V] (out_dtype, ld_out) = g_logp * d logp / d logits + g_entropy * d entropy / d logits
- * (NULL: 0), with lse and entropy (or NULL without g_entropy) of flce_logits.  Rows that are
- * ignored or have nothing left get zeros. */
+ * (NULL: 0), with lse and entropy (or NULL without g_entropy) of flce_logits.  Without split_lse a
+ * probability is off by the rounding of lse, 2^-24 |lse| of itself; with it, by that of z - lse.  Rows
+ * that are ignored or have nothing left get zeros. */
 int flce_logits_backward(const flce_logits_params* params, const flce_logits_rows* rows,
                          const void* logits, const int64_t* labels, const float* lse,
                          const float* entropy, const float* g_logp, const float* g_entropy,

@@ -57,7 +57,8 @@ class FlceLogitsParams(ctypes.Structure):
                 ("temperature", ctypes.c_double), ("dtype", ctypes.c_int32),
                 ("out_dtype", ctypes.c_int32), ("tokens_int64", ctypes.c_int32),
                 ("lens_int64", ctypes.c_int32), ("bias_int64", ctypes.c_int32),
-                ("mask_kind", ctypes.c_int32), ("validate", ctypes.c_int32)]
+                ("mask_kind", ctypes.c_int32), ("validate", ctypes.c_int32),
+                ("split_lse", ctypes.c_int32)]
 
 
 class FlceLogitsRows(ctypes.Structure):

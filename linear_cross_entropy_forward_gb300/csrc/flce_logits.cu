@@ -83,6 +83,7 @@ int common(const flce_logits_params* p, const flce_logits_rows* r, const void* l
   x.lens64 = p->lens_int64;
   x.bias64 = p->bias_int64;
   x.out_f32 = p->out_dtype == FLCE_F32;
+  x.split = p->split_lse != 0;
   return FLCE_OK;
 }
 

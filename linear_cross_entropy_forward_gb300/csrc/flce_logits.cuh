@@ -87,7 +87,7 @@ struct Args {
   int64_t ld_allowed;
   const int64_t* labels;
   int64_t ignore_index;
-  float* lse;
+  float* lse;  // [R], or with `split` [2, R]: what its rounding left off behind it
   float* logp;
   float* entropy;
   const float* g_logp;
@@ -95,7 +95,7 @@ struct Args {
   uint32_t* err;
   int64_t columns, room;  // per block, and of them at a time (whole vectors)
   int32_t passes, stage_bytes;
-  int32_t ids64, lens64, bias64, mask_kind, out_f32, stats;
+  int32_t ids64, lens64, bias64, mask_kind, out_f32, stats, split;
 };
 
 // PROCESS: z, with or without lse.  FORWARD: whatever is asked for.
@@ -327,7 +327,7 @@ __device__ __forceinline__ void zero_columns(const Args& a, uint8_t* out, int l0
 // What all of a block needs to know of its row, found out by one thread.
 struct RowArgs {
   float rep, inv_rep, freq, pres, inv_temp;
-  float lse, g, h, ent;      // the gradient: -p (g + h (ln p + H)) + g [label]
+  float lse, low, g, h, ent;  // the gradient: -p (g + h (ln p + H)) + g [label], ln p = (z - lse) - low
   int label, length, prompt;
   int ignored, bad, zero;    // zero: a gradient of zeros
 };
@@ -354,6 +354,7 @@ __device__ __forceinline__ void read_row(const Args& a, int64_t row, RowArgs& r)
   r.zero = 0;
   if (BACKWARD) {
     r.lse = a.lse[row];
+    r.low = a.split ? a.lse[a.R + row] : 0.0f;
     r.g = a.g_logp ? a.g_logp[row] : 0.0f;
     r.h = a.g_entropy ? a.g_entropy[row] : 0.0f;
     r.ent = a.entropy ? a.entropy[row] : 0.0f;
@@ -566,8 +567,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
     return y;
   };
   auto gradient = [&](float z, float slope, bool label) {
-    const float q = fmaxf(z - r.lse, -200.0f), e = fast_ex2(q * kLog2e);
-    const float dz = -e * (fmaf(r.h, q + r.ent, r.g) + (r.lse - r.lse)) + (label ? r.g : 0.0f);
+    const float q = fmaxf(z - r.lse, -200.0f), e = fast_ex2(fmaf(q, kLog2e, -r.low * kLog2e));
+    const float dz = -e * (fmaf(r.h, q + (r.ent - r.low), r.g) + (r.lse - r.lse)) + (label ? r.g : 0.0f);
     return slope * dz;
   };
   Running run;
@@ -575,9 +576,12 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
   const float rep = COUNT ? r.rep : 1.0f, inv_rep = COUNT ? r.inv_rep : 1.0f;
   const float freq = COUNT ? r.freq : 0.0f, pres = COUNT ? r.pres : 0.0f;
   const bool counted = freq != 0.0f || pres != 0.0f;
-  // the gradient of a column that is not the label's: p (down_h ln p + down_g); a row whose lse is NaN has NaN
+  // The gradient of a column that is not the label's: p (down_h (z - lse) + down_g), where down_g has the rest
+  // of ln p; a row whose lse is NaN has NaN.  z - lse is exact where p is not small, so that p keeps its digits
+  // whatever the size of the logits: without `low`, half a step of the lse is the relative error of p, and 1 - p of
+  // a likely label is off by 0.8 % at a size of 100, by 19 % at 3000.
   const float down_h = BACKWARD ? -r.h * inv_temp : 0.0f;
-  float down_g = BACKWARD ? -fmaf(r.h, r.ent, r.g) * inv_temp + (r.lse - r.lse) : 0.0f;
+  float down_g = BACKWARD ? -fmaf(r.h, r.ent - r.low, r.g) * inv_temp + (r.lse - r.lse) : 0.0f;
   const bool stats = !BACKWARD && a.stats, entropy = !PROCESS && a.entropy;
   const int label = PROCESS ? -1 : r.label;
   int copied = 0;
@@ -745,14 +749,15 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
           if (!PROCESS && !out) continue;
         } else {
           // p and its logarithm from q = max(z - lse, -200): p is 0 there, and -inf stays out of the sums
-          const uint64_t minus = f2_pack(-r.lse, -r.lse), log2 = f2_pack(kLog2e, kLog2e);
+          const float rest = -r.low * kLog2e;
+          const uint64_t minus = f2_pack(-r.lse, -r.lse), log2 = f2_pack(kLog2e, kLog2e), rest2 = f2_pack(rest, rest);
           const uint64_t h2 = f2_pack(down_h, down_h), g2 = f2_pack(down_g, down_g);
 #pragma unroll
           for (int i = 0; i < VEC; i += 2) {
             float q0, q1, t0, t1;
             f2_unpack(f2_add(f2_pack(z[i], z[i + 1]), minus), q0, q1);
             const uint64_t q = f2_pack(fmaxf(q0, -200.0f), fmaxf(q1, -200.0f));
-            f2_unpack(f2_mul(q, log2), t0, t1);
+            f2_unpack(f2_fma(q, log2, rest2), t0, t1);
             const uint64_t p = f2_pack(fast_ex2(t0), fast_ex2(t1));
             f2_unpack(f2_mul(p, f2_fma(h2, q, g2)), z[i], z[i + 1]);
           }
@@ -829,7 +834,13 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
       if (tid != 0) return;
       const float log_d = logf(all.d);
       const bool none = all.m == -INFINITY && all.d == 0.0f;  // nothing is left
-      if (a.lse) a.lse[row] = none ? -INFINITY : all.m + log_d;
+      if (a.lse) {
+        const float lse = none ? -INFINITY : all.m + log_d, part_d = lse - all.m;
+        a.lse[row] = lse;
+        // (what the sum lost, by Knuth's two-sum)
+        if (a.split)
+          a.lse[a.R + row] = isfinite(lse) ? (all.m - (lse - part_d)) + (log_d - part_d) : 0.0f;
+      }
       if (a.logp)
         a.logp[row] = r.ignored ? 0.0f
                       : r.bad   ? NAN

@@ -86,7 +86,7 @@ class _Call:
         temp, temp_at = _per_row(temperature, "temperature", R, index, 1.0)
         p = B.FlceLogitsParams(R, V, 0, logits.stride(0), V, 0, 0, 0, 0, 0, ignore_index, rep, freq,
                                pres, temp, _DTYPES[logits.dtype], _DTYPES[out_dtype], 0, 0, 0, 0,
-                               bool(validate))
+                               bool(validate), 0)
         rows = B.FlceLogitsRows(None, None, None, rep_at, freq_at, pres_at, temp_at)
         if tokens is not None:
             p.ld_tokens = _lists(tokens, "tokens", R, index, tuple(_WHOLE))
@@ -204,26 +204,29 @@ def _refuse_overlap(out, logits):
 def flce_logits_logprob(logits, labels, tokens=None, prompt_lens=None, lengths=None,
                         repetition_penalty=1.0, frequency_penalty=0.0, presence_penalty=0.0,
                         bias_ids=None, bias_values=None, allowed=None, temperature=1.0,
-                        ignore_index=IGNORE_INDEX, validate=False, stream=None):
+                        ignore_index=IGNORE_INDEX, validate=False, stream=None, split_lse=False):
     """(logp, entropy, lse), fp32 [R]: of labels [R] int64 under softmax(z), z not stored.
 
-    The options are flce_process_logits'.  A row whose label is ignore_index has logp and entropy
-    0; a label outside [0, V) gives NaN (with validate the call waits and raises); one that is not
-    allowed -inf."""
+    With split_lse, lse is [2, R]: behind each row's, what its rounding to fp32 left off, for a
+    gradient that keeps its digits where logits are large.  The options are flce_process_logits'.
+    A row whose label is ignore_index has logp and entropy 0; a label outside [0, V) gives NaN
+    (with validate the call waits and raises); one that is not allowed -inf."""
     if stream is not None:
         return _on(stream, flce_logits_logprob, logits, labels, tokens, prompt_lens, lengths,
                    repetition_penalty, frequency_penalty, presence_penalty, bias_ids, bias_values,
-                   allowed, temperature, ignore_index, validate)
+                   allowed, temperature, ignore_index, validate, split_lse=split_lse)
     lib = B._lib or B.load_library()
     c = _Call(logits, tokens, prompt_lens, lengths, repetition_penalty, frequency_penalty,
               presence_penalty, bias_ids, bias_values, allowed, temperature, ignore_index, None,
               validate)
     _labels(labels, c.R, c.index)
-    return _logprob(lib, c, logits, labels)
+    return _logprob(lib, c, logits, labels, split_lse)
 
 
-def _logprob(lib, c, logits, labels):
-    logp, ent, lse = torch.empty(3, c.R, dtype=torch.float32, device=c.index).unbind(0)
+def _logprob(lib, c, logits, labels, split_lse):
+    c.p.split_lse = bool(split_lse)
+    logp, ent = torch.empty(2, c.R, dtype=torch.float32, device=c.index).unbind(0)
+    lse = torch.empty((2, c.R) if split_lse else c.R, dtype=torch.float32, device=c.index)
     ws = c.workspace()
     code = lib.flce_logits(ctypes.byref(c.p), ctypes.byref(c.rows), logits.data_ptr(),
                            labels.data_ptr(), None, lse.data_ptr(), logp.data_ptr(),
@@ -234,10 +237,11 @@ def _logprob(lib, c, logits, labels):
     return logp, ent, lse
 
 
-def _row_grad(g, name, R, index):
-    if g is not None and (g.dtype is not torch.float32 or g.shape != (R,)
+def _row_grad(g, name, R, index, shape=None):
+    shape = shape or (R,)
+    if g is not None and (g.dtype is not torch.float32 or g.shape != shape
                           or g.get_device() != index or not g.is_contiguous()):
-        raise TypeError(f"{name} must be a contiguous fp32 [{R}] tensor on cuda:{index}")
+        raise TypeError(f"{name} must be a contiguous fp32 {list(shape)} tensor on cuda:{index}")
 
 
 def flce_logits_logprob_backward(logits, labels, lse, entropy, g_logp, g_entropy, tokens=None,
@@ -246,7 +250,8 @@ def flce_logits_logprob_backward(logits, labels, lse, entropy, g_logp, g_entropy
                                  bias_values=None, allowed=None, temperature=1.0,
                                  ignore_index=IGNORE_INDEX, grad_dtype=None, stream=None):
     """dlogits [R, V] (logits' type, or fp32 with grad_dtype) for upstream gradients g_logp and
-    g_entropy, fp32 [R] or None (zero); lse and entropy as flce_logits_logprob gave them.  Rows
+    g_entropy, fp32 [R] or None (zero); lse ([R] or [2, R]) and entropy as flce_logits_logprob gave
+    them.  With lse [R] a probability is off by its rounding, 2^-24 |lse| of itself.  Rows
     that are ignored, or of which the mask leaves nothing, get zeros."""
     if stream is not None:
         return _on(stream, flce_logits_logprob_backward, logits, labels, lse, entropy, g_logp,
@@ -258,9 +263,11 @@ def flce_logits_logprob_backward(logits, labels, lse, entropy, g_logp, g_entropy
               presence_penalty, bias_ids, bias_values, allowed, temperature, ignore_index,
               grad_dtype, False)
     _labels(labels, c.R, c.index)
-    for name, t in (("lse", lse), ("entropy", entropy), ("g_logp", g_logp),
-                    ("g_entropy", g_entropy)):
+    split = isinstance(lse, torch.Tensor) and lse.dim() == 2
+    _row_grad(lse, "lse", c.R, c.index, (2, c.R) if split else None)
+    for name, t in (("entropy", entropy), ("g_logp", g_logp), ("g_entropy", g_entropy)):
         _row_grad(t, name, c.R, c.index)
+    c.p.split_lse = split
     if lse is None or (g_entropy is not None and entropy is None):
         raise ValueError("the gradient needs lse, and that of the entropy needs entropy")
     return _logprob_backward(lib, c, logits, labels, lse, entropy, g_logp, g_entropy)
@@ -283,7 +290,7 @@ class _LogitsLogprob(torch.autograd.Function):
         lib = B._lib or B.load_library()
         c = _Call(logits, *options)
         _labels(labels, c.R, c.index)
-        logp, ent, lse = _logprob(lib, c, logits, labels)
+        logp, ent, lse = _logprob(lib, c, logits, labels, True)
         # the options' tensors are saved for the check that nothing has changed them since
         ctx.save_for_backward(logits, labels, lse, ent,
                               *(t for t in options if isinstance(t, torch.Tensor)))
