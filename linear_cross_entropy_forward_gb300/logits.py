@@ -225,8 +225,10 @@ def flce_logits_logprob(logits, labels, tokens=None, prompt_lens=None, lengths=N
 
 def _logprob(lib, c, logits, labels, split_lse):
     c.p.split_lse = bool(split_lse)
-    logp, ent = torch.empty(2, c.R, dtype=torch.float32, device=c.index).unbind(0)
-    lse = torch.empty((2, c.R) if split_lse else c.R, dtype=torch.float32, device=c.index)
+    # (each a tensor of its own: views of one could not be changed in place behind autograd, and would
+    # share the version that its check goes by)
+    logp, ent, lse = (torch.empty(shape, dtype=torch.float32, device=c.index)
+                      for shape in (c.R, c.R, (2, c.R) if split_lse else c.R))
     ws = c.workspace()
     code = lib.flce_logits(ctypes.byref(c.p), ctypes.byref(c.rows), logits.data_ptr(),
                            labels.data_ptr(), None, lse.data_ptr(), logp.data_ptr(),
