@@ -376,6 +376,13 @@ __device__ __forceinline__ void update8(const Slot& s, const StepArgs& a, const 
     v[i] = STATE8 ? s0 : v0;
     v[i + 1] = STATE8 ? s1 : v1;
   }
+  // Behind the tensor's last element the states are zero, as they have been so far: 0 / eps is NaN for an eps
+  // of 0, and so is 0 times a factor that is not finite.
+  if (left < kPer) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (i >= left) w[i] = m[i] = v[i] = 0.0f;
+  }
   uint2 cm, cs;
   if constexpr (STATE8) {
     uint32_t r1[kPer], r2[kPer];
