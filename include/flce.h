@@ -498,6 +498,17 @@ int flce_linear_backward(const flce_linear_params* params, const void* dout, con
                          const void* weight, const void* preact, void* dx, void* dweight,
                          void* dbias, void* workspace, size_t ws_bytes, void* stream);
 
+/* A wait of these two calls' products that runs out (2 s) is reported by flce_status and validate, as
+ * FLCE_ERR_TIMEOUT, and what the product writes is then NaN throughout.  Self-tests: the calls with
+ * copies that never come, at the first block (pair of blocks) of each product. */
+int flce_selftest_linear_timeout(const flce_linear_params* params, const void* x, const void* weight,
+                                 const void* residual, void* y, void* preact, void* workspace,
+                                 size_t ws_bytes, void* stream);
+int flce_selftest_linear_backward_timeout(const flce_linear_params* params, const void* dout,
+                                          const void* x, const void* weight, const void* preact,
+                                          void* dx, void* dweight, void* workspace, size_t ws_bytes,
+                                          void* stream);
+
 /* Rows of logits as a sampler sees them, per row in fp32:
  *   l = seen ? (l > 0 ? l / repetition : l * repetition) : l
  *   l = l - frequency * n - presence * [n > 0] + the sum of its biases

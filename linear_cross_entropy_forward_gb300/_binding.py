@@ -143,7 +143,8 @@ EXPORTED = ("flce_workspace_size", "flce_forward", "flce_backward", "flce_status
             "flce_selftest_policy_timeout", "flce_selftest_preference_timeout",
             "flce_embedding_check_params", "flce_embedding_workspace_size", "flce_embedding",
             "flce_embedding_backward", "flce_linear_check_params", "flce_linear_workspace_size",
-            "flce_linear", "flce_linear_backward", "flce_logits_check_params", "flce_logits",
+            "flce_linear", "flce_linear_backward", "flce_selftest_linear_timeout",
+            "flce_selftest_linear_backward_timeout", "flce_logits_check_params", "flce_logits",
             "flce_logits_backward", "flce_adamw_check_params", "flce_adamw_workspace_size",
             "flce_grad_norm", "flce_adamw_step")
 
@@ -248,6 +249,8 @@ def _open(path: str) -> ctypes.CDLL:
     lib.flce_adamw_workspace_size.restype = sz
     for name, args in (("linear_check_params", [D]), ("linear", [D] + [vp] * 7 + [sz, vp]),
                        ("linear_backward", [D] + [vp] * 8 + [sz, vp]),
+                       ("selftest_linear_timeout", [D] + [vp] * 6 + [sz, vp]),
+                       ("selftest_linear_backward_timeout", [D] + [vp] * 7 + [sz, vp]),
                        ("logits_check_params", [G]), ("logits", [G, W] + [vp] * 7 + [sz, vp]),
                        ("logits_backward", [G, W] + [vp] * 8 + [sz, vp]),
                        ("adamw_check_params", [A]), ("grad_norm", [A, vp, vp, vp, sz, vp]),

@@ -21,6 +21,28 @@ struct LinearOut {
   int32_t out_f32;
 };
 
+// Arrays that a call writes (NULL: none), of which nothing may be taken for a result if a wait runs out.
+// Whole 2-byte elements from a 16-byte boundary on.
+struct Results {
+  void* p[2];
+  int64_t bytes[2];
+};
+
+// Every bit set is NaN in bf16 and in fp32.  By all threads of a block whose wait ran out, at its end: what
+// it has left out is NaN then, and so is what other blocks finished before, seconds ago.
+__device__ __forceinline__ void leave_nan(const Results& r) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    uint8_t* p = static_cast<uint8_t*>(r.p[k]);
+    if (!p) continue;
+    const int64_t whole = r.bytes[k] / 16 * 16;
+    for (int64_t i = int64_t(threadIdx.x) * 16; i < whole; i += int64_t(blockDim.x) * 16)
+      *reinterpret_cast<uint4*>(p + i) = make_uint4(~0u, ~0u, ~0u, ~0u);
+    for (int64_t i = whole + threadIdx.x * 2; i < r.bytes[k]; i += blockDim.x * 2)
+      *reinterpret_cast<uint16_t*>(p + i) = 0xffff;
+  }
+}
+
 __device__ __forceinline__ float sigmoid_fast(float x) {
   return fast_rcp(1.0f + fast_ex2(-kLog2e * x));
 }

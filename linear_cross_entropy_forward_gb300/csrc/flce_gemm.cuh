@@ -146,6 +146,7 @@ struct GemmShape {
   unsigned int* sched;
   // every pair has one tile at most: the counters are not looked at, and may hold anything
   int one_round;
+  int lost;  // the self-test of the bounded waits: the first pair's copies end halfway down a tile's depth
   // extents (inner, outer) of the arrays behind the A and B tensor maps: the
   // FLCE_DEBUG build checks every TMA box against them
   int64_t a_inner, a_outer, b_inner, b_outer;
@@ -191,6 +192,7 @@ struct EpiArgs {
   // EPI_LINEAR
   LinearOut lin;
   int clear;            // the error word is cleared by the kernel itself
+  Results results;      // left as NaN if a wait runs out (the dense layer's; the head's calls report it)
 };
 
 // A bounds check of the FLCE_DEBUG build: true in the regular build; in the debug
@@ -748,6 +750,8 @@ __global__ void __launch_bounds__(pair_threads<EPI>(), 1)
           mapa_shared(smem_u32(const_cast<int*>(abort_flag)), prank ^ 1u);
       uint32_t stage = 0, phase = 0;
       bool ok = true;
+      const bool lost = sh.lost && cid == 0;
+      const int k_blocks = lost ? sh.k_blocks / 2 : sh.k_blocks;
       for (int i = 0; ok; ++i) {
         const int t = take_tile(i, true);
         if (t >= total) break;
@@ -755,7 +759,7 @@ __global__ void __launch_bounds__(pair_threads<EPI>(), 1)
         tile_coords(t, sh, mt, nt);
         const int am0 = mt * PAIR_BM + static_cast<int>(prank) * 128 + sh.a_mn_off;
         const int bn0 = nt * TN + static_cast<int>(prank) * C::B_ROWS + sh.b_mn_off;
-        for (int kb = 0; kb < sh.k_blocks; ++kb) {
+        for (int kb = 0; kb < k_blocks; ++kb) {
           if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, ea.err)) {
             ok = false;
             break;
@@ -783,6 +787,7 @@ __global__ void __launch_bounds__(pair_threads<EPI>(), 1)
             phase ^= 1u;
           }
         }
+        if (lost) ok = false;
       }
       // drain: every stage this CTA filled has been released by the leader's UMMAs
       // (its commits target this CTA's barriers, so they must land before exit)
@@ -986,6 +991,7 @@ __global__ void __launch_bounds__(pair_threads<EPI>(), 1)
   cluster_sync();
   tc_fence_after();
   if (warp == 1) tmem_dealloc_pair(tmem_base, TMEM_COLS);
+  if (*abort_flag) leave_nan(ea.results);
 }
 
 // Host-side launcher of the pair kernel: clusters of 2 CTAs, as many as can be

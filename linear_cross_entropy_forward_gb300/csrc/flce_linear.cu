@@ -122,10 +122,12 @@ struct SplitArgs {
   int32_t M, N;
   int32_t tt, m_tiles, k_blocks, stages;
   int32_t parts;  // accumulators that the depth is spread over
+  int32_t lost;   // the self-test of the bounded waits: the first block's copies end halfway down its depth
   LinearOut out;
   uint32_t* err;
   int32_t clear;
   int64_t a_inner, a_outer, b_inner, b_outer;
+  Results results;
 };
 constexpr int kSplitThreads = 320;  // producer, issuer, eight epilogue warps
 
@@ -186,7 +188,8 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
                      pol_b = l2_policy(L2_EVICT_LAST);
       int stage = 0;
       uint32_t phase = 0;
-      for (int kb = kb0; kb < kb1; ++kb) {
+      const int last = a.lost && blockIdx.x == 0 ? (kb0 + kb1) / 2 : kb1;
+      for (int kb = kb0; kb < last; ++kb) {
         if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, a.err)) break;
         const int k0 = kb * BK;
 #if FLCE_DEBUG
@@ -316,6 +319,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
   }
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, cols);
+  if (*abort_flag) leave_nan(a.results);  // (behind what the cluster's other blocks made of its sums)
 }
 
 // ------------------------------------------------------------------ dz and db
@@ -622,9 +626,14 @@ Plan choose(const Product& g, int sms, bool layer, const LinearOut& o) {
   return best;
 }
 
+Results results_of(const Product& g, const LinearOut& o) {
+  const int64_t n = g.rows * g.cols;
+  return Results{{o.y, o.preact}, {n * (o.out_f32 ? 4 : 2), n * 2}};
+}
+
 template <bool A_MN, bool B_MN>
 int launch_split(const Product& g, const Plan& s, const LinearOut& out, uint32_t* err, bool clear,
-                 cudaStream_t st) {
+                 bool lost, cudaStream_t st) {
   auto kernel = split_kernel<A_MN, B_MN>;
   static std::atomic<uint64_t> ready{0};
   int dev = 0;
@@ -650,8 +659,10 @@ int launch_split(const Product& g, const Plan& s, const LinearOut& out, uint32_t
   a.stages = s.stages;
   a.parts = out.out_f32 ? parts_of(s.tt, a.k_blocks / s.size) : 1;
   a.out = out;
+  a.results = results_of(g, out);
   a.err = err;
   a.clear = clear;
+  a.lost = lost;
   a.a_inner = A_MN ? g.cols : g.depth;
   a.a_outer = A_MN ? g.depth : g.cols;
   a.b_inner = B_MN ? g.rows : g.depth;
@@ -673,10 +684,10 @@ int launch_split(const Product& g, const Plan& s, const LinearOut& out, uint32_t
 }
 
 int run_split(const Product& g, const Plan& s, const LinearOut& out, uint32_t* err, bool clear,
-              cudaStream_t st) {
-  if (g.left_mn) return launch_split<true, true>(g, s, out, err, clear, st);  // dweight: both are
-  return g.right_mn ? launch_split<true, false>(g, s, out, err, clear, st)
-                    : launch_split<false, false>(g, s, out, err, clear, st);
+              bool lost, cudaStream_t st) {
+  if (g.left_mn) return launch_split<true, true>(g, s, out, err, clear, lost, st);  // dweight: both are
+  return g.right_mn ? launch_split<true, false>(g, s, out, err, clear, lost, st)
+                    : launch_split<false, false>(g, s, out, err, clear, lost, st);
 }
 
 // Whether every pair has one tile at most, so that the schedule's counters are not needed.
@@ -686,7 +697,7 @@ bool one_round(const Product& g, bool layer, int width) {
 
 // The product by CTA pairs; kind 0: a layer's output, 1: dx, 2: dweight.
 int run_pair(const Product& p, int width, int kind, const LinearOut& out, uint32_t* err, int slot,
-             bool clear, cudaStream_t st) {
+             bool clear, bool lost, cudaStream_t st) {
   const Product g = kind ? p
                          : Product{p.right, p.left, p.cols, p.rows, p.depth, p.ld_right, p.ld_left,
                                    p.right_mn, p.left_mn};
@@ -703,6 +714,7 @@ int run_pair(const Product& p, int width, int kind, const LinearOut& out, uint32
   sh.raster = 0;
   sh.sched = reinterpret_cast<unsigned int*>(reinterpret_cast<uint8_t*>(err) + kSched + 8 * slot);
   sh.one_round = one_round(p, kind == 0, width);
+  sh.lost = lost;
   sh.a_inner = g.left_mn ? g.rows : g.depth;
   sh.a_outer = g.left_mn ? g.depth : g.rows;
   sh.b_inner = g.right_mn ? g.cols : g.depth;
@@ -713,6 +725,7 @@ int run_pair(const Product& p, int width, int kind, const LinearOut& out, uint32
   ea.cols = static_cast<int>(g.cols);
   ea.err = err;
   ea.clear = clear;
+  ea.results = results_of(p, out);
   const bool wide = width == 256;
   if (kind == 0) {
     ea.lin = out;
@@ -788,43 +801,29 @@ int launch_dz(const DzArgs& a, int64_t strips, cudaStream_t st) {
 
 // One gradient's product.
 int run_gradient(const Product& g, const Plan& plan, int kind, void* out, uint32_t* err, int slot,
-                 cudaStream_t st) {
+                 bool lost, cudaStream_t st) {
   LinearOut o{};
   o.y = out;
   o.ld = g.cols;
-  return plan.width ? run_pair(g, plan.width, kind, o, err, slot, false, st)
-                    : run_split(g, plan, o, err, false, st);
+  return plan.width ? run_pair(g, plan.width, kind, o, err, slot, false, lost, st)
+                    : run_split(g, plan, o, err, false, lost, st);
 }
 
 // Below this many microseconds of the smaller of two products, running them side by side costs the host
 // more than it saves the GPU.
 constexpr double kSideBySide = 10.0;
 
-}  // namespace
-}  // namespace flce
-
-using namespace flce;
-
-extern "C" {
-
-int flce_linear_check_params(const flce_linear_params* p) { return check(p); }
-
-size_t flce_linear_workspace_size(const flce_linear_params* p, int backward) {
-  if (check(p) != FLCE_OK) return 0;
-  if (backward) return bwd_layout(p).total;
-  return kHeader;
-}
-
-int flce_linear(const flce_linear_params* p, const void* x, const void* weight, const void* bias,
-                const void* residual, void* y, void* preact, void* workspace, size_t ws_bytes,
-                void* stream) {
+// The calls; lost: the self-test of the bounded waits.
+int forward(const flce_linear_params* p, const void* x, const void* weight, const void* bias,
+            const void* residual, void* y, void* preact, void* workspace, size_t ws_bytes,
+            void* stream, bool lost) {
   int rc = check(p);
   if (rc) return rc;
   if (!weight || !workspace || (p->M > 0 && (!x || !y))) return FLCE_ERR_BAD_ARG;
   if ((addr(x) | addr(weight) | addr(residual) | addr(y) | addr(preact)) & 15 || addr(bias) & 1 ||
       addr(workspace) & 255)
     return FLCE_ERR_ALIGN;
-  if (ws_bytes < flce_linear_workspace_size(p, 0)) return FLCE_ERR_WS_TOO_SMALL;
+  if (ws_bytes < kHeader) return FLCE_ERR_WS_TOO_SMALL;
   int sms;
   if ((rc = require_device(&sms))) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -849,15 +848,15 @@ int flce_linear(const flce_linear_params* p, const void* x, const void* weight, 
   // microsecond or two of a small layer's ten.
   const bool ahead = FLCE_DEBUG || (plan.width && !one_round(g, true, plan.width));
   if (ahead && (rc = rc_of(cudaMemsetAsync(ws, 0, kHeader, st)))) return rc;
-  rc = plan.width ? run_pair(g, plan.width, 0, o, err, 0, !ahead, st)
-                  : run_split(g, plan, o, err, !ahead, st);
+  rc = plan.width ? run_pair(g, plan.width, 0, o, err, 0, !ahead, lost, st)
+                  : run_split(g, plan, o, err, !ahead, lost, st);
   if (rc) return rc;
   return p->validate ? read_status(ws, st) : FLCE_OK;
 }
 
-int flce_linear_backward(const flce_linear_params* p, const void* dout, const void* x,
-                         const void* weight, const void* preact, void* dx, void* dweight,
-                         void* dbias, void* workspace, size_t ws_bytes, void* stream) {
+int backward(const flce_linear_params* p, const void* dout, const void* x,
+             const void* weight, const void* preact, void* dx, void* dweight, void* dbias,
+             void* workspace, size_t ws_bytes, void* stream, bool lost) {
   int rc = check(p);
   if (rc) return rc;
   if (!workspace || (p->M > 0 && (!dout || (dx && !weight) || (dweight && !x) ||
@@ -919,10 +918,49 @@ int flce_linear_backward(const flce_linear_params* p, const void* dout, const vo
   cudaStream_t side = st;
   const bool both = dx && dweight && x_plan.us >= kSideBySide && w_plan.us >= kSideBySide;
   if (both && (rc = side_fork(st, &side))) return rc;
-  if (dx && (rc = run_gradient(x_product, x_plan, 1, dx, err, 0, st))) return rc;
-  if (dweight && (rc = run_gradient(w_product, w_plan, 2, dweight, err, 1, side))) return rc;
+  if (dx && (rc = run_gradient(x_product, x_plan, 1, dx, err, 0, lost, st))) return rc;
+  if (dweight && (rc = run_gradient(w_product, w_plan, 2, dweight, err, 1, lost, side))) return rc;
   if (both && (rc = side_join(st))) return rc;
   return p->validate ? read_status(ws, st) : FLCE_OK;
+}
+
+}  // namespace
+}  // namespace flce
+
+using namespace flce;
+
+extern "C" {
+
+int flce_linear_check_params(const flce_linear_params* p) { return check(p); }
+
+size_t flce_linear_workspace_size(const flce_linear_params* p, int backward) {
+  if (check(p) != FLCE_OK) return 0;
+  if (backward) return bwd_layout(p).total;
+  return kHeader;
+}
+
+int flce_linear(const flce_linear_params* p, const void* x, const void* weight, const void* bias,
+                const void* residual, void* y, void* preact, void* workspace, size_t ws_bytes,
+                void* stream) {
+  return forward(p, x, weight, bias, residual, y, preact, workspace, ws_bytes, stream, false);
+}
+
+int flce_linear_backward(const flce_linear_params* p, const void* dout, const void* x,
+                         const void* weight, const void* preact, void* dx, void* dweight,
+                         void* dbias, void* workspace, size_t ws_bytes, void* stream) {
+  return backward(p, dout, x, weight, preact, dx, dweight, dbias, workspace, ws_bytes, stream, false);
+}
+
+int flce_selftest_linear_timeout(const flce_linear_params* p, const void* x, const void* weight,
+                                 const void* residual, void* y, void* preact, void* workspace,
+                                 size_t ws_bytes, void* stream) {
+  return forward(p, x, weight, nullptr, residual, y, preact, workspace, ws_bytes, stream, true);
+}
+
+int flce_selftest_linear_backward_timeout(const flce_linear_params* p, const void* dout, const void* x,
+                                          const void* weight, const void* preact, void* dx, void* dweight,
+                                          void* workspace, size_t ws_bytes, void* stream) {
+  return backward(p, dout, x, weight, preact, dx, dweight, nullptr, workspace, ws_bytes, stream, true);
 }
 
 }  // extern "C"
