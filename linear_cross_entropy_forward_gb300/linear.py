@@ -78,6 +78,12 @@ def _apart(outs, inputs):
                 raise ValueError(f"{name} shares memory with {other}")
 
 
+def _aligned(t):
+    """t, or a copy of it from a 16-byte boundary on: a row slice of odd width, as the gradient behind a
+    torch.cat over tokens is, begins anywhere."""
+    return t if t is None or t.data_ptr() & 15 == 0 else t.clone()
+
+
 def flce_linear(x, weight, bias=None, activation=None, residual=None, weight_layout="hv",
                 out_dtype=torch.bfloat16, need_preact=False, validate=False, workspace=None,
                 stream=None, out=None):
@@ -86,7 +92,8 @@ def flce_linear(x, weight, bias=None, activation=None, residual=None, weight_lay
     x [..., K] and weight bf16, K a multiple of 8, and N too for a [K, N] weight; bias bf16 [N];
     activation: None, 'relu', 'gelu', 'gelu_tanh' or 'silu'; residual of y's shape and type (out
     may be the residual itself).  Sums are fp32, rounded once.  With need_preact returns (y, z): z =
-    x W + bias in bf16, as the backward takes it.
+    x W + bias in bf16, as the backward takes it.  x and weight begin at a 16-byte boundary; a
+    residual or out that does not is copied.
     """
     if stream is not None:
         return _on(stream, flce_linear, x, weight, bias, activation, residual, weight_layout,
@@ -110,13 +117,16 @@ def flce_linear(x, weight, bias=None, activation=None, residual=None, weight_lay
         _refuse(x, weight, bias, activation, residual, weight_layout, out_dtype, out)
         raise
     p = B.FlceLinearParams(x.numel() // K if K else 0, N, K, layout, act, out_code, bool(validate))
-    given = out is not None
-    if not given:
+    given = out
+    if given is None:
         out = torch.empty(shape, dtype=out_dtype, device=x.device)
     else:
         own = residual is not None and out.data_ptr() == residual.data_ptr()
         _apart([("out", out)], [("x", x), ("weight", weight), ("bias", bias),
                                 ("residual", None if own else residual)])
+        if out.data_ptr() & 15:
+            out = torch.empty(shape, dtype=out_dtype, device=x.device)
+    residual = _aligned(residual)
     z = torch.empty(shape, dtype=bf16, device=x.device) if need_preact else None
     ws = torch.empty(_HEADER, dtype=torch.uint8, device=x.device) if workspace is None \
         else _workspace(linear_workspace_size(p), dev, workspace)
@@ -125,7 +135,10 @@ def flce_linear(x, weight, bias=None, activation=None, residual=None, weight_lay
                            _raw_stream(dev))
     if code:
         B._check(code)
-    if given:
+    if given is not None:
+        if out is not given:
+            given.detach().copy_(out)
+            out = given
         _written(out)
     return (out, z) if need_preact else out
 
@@ -147,8 +160,9 @@ def flce_linear_backward(dout, x, weight, preact=None, activation=None, weight_l
                          workspace=None, stream=None, out=None):
     """(dx, dweight, dbias) of flce_linear, bf16, shaped like x, weight and [N]; None where not
     wanted.  dout: of y's shape and type (bf16 or fp32); it is the residual's gradient as it is.
-    preact: z of the forward, where there is an activation.  dz = dout act'(z) is rounded to bf16
-    for the products; dbias sums it unrounded.  out: (dx, dweight, dbias) to write into."""
+    preact: z of the forward, where there is an activation; it and dout are copied where they do
+    not begin at a 16-byte boundary.  dz = dout act'(z) is rounded to bf16 for the products; dbias
+    sums it unrounded.  out: (dx, dweight, dbias) to write into."""
     if stream is not None:
         return _on(stream, flce_linear_backward, dout, x, weight, preact, activation,
                    weight_layout, need_dx, need_dweight, need_dbias, validate, workspace, out=out)
@@ -187,6 +201,7 @@ def flce_linear_backward(dout, x, weight, preact=None, activation=None, weight_l
         _apart([(name, t) for (name, _, _), t in zip(wanted, out)],
                [("dout", dout), ("x", x), ("weight", weight), ("preact", preact if act else None)])
     dx, dw, db = out
+    dout, preact = _aligned(dout), _aligned(preact) if act else None
     ws = _workspace(size, dev, workspace)
     code = lib.flce_linear_backward(
         ctypes.byref(p), dout.data_ptr(), x.data_ptr(), weight.data_ptr(),
