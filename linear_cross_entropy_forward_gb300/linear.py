@@ -254,4 +254,6 @@ def linear(x, weight, bias=None, activation=None, residual=None, weight_layout="
            out_dtype=torch.bfloat16):
     """act(x W + bias) + residual, differentiable by x, weight, bias and residual; see
     flce_linear."""
+    if not torch.is_grad_enabled():  # (a Function is told that its inputs want gradients all the same)
+        return flce_linear(x, weight, bias, activation, residual, weight_layout, out_dtype)
     return _Linear.apply(x, weight, bias, residual, activation, weight_layout, out_dtype)
