@@ -844,7 +844,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
       if (a.logp)
         a.logp[row] = r.ignored ? 0.0f
                       : r.bad   ? NAN
-                                : none || zy == -INFINITY ? -INFINITY : (zy - all.m) - log_d;
+                      : none    ? -INFINITY
+                                : (zy - all.m) - log_d;
       if (a.entropy) {
         const float H = none ? 0.0f : log_d - kLn2 * __fdiv_rn(all.s, all.d);
         a.entropy[row] = r.ignored ? 0.0f : r.bad ? NAN : H;
