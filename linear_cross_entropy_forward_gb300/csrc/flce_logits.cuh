@@ -19,7 +19,7 @@
 // thread per entry beside the pass over all logits: 87 and 240.  Sorting a row's tokens by blocks in a
 // launch ahead: 192 against 195 after 8192 tokens, 205 against 190 for 700 x 152064 after 4000, and ahead
 // only after tens of thousands.)  Biases only mark their columns' counters; a
-// marked column sums its biases from the row's list, in the list's order.
+// marked column adds its biases from the row's list, one by one in the list's order.
 //
 // The running maximum m, d = sum 2^u and s = sum 2^u u with u = log2(e) (z - m) stay in registers, are
 // joined in the block and then in the cluster, in a fixed order:  lse = m + ln d,
@@ -558,11 +558,9 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
       if (n & COUNTER::kCount) y = fmaf(-r.freq, static_cast<float>(n & COUNTER::kCount), y) - r.pres;
     }
     if (n & COUNTER::kBiased) {
-      float sum = 0.0f;
 #pragma unroll 1
       for (int j = 0; j < n_bias; ++j)
-        if (bias_col[j] == c) sum += bias_val[j];
-      y += sum;
+        if (bias_col[j] == c) y += bias_val[j];
     }
     return y;
   };
