@@ -80,6 +80,11 @@ def flce_grad_norm(grads, scale=1.0, workspace=None, stream=None):
     return norm
 
 
+def _refuse_max_norm(max_norm):
+    if max_norm is not None and not max_norm > 0:
+        raise ValueError(f"max_norm must be positive or None, got {max_norm}")
+
+
 class AdamW:
     """AdamW on a list of CUDA tensors (bf16, fp16 or fp32, contiguous, of one device).
 
@@ -100,6 +105,9 @@ class AdamW:
         norm is infinite or NaN changes nothing (fp16 gradients under a loss scale, which
         grad_scale divides out).
 
+    lr, max_norm and grad_scale are attributes that each step reads, so that a schedule or a loss scale
+    may change them; a captured step keeps those of its capture, but for an lr that is a tensor.
+
     The states of all tensors lie in flat tensors, each tensor's from a multiple of 128 on
     (`offsets`): state_dict() has them, as they are, not copies.
     """
@@ -112,8 +120,7 @@ class AdamW:
             raise ValueError("AdamW needs at least one tensor")
         if state_bits not in _STATE:
             raise ValueError(f"state_bits must be 32 or 8, got {state_bits!r}")
-        if max_norm is not None and not max_norm > 0:
-            raise ValueError(f"max_norm must be positive or None, got {max_norm}")
+        _refuse_max_norm(max_norm)
         index = _current_device()
         for i, p in enumerate(self.params):
             if not (isinstance(p, torch.Tensor) and p.dtype in _DTYPES
@@ -141,8 +148,8 @@ class AdamW:
         self._table["offset"] = np.cumsum(padded) - padded
         self.offsets = self._table["offset"].tolist()
         numel = int(padded.sum())
-        self.lr, self.state_bits, self.max_norm = lr, state_bits, max_norm
-        self._need_norm = max_norm is not None or skip_nonfinite
+        self.lr, self.state_bits = lr, state_bits
+        self.max_norm, self.grad_scale, self._skip = max_norm, grad_scale, bool(skip_nonfinite)
         self._params = _adamw_params(n, numel, 0.0 if isinstance(lr, torch.Tensor) else lr, betas,
                                      eps, grad_scale, max_norm, state_bits, seed, skip_nonfinite)
         self._ref = ctypes.byref(self._params)
@@ -175,7 +182,8 @@ class AdamW:
         return {"step": self.step_count, "master": self.master, **self._state}
 
     def load_state_dict(self, state):
-        """Copies what state_dict() of an optimizer over the same tensors gave."""
+        """Copies what state_dict() of an optimizer over the same tensors, in the same order, gave.
+        (Of the flat tensors only the sizes together can be compared.)"""
         mine = self.state_dict()
         if set(state) != set(mine):
             raise ValueError(f"state must hold {sorted(mine)}, got {sorted(state)}")
@@ -223,10 +231,12 @@ class AdamW:
             lr_ptr = self.lr.data_ptr()
         else:
             self._params.lr = self.lr
+        _refuse_max_norm(self.max_norm)
+        self._params.max_norm, self._params.grad_scale = self.max_norm or 0.0, self.grad_scale
         stream = _raw_stream(index)
         ws = self._workspace
         norm = None
-        if self._need_norm:
+        if self._skip or self.max_norm is not None:
             norm = torch.empty(1, dtype=torch.float32, device=index)
             code = lib.flce_grad_norm(self._ref, table, norm.data_ptr(),
                                       ws.data_ptr(), ws.numel(), stream)
