@@ -169,6 +169,7 @@ class AdamW:
                 codes = torch.zeros(numel, dtype=torch.uint8, device=index)
                 self._state[name] = codes.view(torch.float8_e4m3fn)
                 self._state[name + "_scale"] = torch.zeros(numel // BLOCK, device=index)
+        self._kept = [t for t in self.state_dict().values() if t is not None]
         if master:
             self.load_master()
 
@@ -254,5 +255,5 @@ class AdamW:
             self.step_count.data_ptr(), ws.data_ptr(), ws.numel(), stream)
         if code:
             B._check(code)
-        _written(*self.params, self.step_count, self.master, *s.values())
+        _written(self.params + self._kept)
         return norm

@@ -210,7 +210,7 @@ def flce_linear_backward(dout, x, weight, preact=None, activation=None, weight_l
     if code:
         B._check(code)
     if given:
-        _written(dx, dw, db)
+        _written([t for t in (dx, dw, db) if t is not None])
     return dx, dw, db
 
 

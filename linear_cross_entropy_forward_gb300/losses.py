@@ -55,10 +55,10 @@ def _on(stream, call, *args, **kw):
         return call(*args, **kw)
 
 
-def _written(*tensors):
-    """Tells autograd that the library has changed these tensors (or None) of the caller's: a backward
-    that saved one of them then raises instead of using the new values."""
-    torch.autograd.graph.increment_version([t for t in tensors if t is not None])
+def _written(tensors):
+    """Tells autograd that the library has changed these tensors (one, or a list) of the caller's: a
+    backward that saved one of them then raises instead of using the new values."""
+    torch.autograd.graph.increment_version(tensors)
 
 
 def _refuse(t, name, dtype, shape, index):
