@@ -28,6 +28,12 @@ struct Results {
   int64_t bytes[2];
 };
 
+// Whether `left` rows (as many as `most` of them) of a column from element `at` on lie in the output.
+__device__ __forceinline__ bool column_ok(const LinearOut& o, const Results& r, int64_t at, int left, int most) {
+  const int rows = left < most ? left : most;
+  return rows <= 0 || (at >= 0 && (at + (rows - 1) * o.ld) * (o.out_f32 ? 4 : 2) < r.bytes[0]);
+}
+
 // Every bit set is NaN in bf16 and in fp32.  By all threads of a block whose wait ran out, at its end: what
 // it has left out is NaN then, and so is what other blocks finished before, seconds ago.
 __device__ __forceinline__ void leave_nan(const Results& r) {

@@ -625,7 +625,8 @@ struct Epilogue<EPI_LINEAR> {
       token += 16;
       if constexpr (AHEAD)
         if (more) linear_residual(ea.lin, at(), left(), next);
-      linear_store_column(ea.lin, to, rows, b, res, v);
+      if (FLCE_CHECK(column_ok(ea.lin, ea.results, to, rows, 16), ea.err))
+        linear_store_column(ea.lin, to, rows, b, res, v);
     }
   };
   template <int CH>

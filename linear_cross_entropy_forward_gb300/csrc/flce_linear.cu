@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
       if (size > 1) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) part[(c + i) * kRows + nl] = x[i];
-      } else if (n_ok) {
+      } else if (n_ok && FLCE_CHECK(column_ok(a.out, a.results, at, rows - c, 16), a.err)) {
         linear_store_column(a.out, at, rows - c, bias, res, x);
       }
     }
@@ -309,7 +309,8 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
           for (int i = 0; i < kDeep; ++i)
             if (m + i < r1) sum[i] += ld_cluster(from + (m + i) * kRows * 4);
         }
-        linear_store_column(a.out, at, r1 - m, bias, res, sum);
+        if (FLCE_CHECK(column_ok(a.out, a.results, at, r1 - m, kDeep), a.err))
+          linear_store_column(a.out, at, r1 - m, bias, res, sum);
       }
     }
     __syncwarp();
