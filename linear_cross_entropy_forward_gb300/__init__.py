@@ -11,7 +11,7 @@ keeps one token chunk's logits instead and skips the backward's recompute.
 Around the head: policy_loss and preference_loss read its log-probabilities,
 linear_policy_loss is the first on top of the head in one call, and embedding is the
 lookup in a (tied) table, each with its gradient.  linear is the dense layer below the head (or
-its logits), process_logits and logits_logprob the distribution that a sampler sees of them, and
+its logits), flce_process_logits and logits_logprob the distribution that a sampler sees of them, and
 AdamW the step that the gradients go into.
 """
 from .adamw import AdamW, flce_grad_norm  # noqa: F401

@@ -45,7 +45,8 @@ def _adamw_params(n_tensors, numel=0, lr=0.0, betas=(0.9, 0.999), eps=1e-8, grad
 def flce_grad_norm(grads, scale=1.0, workspace=None, stream=None):
     """2-norm [1] fp32 of scale * all the given tensors together (bf16, fp16 or fp32, contiguous).
 
-    Squares are summed in fp32 by eight, in 64 bits from there on, in a fixed order.
+    Squares are summed in fp32 by eight (one that leaves fp32's range is infinite, or 0), these in
+    a pair of floats per thread and in 64 bits from the blocks on, in a fixed order.
     workspace: uint8, zero at first and left so, as flce_adamw_workspace_size says."""
     if stream is not None:
         return _on(stream, flce_grad_norm, grads, scale, workspace)

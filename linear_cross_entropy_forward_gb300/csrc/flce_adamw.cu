@@ -178,6 +178,7 @@ __device__ __forceinline__ void store_raw(void* base, int64_t e, int64_t left, i
 }
 
 // ------------------------------------------------------------------ 8-bit states
+// Chris Wellons' lowbias32 (xor-shifts and odd multipliers found by a search for the least bias).
 __device__ __forceinline__ uint32_t mix(uint32_t x) {
   x ^= x >> 16;
   x *= 0x7FEB352Du;
@@ -428,8 +429,8 @@ __device__ __forceinline__ int find_run(const Table<CAP>& t, uint32_t& u, uint32
 }
 
 // Two blocks per SM's worth of registers for fp32 states, whose loads are all of a unit's bytes (600M
-// with masters 2.64 ms, 5.8 TB/s; for four blocks 2.70), four for 8 bits, bound by their arithmetic, some 85
-// instructions per element (300M: 1.01 ms, 4.6 TB/s; for two 1.08).
+// with masters 2.66 ms, 6.3 TB/s; for four blocks 2 % more), four for 8 bits, bound by their arithmetic, some 85
+// instructions per element (300M with masters: 0.97 ms, 5.0 TB/s; for two 7 % more).
 template <bool STATE8, bool MASTER, int CAP>
 __global__ void __launch_bounds__(kThreads, STATE8 ? 4 : 2)
     adamw_kernel(const __grid_constant__ Table<CAP> t, const __grid_constant__ StepArgs a) {

@@ -1096,7 +1096,6 @@ FLCE_DECLARE_LAUNCHER(launch_bwd_dhidden);   // dlogits (K) x weight (K)
 FLCE_DECLARE_LAUNCHER(launch_fwd_stats_vh);    // hidden (K) x weight (K)
 FLCE_DECLARE_LAUNCHER(launch_bwd_dlogits_vh);  // hidden (K) x weight (K)
 FLCE_DECLARE_LAUNCHER(launch_bwd_dhidden_vh);  // dlogits (K) x weight (MN)
-// a dense layer's forward
 // a dense layer's output, transposed
 FLCE_DECLARE_LAUNCHER(launch_linear);     // weight [K,N] (MN) x x (K)
 FLCE_DECLARE_LAUNCHER(launch_linear_vh);  // weight [N,K] (K) x x (K)

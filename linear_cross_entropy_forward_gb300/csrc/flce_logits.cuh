@@ -4,6 +4,7 @@
 //   z = (seen ? (l > 0 ? l / rp : l rp) : l) - fp n - pp [n > 0] + (sum of the biases on it)
 //   z = -inf where not allowed;  z = z / T
 //
+// (the divisions are multiplications by the rounded reciprocals, a rounding of fp32 more)
 // n counts a token among the row's generated tokens, seen says whether it is among prompt or
 // generated ones.  One pass over the logits, so bound by their bytes, in and out.
 //

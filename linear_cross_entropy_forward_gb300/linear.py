@@ -161,8 +161,8 @@ def flce_linear_backward(dout, x, weight, preact=None, activation=None, weight_l
     """(dx, dweight, dbias) of flce_linear, bf16, shaped like x, weight and [N]; None where not
     wanted.  dout: of y's shape and type (bf16 or fp32); it is the residual's gradient as it is.
     preact: z of the forward, where there is an activation; it and dout are copied where they do
-    not begin at a 16-byte boundary.  dz = dout act'(z) is rounded to bf16 for the products; dbias
-    sums it unrounded.  out: (dx, dweight, dbias) to write into."""
+    not begin at a 16-byte boundary.  dz = dout act'(z), of the bf16 z, is rounded to bf16 for the
+    products; dbias sums it unrounded.  out: (dx, dweight, dbias) to write into."""
     if stream is not None:
         return _on(stream, flce_linear_backward, dout, x, weight, preact, activation,
                    weight_layout, need_dx, need_dweight, need_dbias, validate, workspace, out=out)
